@@ -371,6 +371,134 @@ nvfp4_status nvfp4_tree_verify(int64_t M, int64_t K, int64_t N,
                                const int32_t* parent, const int32_t* draft, float* logits, int32_t* greedy,
                                int32_t* result, uint64_t* keys, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged FP8 KV cache: append, attention, compaction, page sharing.
+ *
+ * Layout.  A page holds page_size tokens of every KV head: uint8
+ * [H][page_size][D], E4M3FN bytes under one static decode scale per tensor (as
+ * nvfp4_kv_fp8_encode writes them).  Page p of a layer starts at pages +
+ * p * page_stride bytes, in k_pages and v_pages alike; layer l of a cache of L
+ * layers starts layer_stride bytes after layer l - 1.  table is int32 [B][W]:
+ * token t of sequence b is slot t % page_size of page table[b][t / page_size].
+ * lens is int32 [B]: the committed tokens of each sequence; a negative length
+ * marks a row that is not in use.  The M nodes (rows) of a step are the tokens
+ * lens[b] .. lens[b] + M - 1; with counts (int32 [B], may be NULL) sequence b
+ * has only its first counts[b] of them (more than M counts as M).
+ *   Shapes: D 64, 128 or 256; page_size a power of two, 16 .. 1024; 1 <= H <=
+ *   1024; B <= 65535; W * page_size <= 2^30 and B * W <= 2^29; M <= 65535 and
+ *   B * M <= 2^24; 1 <= P < 2^31 pages; page_stride a multiple of 16, at least
+ *   H * page_size * D and below 2^31.  layer_stride a multiple of 16.
+ *   What the device arrays hold is checked on the device: a token whose
+ *   position lies outside the table, or whose page id lies outside [0, P), is
+ *   not written, not read and not attended.
+ * Row strides (q_stride, k_stride, v_stride) are in values from row b * M + v
+ * to the next, so that q, k and v may be column ranges of one projection's
+ * output; they must be multiples of 16 bytes.
+ * Cites: the page sections "Using NVFP4 quantization to accelerate
+ * Qwen3.6-27B inference" (the KV cache is FP8), "Using tree-based multi-token
+ * prediction to accelerate LLM inference" (one pass over the drafted tree) and
+ * "Reusing KV cache across agent turns" (turns share cached pages and prefill
+ * their suffix). */
+
+/* Writes a step's keys and values into the cache.
+ *   k, v     [B * M] rows of H * D values in dt, device.
+ *   k_scale, v_scale  device floats; the bytes are those of
+ *            nvfp4_kv_fp8_encode with that scale.
+ * Node v of sequence b is written at token lens[b] + v of one layer's pages;
+ * lens is not changed.  Two sequences that share a page must not both append
+ * to it (nvfp4_kv_fork gives each its own partial page). */
+nvfp4_status nvfp4_kv_append(int64_t B, int64_t M, int64_t H, int64_t D, int64_t page_size, int64_t P, int64_t W,
+                             const void* k, const void* v, nvfp4_dtype dt, int64_t k_stride, int64_t v_stride,
+                             const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,
+                             int64_t page_stride, const int32_t* table, const int32_t* lens, const int32_t* counts,
+                             void* stream);
+
+/* Size in bytes of the workspace with which nvfp4_kv_attention splits long
+ * sequences over workgroups (0 for an invalid or empty call).  A function of
+ * its arguments and the current device's compute-unit count. */
+int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size,
+                                           int64_t W, nvfp4_dtype dt);
+
+/* Attention of a step's nodes over the cache, the nodes' own keys and values
+ * included (append them first).  Query head h reads KV head h / (Hq / H).
+ *   q        [B * M] rows of Hq * D values in dt, device.
+ *   sm_scale finite factor of the scores (1 / sqrt(D) in most models).
+ *   parent   int32 [B][M], device, M <= 64: the drafted trees, as
+ *            nvfp4_tree_accept takes them: node v sees the committed tokens,
+ *            itself and its ancestors; a node whose parent lies outside
+ *            [0, v) is a root.  NULL: the nodes are a chain of any length
+ *            (M = 1: the next token; a long chain: a suffix prefill), node v
+ *            sees the committed tokens and nodes 0 .. v.
+ *   out      [B][M][Hq][D] in dt:  sum_t p_t * v_hat_t, p the softmax of
+ *            sm_scale * q . k_hat_t over the tokens the node sees, k_hat and
+ *            v_hat the decoded cache.
+ *   lse      optional out [B][M][Hq] fp32: the logarithm of the softmax's sum.
+ *   workspace  device memory, 16-byte aligned, of workspace_bytes bytes, or
+ *            NULL; with less than nvfp4_kv_attention_workspace_bytes the
+ *            sequences are not split (slower, same contract).  It needs no
+ *            clearing.  Calls that may overlap need one each.
+ * A row that sees nothing (an unused sequence, a node behind counts[b]) gives
+ * zeros and lse = -infinity.  Scores, softmax statistics and sums are fp32; in
+ * bf16 calls the probabilities are rounded to f16 (11 bits) for the product
+ * with the values, in fp32 calls they keep 22 bits.  Cache bytes that no row
+ * sees may hold anything, NaN codes included, behind a sequence's last node. */
+nvfp4_status nvfp4_kv_attention(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t P,
+                                int64_t W, const void* q, nvfp4_dtype dt, int64_t q_stride, float sm_scale,
+                                const float* k_scale, const float* v_scale, const uint8_t* k_pages,
+                                const uint8_t* v_pages, int64_t page_stride, const int32_t* table,
+                                const int32_t* lens, const int32_t* parent, const int32_t* counts, void* out,
+                                float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Keeps the accepted path of each sequence's tree, in all L layers.
+ *   result   int32 [B][3 + M], device, M <= 64: rows as nvfp4_tree_accept and
+ *            nvfp4_tree_verify write them (end node, L accepted, bonus token,
+ *            the path in ascending order).
+ *   new_lens out int32 [B]: lens[b] + 1 + L (the root and the path are now
+ *            committed); an unused row keeps its length.  Must not overlap
+ *            lens.
+ * Token lens[b] + path[i] is moved to token lens[b] + 1 + i.  A path entry
+ * outside [0, M) is not moved. */
+nvfp4_status nvfp4_kv_compact(int64_t L, int64_t B, int64_t M, int64_t H, int64_t D, int64_t page_size, int64_t P,
+                              int64_t W, uint8_t* k_pages, uint8_t* v_pages, int64_t layer_stride,
+                              int64_t page_stride, const int32_t* table, const int32_t* lens, const int32_t* result,
+                              int32_t* new_lens, void* stream);
+
+/* Page pool: which sequence holds which pages, on the device.
+ *   table    int32 [S][W]: the page ids of each sequence, -1 behind them.
+ *   held     int32 [S]: how many pages each sequence holds.
+ *   refs     int32 [P]: how many sequences hold each page.
+ *   free_list int32 [1 + P]: the number F of free pages, then a stack of their
+ *            ids whose top is free_list[F].
+ * An empty pool has table -1, held 0, refs 0 and all P pages on free_list.
+ *
+ * nvfp4_kv_resize: sequence seqs[i] holds ceil(tokens[i] / page_size) pages
+ * afterwards (n <= 1024 entries): missing pages are popped from free_list in
+ * the order of the entries, surplus ones are given up from the back (tokens
+ * 0: all of them).  A given-up page has one holder less, and one that has none
+ * left is pushed onto free_list, in the order of the entries and of the pages
+ * within them.  Pops come before pushes.  An entry is passed over if its
+ * sequence lies outside [0, S), an earlier entry names the same sequence, its
+ * tokens are negative, or it needs more than W pages.
+ *   shortage out int32 [1]: 0, or, when free_list has fewer pages than the
+ *            entries need, how many are missing: nothing is changed then. */
+nvfp4_status nvfp4_kv_resize(int64_t n, int64_t S, int64_t W, int64_t P, int64_t page_size, int32_t* table,
+                             int32_t* held, int32_t* refs, int32_t* free_list, const int32_t* seqs,
+                             const int32_t* tokens, int32_t* shortage, void* stream);
+
+/* Sequence dst[i] becomes the first tokens[i] tokens of sequence src[i]
+ * (n <= 1024 entries): it shares src's whole pages, and a partial last page is
+ * copied (the used slots, in all L layers) into a page popped from free_list,
+ * in the order of the entries.  What dst held before is given up as in
+ * nvfp4_kv_resize.  An entry is passed over if a sequence lies outside [0, S),
+ * an earlier entry has the same dst, its src is any entry's dst, or src holds
+ * fewer than tokens[i] tokens' pages.
+ *   shortage as above.   moves  workspace of 3 * n int32, device. */
+nvfp4_status nvfp4_kv_fork(int64_t n, int64_t S, int64_t W, int64_t P, int64_t page_size, int32_t* table,
+                           int32_t* held, int32_t* refs, int32_t* free_list, const int32_t* src, const int32_t* dst,
+                           const int32_t* tokens, int32_t* shortage, int32_t* moves, int64_t L, int64_t H, int64_t D,
+                           uint8_t* k_pages, uint8_t* v_pages, int64_t layer_stride, int64_t page_stride,
+                           void* stream);
+
 /* Read-only streaming ceiling: reads the a_bytes bytes at a and the b_bytes
  * bytes at b once (16-byte loads, each wave a contiguous span, the loads
  * marked non-temporal); every lane folds the four words of each of its loads

@@ -10,6 +10,7 @@ these functions raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -31,7 +32,9 @@ KERNEL_NAMES = {KERNEL_GEMV_FP4: "gemv_fp4_kernel", KERNEL_GEMV_FLAT: "gemv_flat
                 KERNEL_M16_STREAM: "gemm_m16_stream_kernel"}
 
 EXPORTS = ("nvfp4_abi_version", "nvfp4_act_global_scale", "nvfp4_gemm", "nvfp4_gemm_dispatch", "nvfp4_gemm_ex",
-           "nvfp4_gemm_quantize_output", "nvfp4_gemm_scratch", "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_ws", "nvfp4_kv_fp8_decode", "nvfp4_kv_fp8_encode",
+           "nvfp4_gemm_quantize_output", "nvfp4_gemm_scratch", "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_ws",
+           "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_kv_compact",
+           "nvfp4_kv_fork", "nvfp4_kv_fp8_decode", "nvfp4_kv_fp8_encode", "nvfp4_kv_resize",
            "nvfp4_quantize_act",
            "nvfp4_quantize_gemm", "nvfp4_quantize_gemm_dynamic", "nvfp4_quantize_weights", "nvfp4_status_string",
            "nvfp4_stream_read",
@@ -75,7 +78,16 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_act_global_scale.argtypes = [p, i32, i64, i64, p, p]
     lib.nvfp4_kv_fp8_decode.argtypes = [p, i64, p, p, i32, p]
     lib.nvfp4_tree_verify.argtypes = [i64, i64, i64, p, p, p, p, p, p, p, p, p, p, p, p, p]
-    for f in ("nvfp4_quantize_weights", "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_gemm_ws",
+    f32 = ctypes.c_float
+    lib.nvfp4_kv_append.argtypes = [i64] * 7 + [p, p, i32, i64, i64, p, p, p, p, i64, p, p, p, p]
+    lib.nvfp4_kv_attention_workspace_bytes.argtypes = [i64] * 7 + [i32]
+    lib.nvfp4_kv_attention_workspace_bytes.restype = i64
+    lib.nvfp4_kv_attention.argtypes = [i64] * 8 + [p, i32, i64, f32, p, p, p, p, i64, p, p, p, p, p, p, p, i64, p]
+    lib.nvfp4_kv_compact.argtypes = [i64] * 8 + [p, p, i64, i64, p, p, p, p, p]
+    lib.nvfp4_kv_resize.argtypes = [i64] * 5 + [p] * 8
+    lib.nvfp4_kv_fork.argtypes = [i64] * 5 + [p] * 9 + [i64] * 3 + [p, p, i64, i64, p]
+    for f in ("nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_compact", "nvfp4_kv_resize", "nvfp4_kv_fork",
+              "nvfp4_quantize_weights", "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_gemm_ws",
               "nvfp4_gemm_scratch",
               "nvfp4_gemm_quantize_output",
               "nvfp4_quantize_gemm", "nvfp4_tree_accept", "nvfp4_tree_verify", "nvfp4_kv_fp8_encode",
@@ -478,3 +490,234 @@ def nvfp4_stream_read(a: torch.Tensor, b: torch.Tensor, sink: Optional[torch.Ten
                                     b.numel() * b.element_size(), sink.data_ptr(), magic, _stream(dev)),
            "nvfp4_stream_read")
     return sink
+
+
+# Paged FP8 KV cache.  Pages are uint8 [P, H, page_size, D] per layer ([L, P, H, page_size, D] for
+# all layers), tables int32 [B, W], lengths int32 [B]; include/nvfp4.h states the layout.
+
+def _call(dev: torch.device, where: str, fn, *args) -> None:
+    """Calls fn(*args, stream) with `dev` current and its current stream."""
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != NVFP4_OK:
+        raise NVFP4Error(status, where)
+
+
+def _ints(dev: torch.device, **ts: torch.Tensor) -> None:
+    for name, t in ts.items():
+        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+
+
+def _kv_scale(dev: torch.device, **ts: torch.Tensor) -> None:
+    for name, t in ts.items():
+        if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
+            raise ValueError(f"{name} must be a float32 tensor of one element on {dev}")
+
+
+def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[torch.device, int, int]:
+    """Checks a pair of page tensors of `dim` dimensions (same shape and strides, whole pages);
+    returns their device and the bytes from a layer to the next and from a page to the next."""
+    dev = k_pages.device
+    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8 or dev.type != "cuda" or v_pages.device != dev:
+        raise ValueError("pages must be uint8 tensors on one GPU")
+    st, shape = k_pages.stride(), k_pages.shape
+    if len(shape) != dim or shape != v_pages.shape or st != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same shape "
+                         + ("[L, P, H, page_size, D]" if dim == 5 else "[P, H, page_size, D]") + " and strides")
+    P, H, page, D = shape[-4:]
+    if (st[-1] != 1 and D > 1) or (st[-2] != D and page > 1) or (st[-3] != page * D and H > 1):
+        raise ValueError("a page must be contiguous [H, page_size, D]")
+    return dev, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
+
+
+def _kv_rows(x: torch.Tensor, dev: torch.device, name: str) -> int:
+    """x [B, M, heads, D] whose rows are contiguous; returns the values from a row to the next."""
+    B, M, H, D = x.shape
+    sb, sm, sh, sd = x.stride()
+    if x.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if x.numel() == 0:
+        return H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"the rows of {name} must be contiguous [heads, D]")
+    row = sm if M > 1 else sb if B > 1 else H * D
+    if B > 1 and M > 1 and sb != M * sm:
+        raise ValueError(f"the rows of {name} must be equally spaced")
+    return row
+
+
+def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                    counts: Optional[torch.Tensor] = None) -> None:
+    """Writes k and v [B, M, H, D] (float32/bfloat16; rows may be column ranges of a wider tensor) as
+    E4M3 bytes at tokens lens[b] .. lens[b] + M - 1 (counts[b] of them) of the sequences' pages."""
+    dev, _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [B, M, H, D] of one dtype")
+    B, M, H, D = k.shape
+    P, Hp, page, Dp = k_pages.shape
+    if (H, D) != (Hp, Dp) or table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+        raise ValueError("k, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
+    _ints(dev, table=table, lens=lens)
+    if counts is not None:
+        _ints(dev, counts=counts)
+        if counts.shape != (B,):
+            raise ValueError("counts must be [B]")
+    _kv_scale(dev, k_scale=k_scale, v_scale=v_scale)
+    _call(dev, "nvfp4_kv_append", load().nvfp4_kv_append, B, M, H, D, page, P, table.shape[1], k.data_ptr(),
+          v.data_ptr(), _dt(k.dtype), _kv_rows(k, dev, "k"), _kv_rows(v, dev, "v"), k_scale.data_ptr(),
+          v_scale.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_stride, table.data_ptr(),
+          lens.data_ptr(), counts.data_ptr() if counts is not None else None)
+
+
+def nvfp4_kv_attention(q: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, k_pages: torch.Tensor,
+                       v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                       parent: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                       sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                       workspace: Optional[torch.Tensor] = None):
+    """Attention of the nodes q [B, M, Hq, D] (float32/bfloat16) over one layer of the cache, in which
+    the nodes' own keys and values already stand behind lens[b].  parent int32 [B, M]: drafted trees (M <=
+    64); None: a chain.  sm_scale defaults to 1/sqrt(D).  Returns out [B, M, Hq, D] of q's dtype, or
+    (out, lse float32 [B, M, Hq]) with want_lse.  workspace: uint8 scratch; None allocates it."""
+    dev, _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, M, Hq, D]")
+    B, M, Hq, D = q.shape
+    P, H, page, Dp = k_pages.shape
+    if D != Dp or H < 1 or Hq % H or table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+        raise ValueError("q, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
+    _ints(dev, table=table, lens=lens)
+    if parent is not None:
+        _ints(dev, parent=parent)
+        if parent.shape != (B, M):
+            raise ValueError("parent must be [B, M]")
+    if counts is not None:
+        _ints(dev, counts=counts)
+        if counts.shape != (B,):
+            raise ValueError("counts must be [B]")
+    _kv_scale(dev, k_scale=k_scale, v_scale=v_scale)
+    stride = _kv_rows(q, dev, "q")
+    dt, W = _dt(q.dtype), table.shape[1]
+    if out is None:
+        out = torch.empty((B, M, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [B, M, Hq, D] of q's dtype on its GPU")
+    lse = torch.empty((B, M, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    lib = load()
+    if workspace is None:
+        if dev.index == torch.cuda.current_device():
+            need = lib.nvfp4_kv_attention_workspace_bytes(B, M, Hq, H, D, page, W, dt)
+        else:
+            with torch.cuda.device(dev):
+                need = lib.nvfp4_kv_attention_workspace_bytes(B, M, Hq, H, D, page, W, dt)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
+    _call(dev, "nvfp4_kv_attention", lib.nvfp4_kv_attention, B, M, Hq, H, D, page, P, W, q.data_ptr(), dt, stride,
+          1.0 / math.sqrt(D) if sm_scale is None else sm_scale, k_scale.data_ptr(), v_scale.data_ptr(),
+          k_pages.data_ptr(), v_pages.data_ptr(), page_stride, table.data_ptr(), lens.data_ptr(),
+          parent.data_ptr() if parent is not None else None, counts.data_ptr() if counts is not None else None,
+          out.data_ptr(), lse.data_ptr() if lse is not None else None,
+          workspace.data_ptr() if workspace is not None else None,
+          workspace.numel() if workspace is not None else 0)
+    return (out, lse) if want_lse else out
+
+
+def nvfp4_kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                     result: torch.Tensor, new_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Moves the accepted path of each sequence's tree to the front in all layers of pages [L, P, H,
+    page_size, D]; result int32 [B, 3 + M]: rows of nvfp4_tree_accept / nvfp4_tree_verify.  Returns
+    new_lens int32 [B] = lens + 1 + accepted (a tensor of its own: lens is not changed)."""
+    dev, layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    L, P, H, page, D = k_pages.shape
+    if table.dim() != 2 or result.dim() != 2 or lens.shape != (table.shape[0],) or \
+            result.shape[0] != table.shape[0]:
+        raise ValueError("table [B, W], lens [B] and result [B, 3 + M] do not fit together")
+    B, W = table.shape
+    _ints(dev, table=table, lens=lens, result=result)
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    else:
+        _ints(dev, new_lens=new_lens)
+        if new_lens.shape != lens.shape:
+            raise ValueError("new_lens must be [B]")
+    _call(dev, "nvfp4_kv_compact", load().nvfp4_kv_compact, L, B, result.shape[1] - 3, H, D, page, P, W,
+          k_pages.data_ptr(), v_pages.data_ptr(), layer_stride, page_stride, table.data_ptr(),
+          lens.data_ptr(), result.data_ptr(), new_lens.data_ptr())
+    return new_lens
+
+
+def kv_pool(seqs: int, width: int, pages: int, dev) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """An empty page pool on `dev`: (table [seqs, width], held [seqs], refs [pages], free_list [1 +
+    pages]); pages are handed out in ascending order."""
+    table = torch.full((seqs, width), -1, dtype=torch.int32, device=dev)
+    held = torch.zeros((seqs,), dtype=torch.int32, device=dev)
+    refs = torch.zeros((pages,), dtype=torch.int32, device=dev)
+    return table, held, refs, torch.arange(pages, -1, -1, dtype=torch.int32, device=dev)
+
+
+def _pool(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor) -> torch.device:
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError("the page pool must be on a GPU")
+    _ints(dev, table=table, held=held, refs=refs, free_list=free_list)
+    if table.dim() != 2 or held.shape != (table.shape[0],) or refs.dim() != 1 or \
+            free_list.shape != (refs.shape[0] + 1,):
+        raise ValueError("table [S, W], held [S], refs [P] and free_list [1 + P] do not fit together")
+    return dev
+
+
+def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor,
+                    page_size: int, seqs: torch.Tensor, tokens: torch.Tensor,
+                    shortage: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Lets each sequence of seqs int32 [n] hold the pages of tokens int32 [n] tokens (0 frees it).
+    Returns shortage int32 [1]: 0, or how many pages were missing (then nothing is changed)."""
+    dev = _pool(table, held, refs, free_list)
+    _ints(dev, seqs=seqs, tokens=tokens)
+    if seqs.dim() != 1 or tokens.shape != seqs.shape:
+        raise ValueError("seqs and tokens must be [n]")
+    if shortage is None:
+        shortage = torch.empty((1,), dtype=torch.int32, device=dev)
+    else:
+        _ints(dev, shortage=shortage)
+        if shortage.numel() != 1:
+            raise ValueError("shortage must have one element")
+    S, W = table.shape
+    _call(dev, "nvfp4_kv_resize", load().nvfp4_kv_resize, seqs.shape[0], S, W, refs.shape[0], page_size,
+          table.data_ptr(), held.data_ptr(), refs.data_ptr(), free_list.data_ptr(), seqs.data_ptr(),
+          tokens.data_ptr(), shortage.data_ptr())
+    return shortage
+
+
+def nvfp4_kv_fork(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor,
+                  k_pages: torch.Tensor, v_pages: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                  tokens: torch.Tensor, shortage: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Sequence dst[i] becomes the first tokens[i] tokens of src[i] (int32 [n] each): whole pages are
+    shared, a partial one is copied in all layers of pages [L, P, H, page_size, D], what dst held is
+    given up.  Returns shortage as nvfp4_kv_resize."""
+    dev = _pool(table, held, refs, free_list)
+    on, layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    if on != dev or k_pages.shape[1] != refs.shape[0]:
+        raise ValueError("pages must be [L, P, H, page_size, D] of the pool's P pages, on its GPU")
+    _ints(dev, src=src, dst=dst, tokens=tokens)
+    if src.dim() != 1 or dst.shape != src.shape or tokens.shape != src.shape:
+        raise ValueError("src, dst and tokens must be [n]")
+    if shortage is None:
+        shortage = torch.empty((1,), dtype=torch.int32, device=dev)
+    else:
+        _ints(dev, shortage=shortage)
+        if shortage.numel() != 1:
+            raise ValueError("shortage must have one element")
+    S, W = table.shape
+    L, P, H, page, D = k_pages.shape
+    n = src.shape[0]
+    moves = torch.empty((3 * n,), dtype=torch.int32, device=dev)
+    _call(dev, "nvfp4_kv_fork", load().nvfp4_kv_fork, n, S, W, P, page, table.data_ptr(), held.data_ptr(),
+          refs.data_ptr(), free_list.data_ptr(), src.data_ptr(), dst.data_ptr(), tokens.data_ptr(),
+          shortage.data_ptr(), moves.data_ptr(), L, H, D, k_pages.data_ptr(), v_pages.data_ptr(), layer_stride,
+          page_stride)
+    return shortage

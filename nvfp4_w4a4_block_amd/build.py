@@ -31,10 +31,14 @@ SOURCES = {
     "gemm_m16_stream.hip": [],
     "tree.hip": [],
     "kv_fp8.hip": [],
+    "kv_pages.hip": [],
+    "kv_pool.hip": [],
+    "kv_attention.hip": [],
     "gemm_tiled.hip": [],
     "stream.hip": [],
     "scratch.hip": [],
     "abi.cpp": [],
+    "abi_kv.cpp": [],
 }
 
 COMMON = [
