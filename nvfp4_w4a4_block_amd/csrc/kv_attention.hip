@@ -1,12 +1,149 @@
 // Attention of a step's nodes over the paged FP8 KV cache.
 //
-// Simple form: one workgroup per (sequence, node, query head); 256 keys per
-// pass, one key per thread, running maximum and sum.
+// The page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic Benchmark
+// 6.4x Faster on Jetson AGX Thor" verifies a 16-node tree of drafted tokens in
+// one pass over an FP8 cache of up to 23.5K tokens (sections "Using tree-based
+// multi-token prediction to accelerate LLM inference", "Using NVFP4
+// quantization to accelerate Qwen3.6-27B inference") and prefills the suffix
+// of a turn over its reused prefix ("Reusing KV cache across agent turns").
+//
+// Mathematics.  For a row (node v, query head) z_t = c * sum_d q_d k_td in
+// exponent units of 2 (c = sm_scale * k_scale * log2 e), p_t = 2^(z_t - m), out
+// = v_scale * sum_t p_t v_t / sum_t p_t.  Any m gives the same quotient, so m
+// follows the running maximum lazily: it moves only when a score exceeds it by
+// more than 8, and the sums are rescaled only then.  p is held as 2^(z - m +
+// 7): at most 2^15, inside f16's range, and normal down to 2^-21 of the
+// largest.
+//
+// Work.  The rows that share a KV head (nodes x group) are packed into tiles
+// of 16; an item is RT row tiles of one (sequence, KV head).  A key tile is 128
+// tokens; the four waves of a workgroup take 32 of them each and hold all the
+// item's rows, so every cache byte is loaded and converted by one wave, once,
+// straight from memory to registers, and the loop has no barrier.  The tiles of
+// all items form one list, cut into equal ranges over a fixed grid: long and
+// short sequences of a batch share the chip evenly, and a range that cuts an
+// item leaves a partial sum (at most two per workgroup) that a second kernel
+// joins.
+//
+// Operands.  Scores are computed transposed (A = keys, B = queries), 16x16x32
+// bf16: E4M3 is exact in bf16, and so is a bf16 query.  The result has a
+// query's scores in the lanes that need them as the B operand of the second
+// product (A = values transposed, f16: E4M3 is exact there too), if that
+// product's key order is 4q .. 4q + 3 and 16 + 4q .. for lane group q, which
+// the value loads follow; the 2 x 2 byte transposes are v_perm.  fp32 calls
+// split q into three bf16 parts and p into two f16 parts.
 #include "device_common.h"
 #include "launch.h"
 
 namespace nvfp4 {
 namespace {
+
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 128;             // tokens of a key tile
+constexpr float kStart = -1e30f;       // running maximum before the first score
+constexpr float kLead = 8.0f;          // how far a score may exceed it
+constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
+
+struct Plan {
+  int items;      // per KV head: sequences * row tiles
+  int row_items;  // items of a sequence
+  int groups;     // workgroups that share the list; 0: one per item, nothing is cut
+  int64_t cap;    // tokens a table row covers
+  int end_tiles;  // tiles of cap
+  float* part;    // [2 * groups][rows][dim], then [2 * groups][rows][2]
+};
+
+// Committed length (negative: unused), nodes and first row of an item.
+struct Item {
+  int b, len, count, row0;
+};
+
+__device__ __forceinline__ Item item_of(const KvAttentionArgs& a, const Plan& p, int it, int rows) {
+  Item x;
+  x.b = p.row_items == 1 ? it : it / p.row_items;
+  x.row0 = (it - x.b * p.row_items) * rows;
+  x.len = a.c.lens[x.b];
+  int n = a.counts ? a.counts[x.b] : a.nodes;
+  n = n < a.nodes ? n : a.nodes;
+  x.count = n > 0 && x.len >= 0 ? n : 0;
+  return x;
+}
+
+// Tokens the item's rows may see: 0 .. end - 1.
+__device__ __forceinline__ int item_end(const KvAttentionArgs& a, const Plan& p, const Item& x, int rows) {
+  if (x.row0 >= x.count * a.group) return 0;
+  int last = x.count;
+  if (!a.parent) {
+    const int n = (x.row0 + rows - 1) / a.group + 1;
+    last = n < last ? n : last;
+  }
+  const int64_t end = (int64_t)x.len + last;
+  return (int)(end < p.cap ? end : p.cap);
+}
+
+__device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& p, int it, int rows) {
+  const int end = item_end(a, p, item_of(a, p, it, rows), rows);
+  return end > kTile ? (end + kTile - 1) / kTile : 1;
+}
+
+// Sum of the items' tiles and this thread's exclusive part of it; every thread
+// of the workgroup calls it.  Thread t has the items [t * per, (t + 1) * per).
+struct Scan {
+  int per;
+  int64_t before, total;
+};
+
+__device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int rows, int64_t* sums) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  Scan s;
+  s.per = (p.items + 255) / 256;
+  int64_t mine = 0;
+  for (int i = 0; i < s.per; ++i) {
+    const int it = t * s.per + i;
+    if (it < p.items) mine += item_tiles(a, p, it, rows);
+  }
+  int64_t v = mine;
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t o = __shfl_up(v, off);
+    v += lane >= off ? o : 0;
+  }
+  if (lane == 63) sums[wave] = v;
+  __syncthreads();
+  s.total = 0;
+  s.before = v - mine;
+  for (int w = 0; w < 4; ++w) {
+    const int64_t x = sums[w];
+    s.before += w < wave ? x : 0;
+    s.total += x;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The item with tile `at` of one head's list: found[0] the item, found[1] the
+// tiles of the list before it.
+__device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, int rows, const Scan& s, int64_t at,
+                                          int64_t* found) {
+  const int t = threadIdx.x;
+  int64_t x = s.before;
+  for (int i = 0; i < s.per && x <= at; ++i) {
+    const int it = t * s.per + i;
+    if (it >= p.items) break;
+    const int n = item_tiles(a, p, it, rows);
+    if (at < x + n) {
+      found[0] = it;
+      found[1] = x;
+    }
+    x += n;
+  }
+  __syncthreads();
+}
 
 // Ancestor-or-self bits of node v of a tree of at most 64 nodes, lane = node:
 // parent pointers doubled six times.  A parent outside [0, v) makes v a root.
@@ -14,6 +151,7 @@ __device__ __forceinline__ uint64_t ancestors_of_wave(int par) {
   const int lane = threadIdx.x & 63;
   uint64_t mask = 1ull << lane;
   int p = par >= 0 && par < lane ? par : -1;
+#pragma unroll
   for (int s = 0; s < 6; ++s) {
     const int at = p < 0 ? lane : p;
     const uint64_t up = __shfl(mask, at);
@@ -26,99 +164,604 @@ __device__ __forceinline__ uint64_t ancestors_of_wave(int par) {
   return mask;
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void kv_attention_simple_kernel(KvAttentionArgs a) {
-  __shared__ float qs[256], ps[256], red[4];
-  __shared__ int64_t rows[256];
-  __shared__ uint64_t line;
-  const KvCache& c = a.c;
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int hq = blockIdx.x, v = blockIdx.y, b = blockIdx.z;
-  const int heads_q = c.heads * a.group, h = hq / a.group, D = c.dim;
-  const int64_t row = (int64_t)b * a.nodes + v;
-  const int64_t out_at = (row * heads_q + hq) * D;
-  const int len = c.lens[b];
-  int count = a.counts ? a.counts[b] : a.nodes;
-  count = count < a.nodes ? count : a.nodes;
-  const bool here = len >= 0 && v < count;
-  if (!here) {
-    if (t < D) {
-      if (BF16) static_cast<uint16_t*>(a.out)[out_at + t] = 0;
-      else static_cast<float*>(a.out)[out_at + t] = 0.0f;
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+
+// One wave's 32 tokens of a key tile: E4M3 bytes as loaded.
+template <int D>
+struct KeyTile {
+  u4_t k[2][D / 64];          // block kb, 64-byte chunk: token lane % 16, bytes 16 (lane / 16) ..
+  Words<D / 64> v[8];         // token 16 (e / 4) + 4 (lane / 16) + e % 4, bytes (D / 16) (lane % 16) ..
+  bool there[2];              // the block's page exists
+};
+
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N == 1) {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const u2_t x = *reinterpret_cast<const u2_t*>(p);
+    r.w[0] = x.x;
+    r.w[1] = x.y;
+  } else {
+    const u4_t x = *reinterpret_cast<const u4_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = x[i];
+  }
+  return r;
+}
+
+// Page ids of the two 16-token blocks at token `key` (wave-uniform); -1 where
+// there is none.
+__device__ __forceinline__ void page_ids(const KvAttentionArgs& a, const int32_t* row, int key, int* id) {
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    const int at = (key + 16 * kb) >> a.c.page_shift;
+    const int p = row[at < a.c.width ? at : a.c.width - 1];
+    id[kb] = at < a.c.width && p >= 0 && p < a.c.pages ? p : -1;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, int h, int key, const int* id, KeyTile<D>& t) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int page = 1 << a.c.page_shift;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    t.there[kb] = id[kb] >= 0;
+    const int64_t at = (t.there[kb] ? id[kb] : 0) * a.c.page_stride +
+                       (int64_t)((h << a.c.page_shift) + ((key + 16 * kb) & (page - 1))) * D;
+    const uint8_t* k = a.c.k + at;
+    const uint8_t* v = a.c.v + at;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) t.k[kb][c] = *reinterpret_cast<const u4_t*>(k + i * D + 64 * c + 16 * q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t.v[4 * kb + e] = load_words<D / 64>(v + (4 * q + e) * D + (D / 16) * i);
+  }
+}
+
+// Eight E4M3 bytes (two words) -> eight bf16, exact.
+__device__ __forceinline__ bf8_t to_bf16x8(uint32_t lo, uint32_t hi) {
+  const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Four words of E4M3 byte pairs (half `hi` of each) -> eight f16, exact.
+template <bool HI>
+__device__ __forceinline__ h8_t to_f16x8(const uint32_t (&w)[4]) {
+  const h2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[0], 1.0f, HI);
+  const h2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[1], 1.0f, HI);
+  const h2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[2], 1.0f, HI);
+  const h2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[3], 1.0f, HI);
+  return h8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+__device__ __forceinline__ f4_t mfma_bf16(bf8_t a, bf8_t b, f4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+template <int D, int RT, bool F32>
+struct Smem {
+  float o[4][16][D + 4];        // one row tile of the four waves' sums (rows padded by 16 bytes)
+  float m[4][16 * RT], l[4][16 * RT];
+  uint64_t line[16 * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
+  uint64_t tree[64];            // ancestors of the nodes
+  int64_t sums[4], found[2];
+};
+
+template <int D, int RT, bool F32>
+__global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Plan plan) {
+  constexpr int R = 16 * RT, KS = D / 32, NT = D / 16, NQ = F32 ? 3 : 1;
+  __shared__ Smem<D, RT, F32> sm;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int j = lane & 15, q4 = lane >> 4;
+  const int rows_all = a.nodes * a.group;
+  const float c0 = a.sm_scale * *a.k_scale * 1.44269504088896340736f;
+  const float c = __builtin_fabsf(c0);
+  const bool flip = c0 < 0.0f;
+  const float vs = *a.v_scale;
+
+  // This workgroup's range of the list.
+  int h, it;
+  int64_t at, left;  // first tile within the item, tiles to do
+  int group = 0;
+  if (plan.groups == 0) {
+    h = blockIdx.x / plan.items;
+    it = blockIdx.x - h * plan.items;
+    at = 0;
+    left = item_tiles(a, plan, it, R);
+  } else {
+    Scan s;
+    if (plan.items == 1) {
+      s.total = item_tiles(a, plan, 0, R);
+    } else {
+      s = scan_items(a, plan, R, sm.sums);
     }
-    if (t == 0 && a.lse) a.lse[row * heads_q + hq] = -__builtin_inff();
-    return;
+    s.total = uniform64(s.total);
+    const int64_t all = s.total * a.c.heads;
+    const int64_t n = plan.groups < all ? plan.groups : all;
+    group = blockIdx.x;
+    if (group >= n) return;
+    const int64_t begin = group * all / n, end = (group + 1) * all / n;
+    h = (int)(begin / s.total);
+    at = begin - h * s.total;
+    left = end - begin;
+    it = 0;
+    if (plan.items > 1) {
+      find_item(a, plan, R, s, at, sm.found);
+      it = __builtin_amdgcn_readfirstlane((int)sm.found[0]);
+      at -= uniform64(sm.found[1]);
+    }
   }
-  if (wave == 0) {
-    const int par = a.parent && lane < a.nodes ? a.parent[(int64_t)b * a.nodes + lane] : -1;
-    const uint64_t m = ancestors_of_wave(par);
-    if (lane == (v & 63)) line = m;
-  }
-  if (t < D) {
-    const int64_t at = row * a.q_stride + (int64_t)hq * D + t;
-    qs[t] = BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.q)[at] << 16)
-                 : static_cast<const float*>(a.q)[at];
-  }
-  __syncthreads();
-  const float ks = *a.k_scale * a.sm_scale, vs = *a.v_scale;
-  const int end = len + (a.parent ? count : v + 1);
-  float m = -__builtin_inff(), l = 0.0f, acc = 0.0f;
-  for (int k0 = 0; k0 < end; k0 += 256) {
-    const int pos = k0 + t;
-    float s = -__builtin_inff();
-    rows[t] = -1;
-    if (pos < end && (pos < len || !a.parent || ((line >> (pos - len)) & 1))) {
-      const int at = pos >> c.page_shift;
-      const int page = at < c.width ? c.table[(int64_t)b * c.width + at] : -1;
-      if (page >= 0 && page < c.pages) {
-        const int64_t off =
-            page * c.page_stride + (((int64_t)h << c.page_shift) + (pos & ((1 << c.page_shift) - 1))) * D;
-        rows[t] = off;
-        float dot = 0.0f;
-        for (int d = 0; d < D; ++d) dot += qs[d] * e4m3_to_f32(c.k[off + d]);
-        s = dot * ks;
+
+  while (left > 0) {
+    const Item x = item_of(a, plan, it, R);
+    const int end = item_end(a, plan, x, R);
+    const int tiles = end > kTile ? (end + kTile - 1) / kTile : 1;
+    const int t0 = (int)at;
+    const int t1 = (int)(at + left < tiles ? at + left : tiles);
+    const int limit = x.len + x.count;                    // the first token nobody sees
+    const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
+    __syncthreads();  // the last item's sums have been read
+
+    // What the rows see of the nodes.
+    if (a.parent && wave == 0) {
+      const int par = lane < a.nodes ? a.parent[(int64_t)x.b * a.nodes + lane] : -1;
+      sm.tree[lane] = ancestors_of_wave(par);
+    }
+    // Queries: lane (j, q4) holds values 64 c + 16 q4 + 8 half + e of row j.
+    bf8_t qr[NQ][RT][KS];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      int row = x.row0 + 16 * r + j;
+      row = row < rows_all ? row : rows_all - 1;
+      const int node = row / a.group;
+      const int64_t from = ((int64_t)x.b * a.nodes + node) * a.q_stride +
+                           (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int64_t off = from + 64 * (s >> 1) + 8 * (s & 1);
+        if constexpr (F32) {
+          const f4_t* p = reinterpret_cast<const f4_t*>(static_cast<const float*>(a.q) + off);
+          const f4_t lo = p[0], hi = p[1];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float y = e < 4 ? lo[e & 3] : hi[e & 3];
+            y = flip ? -y : y;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              const __bf16 b = (__bf16)y;
+              qr[n][r][s][e] = b;
+              y -= (float)b;
+            }
+          }
+        } else {
+          u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(a.q) + off);
+          if (flip) w ^= 0x80008000u;
+          qr[0][r][s] = __builtin_bit_cast(bf8_t, w);
+        }
       }
     }
-    float top = s;
-    for (int off = 32; off > 0; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
-    if (lane == 0) red[wave] = top;
     __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
-    const float mn = __builtin_fmaxf(m, top);
-    const float p = s == -__builtin_inff() ? 0.0f : expf(s - mn);
-    const float f = m == -__builtin_inff() ? 0.0f : expf(m - mn);
-    ps[t] = p;
-    float sum = p;
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    __syncthreads();
-    if (lane == 0) red[wave] = sum;
-    __syncthreads();
-    l = l * f + (red[0] + red[1] + red[2] + red[3]);
-    m = mn;
-    if (t < D) {
-      acc *= f;
-      for (int j = 0; j < 256; ++j)
-        if (rows[j] >= 0) acc += ps[j] * e4m3_to_f32(c.v[rows[j] + t]);
+    if (t < R) {
+      int row = x.row0 + t;
+      row = row < rows_all ? row : rows_all - 1;
+      const int node = row / a.group;
+      sm.line[t] = a.parent ? sm.tree[node] : (uint64_t)node;
     }
     __syncthreads();
+
+    f4_t o[RT][NT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      m[r] = kStart;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    const int32_t* pages = a.c.table + (int64_t)x.b * a.c.width;
+    KeyTile<D> cur, nxt;
+    int id[2];
+    page_ids(a, pages, t0 * kTile + 32 * wave, id);
+    load_tile<D>(a, h, t0 * kTile + 32 * wave, id, cur);
+    page_ids(a, pages, (t0 + 1) * kTile + 32 * wave, id);
+    for (int tile = t0; tile < t1; ++tile) {
+      const int key0 = tile * kTile + 32 * wave;
+      if (tile + 1 < t1) {
+        load_tile<D>(a, h, key0 + kTile, id, nxt);
+        page_ids(a, pages, key0 + 2 * kTile, id);
+      }
+      const bool masked = key0 + 32 > clear || !cur.there[0] || !cur.there[1];
+
+      // z of 32 tokens x R rows.
+      f4_t z[2][RT];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) z[kb][r] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const u4_t w = cur.k[kb][s >> 1];
+          const bf8_t kop = (s & 1) ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
+#pragma unroll
+          for (int n = NQ - 1; n >= 0; --n)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) z[kb][r] = mfma_bf16(kop, qr[n][r][s], z[kb][r]);
+        }
+      }
+      if (masked) {
+        // Values of tokens that nobody sees may be anything: their bytes are cleared.
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3);
+          const bool keep = cur.there[e >> 2] && pos < limit;
+#pragma unroll
+          for (int n = 0; n < D / 64; ++n) cur.v[e].w[n] = keep ? cur.v[e].w[n] : 0u;
+        }
+      }
+
+      h8_t ph[RT], pl[F32 ? RT : 1];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        uint32_t seen = 0xFFu;
+        if (masked) {
+          seen = 0u;
+          const uint64_t line = sm.line[16 * r + j];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3);
+            const int u = pos - x.len;
+            const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
+            const bool ok = cur.there[e >> 2] && pos < limit && (u < 0 || node);
+            seen |= ok ? 1u << e : 0u;
+            z[e >> 2][r][e & 3] = ok ? z[e >> 2][r][e & 3] : -__builtin_inff();
+          }
+        }
+        float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
+                                                    __builtin_fmaxf(z[0][r][2], z[0][r][3])),
+                                    __builtin_fmaxf(__builtin_fmaxf(z[1][r][0], z[1][r][1]),
+                                                    __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
+        if (__any(top > m[r] + kLead)) {
+          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+          const float mn = __builtin_fmaxf(m[r], top);
+          const float f = __builtin_amdgcn_exp2f(m[r] - mn);
+          m[r] = mn;
+          l[r] *= f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[r][n] *= f;
+        }
+        const float lift = kLift - m[r];
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.0f;
+        }
+        l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const _Float16 x16 = (_Float16)p[e];
+          ph[r][e] = x16;
+          if constexpr (F32) pl[r][e] = (_Float16)(p[e] - (float)x16);
+        }
+      }
+
+      // O += V^T P: word n of a token's bytes holds d = (D / 16) i + 4 n ..
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = __builtin_amdgcn_perm(cur.v[2 * e + 1].w[n], cur.v[2 * e].w[n], 0x05010400u);
+          hi[e] = __builtin_amdgcn_perm(cur.v[2 * e + 1].w[n], cur.v[2 * e].w[n], 0x07030602u);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const h8_t vop = u == 0 ? to_f16x8<false>(lo) : u == 1 ? to_f16x8<true>(lo)
+                         : u == 2 ? to_f16x8<false>(hi) : to_f16x8<true>(hi);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            if constexpr (F32) o[r][4 * n + u] = mfma16x16x32(vop, pl[r], o[r][4 * n + u]);
+            o[r][4 * n + u] = mfma16x16x32(vop, ph[r], o[r][4 * n + u]);
+          }
+        }
+      }
+      cur = nxt;
+    }
+
+    // Join the four waves, one row tile at a time.
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int slot = 2 * group + (t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      l[r] += __shfl_xor(l[r], 16);
+      l[r] += __shfl_xor(l[r], 32);
+      if (q4 == 0) {
+        sm.m[wave][16 * r + j] = m[r];
+        sm.l[wave][16 * r + j] = l[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (r > 0) __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int n = 0; n < NT; n += 4)
+          *reinterpret_cast<f4_t*>(&sm.o[wave][j][NT * (4 * q4 + e) + n]) =
+              f4_t{o[r][n][e], o[r][n + 1][e], o[r][n + 2][e], o[r][n + 3][e]};
+      __syncthreads();
+      const int row16 = t >> 4, d0 = NT * (t & 15), row = 16 * r + row16;
+      float top = kStart;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, sm.m[w][row]);
+      float sum = 0.0f, acc[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sm.m[w][row] - top);
+        sum += f * sm.l[w][row];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] += f * sm.o[w][row16][d0 + n];
+      }
+      if (!whole) {
+        float* to = plan.part + ((int64_t)slot * R + row) * D + d0;
+#pragma unroll
+        for (int n = 0; n < NT; n += 4)
+          *reinterpret_cast<f4_t*>(to + n) = f4_t{acc[n], acc[n + 1], acc[n + 2], acc[n + 3]};
+        if ((t & 15) == 0) {
+          float* ml = plan.part + (int64_t)2 * plan.groups * R * D + ((int64_t)slot * R + row) * 2;
+          ml[0] = top;
+          ml[1] = sum;
+        }
+        continue;
+      }
+      const int grow = x.row0 + row;
+      if (grow >= rows_all) continue;
+      const int node = grow / a.group;
+      const bool live = node < x.count && sum > 0.0f;
+      const float f = live ? vs / sum : 0.0f;
+      const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group +
+                           (grow - node * a.group);
+      if constexpr (F32) {
+        float* to = static_cast<float*>(a.out) + orow * D + d0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[n] = live ? acc[n] * f : 0.0f;
+      } else {
+        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + d0);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2)
+          to[n / 2] = live ? (uint32_t)f32_to_bf16_rne(acc[n] * f) | ((uint32_t)f32_to_bf16_rne(acc[n + 1] * f) << 16)
+                           : 0u;
+      }
+      if (a.lse && (t & 15) == 0)
+        a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
+    }
+
+    // The next item of the list.
+    left -= t1 - t0;
+    at = 0;
+    if (++it == plan.items) {
+      it = 0;
+      ++h;
+    }
   }
-  if (t < D) {
-    const float o = l > 0.0f ? acc / l * vs : 0.0f;
-    if (BF16) static_cast<uint16_t*>(a.out)[out_at + t] = f32_to_bf16_rne(o);
-    else static_cast<float*>(a.out)[out_at + t] = o;
+}
+
+// Joins the partial sums of the items that a range boundary cut: block (item
+// or boundary, four rows), a wave a row.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan, int R, int by_item) {
+  __shared__ int64_t sums[4], found[2];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  int h, it;
+  int64_t before;  // tiles of the head's list before the item
+  Scan s;
+  if (plan.items == 1) {
+    s.total = item_tiles(a, plan, 0, R);
+  } else {
+    s = scan_items(a, plan, R, sums);
   }
-  if (t == 0 && a.lse) a.lse[row * heads_q + hq] = l > 0.0f ? m + logf(l) : -__builtin_inff();
+  const int64_t all = s.total * a.c.heads;
+  const int64_t n = plan.groups < all ? plan.groups : all;
+  if (by_item) {
+    h = blockIdx.x / plan.items;
+    it = blockIdx.x - h * plan.items;
+    before = 0;
+    if (plan.items > 1) {
+      if (it / s.per == t) {
+        int64_t y = s.before;
+        for (int i = t * s.per; i < it; ++i) y += item_tiles(a, plan, i, R);
+        found[1] = y;
+      }
+      __syncthreads();
+      before = found[1];
+    }
+  } else {
+    const int64_t g = (int64_t)blockIdx.x + 1;
+    if (g >= n) return;
+    const int64_t begin = g * all / n;
+    h = (int)(begin / s.total);
+    it = 0;
+    before = 0;
+    if (plan.items > 1) {
+      find_item(a, plan, R, s, begin - h * s.total, found);
+      it = (int)found[0];
+      before = found[1];
+    }
+    const int64_t first = h * s.total + before;
+    // only the boundary behind the item's first range joins it
+    if (first == begin || ((first + 1) * n - 1) / all != g - 1) return;
+  }
+  const Item x = item_of(a, plan, it, R);
+  const int end = item_end(a, plan, x, R);
+  const int tiles = end > kTile ? (end + kTile - 1) / kTile : 1;
+  const int64_t first = h * s.total + before;
+  const int g0 = (int)(((first + 1) * n - 1) / all), g1 = (int)(((first + tiles) * n - 1) / all);
+  if (g0 == g1) return;
+
+  const int row = blockIdx.y * 4 + wave, grow = x.row0 + row, rows_all = a.nodes * a.group;
+  if (grow >= rows_all) return;
+  const float* ml = plan.part + (int64_t)2 * plan.groups * R * D;
+  float top = kStart;
+  for (int g = g0 + lane; g <= g1; g += 64) {
+    const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
+    top = __builtin_fmaxf(top, ml[(slot * R + row) * 2]);
+  }
+  for (int off = 32; off > 0; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+  constexpr int N = D / 64;
+  float sum = 0.0f, acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  for (int base = g0; base <= g1; base += 64) {
+    float f = 0.0f;
+    if (base + lane <= g1) {
+      const int g = base + lane;
+      const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
+      const float* y = ml + (slot * R + row) * 2;
+      f = __builtin_amdgcn_exp2f(y[0] - top);
+      sum += f * y[1];
+    }
+    const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
+    for (int k = 0; k < many; k += 8) {  // eight loads in flight
+      float y[8][N];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int g = base + (k + u < many ? k + u : k);
+        const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
+        const float* from = plan.part + (slot * R + row) * D + N * lane;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[u][i] = from[i];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = k + u < many ? __shfl(f, k + u) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += w * y[u][i];
+      }
+    }
+  }
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  const int node = grow / a.group;
+  const bool live = node < x.count && sum > 0.0f;
+  const float f = live ? *a.v_scale / sum : 0.0f;
+  const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = live ? acc[i] * f : 0.0f;
+    if constexpr (F32) static_cast<float*>(a.out)[orow * D + N * lane + i] = y;
+    else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
+  }
+  if (a.lse && lane == 0)
+    a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
+}
+
+int compute_units() {
+  static int cus[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cus[dev] == 0) {
+    int v = 0;
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
+    cus[dev] = v;
+  }
+  return cus[dev];
+}
+
+// Row tiles of an item: as many as the registers hold (queries and sums of a
+// tile take D / 8 + D / 4 registers, three times the queries in fp32), the
+// tiles of a KV head spread evenly over its items.
+int row_tiles(const KvAttentionArgs& a, int* row_items) {
+  const int most = !a.bf16 ? 2 : a.c.dim == 64 ? 8 : a.c.dim == 128 ? 6 : 3;
+  const int all = (int)(((int64_t)a.nodes * a.group + 15) / 16);
+  *row_items = (all + most - 1) / most;
+  return (all + *row_items - 1) / *row_items;
+}
+
+int groups_per_cu(int dim, int rt) { return rt * dim <= 128 ? 4 : rt * dim <= 256 ? 2 : 1; }
+
+Plan make_plan(const KvAttentionArgs& a, int* rt, int64_t* bytes) {
+  Plan p;
+  *rt = row_tiles(a, &p.row_items);
+  p.items = a.c.seqs * p.row_items;
+  p.cap = (int64_t)a.c.width << a.c.page_shift;
+  p.end_tiles = (int)((p.cap + kTile - 1) / kTile);
+  const int64_t most = (int64_t)p.items * a.c.heads * p.end_tiles;
+  const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt);
+  p.groups = p.end_tiles == 1 ? 0 : (int)(groups < most ? groups : most);
+  *bytes = (int64_t)2 * p.groups * 16 * *rt * (a.c.dim + 2) * 4;
+  p.part = nullptr;
+  return p;
+}
+
+template <int D, int RT, bool F32>
+hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t stream) {
+  const int64_t items = (int64_t)p.items * a.c.heads;
+  kv_attention_kernel<D, RT, F32><<<(unsigned)(p.groups ? p.groups : items), 256, 0, stream>>>(a, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.groups < 2) return e;
+  const int by_item = items < p.groups ? 1 : 0;
+  kv_attention_join_kernel<D, F32><<<dim3((unsigned)(by_item ? items : p.groups - 1), 4 * RT), 256, 0, stream>>>(
+      a, p, 16 * RT, by_item);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_dim(const KvAttentionArgs& a, const Plan& p, int rt, hipStream_t stream) {
+  if (!a.bf16) return rt == 1 ? launch_one<D, 1, true>(a, p, stream) : launch_one<D, 2, true>(a, p, stream);
+  switch (rt) {
+    case 1: return launch_one<D, 1, false>(a, p, stream);
+    case 2: return launch_one<D, 2, false>(a, p, stream);
+    case 3: return launch_one<D, 3, false>(a, p, stream);
+    default: break;
+  }
+  if constexpr (D <= 128) {
+    switch (rt) {
+      case 4: return launch_one<D, 4, false>(a, p, stream);
+      case 5: return launch_one<D, 5, false>(a, p, stream);
+      case 6: return launch_one<D, 6, false>(a, p, stream);
+      default: break;
+    }
+  }
+  if constexpr (D <= 64) {
+    if (rt == 7) return launch_one<D, 7, false>(a, p, stream);
+    if (rt == 8) return launch_one<D, 8, false>(a, p, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-int64_t kv_attention_workspace_bytes(const KvAttentionArgs&) { return 0; }
+int64_t kv_attention_workspace_bytes(const KvAttentionArgs& a) {
+  int rt;
+  int64_t bytes;
+  make_plan(a, &rt, &bytes);
+  return bytes;
+}
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {
-  const dim3 grid(a.c.heads * a.group, a.nodes, a.c.seqs);
-  if (a.bf16) kv_attention_simple_kernel<true><<<grid, 256, 0, stream>>>(a);
-  else kv_attention_simple_kernel<false><<<grid, 256, 0, stream>>>(a);
-  return hipGetLastError();
+  int rt;
+  int64_t bytes;
+  Plan p = make_plan(a, &rt, &bytes);
+  if (a.workspace_bytes < bytes) p.groups = 0;
+  p.part = static_cast<float*>(a.workspace);
+  switch (a.c.dim) {
+    case 64: return launch_dim<64>(a, p, rt, stream);
+    case 128: return launch_dim<128>(a, p, rt, stream);
+    default: return launch_dim<256>(a, p, rt, stream);
+  }
 }
 
 }  // namespace nvfp4
