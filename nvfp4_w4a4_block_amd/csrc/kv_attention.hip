@@ -41,7 +41,8 @@ namespace {
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kTile = 128;             // tokens of a key tile
+constexpr int kWaves = 8;              // waves of a workgroup
+constexpr int kTile = 32 * kWaves;     // tokens of a key tile
 constexpr float kStart = -1e30f;       // running maximum before the first score
 constexpr float kLead = 8.0f;          // how far a score may exceed it
 constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
@@ -95,10 +96,11 @@ struct Scan {
   int64_t before, total;
 };
 
+template <int WAVES>
 __device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int rows, int64_t* sums) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   Scan s;
-  s.per = (p.items + 255) / 256;
+  s.per = (p.items + 64 * WAVES - 1) / (64 * WAVES);
   int64_t mine = 0;
   for (int i = 0; i < s.per; ++i) {
     const int it = t * s.per + i;
@@ -113,7 +115,7 @@ __device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan&
   __syncthreads();
   s.total = 0;
   s.before = v - mine;
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const int64_t x = sums[w];
     s.before += w < wave ? x : 0;
     s.total += x;
@@ -164,17 +166,25 @@ __device__ __forceinline__ uint64_t ancestors_of_wave(int par) {
   return mask;
 }
 
+// The thread's index, computed anew where it is called: what derives from it is
+// not kept in registers over the loop.
+__device__ __forceinline__ int fresh_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 template <int N>
 struct Words {
   uint32_t w[N];
 };
 
-// One wave's 32 tokens of a key tile: E4M3 bytes as loaded.
+// One wave's 32 tokens of a key tile, as loaded.  Each half is refilled as soon
+// as its product has read it, so no second buffer is needed.
 template <int D>
 struct KeyTile {
   u4_t k[2][D / 64];          // block kb, 64-byte chunk: token lane % 16, bytes 16 (lane / 16) ..
   Words<D / 64> v[8];         // token 16 (e / 4) + 4 (lane / 16) + e % 4, bytes (D / 16) (lane % 16) ..
-  bool there[2];              // the block's page exists
 };
 
 template <int N>
@@ -194,33 +204,43 @@ __device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
   return r;
 }
 
-// Page ids of the two 16-token blocks at token `key` (wave-uniform); -1 where
-// there is none.
-__device__ __forceinline__ void page_ids(const KvAttentionArgs& a, const int32_t* row, int key, int* id) {
+// Where the two 16-token blocks at a token stand (wave-uniform); a block whose
+// page does not exist is read from page 0 and masked.
+struct Blocks {
+  int64_t at[2];
+  bool there[2];
+};
+
+__device__ __forceinline__ Blocks find_blocks(const KvAttentionArgs& a, const int32_t* row, int h, int key) {
+  Blocks b;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
-    const int at = (key + 16 * kb) >> a.c.page_shift;
+    const int pos = key + 16 * kb, at = pos >> a.c.page_shift;
     const int p = row[at < a.c.width ? at : a.c.width - 1];
-    id[kb] = at < a.c.width && p >= 0 && p < a.c.pages ? p : -1;
+    b.there[kb] = at < a.c.width && p >= 0 && p < a.c.pages;
+    b.at[kb] = (b.there[kb] ? p : 0) * a.c.page_stride +
+               (int64_t)((h << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1))) * a.c.dim;
   }
+  return b;
 }
 
 template <int D>
-__device__ __forceinline__ void load_tile(const KvAttentionArgs& a, int h, int key, const int* id, KeyTile<D>& t) {
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  const int page = 1 << a.c.page_shift;
+__device__ __forceinline__ void load_keys(const KvAttentionArgs& a, const Blocks& b, KeyTile<D>& t) {
+  const uint32_t lane = threadIdx.x & 63, off = (lane & 15) * D + 16 * (lane >> 4);
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb) {
-    t.there[kb] = id[kb] >= 0;
-    const int64_t at = (t.there[kb] ? id[kb] : 0) * a.c.page_stride +
-                       (int64_t)((h << a.c.page_shift) + ((key + 16 * kb) & (page - 1))) * D;
-    const uint8_t* k = a.c.k + at;
-    const uint8_t* v = a.c.v + at;
+  for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) t.k[kb][c] = *reinterpret_cast<const u4_t*>(k + i * D + 64 * c + 16 * q);
+    for (int c = 0; c < D / 64; ++c)
+      t.k[kb][c] = *reinterpret_cast<const u4_t*>(a.c.k + b.at[kb] + (off + 64 * c));
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const KvAttentionArgs& a, const Blocks& b, KeyTile<D>& t) {
+  const uint32_t lane = threadIdx.x & 63, off = 4 * (lane >> 4) * D + (D / 16) * (lane & 15);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t.v[4 * kb + e] = load_words<D / 64>(v + (4 * q + e) * D + (D / 16) * i);
-  }
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t.v[4 * kb + e] = load_words<D / 64>(a.c.v + b.at[kb] + (off + e * D));
 }
 
 // Eight E4M3 bytes (two words) -> eight bf16, exact.
@@ -248,22 +268,154 @@ __device__ __forceinline__ f4_t mfma_bf16(bf8_t a, bf8_t b, f4_t c) {
 
 template <int D, int RT, bool F32>
 struct Smem {
-  float o[4][16][D + 4];        // one row tile of the four waves' sums (rows padded by 16 bytes)
-  float m[4][16 * RT], l[4][16 * RT];
+  union {
+    bf8_t q[F32 ? 3 : 1][RT][D / 32][64];  // queries in operand order: value 64 (s / 2) + 16 (lane / 16) + 8 (s % 2)
+                                           // + e of row lane % 16
+    float o[kWaves][16][D + 4];            // one row tile of the waves' sums (rows padded by 16 bytes)
+  };
+  float m[kWaves][16 * RT], l[kWaves][16 * RT];
   uint64_t line[16 * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
   uint64_t tree[64];            // ancestors of the nodes
-  int64_t sums[4], found[2];
+  int64_t sums[kWaves], found[2];
 };
 
+template <int RT, int NT>
+struct Sums {
+  f4_t o[RT][NT];
+  float m[RT], l[RT];
+};
+
+// Scores of a wave's 32 tokens against the R rows.
 template <int D, int RT, bool F32>
-__global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Plan plan) {
-  constexpr int R = 16 * RT, KS = D / 32, NT = D / 16, NQ = F32 ? 3 : 1;
+__device__ __forceinline__ void score(const Smem<D, RT, F32>& sm, const KeyTile<D>& kt, f4_t (&z)[2][RT]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) z[kb][r] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s) {
+    bf8_t kop[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const u4_t w = kt.k[kb][s >> 1];
+      kop[kb] = (s & 1) ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
+    }
+#pragma unroll
+    for (int n = F32 ? 2 : 0; n >= 0; --n)  // small parts first
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const bf8_t qop = sm.q[n][r][s][lane];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) z[kb][r] = mfma_bf16(kop[kb], qop, z[kb][r]);
+      }
+  }
+}
+
+// Scores of tokens that a row does not see become -infinity, and the values of
+// tokens that nobody sees, which may be anything, zero.
+template <int D, int RT, bool F32>
+__device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT, F32>& sm, KeyTile<D>& kt,
+                                     f4_t (&z)[2][RT], int key0, int len, int limit, const Blocks& here) {
+  const int lane = fresh_thread() & 63, j = lane & 15, q4 = lane >> 4;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3), u = pos - len;
+    const bool there = here.there[e >> 2] && pos < limit;
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) kt.v[e].w[n] = there ? kt.v[e].w[n] : 0u;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const uint64_t line = sm.line[16 * r + j];
+      const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
+      z[e >> 2][r][e & 3] = there && (u < 0 || node) ? z[e >> 2][r][e & 3] : -__builtin_inff();
+    }
+  }
+}
+
+// Softmax of the scores and O += V^T P.
+template <int D, int RT, bool F32>
+__device__ __forceinline__ void accumulate(const KeyTile<D>& kt, const f4_t (&z)[2][RT], Sums<RT, D / 16>& acc,
+                                           float c) {
+  float top[RT];
+  bool rises = false;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    top[r] = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
+                                             __builtin_fmaxf(z[0][r][2], z[0][r][3])),
+                             __builtin_fmaxf(__builtin_fmaxf(z[1][r][0], z[1][r][1]),
+                                             __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
+    rises |= top[r] > acc.m[r] + kLead;
+  }
+  if (__any(rises)) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float x = __builtin_fmaxf(top[r], __shfl_xor(top[r], 16));
+      x = __builtin_fmaxf(x, __shfl_xor(x, 32));
+      x = __builtin_fmaxf(acc.m[r], x);
+      const float f = __builtin_amdgcn_exp2f(acc.m[r] - x);
+      acc.m[r] = x;
+      acc.l[r] *= f;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) acc.o[r][n] *= f;
+    }
+  }
+  h8_t ph[RT], pl[F32 ? RT : 1];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float lift = kLift - acc.m[r];
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const h2_t y = {(_Float16)p[e], (_Float16)p[e + 1]};
+      ph[r][e] = y.x;
+      ph[r][e + 1] = y.y;
+      if constexpr (F32) {
+        pl[r][e] = (_Float16)(p[e] - (float)y.x);
+        pl[r][e + 1] = (_Float16)(p[e + 1] - (float)y.y);
+      }
+    }
+    acc.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  }
+  // word n of a token's bytes holds d = (D / 16) i + 4 n ..
+#pragma unroll
+  for (int n = 0; n < D / 64; ++n) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x05010400u);
+      hi[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x07030602u);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const h8_t vop = u == 0 ? to_f16x8<false>(lo) : u == 1 ? to_f16x8<true>(lo)
+                     : u == 2 ? to_f16x8<false>(hi) : to_f16x8<true>(hi);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if constexpr (F32) acc.o[r][4 * n + u] = mfma16x16x32(vop, pl[r], acc.o[r][4 * n + u]);
+        acc.o[r][4 * n + u] = mfma16x16x32(vop, ph[r], acc.o[r][4 * n + u]);
+      }
+    }
+  }
+}
+
+// Waves per SIMD that the registers are limited for (256 at two: the matrix
+// instructions then keep their sums in ordinary registers).
+constexpr int waves_per_simd(int dim, int rt, bool f32) { return rt * dim <= 128 && !f32 ? 4 : 2; }
+
+template <int D, int RT, bool F32>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_attention_kernel(KvAttentionArgs a,
+                                                                                              Plan plan) {
+  constexpr int R = 16 * RT, KS = D / 32, NT = D / 16;
   __shared__ Smem<D, RT, F32> sm;
-  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int j = lane & 15, q4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows_all = a.nodes * a.group;
   const float c0 = a.sm_scale * *a.k_scale * 1.44269504088896340736f;
-  const float c = __builtin_fabsf(c0);
+  const float c = __builtin_fmaxf(__builtin_fabsf(c0), 1.17549435e-38f);  // not 0: a masked score stays -infinity
   const bool flip = c0 < 0.0f;
   const float vs = *a.v_scale;
 
@@ -281,7 +433,7 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Pl
     if (plan.items == 1) {
       s.total = item_tiles(a, plan, 0, R);
     } else {
-      s = scan_items(a, plan, R, sm.sums);
+      s = scan_items<kWaves>(a, plan, R, sm.sums);
     }
     s.total = uniform64(s.total);
     const int64_t all = s.total * a.c.heads;
@@ -308,44 +460,49 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Pl
     const int t1 = (int)(at + left < tiles ? at + left : tiles);
     const int limit = x.len + x.count;                    // the first token nobody sees
     const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
-    __syncthreads();  // the last item's sums have been read
 
-    // What the rows see of the nodes.
+    const int32_t* pages = a.c.table + (int64_t)x.b * a.c.width;
+    KeyTile<D> kt;
+    int key0 = t0 * kTile + 32 * wave;
+    Blocks here = find_blocks(a, pages, h, key0);
+    load_keys<D>(a, here, kt);
+    load_values<D>(a, here, kt);
+    Blocks next = find_blocks(a, pages, h, key0 + kTile);
+
+    const int t = fresh_thread(), lane = t & 63, j = lane & 15, q4 = lane >> 4;
+    __syncthreads();  // the last item's sums have been read
     if (a.parent && wave == 0) {
       const int par = lane < a.nodes ? a.parent[(int64_t)x.b * a.nodes + lane] : -1;
       sm.tree[lane] = ancestors_of_wave(par);
     }
-    // Queries: lane (j, q4) holds values 64 c + 16 q4 + 8 half + e of row j.
-    bf8_t qr[NQ][RT][KS];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int f = wave; f < RT * KS; f += kWaves) {  // one operand of the queries at a time
+      const int r = f / KS, s = f - r * KS;
       int row = x.row0 + 16 * r + j;
       row = row < rows_all ? row : rows_all - 1;
       const int node = row / a.group;
-      const int64_t from = ((int64_t)x.b * a.nodes + node) * a.q_stride +
-                           (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4;
+      const int64_t off = ((int64_t)x.b * a.nodes + node) * a.q_stride +
+                          (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4 + 64 * (s >> 1) + 8 * (s & 1);
+      if constexpr (F32) {
+        const f4_t* p = reinterpret_cast<const f4_t*>(static_cast<const float*>(a.q) + off);
+        const f4_t lo = p[0], hi = p[1];
+        bf8_t part[3];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int64_t off = from + 64 * (s >> 1) + 8 * (s & 1);
-        if constexpr (F32) {
-          const f4_t* p = reinterpret_cast<const f4_t*>(static_cast<const float*>(a.q) + off);
-          const f4_t lo = p[0], hi = p[1];
+        for (int e = 0; e < 8; ++e) {
+          float y = e < 4 ? lo[e & 3] : hi[e & 3];
+          y = flip ? -y : y;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float y = e < 4 ? lo[e & 3] : hi[e & 3];
-            y = flip ? -y : y;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              const __bf16 b = (__bf16)y;
-              qr[n][r][s][e] = b;
-              y -= (float)b;
-            }
+          for (int n = 0; n < 3; ++n) {
+            const __bf16 b = (__bf16)y;
+            part[n][e] = b;
+            y -= (float)b;
           }
-        } else {
-          u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(a.q) + off);
-          if (flip) w ^= 0x80008000u;
-          qr[0][r][s] = __builtin_bit_cast(bf8_t, w);
         }
+#pragma unroll
+        for (int n = 0; n < 3; ++n) sm.q[n][r][s][lane] = part[n];
+      } else {
+        u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(a.q) + off);
+        if (flip) w ^= 0x80008000u;
+        sm.q[0][r][s][lane] = __builtin_bit_cast(bf8_t, w);
       }
     }
     __syncthreads();
@@ -357,175 +514,77 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Pl
     }
     __syncthreads();
 
-    f4_t o[RT][NT];
-    float m[RT], l[RT];
+    Sums<RT, NT> acc;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      m[r] = kStart;
-      l[r] = 0.0f;
+      acc.m[r] = kStart;
+      acc.l[r] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < NT; ++n) acc.o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-
-    const int32_t* pages = a.c.table + (int64_t)x.b * a.c.width;
-    KeyTile<D> cur, nxt;
-    int id[2];
-    page_ids(a, pages, t0 * kTile + 32 * wave, id);
-    load_tile<D>(a, h, t0 * kTile + 32 * wave, id, cur);
-    page_ids(a, pages, (t0 + 1) * kTile + 32 * wave, id);
     for (int tile = t0; tile < t1; ++tile) {
-      const int key0 = tile * kTile + 32 * wave;
-      if (tile + 1 < t1) {
-        load_tile<D>(a, h, key0 + kTile, id, nxt);
-        page_ids(a, pages, key0 + 2 * kTile, id);
-      }
-      const bool masked = key0 + 32 > clear || !cur.there[0] || !cur.there[1];
-
-      // z of 32 tokens x R rows.
+      const bool more = tile + 1 < t1;
+      asm volatile("" ::: "memory");  // the queries are read again from LDS: kept in registers they would spill
       f4_t z[2][RT];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) z[kb][r] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const u4_t w = cur.k[kb][s >> 1];
-          const bf8_t kop = (s & 1) ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
-#pragma unroll
-          for (int n = NQ - 1; n >= 0; --n)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) z[kb][r] = mfma_bf16(kop, qr[n][r][s], z[kb][r]);
-        }
-      }
-      if (masked) {
-        // Values of tokens that nobody sees may be anything: their bytes are cleared.
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3);
-          const bool keep = cur.there[e >> 2] && pos < limit;
-#pragma unroll
-          for (int n = 0; n < D / 64; ++n) cur.v[e].w[n] = keep ? cur.v[e].w[n] : 0u;
-        }
-      }
-
-      h8_t ph[RT], pl[F32 ? RT : 1];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        uint32_t seen = 0xFFu;
-        if (masked) {
-          seen = 0u;
-          const uint64_t line = sm.line[16 * r + j];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3);
-            const int u = pos - x.len;
-            const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
-            const bool ok = cur.there[e >> 2] && pos < limit && (u < 0 || node);
-            seen |= ok ? 1u << e : 0u;
-            z[e >> 2][r][e & 3] = ok ? z[e >> 2][r][e & 3] : -__builtin_inff();
-          }
-        }
-        float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
-                                                    __builtin_fmaxf(z[0][r][2], z[0][r][3])),
-                                    __builtin_fmaxf(__builtin_fmaxf(z[1][r][0], z[1][r][1]),
-                                                    __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
-        if (__any(top > m[r] + kLead)) {
-          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-          const float mn = __builtin_fmaxf(m[r], top);
-          const float f = __builtin_amdgcn_exp2f(m[r] - mn);
-          m[r] = mn;
-          l[r] *= f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) o[r][n] *= f;
-        }
-        const float lift = kLift - m[r];
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.0f;
-        }
-        l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const _Float16 x16 = (_Float16)p[e];
-          ph[r][e] = x16;
-          if constexpr (F32) pl[r][e] = (_Float16)(p[e] - (float)x16);
-        }
-      }
-
-      // O += V^T P: word n of a token's bytes holds d = (D / 16) i + 4 n ..
-#pragma unroll
-      for (int n = 0; n < D / 64; ++n) {
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo[e] = __builtin_amdgcn_perm(cur.v[2 * e + 1].w[n], cur.v[2 * e].w[n], 0x05010400u);
-          hi[e] = __builtin_amdgcn_perm(cur.v[2 * e + 1].w[n], cur.v[2 * e].w[n], 0x07030602u);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const h8_t vop = u == 0 ? to_f16x8<false>(lo) : u == 1 ? to_f16x8<true>(lo)
-                         : u == 2 ? to_f16x8<false>(hi) : to_f16x8<true>(hi);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if constexpr (F32) o[r][4 * n + u] = mfma16x16x32(vop, pl[r], o[r][4 * n + u]);
-            o[r][4 * n + u] = mfma16x16x32(vop, ph[r], o[r][4 * n + u]);
-          }
-        }
-      }
-      cur = nxt;
+      score<D, RT, F32>(sm, kt, z);
+      if (more) load_keys<D>(a, next, kt);
+      if (key0 + 32 > clear || !here.there[0] || !here.there[1])
+        mask<D, RT, F32>(a, sm, kt, z, key0, x.len, limit, here);
+      accumulate<D, RT, F32>(kt, z, acc, c);
+      if (more) load_values<D>(a, next, kt);
+      here = next;
+      key0 += kTile;
+      if (more) next = find_blocks(a, pages, h, key0 + kTile);
     }
 
-    // Join the four waves, one row tile at a time.
+    // Join the waves, one row tile at a time.
+    const int te = fresh_thread(), le = te & 63, je = le & 15, qe = le >> 4;
     const bool whole = t0 == 0 && t1 == tiles;
     const int slot = 2 * group + (t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      l[r] += __shfl_xor(l[r], 16);
-      l[r] += __shfl_xor(l[r], 32);
-      if (q4 == 0) {
-        sm.m[wave][16 * r + j] = m[r];
-        sm.l[wave][16 * r + j] = l[r];
+      float l = acc.l[r];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (qe == 0) {
+        sm.m[wave][16 * r + je] = acc.m[r];
+        sm.l[wave][16 * r + je] = l;
       }
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      if (r > 0) __syncthreads();
+      __syncthreads();
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int n = 0; n < NT; n += 4)
-          *reinterpret_cast<f4_t*>(&sm.o[wave][j][NT * (4 * q4 + e) + n]) =
-              f4_t{o[r][n][e], o[r][n + 1][e], o[r][n + 2][e], o[r][n + 3][e]};
+          *reinterpret_cast<f4_t*>(&sm.o[wave][je][NT * (4 * qe + e) + n]) =
+              f4_t{acc.o[r][n][e], acc.o[r][n + 1][e], acc.o[r][n + 2][e], acc.o[r][n + 3][e]};
       __syncthreads();
-      const int row16 = t >> 4, d0 = NT * (t & 15), row = 16 * r + row16;
-      float top = kStart;
+      constexpr int PER = 16 * D / (64 * kWaves), LANES = D / PER;  // values per thread, threads per row
+      const int row16 = te / LANES, d0 = PER * (te % LANES), row = 16 * r + row16;
+      float mw[kWaves], top = kStart, sum = 0.0f, y[PER];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, sm.m[w][row]);
-      float sum = 0.0f, acc[NT];
+      for (int w = 0; w < kWaves; ++w) {
+        mw[w] = sm.m[w][row];
+        top = __builtin_fmaxf(top, mw[w]);
+      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n] = 0.0f;
+      for (int n = 0; n < PER; ++n) y[n] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm.m[w][row] - top);
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(mw[w] - top);
         sum += f * sm.l[w][row];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] += f * sm.o[w][row16][d0 + n];
+        for (int n = 0; n < PER; ++n) y[n] += f * sm.o[w][row16][d0 + n];
       }
       if (!whole) {
         float* to = plan.part + ((int64_t)slot * R + row) * D + d0;
 #pragma unroll
-        for (int n = 0; n < NT; n += 4)
-          *reinterpret_cast<f4_t*>(to + n) = f4_t{acc[n], acc[n + 1], acc[n + 2], acc[n + 3]};
-        if ((t & 15) == 0) {
-          float* ml = plan.part + (int64_t)2 * plan.groups * R * D + ((int64_t)slot * R + row) * 2;
-          ml[0] = top;
-          ml[1] = sum;
-        }
+        for (int n = 0; n < PER; n += 2) *reinterpret_cast<f2_t*>(to + n) = f2_t{y[n], y[n + 1]};
+        if (d0 == 0)
+          *reinterpret_cast<f2_t*>(plan.part + (int64_t)2 * plan.groups * R * D + ((int64_t)slot * R + row) * 2) =
+              f2_t{top, sum};
         continue;
       }
       const int grow = x.row0 + row;
@@ -538,15 +597,15 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(KvAttentionArgs a, Pl
       if constexpr (F32) {
         float* to = static_cast<float*>(a.out) + orow * D + d0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) to[n] = live ? acc[n] * f : 0.0f;
+        for (int n = 0; n < PER; ++n) to[n] = live ? y[n] * f : 0.0f;
       } else {
         uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + d0);
 #pragma unroll
-        for (int n = 0; n < NT; n += 2)
-          to[n / 2] = live ? (uint32_t)f32_to_bf16_rne(acc[n] * f) | ((uint32_t)f32_to_bf16_rne(acc[n + 1] * f) << 16)
+        for (int n = 0; n < PER; n += 2)
+          to[n / 2] = live ? (uint32_t)f32_to_bf16_rne(y[n] * f) | ((uint32_t)f32_to_bf16_rne(y[n + 1] * f) << 16)
                            : 0u;
       }
-      if (a.lse && (t & 15) == 0)
+      if (a.lse && d0 == 0)
         a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
     }
 
@@ -572,7 +631,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   if (plan.items == 1) {
     s.total = item_tiles(a, plan, 0, R);
   } else {
-    s = scan_items(a, plan, R, sums);
+    s = scan_items<4>(a, plan, R, sums);
   }
   const int64_t all = s.total * a.c.heads;
   const int64_t n = plan.groups < all ? plan.groups : all;
@@ -684,13 +743,13 @@ int compute_units() {
 // tile take D / 8 + D / 4 registers, three times the queries in fp32), the
 // tiles of a KV head spread evenly over its items.
 int row_tiles(const KvAttentionArgs& a, int* row_items) {
-  const int most = !a.bf16 ? 2 : a.c.dim == 64 ? 8 : a.c.dim == 128 ? 6 : 3;
+  const int most = !a.bf16 ? (a.c.dim == 256 ? 1 : 2) : a.c.dim == 64 ? 6 : a.c.dim == 128 ? 4 : 2;
   const int all = (int)(((int64_t)a.nodes * a.group + 15) / 16);
   *row_items = (all + most - 1) / most;
   return (all + *row_items - 1) / *row_items;
 }
 
-int groups_per_cu(int dim, int rt) { return rt * dim <= 128 ? 4 : rt * dim <= 256 ? 2 : 1; }
+int groups_per_cu(int dim, int rt, bool f32) { return waves_per_simd(dim, rt, f32) * 4 / kWaves; }
 
 Plan make_plan(const KvAttentionArgs& a, int* rt, int64_t* bytes) {
   Plan p;
@@ -699,7 +758,7 @@ Plan make_plan(const KvAttentionArgs& a, int* rt, int64_t* bytes) {
   p.cap = (int64_t)a.c.width << a.c.page_shift;
   p.end_tiles = (int)((p.cap + kTile - 1) / kTile);
   const int64_t most = (int64_t)p.items * a.c.heads * p.end_tiles;
-  const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt);
+  const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt, !a.bf16);
   p.groups = p.end_tiles == 1 ? 0 : (int)(groups < most ? groups : most);
   *bytes = (int64_t)2 * p.groups * 16 * *rt * (a.c.dim + 2) * 4;
   p.part = nullptr;
@@ -709,7 +768,7 @@ Plan make_plan(const KvAttentionArgs& a, int* rt, int64_t* bytes) {
 template <int D, int RT, bool F32>
 hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t stream) {
   const int64_t items = (int64_t)p.items * a.c.heads;
-  kv_attention_kernel<D, RT, F32><<<(unsigned)(p.groups ? p.groups : items), 256, 0, stream>>>(a, p);
+  kv_attention_kernel<D, RT, F32><<<(unsigned)(p.groups ? p.groups : items), 64 * kWaves, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups < 2) return e;
   const int by_item = items < p.groups ? 1 : 0;
@@ -720,24 +779,20 @@ hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t strea
 
 template <int D>
 hipError_t launch_dim(const KvAttentionArgs& a, const Plan& p, int rt, hipStream_t stream) {
-  if (!a.bf16) return rt == 1 ? launch_one<D, 1, true>(a, p, stream) : launch_one<D, 2, true>(a, p, stream);
-  switch (rt) {
-    case 1: return launch_one<D, 1, false>(a, p, stream);
-    case 2: return launch_one<D, 2, false>(a, p, stream);
-    case 3: return launch_one<D, 3, false>(a, p, stream);
-    default: break;
+  if (!a.bf16) {
+    if constexpr (D <= 128)
+      if (rt == 2) return launch_one<D, 2, true>(a, p, stream);
+    return rt == 1 ? launch_one<D, 1, true>(a, p, stream) : hipErrorInvalidValue;
   }
+  if (rt == 1) return launch_one<D, 1, false>(a, p, stream);
+  if (rt == 2) return launch_one<D, 2, false>(a, p, stream);
   if constexpr (D <= 128) {
-    switch (rt) {
-      case 4: return launch_one<D, 4, false>(a, p, stream);
-      case 5: return launch_one<D, 5, false>(a, p, stream);
-      case 6: return launch_one<D, 6, false>(a, p, stream);
-      default: break;
-    }
+    if (rt == 3) return launch_one<D, 3, false>(a, p, stream);
+    if (rt == 4) return launch_one<D, 4, false>(a, p, stream);
   }
   if constexpr (D <= 64) {
-    if (rt == 7) return launch_one<D, 7, false>(a, p, stream);
-    if (rt == 8) return launch_one<D, 8, false>(a, p, stream);
+    if (rt == 5) return launch_one<D, 5, false>(a, p, stream);
+    if (rt == 6) return launch_one<D, 6, false>(a, p, stream);
   }
   return hipErrorInvalidValue;
 }
