@@ -42,7 +42,6 @@ typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;              // waves of a workgroup
-constexpr int kTile = 32 * kWaves;     // tokens of a key tile
 constexpr float kStart = -1e30f;       // running maximum before the first score
 constexpr float kLead = 8.0f;          // how far a score may exceed it
 constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
@@ -50,9 +49,10 @@ constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
 struct Plan {
   int items;      // per KV head: sequences * row tiles
   int row_items;  // items of a sequence
+  int rows;       // rows of an item
+  int tile;       // tokens of a key tile
   int groups;     // workgroups that share the list; 0: one per item, nothing is cut
   int64_t cap;    // tokens a table row covers
-  int end_tiles;  // tiles of cap
   float* part;    // [2 * groups][rows][dim], then [2 * groups][rows][2]
 };
 
@@ -61,10 +61,10 @@ struct Item {
   int b, len, count, row0;
 };
 
-__device__ __forceinline__ Item item_of(const KvAttentionArgs& a, const Plan& p, int it, int rows) {
+__device__ __forceinline__ Item item_of(const KvAttentionArgs& a, const Plan& p, int it) {
   Item x;
   x.b = p.row_items == 1 ? it : it / p.row_items;
-  x.row0 = (it - x.b * p.row_items) * rows;
+  x.row0 = (it - x.b * p.row_items) * p.rows;
   x.len = a.c.lens[x.b];
   int n = a.counts ? a.counts[x.b] : a.nodes;
   n = n < a.nodes ? n : a.nodes;
@@ -73,20 +73,21 @@ __device__ __forceinline__ Item item_of(const KvAttentionArgs& a, const Plan& p,
 }
 
 // Tokens the item's rows may see: 0 .. end - 1.
-__device__ __forceinline__ int item_end(const KvAttentionArgs& a, const Plan& p, const Item& x, int rows) {
+__device__ __forceinline__ int item_end(const KvAttentionArgs& a, const Plan& p, const Item& x) {
   if (x.row0 >= x.count * a.group) return 0;
   int last = x.count;
   if (!a.parent) {
-    const int n = (x.row0 + rows - 1) / a.group + 1;
+    const int n = (x.row0 + p.rows - 1) / a.group + 1;
     last = n < last ? n : last;
   }
   const int64_t end = (int64_t)x.len + last;
   return (int)(end < p.cap ? end : p.cap);
 }
 
-__device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& p, int it, int rows) {
-  const int end = item_end(a, p, item_of(a, p, it, rows), rows);
-  return end > kTile ? (end + kTile - 1) / kTile : 1;
+__device__ __forceinline__ int tiles_of(const Plan& p, int end) { return end > p.tile ? (end + p.tile - 1) / p.tile : 1; }
+
+__device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& p, int it) {
+  return tiles_of(p, item_end(a, p, item_of(a, p, it)));
 }
 
 // Sum of the items' tiles and this thread's exclusive part of it; every thread
@@ -97,14 +98,14 @@ struct Scan {
 };
 
 template <int WAVES>
-__device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int rows, int64_t* sums) {
+__device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int64_t* sums) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   Scan s;
   s.per = (p.items + 64 * WAVES - 1) / (64 * WAVES);
   int64_t mine = 0;
   for (int i = 0; i < s.per; ++i) {
     const int it = t * s.per + i;
-    if (it < p.items) mine += item_tiles(a, p, it, rows);
+    if (it < p.items) mine += item_tiles(a, p, it);
   }
   int64_t v = mine;
   for (int off = 1; off < 64; off <<= 1) {
@@ -130,14 +131,14 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
 
 // The item with tile `at` of one head's list: found[0] the item, found[1] the
 // tiles of the list before it.
-__device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, int rows, const Scan& s, int64_t at,
+__device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, const Scan& s, int64_t at,
                                           int64_t* found) {
   const int t = threadIdx.x;
   int64_t x = s.before;
   for (int i = 0; i < s.per && x <= at; ++i) {
     const int it = t * s.per + i;
     if (it >= p.items) break;
-    const int n = item_tiles(a, p, it, rows);
+    const int n = item_tiles(a, p, it);
     if (at < x + n) {
       found[0] = it;
       found[1] = x;
@@ -204,29 +205,51 @@ __device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
   return r;
 }
 
-// Where the two 16-token blocks at a token stand (wave-uniform); a block whose
-// page does not exist is read from page 0 and masked.
+// Page table entries are read through the scalar cache: a wave-uniform vector
+// load would be waited for together with every key and value load before it.
+typedef const int32_t __attribute__((address_space(4))) * table_ptr;
+
+// Table entries of the two 16-token blocks at a token (wave-uniform), fetched a
+// step before they are used.
+struct Entries {
+  int page[2];
+};
+
+__device__ __forceinline__ Entries fetch_entries(const KvAttentionArgs& a, table_ptr row, int key) {
+  Entries e;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    const int at = (key + 16 * kb) >> a.c.page_shift;
+    e.page[kb] = row[at < a.c.width ? at : a.c.width - 1];
+  }
+  return e;
+}
+
+// Where the blocks stand; one whose page does not exist is read from page 0 and
+// masked.
 struct Blocks {
   int64_t at[2];
   bool there[2];
 };
 
-__device__ __forceinline__ Blocks find_blocks(const KvAttentionArgs& a, const int32_t* row, int h, int key) {
+__device__ __forceinline__ Blocks find_blocks(const KvAttentionArgs& a, const Entries& e, int h, int key) {
   Blocks b;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
-    const int pos = key + 16 * kb, at = pos >> a.c.page_shift;
-    const int p = row[at < a.c.width ? at : a.c.width - 1];
-    b.there[kb] = at < a.c.width && p >= 0 && p < a.c.pages;
+    const int pos = key + 16 * kb, p = e.page[kb];
+    b.there[kb] = pos >> a.c.page_shift < a.c.width && p >= 0 && p < a.c.pages;
     b.at[kb] = (b.there[kb] ? p : 0) * a.c.page_stride +
                (int64_t)((h << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1))) * a.c.dim;
   }
   return b;
 }
 
+// `lanes` is all ones, or zero for a load that is not needed: the loop issues
+// the same loads in every step, so that the wait for one kind never includes
+// the other, and an unneeded one reads a single line.
 template <int D>
-__device__ __forceinline__ void load_keys(const KvAttentionArgs& a, const Blocks& b, KeyTile<D>& t) {
-  const uint32_t lane = threadIdx.x & 63, off = (lane & 15) * D + 16 * (lane >> 4);
+__device__ __forceinline__ void load_keys(const KvAttentionArgs& a, const Blocks& b, uint32_t lanes, KeyTile<D>& t) {
+  const uint32_t lane = threadIdx.x & 63, off = ((lane & 15) * D + 16 * (lane >> 4)) & lanes;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -235,8 +258,9 @@ __device__ __forceinline__ void load_keys(const KvAttentionArgs& a, const Blocks
 }
 
 template <int D>
-__device__ __forceinline__ void load_values(const KvAttentionArgs& a, const Blocks& b, KeyTile<D>& t) {
-  const uint32_t lane = threadIdx.x & 63, off = 4 * (lane >> 4) * D + (D / 16) * (lane & 15);
+__device__ __forceinline__ void load_values(const KvAttentionArgs& a, const Blocks& b, uint32_t lanes,
+                                            KeyTile<D>& t) {
+  const uint32_t lane = threadIdx.x & 63, off = (4 * (lane >> 4) * D + (D / 16) * (lane & 15)) & lanes;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -266,15 +290,15 @@ __device__ __forceinline__ f4_t mfma_bf16(bf8_t a, bf8_t b, f4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-template <int D, int RT, bool F32>
+template <int D, int RT, int RG, bool F32>
 struct Smem {
   union {
-    bf8_t q[F32 ? 3 : 1][RT][D / 32][64];  // queries in operand order: value 64 (s / 2) + 16 (lane / 16) + 8 (s % 2)
+    bf8_t q[F32 ? 3 : 1][RG * RT][D / 32][64];  // queries in operand order: value 64 (s / 2) + 16 (lane / 16) + 8 (s % 2)
                                            // + e of row lane % 16
     float o[kWaves][16][D + 4];            // one row tile of the waves' sums (rows padded by 16 bytes)
   };
   float m[kWaves][16 * RT], l[kWaves][16 * RT];
-  uint64_t line[16 * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
+  uint64_t line[16 * RG * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
   uint64_t tree[64];            // ancestors of the nodes
   int64_t sums[kWaves], found[2];
 };
@@ -285,9 +309,10 @@ struct Sums {
   float m[RT], l[RT];
 };
 
-// Scores of a wave's 32 tokens against the R rows.
-template <int D, int RT, bool F32>
-__device__ __forceinline__ void score(const Smem<D, RT, F32>& sm, const KeyTile<D>& kt, f4_t (&z)[2][RT]) {
+// Scores of a wave's 32 tokens against its row tiles r0 .. r0 + RT - 1.
+template <int D, int RT, int RG, bool F32>
+__device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyTile<D>& kt, int r0,
+                                      f4_t (&z)[2][RT]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
@@ -305,7 +330,7 @@ __device__ __forceinline__ void score(const Smem<D, RT, F32>& sm, const KeyTile<
     for (int n = F32 ? 2 : 0; n >= 0; --n)  // small parts first
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const bf8_t qop = sm.q[n][r][s][lane];
+        const bf8_t qop = sm.q[n][r0 + r][s][lane];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) z[kb][r] = mfma_bf16(kop[kb], qop, z[kb][r]);
       }
@@ -314,9 +339,9 @@ __device__ __forceinline__ void score(const Smem<D, RT, F32>& sm, const KeyTile<
 
 // Scores of tokens that a row does not see become -infinity, and the values of
 // tokens that nobody sees, which may be anything, zero.
-template <int D, int RT, bool F32>
-__device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT, F32>& sm, KeyTile<D>& kt,
-                                     f4_t (&z)[2][RT], int key0, int len, int limit, const Blocks& here) {
+template <int D, int RT, int RG, bool F32>
+__device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT, RG, F32>& sm, KeyTile<D>& kt,
+                                     int r0, f4_t (&z)[2][RT], int key0, int len, int limit, const Blocks& here) {
   const int lane = fresh_thread() & 63, j = lane & 15, q4 = lane >> 4;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -326,7 +351,7 @@ __device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT,
     for (int n = 0; n < D / 64; ++n) kt.v[e].w[n] = there ? kt.v[e].w[n] : 0u;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const uint64_t line = sm.line[16 * r + j];
+      const uint64_t line = sm.line[16 * (r0 + r) + j];
       const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
       z[e >> 2][r][e & 3] = there && (u < 0 || node) ? z[e >> 2][r][e & 3] : -__builtin_inff();
     }
@@ -407,12 +432,13 @@ __device__ __forceinline__ void accumulate(const KeyTile<D>& kt, const f4_t (&z)
 // instructions then keep their sums in ordinary registers).
 constexpr int waves_per_simd(int dim, int rt, bool f32) { return rt * dim <= 128 && !f32 ? 4 : 2; }
 
-template <int D, int RT, bool F32>
+template <int D, int RT, int RG, bool F32>
 __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_attention_kernel(KvAttentionArgs a,
                                                                                               Plan plan) {
-  constexpr int R = 16 * RT, KS = D / 32, NT = D / 16;
-  __shared__ Smem<D, RT, F32> sm;
+  constexpr int R = 16 * RT * RG, KS = D / 32, NT = D / 16, KW = kWaves / RG, TILE = 32 * KW;
+  __shared__ Smem<D, RT, RG, F32> sm;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % KW, r0 = wave / KW * RT;  // which 32 tokens of a tile, which row tiles
   const int rows_all = a.nodes * a.group;
   const float c0 = a.sm_scale * *a.k_scale * 1.44269504088896340736f;
   const float c = __builtin_fmaxf(__builtin_fabsf(c0), 1.17549435e-38f);  // not 0: a masked score stays -infinity
@@ -427,13 +453,13 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     h = blockIdx.x / plan.items;
     it = blockIdx.x - h * plan.items;
     at = 0;
-    left = item_tiles(a, plan, it, R);
+    left = item_tiles(a, plan, it);
   } else {
     Scan s;
     if (plan.items == 1) {
-      s.total = item_tiles(a, plan, 0, R);
+      s.total = item_tiles(a, plan, 0);
     } else {
-      s = scan_items<kWaves>(a, plan, R, sm.sums);
+      s = scan_items<kWaves>(a, plan, sm.sums);
     }
     s.total = uniform64(s.total);
     const int64_t all = s.total * a.c.heads;
@@ -446,28 +472,29 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     left = end - begin;
     it = 0;
     if (plan.items > 1) {
-      find_item(a, plan, R, s, at, sm.found);
+      find_item(a, plan, s, at, sm.found);
       it = __builtin_amdgcn_readfirstlane((int)sm.found[0]);
       at -= uniform64(sm.found[1]);
     }
   }
 
   while (left > 0) {
-    const Item x = item_of(a, plan, it, R);
-    const int end = item_end(a, plan, x, R);
-    const int tiles = end > kTile ? (end + kTile - 1) / kTile : 1;
+    const Item x = item_of(a, plan, it);
+    const int end = item_end(a, plan, x);
+    const int tiles = tiles_of(plan, end);
     const int t0 = (int)at;
     const int t1 = (int)(at + left < tiles ? at + left : tiles);
     const int limit = x.len + x.count;                    // the first token nobody sees
     const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
 
-    const int32_t* pages = a.c.table + (int64_t)x.b * a.c.width;
+    const table_ptr pages = (table_ptr)(uintptr_t)(a.c.table + (int64_t)x.b * a.c.width);
     KeyTile<D> kt;
-    int key0 = t0 * kTile + 32 * wave;
-    Blocks here = find_blocks(a, pages, h, key0);
-    load_keys<D>(a, here, kt);
-    load_values<D>(a, here, kt);
-    Blocks next = find_blocks(a, pages, h, key0 + kTile);
+    int key0 = t0 * TILE + 32 * kw;
+    Entries entries = fetch_entries(a, pages, key0);
+    Blocks here = find_blocks(a, entries, h, key0);
+    load_keys<D>(a, here, ~0u, kt);
+    load_values<D>(a, here, ~0u, kt);
+    entries = fetch_entries(a, pages, key0 + TILE);
 
     const int t = fresh_thread(), lane = t & 63, j = lane & 15, q4 = lane >> 4;
     __syncthreads();  // the last item's sums have been read
@@ -475,7 +502,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       const int par = lane < a.nodes ? a.parent[(int64_t)x.b * a.nodes + lane] : -1;
       sm.tree[lane] = ancestors_of_wave(par);
     }
-    for (int f = wave; f < RT * KS; f += kWaves) {  // one operand of the queries at a time
+    for (int f = wave; f < RG * RT * KS; f += kWaves) {  // one operand of the queries at a time
       const int r = f / KS, s = f - r * KS;
       int row = x.row0 + 16 * r + j;
       row = row < rows_all ? row : rows_all - 1;
@@ -523,18 +550,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       for (int n = 0; n < NT; ++n) acc.o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     for (int tile = t0; tile < t1; ++tile) {
-      const bool more = tile + 1 < t1;
+      const uint32_t more = tile + 1 < t1 ? ~0u : 0u;
       asm volatile("" ::: "memory");  // the queries are read again from LDS: kept in registers they would spill
       f4_t z[2][RT];
-      score<D, RT, F32>(sm, kt, z);
-      if (more) load_keys<D>(a, next, kt);
+      score(sm, kt, r0, z);
+      const Blocks next = find_blocks(a, entries, h, key0 + TILE);
+      load_keys<D>(a, next, more, kt);
+      entries = fetch_entries(a, pages, key0 + 2 * TILE);
       if (key0 + 32 > clear || !here.there[0] || !here.there[1])
-        mask<D, RT, F32>(a, sm, kt, z, key0, x.len, limit, here);
+        mask(a, sm, kt, r0, z, key0, x.len, limit, here);
       accumulate<D, RT, F32>(kt, z, acc, c);
-      if (more) load_values<D>(a, next, kt);
+      load_values<D>(a, next, more, kt);
       here = next;
-      key0 += kTile;
-      if (more) next = find_blocks(a, pages, h, key0 + kTile);
+      key0 += TILE;
     }
 
     // Join the waves, one row tile at a time.
@@ -561,22 +589,23 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
           *reinterpret_cast<f4_t*>(&sm.o[wave][je][NT * (4 * qe + e) + n]) =
               f4_t{acc.o[r][n][e], acc.o[r][n + 1][e], acc.o[r][n + 2][e], acc.o[r][n + 3][e]};
       __syncthreads();
-      constexpr int PER = 16 * D / (64 * kWaves), LANES = D / PER;  // values per thread, threads per row
-      const int row16 = te / LANES, d0 = PER * (te % LANES), row = 16 * r + row16;
-      float mw[kWaves], top = kStart, sum = 0.0f, y[PER];
+      constexpr int THREADS = 64 * KW, PER = 16 * D / THREADS, LANES = D / PER;  // of a row tile, of a thread, of a row
+      const int rg = te / THREADS, row16 = te % THREADS / LANES, d0 = PER * (te % LANES);
+      const int row = 16 * (rg * RT + r) + row16;
+      float mw[KW], top = kStart, sum = 0.0f, y[PER];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        mw[w] = sm.m[w][row];
+      for (int w = 0; w < KW; ++w) {
+        mw[w] = sm.m[rg * KW + w][16 * r + row16];
         top = __builtin_fmaxf(top, mw[w]);
       }
 #pragma unroll
       for (int n = 0; n < PER; ++n) y[n] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < KW; ++w) {
         const float f = __builtin_amdgcn_exp2f(mw[w] - top);
-        sum += f * sm.l[w][row];
+        sum += f * sm.l[rg * KW + w][16 * r + row16];
 #pragma unroll
-        for (int n = 0; n < PER; ++n) y[n] += f * sm.o[w][row16][d0 + n];
+        for (int n = 0; n < PER; ++n) y[n] += f * sm.o[rg * KW + w][row16][d0 + n];
       }
       if (!whole) {
         float* to = plan.part + ((int64_t)slot * R + row) * D + d0;
@@ -622,16 +651,17 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 // Joins the partial sums of the items that a range boundary cut: block (item
 // or boundary, four rows), a wave a row.
 template <int D, bool F32>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan, int R, int by_item) {
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan, int by_item) {
+  const int R = plan.rows;
   __shared__ int64_t sums[4], found[2];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   int h, it;
   int64_t before;  // tiles of the head's list before the item
   Scan s;
   if (plan.items == 1) {
-    s.total = item_tiles(a, plan, 0, R);
+    s.total = item_tiles(a, plan, 0);
   } else {
-    s = scan_items<4>(a, plan, R, sums);
+    s = scan_items<4>(a, plan, sums);
   }
   const int64_t all = s.total * a.c.heads;
   const int64_t n = plan.groups < all ? plan.groups : all;
@@ -642,7 +672,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     if (plan.items > 1) {
       if (it / s.per == t) {
         int64_t y = s.before;
-        for (int i = t * s.per; i < it; ++i) y += item_tiles(a, plan, i, R);
+        for (int i = t * s.per; i < it; ++i) y += item_tiles(a, plan, i);
         found[1] = y;
       }
       __syncthreads();
@@ -656,7 +686,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     it = 0;
     before = 0;
     if (plan.items > 1) {
-      find_item(a, plan, R, s, begin - h * s.total, found);
+      find_item(a, plan, s, begin - h * s.total, found);
       it = (int)found[0];
       before = found[1];
     }
@@ -664,9 +694,9 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     // only the boundary behind the item's first range joins it
     if (first == begin || ((first + 1) * n - 1) / all != g - 1) return;
   }
-  const Item x = item_of(a, plan, it, R);
-  const int end = item_end(a, plan, x, R);
-  const int tiles = end > kTile ? (end + kTile - 1) / kTile : 1;
+  const Item x = item_of(a, plan, it);
+  const int end = item_end(a, plan, x);
+  const int tiles = tiles_of(plan, end);
   const int64_t first = h * s.total + before;
   const int g0 = (int)(((first + 1) * n - 1) / all), g1 = (int)(((first + tiles) * n - 1) / all);
   if (g0 == g1) return;
@@ -739,83 +769,90 @@ int compute_units() {
   return cus[dev];
 }
 
-// Row tiles of an item: as many as the registers hold (queries and sums of a
-// tile take D / 8 + D / 4 registers, three times the queries in fp32), the
-// tiles of a KV head spread evenly over its items.
-int row_tiles(const KvAttentionArgs& a, int* row_items) {
-  const int most = !a.bf16 ? (a.c.dim == 256 ? 1 : 2) : a.c.dim == 64 ? 6 : a.c.dim == 128 ? 4 : 2;
+// A wave holds up to `most` row tiles (a tile's sums take D / 4 registers); the
+// waves of a workgroup are shared out over 1, 2 or 4 groups of rows, the fewest
+// that hold all rows, and only rows beyond that take a further item, which
+// reads the cache again.
+constexpr int most_row_tiles(int dim, bool f32) {
+  return f32 ? (dim == 256 ? 1 : 2) : dim == 64 ? 6 : dim == 128 ? 4 : 2;
+}
+
+void row_split(const KvAttentionArgs& a, int* rt, int* rg, int* row_items) {
+  const int most = most_row_tiles(a.c.dim, !a.bf16);
   const int all = (int)(((int64_t)a.nodes * a.group + 15) / 16);
-  *row_items = (all + most - 1) / most;
-  return (all + *row_items - 1) / *row_items;
+  *rg = all <= most ? 1 : all <= 2 * most ? 2 : 4;
+  *row_items = (all + *rg * most - 1) / (*rg * most);
+  *rt = (all + *row_items * *rg - 1) / (*row_items * *rg);
 }
 
 int groups_per_cu(int dim, int rt, bool f32) { return waves_per_simd(dim, rt, f32) * 4 / kWaves; }
 
-Plan make_plan(const KvAttentionArgs& a, int* rt, int64_t* bytes) {
+Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
   Plan p;
-  *rt = row_tiles(a, &p.row_items);
+  row_split(a, rt, rg, &p.row_items);
   p.items = a.c.seqs * p.row_items;
+  p.rows = 16 * *rt * *rg;
+  p.tile = 32 * kWaves / *rg;
   p.cap = (int64_t)a.c.width << a.c.page_shift;
-  p.end_tiles = (int)((p.cap + kTile - 1) / kTile);
-  const int64_t most = (int64_t)p.items * a.c.heads * p.end_tiles;
+  const int64_t tiles = (p.cap + p.tile - 1) / p.tile, most = (int64_t)p.items * a.c.heads * tiles;
   const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt, !a.bf16);
-  p.groups = p.end_tiles == 1 ? 0 : (int)(groups < most ? groups : most);
-  *bytes = (int64_t)2 * p.groups * 16 * *rt * (a.c.dim + 2) * 4;
+  p.groups = tiles == 1 ? 0 : (int)(groups < most ? groups : most);
+  *bytes = (int64_t)2 * p.groups * p.rows * (a.c.dim + 2) * 4;
   p.part = nullptr;
   return p;
 }
 
-template <int D, int RT, bool F32>
+template <int D, int RT, int RG, bool F32>
 hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t stream) {
   const int64_t items = (int64_t)p.items * a.c.heads;
-  kv_attention_kernel<D, RT, F32><<<(unsigned)(p.groups ? p.groups : items), 64 * kWaves, 0, stream>>>(a, p);
+  kv_attention_kernel<D, RT, RG, F32><<<(unsigned)(p.groups ? p.groups : items), 64 * kWaves, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups < 2) return e;
   const int by_item = items < p.groups ? 1 : 0;
-  kv_attention_join_kernel<D, F32><<<dim3((unsigned)(by_item ? items : p.groups - 1), 4 * RT), 256, 0, stream>>>(
-      a, p, 16 * RT, by_item);
+  kv_attention_join_kernel<D, F32><<<dim3((unsigned)(by_item ? items : p.groups - 1), p.rows / 4), 256, 0, stream>>>(
+      a, p, by_item);
   return hipGetLastError();
 }
 
+// RT row tiles a wave, for the numbers of row groups that lead to it.
+template <int D, int RT, bool F32>
+hipError_t launch_tiles(const KvAttentionArgs& a, const Plan& p, int rt, int rg, hipStream_t stream) {
+  constexpr int most = most_row_tiles(D, F32);
+  if (rt != RT) {
+    if constexpr (RT < most) return launch_tiles<D, RT + 1, F32>(a, p, rt, rg, stream);
+    return hipErrorInvalidValue;
+  }
+  if constexpr (2 * RT > most) {  // more than `most` tiles over the groups
+    if (rg == 2) return launch_one<D, RT, 2, F32>(a, p, stream);
+    if (rg == 4) return launch_one<D, RT, 4, F32>(a, p, stream);
+  }
+  return rg == 1 ? launch_one<D, RT, 1, F32>(a, p, stream) : hipErrorInvalidValue;
+}
+
 template <int D>
-hipError_t launch_dim(const KvAttentionArgs& a, const Plan& p, int rt, hipStream_t stream) {
-  if (!a.bf16) {
-    if constexpr (D <= 128)
-      if (rt == 2) return launch_one<D, 2, true>(a, p, stream);
-    return rt == 1 ? launch_one<D, 1, true>(a, p, stream) : hipErrorInvalidValue;
-  }
-  if (rt == 1) return launch_one<D, 1, false>(a, p, stream);
-  if (rt == 2) return launch_one<D, 2, false>(a, p, stream);
-  if constexpr (D <= 128) {
-    if (rt == 3) return launch_one<D, 3, false>(a, p, stream);
-    if (rt == 4) return launch_one<D, 4, false>(a, p, stream);
-  }
-  if constexpr (D <= 64) {
-    if (rt == 5) return launch_one<D, 5, false>(a, p, stream);
-    if (rt == 6) return launch_one<D, 6, false>(a, p, stream);
-  }
-  return hipErrorInvalidValue;
+hipError_t launch_dim(const KvAttentionArgs& a, const Plan& p, int rt, int rg, hipStream_t stream) {
+  return a.bf16 ? launch_tiles<D, 1, false>(a, p, rt, rg, stream) : launch_tiles<D, 1, true>(a, p, rt, rg, stream);
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(const KvAttentionArgs& a) {
-  int rt;
+  int rt, rg;
   int64_t bytes;
-  make_plan(a, &rt, &bytes);
+  make_plan(a, &rt, &rg, &bytes);
   return bytes;
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream) {
-  int rt;
+  int rt, rg;
   int64_t bytes;
-  Plan p = make_plan(a, &rt, &bytes);
+  Plan p = make_plan(a, &rt, &rg, &bytes);
   if (a.workspace_bytes < bytes) p.groups = 0;
   p.part = static_cast<float*>(a.workspace);
   switch (a.c.dim) {
-    case 64: return launch_dim<64>(a, p, rt, stream);
-    case 128: return launch_dim<128>(a, p, rt, stream);
-    default: return launch_dim<256>(a, p, rt, stream);
+    case 64: return launch_dim<64>(a, p, rt, rg, stream);
+    case 128: return launch_dim<128>(a, p, rt, rg, stream);
+    default: return launch_dim<256>(a, p, rt, rg, stream);
   }
 }
 
