@@ -10,10 +10,11 @@
 // Mathematics.  For a row (node v, query head) z_t = c * sum_d q_d k_td in
 // exponent units of 2 (c = sm_scale * k_scale * log2 e), p_t = 2^(z_t - m), out
 // = v_scale * sum_t p_t v_t / sum_t p_t.  Any m gives the same quotient, so m
-// follows the running maximum lazily: it moves only when a score exceeds it by
-// more than 8, and the sums are rescaled only then.  p is held as 2^(z - m +
-// 7): at most 2^15, inside f16's range, and normal down to 2^-21 of the
-// largest.
+// follows the running maximum lazily: p is held as 2^(z - m + 7), and only when
+// the sum of a lane's eight p, which the softmax needs anyway, exceeds 2^15 (a
+// score is 5 to 8 above m, or more) does m move up to the maximum, the sums are
+// rescaled and the eight are taken again.  So p stays inside f16's range, normal
+// down to 2^-21 of the largest, and no maximum is taken in an ordinary step.
 //
 // Work.  The rows that share a KV head (nodes x group) are packed into tiles
 // of 16; an item is RT row tiles of one (sequence, KV head).  A key tile is 128
@@ -32,6 +33,8 @@
 // product's key order is 4q .. 4q + 3 and 16 + 4q .. for lane group q, which
 // the value loads follow; the 2 x 2 byte transposes are v_perm.  fp32 calls
 // split q into three bf16 parts and p into two f16 parts.
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -43,8 +46,8 @@ typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;              // waves of a workgroup
 constexpr float kStart = -1e30f;       // running maximum before the first score
-constexpr float kLead = 8.0f;          // how far a score may exceed it
 constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
+constexpr float kMost = 32768.0f;      // a lane's eight p sum up to no more, so each fits f16
 
 struct Plan {
   int items;      // per KV head: sequences * row tiles
@@ -127,6 +130,12 @@ __device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan&
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// x / y of non-negative numbers, in 32 bits where they fit (a 64-bit division
+// takes hundreds of instructions).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
 
 // The item with tile `at` of one head's list: found[0] the item, found[1] the
@@ -215,31 +224,35 @@ struct Entries {
   int page[2];
 };
 
+__device__ __forceinline__ int entry_at(const KvAttentionArgs& a, table_ptr row, int pos) {
+  const int at = pos >> a.c.page_shift;
+  const int p = row[at < a.c.width ? at : a.c.width - 1];
+  return at < a.c.width ? p : -1;
+}
+
 __device__ __forceinline__ Entries fetch_entries(const KvAttentionArgs& a, table_ptr row, int key) {
   Entries e;
-#pragma unroll
-  for (int kb = 0; kb < 2; ++kb) {
-    const int at = (key + 16 * kb) >> a.c.page_shift;
-    e.page[kb] = row[at < a.c.width ? at : a.c.width - 1];
-  }
+  e.page[0] = entry_at(a, row, key);
+  e.page[1] = a.c.page_shift >= 5 ? e.page[0] : entry_at(a, row, key + 16);
   return e;
 }
 
 // Where the blocks stand; one whose page does not exist is read from page 0 and
 // masked.
 struct Blocks {
-  int64_t at[2];
+  uint64_t at[2];
   bool there[2];
 };
 
 __device__ __forceinline__ Blocks find_blocks(const KvAttentionArgs& a, const Entries& e, int h, int key) {
   Blocks b;
+  const uint32_t shift = a.c.page_shift, pages = a.c.pages, slots = (1u << shift) - 1;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
-    const int pos = key + 16 * kb, p = e.page[kb];
-    b.there[kb] = pos >> a.c.page_shift < a.c.width && p >= 0 && p < a.c.pages;
-    b.at[kb] = (b.there[kb] ? p : 0) * a.c.page_stride +
-               (int64_t)((h << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1))) * a.c.dim;
+    const uint32_t p = e.page[kb];  // a negative entry is past the pages, too
+    b.there[kb] = p < pages;
+    b.at[kb] = (uint64_t)(b.there[kb] ? p : 0u) * (uint32_t)a.c.page_stride +
+               (((uint32_t)h << shift) + ((uint32_t)(key + 16 * kb) & slots)) * (uint32_t)a.c.dim;
   }
   return b;
 }
@@ -309,37 +322,44 @@ struct Sums {
   float m[RT], l[RT];
 };
 
-// Scores of a wave's 32 tokens against its row tiles r0 .. r0 + RT - 1.
-template <int D, int RT, int RG, bool F32>
-__device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyTile<D>& kt, int r0,
+// Barrier for what is passed through LDS: unlike __syncthreads it does not wait
+// for the workgroup's loads and stores in memory.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Nothing is moved across: without it the compiler converts all operands early
+// and runs out of registers.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Scores of a wave's 32 tokens against its row tiles r0 .. r0 + RT - 1: their
+// sum over the 32 values of step s.
+template <int NR, int D, int RT, int RG, bool F32>
+__device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyTile<D>& kt, int r0, int s,
                                       f4_t (&z)[2][RT]) {
   const int lane = threadIdx.x & 63;
+  bf8_t kop[2];
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) z[kb][r] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int s = 0; s < D / 32; ++s) {
-    bf8_t kop[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const u4_t w = kt.k[kb][s >> 1];
-      kop[kb] = (s & 1) ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
-    }
-#pragma unroll
-    for (int n = F32 ? 2 : 0; n >= 0; --n)  // small parts first
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const bf8_t qop = sm.q[n][r0 + r][s][lane];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) z[kb][r] = mfma_bf16(kop[kb], qop, z[kb][r]);
-      }
+  for (int kb = 0; kb < 2; ++kb) {
+    const u4_t w = kt.k[kb][s >> 1];
+    kop[kb] = (s & 1) ? to_bf16x8(w.z, w.w) : to_bf16x8(w.x, w.y);
   }
+#pragma unroll
+  for (int n = F32 ? 2 : 0; n >= 0; --n)  // small parts first
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bf8_t qop = sm.q[n][r0 + r][s][lane];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        z[kb][r] = mfma_bf16(kop[kb], qop, s == 0 && n == (F32 ? 2 : 0) ? f4_t{0.0f, 0.0f, 0.0f, 0.0f} : z[kb][r]);
+    }
 }
 
 // Scores of tokens that a row does not see become -infinity, and the values of
 // tokens that nobody sees, which may be anything, zero.
-template <int D, int RT, int RG, bool F32>
+template <int NR, int D, int RT, int RG, bool F32>
 __device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT, RG, F32>& sm, KeyTile<D>& kt,
                                      int r0, f4_t (&z)[2][RT], int key0, int len, int limit, const Blocks& here) {
   const int lane = fresh_thread() & 63, j = lane & 15, q4 = lane >> 4;
@@ -350,50 +370,46 @@ __device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT,
 #pragma unroll
     for (int n = 0; n < D / 64; ++n) kt.v[e].w[n] = there ? kt.v[e].w[n] : 0u;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int r = 0; r < NR; ++r) {
       const uint64_t line = sm.line[16 * (r0 + r) + j];
       const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
       z[e >> 2][r][e & 3] = there && (u < 0 || node) ? z[e >> 2][r][e & 3] : -__builtin_inff();
     }
+    fence();
   }
 }
 
-// Softmax of the scores and O += V^T P.
-template <int D, int RT, bool F32>
-__device__ __forceinline__ void accumulate(const KeyTile<D>& kt, const f4_t (&z)[2][RT], Sums<RT, D / 16>& acc,
-                                           float c) {
-  float top[RT];
-  bool rises = false;
+// Moves the running maxima to the largest score so far.
+template <int NR, int RT, int NT>
+__device__ __forceinline__ void raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc, float c) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    top[r] = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
-                                             __builtin_fmaxf(z[0][r][2], z[0][r][3])),
-                             __builtin_fmaxf(__builtin_fmaxf(z[1][r][0], z[1][r][1]),
-                                             __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
-    rises |= top[r] > acc.m[r] + kLead;
+  for (int r = 0; r < NR; ++r) {
+    float x = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
+                                              __builtin_fmaxf(z[0][r][2], z[0][r][3])),
+                              __builtin_fmaxf(__builtin_fmaxf(z[1][r][0], z[1][r][1]),
+                                              __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
+    x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+    x = __builtin_fmaxf(x, __shfl_xor(x, 32));
+    x = __builtin_fmaxf(acc.m[r], x);
+    const float f = __builtin_amdgcn_exp2f(acc.m[r] - x);
+    acc.m[r] = x;
+    acc.l[r] *= f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc.o[r][n] *= f;
+    fence();
   }
-  if (__any(rises)) {
+}
+
+// Softmax of the scores; the lane's sums of p, by row tile, in `sum`.
+template <int NR, bool F32, int NT, int RT>
+__device__ __forceinline__ void weigh(const f4_t (&z)[2][RT], const Sums<RT, NT>& acc, float c, h8_t (&ph)[RT],
+                                      h8_t (&pl)[F32 ? RT : 1], float (&sum)[RT]) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float x = __builtin_fmaxf(top[r], __shfl_xor(top[r], 16));
-      x = __builtin_fmaxf(x, __shfl_xor(x, 32));
-      x = __builtin_fmaxf(acc.m[r], x);
-      const float f = __builtin_amdgcn_exp2f(acc.m[r] - x);
-      acc.m[r] = x;
-      acc.l[r] *= f;
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) acc.o[r][n] *= f;
-    }
-  }
-  h8_t ph[RT], pl[F32 ? RT : 1];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
+  for (int r = 0; r < NR; ++r) {
     const float lift = kLift - acc.m[r];
     float p[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
-    }
+    for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const h2_t y = {(_Float16)p[e], (_Float16)p[e + 1]};
@@ -404,26 +420,29 @@ __device__ __forceinline__ void accumulate(const KeyTile<D>& kt, const f4_t (&z)
         pl[r][e + 1] = (_Float16)(p[e + 1] - (float)y.y);
       }
     }
-    acc.l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    sum[r] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    if (r & 1) fence();
   }
-  // word n of a token's bytes holds d = (D / 16) i + 4 n ..
+}
+
+// O += V^T P for word n of the tokens' bytes: it holds d = (D / 16) i + 4 n ..
+template <int NR, bool F32, int D, int RT>
+__device__ __forceinline__ void accumulate(const KeyTile<D>& kt, int n, const h8_t (&ph)[RT],
+                                           const h8_t (&pl)[F32 ? RT : 1], Sums<RT, D / 16>& acc) {
+  uint32_t lo[4], hi[4];
 #pragma unroll
-  for (int n = 0; n < D / 64; ++n) {
-    uint32_t lo[4], hi[4];
+  for (int e = 0; e < 4; ++e) {
+    lo[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x05010400u);
+    hi[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x07030602u);
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x05010400u);
-      hi[e] = __builtin_amdgcn_perm(kt.v[2 * e + 1].w[n], kt.v[2 * e].w[n], 0x07030602u);
-    }
+  for (int u = 0; u < 4; ++u) {
+    const h8_t vop = u == 0 ? to_f16x8<false>(lo) : u == 1 ? to_f16x8<true>(lo)
+                   : u == 2 ? to_f16x8<false>(hi) : to_f16x8<true>(hi);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const h8_t vop = u == 0 ? to_f16x8<false>(lo) : u == 1 ? to_f16x8<true>(lo)
-                     : u == 2 ? to_f16x8<false>(hi) : to_f16x8<true>(hi);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if constexpr (F32) acc.o[r][4 * n + u] = mfma16x16x32(vop, pl[r], acc.o[r][4 * n + u]);
-        acc.o[r][4 * n + u] = mfma16x16x32(vop, ph[r], acc.o[r][4 * n + u]);
-      }
+    for (int r = 0; r < NR; ++r) {
+      if constexpr (F32) acc.o[r][4 * n + u] = mfma16x16x32(vop, pl[r], acc.o[r][4 * n + u]);
+      acc.o[r][4 * n + u] = mfma16x16x32(vop, ph[r], acc.o[r][4 * n + u]);
     }
   }
 }
@@ -438,7 +457,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
   constexpr int R = 16 * RT * RG, KS = D / 32, NT = D / 16, KW = kWaves / RG, TILE = 32 * KW;
   __shared__ Smem<D, RT, RG, F32> sm;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = wave % KW, r0 = wave / KW * RT;  // which 32 tokens of a tile, which row tiles
+  const int kw = wave % KW;  // which 32 tokens of a tile
   const int rows_all = a.nodes * a.group;
   const float c0 = a.sm_scale * *a.k_scale * 1.44269504088896340736f;
   const float c = __builtin_fmaxf(__builtin_fabsf(c0), 1.17549435e-38f);  // not 0: a masked score stays -infinity
@@ -462,12 +481,11 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       s = scan_items<kWaves>(a, plan, sm.sums);
     }
     s.total = uniform64(s.total);
-    const int64_t all = s.total * a.c.heads;
-    const int64_t n = plan.groups < all ? plan.groups : all;
+    const int64_t all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
     group = blockIdx.x;
     if (group >= n) return;
-    const int64_t begin = group * all / n, end = (group + 1) * all / n;
-    h = (int)(begin / s.total);
+    const int64_t begin = divide(group * all, n), end = divide((group + 1) * all, n);
+    h = (int)divide(begin, s.total);
     at = begin - h * s.total;
     left = end - begin;
     it = 0;
@@ -487,6 +505,28 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     const int limit = x.len + x.count;                    // the first token nobody sees
     const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
 
+    // The item's row tiles in use are shared out evenly over the row groups.
+    int used = (rows_all - x.row0 + 15) / 16;
+    used = used < RG * RT ? used : RG * RT;
+    const int r0 = wave / KW * used / RG, mine = (wave / KW + 1) * used / RG - r0;
+
+    const int t = fresh_thread(), lane = t & 63, j = lane & 15, q4 = lane >> 4;
+    // The queries, one operand of one row tile at a time, all loads first.
+    constexpr int FRAGS = RG * RT * KS, PER_WAVE = (FRAGS + kWaves - 1) / kWaves, NV = F32 ? 2 : 1;
+    u4_t raw[PER_WAVE][NV];
+#pragma unroll
+    for (int i = 0; i < PER_WAVE; ++i) {
+      const int f = i * kWaves + wave < FRAGS ? i * kWaves + wave : FRAGS - 1;
+      const int s = f % KS;
+      int row = x.row0 + 16 * (f / KS) + j;
+      row = row < rows_all ? row : rows_all - 1;
+      const int node = row / a.group;
+      const int64_t off = ((int64_t)x.b * a.nodes + node) * a.q_stride +
+                          (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4 + 64 * (s >> 1) + 8 * (s & 1);
+      const u4_t* from = reinterpret_cast<const u4_t*>(static_cast<const char*>(a.q) + off * (F32 ? 4 : 2));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) raw[i][v] = from[v];
+    }
     const table_ptr pages = (table_ptr)(uintptr_t)(a.c.table + (int64_t)x.b * a.c.width);
     KeyTile<D> kt;
     int key0 = t0 * TILE + 32 * kw;
@@ -496,26 +536,20 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     load_values<D>(a, here, ~0u, kt);
     entries = fetch_entries(a, pages, key0 + TILE);
 
-    const int t = fresh_thread(), lane = t & 63, j = lane & 15, q4 = lane >> 4;
+    int par = -1;
+    if (a.parent && wave == 0 && lane < a.nodes) par = a.parent[(int64_t)x.b * a.nodes + lane];
     __syncthreads();  // the last item's sums have been read
-    if (a.parent && wave == 0) {
-      const int par = lane < a.nodes ? a.parent[(int64_t)x.b * a.nodes + lane] : -1;
-      sm.tree[lane] = ancestors_of_wave(par);
-    }
-    for (int f = wave; f < RG * RT * KS; f += kWaves) {  // one operand of the queries at a time
-      const int r = f / KS, s = f - r * KS;
-      int row = x.row0 + 16 * r + j;
-      row = row < rows_all ? row : rows_all - 1;
-      const int node = row / a.group;
-      const int64_t off = ((int64_t)x.b * a.nodes + node) * a.q_stride +
-                          (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4 + 64 * (s >> 1) + 8 * (s & 1);
+    if (a.parent && wave == 0) sm.tree[lane] = ancestors_of_wave(par);
+#pragma unroll
+    for (int i = 0; i < PER_WAVE; ++i) {
+      const int f = i * kWaves + wave;
+      if (f >= FRAGS) continue;
+      const int r = f / KS, s = f % KS;
       if constexpr (F32) {
-        const f4_t* p = reinterpret_cast<const f4_t*>(static_cast<const float*>(a.q) + off);
-        const f4_t lo = p[0], hi = p[1];
         bf8_t part[3];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float y = e < 4 ? lo[e & 3] : hi[e & 3];
+          float y = __uint_as_float(raw[i][e >> 2][e & 3]);
           y = flip ? -y : y;
 #pragma unroll
           for (int n = 0; n < 3; ++n) {
@@ -527,7 +561,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 #pragma unroll
         for (int n = 0; n < 3; ++n) sm.q[n][r][s][lane] = part[n];
       } else {
-        u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(a.q) + off);
+        u4_t w = raw[i][0];
         if (flip) w ^= 0x80008000u;
         sm.q[0][r][s][lane] = __builtin_bit_cast(bf8_t, w);
       }
@@ -549,21 +583,55 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc.o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int tile = t0; tile < t1; ++tile) {
-      const uint32_t more = tile + 1 < t1 ? ~0u : 0u;
-      asm volatile("" ::: "memory");  // the queries are read again from LDS: kept in registers they would spill
-      f4_t z[2][RT];
-      score(sm, kt, r0, z);
-      const Blocks next = find_blocks(a, entries, h, key0 + TILE);
-      load_keys<D>(a, next, more, kt);
-      entries = fetch_entries(a, pages, key0 + 2 * TILE);
-      if (key0 + 32 > clear || !here.there[0] || !here.there[1])
-        mask(a, sm, kt, r0, z, key0, x.len, limit, here);
-      accumulate<D, RT, F32>(kt, z, acc, c);
-      load_values<D>(a, next, more, kt);
-      here = next;
-      key0 += TILE;
-    }
+    // NR: the row tiles that the wave works on.
+    auto walk = [&](auto nr) {
+      constexpr int NR = decltype(nr)::value;
+      for (int tile = t0; tile < t1; ++tile) {
+        const uint32_t more = tile + 1 < t1 ? ~0u : 0u;
+        // A SIMD's two waves take turns to go first: left alone the older one does, and the younger one
+        // works on by itself at the end.
+        if ((tile ^ (wave >> 2)) & 1) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
+        asm volatile("" ::: "memory");  // the queries are read again from LDS: kept in registers they would spill
+        f4_t z[2][RT];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          score<NR>(sm, kt, r0, s, z);
+          fence();
+        }
+        const Blocks next = find_blocks(a, entries, h, key0 + TILE);
+        load_keys<D>(a, next, more, kt);
+        entries = fetch_entries(a, pages, key0 + 2 * TILE);
+        if (key0 + 32 > clear || !here.there[0] || !here.there[1])
+          mask<NR>(a, sm, kt, r0, z, key0, x.len, limit, here);
+        h8_t ph[RT], pl[F32 ? RT : 1];
+        float sum[RT];
+        weigh<NR, F32>(z, acc, c, ph, pl, sum);
+        float most = sum[0];
+#pragma unroll
+        for (int r = 1; r < NR; ++r) most = __builtin_fmaxf(most, sum[r]);
+        fence();
+        if (__any(most > kMost)) {
+          raise<NR>(z, acc, c);
+          weigh<NR, F32>(z, acc, c, ph, pl, sum);
+          fence();
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) acc.l[r] += sum[r];
+        fence();
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n) {
+          accumulate<NR, F32>(kt, n, ph, pl, acc);
+          fence();
+        }
+        load_values<D>(a, next, more, kt);
+        here = next;
+        key0 += TILE;
+      }
+    };
+    if (RT == 1 || mine == RT) walk(std::integral_constant<int, RT>{});
+    else walk(std::integral_constant<int, RT == 1 ? 1 : RT - 1>{});
+    __builtin_amdgcn_s_setprio(0);
 
     // Join the waves, one row tile at a time.
     const int te = fresh_thread(), le = te & 63, je = le & 15, qe = le >> 4;
@@ -581,58 +649,69 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      __syncthreads();
+      lds_barrier();
+      if (r < mine) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int n = 0; n < NT; n += 4)
           *reinterpret_cast<f4_t*>(&sm.o[wave][je][NT * (4 * qe + e) + n]) =
               f4_t{acc.o[r][n][e], acc.o[r][n + 1][e], acc.o[r][n + 2][e], acc.o[r][n + 3][e]};
-      __syncthreads();
-      constexpr int THREADS = 64 * KW, PER = 16 * D / THREADS, LANES = D / PER;  // of a row tile, of a thread, of a row
-      const int rg = te / THREADS, row16 = te % THREADS / LANES, d0 = PER * (te % LANES);
-      const int row = 16 * (rg * RT + r) + row16;
-      float mw[KW], top = kStart, sum = 0.0f, y[PER];
+      }
+      lds_barrier();
+      constexpr int THREADS = 64 * KW, PER = 16 * D / THREADS;  // of a row tile, values of a thread
+      constexpr int VEC = PER < 4 ? PER : 4, LANES = D / PER;   // values side by side, threads of a row
+      typedef float vec_t __attribute__((ext_vector_type(VEC)));
+      const int rg = te / THREADS, row16 = te % THREADS / LANES, d0 = VEC * (te % LANES);
+      const int first = rg * used / RG, row = 16 * (first + r) + row16, grow = x.row0 + row;
+      float mw[KW], top = kStart, sum = 0.0f;
+      vec_t y[PER / VEC];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         mw[w] = sm.m[rg * KW + w][16 * r + row16];
         top = __builtin_fmaxf(top, mw[w]);
       }
 #pragma unroll
-      for (int n = 0; n < PER; ++n) y[n] = 0.0f;
+      for (int n = 0; n < PER / VEC; ++n) y[n] = 0.0f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         const float f = __builtin_amdgcn_exp2f(mw[w] - top);
         sum += f * sm.l[rg * KW + w][16 * r + row16];
 #pragma unroll
-        for (int n = 0; n < PER; ++n) y[n] += f * sm.o[rg * KW + w][row16][d0 + n];
+        for (int n = 0; n < PER / VEC; ++n)
+          y[n] += f * *reinterpret_cast<const vec_t*>(&sm.o[rg * KW + w][row16][d0 + VEC * LANES * n]);
       }
+      if (grow >= rows_all || first + r >= (rg + 1) * used / RG) continue;
       if (!whole) {
         float* to = plan.part + ((int64_t)slot * R + row) * D + d0;
 #pragma unroll
-        for (int n = 0; n < PER; n += 2) *reinterpret_cast<f2_t*>(to + n) = f2_t{y[n], y[n + 1]};
+        for (int n = 0; n < PER / VEC; ++n) *reinterpret_cast<vec_t*>(to + VEC * LANES * n) = y[n];
         if (d0 == 0)
           *reinterpret_cast<f2_t*>(plan.part + (int64_t)2 * plan.groups * R * D + ((int64_t)slot * R + row) * 2) =
               f2_t{top, sum};
         continue;
       }
-      const int grow = x.row0 + row;
-      if (grow >= rows_all) continue;
       const int node = grow / a.group;
       const bool live = node < x.count && sum > 0.0f;
       const float f = live ? vs / sum : 0.0f;
       const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group +
                            (grow - node * a.group);
-      if constexpr (F32) {
-        float* to = static_cast<float*>(a.out) + orow * D + d0;
 #pragma unroll
-        for (int n = 0; n < PER; ++n) to[n] = live ? y[n] * f : 0.0f;
-      } else {
-        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + d0);
+      for (int n = 0; n < PER / VEC; ++n) {
+        const int64_t to = orow * D + d0 + VEC * LANES * n;
+        const vec_t out = live ? y[n] * f : (vec_t)0.0f;
+        if constexpr (F32) {
+          *reinterpret_cast<vec_t*>(static_cast<float*>(a.out) + to) = out;
+        } else {
+          uint32_t w[VEC / 2];
 #pragma unroll
-        for (int n = 0; n < PER; n += 2)
-          to[n / 2] = live ? (uint32_t)f32_to_bf16_rne(y[n] * f) | ((uint32_t)f32_to_bf16_rne(y[n + 1] * f) << 16)
-                           : 0u;
+          for (int i = 0; i < VEC; i += 2)
+            w[i / 2] = (uint32_t)f32_to_bf16_rne(out[i]) | ((uint32_t)f32_to_bf16_rne(out[i + 1]) << 16);
+          if constexpr (VEC == 4)
+            *reinterpret_cast<u2_t*>(static_cast<uint16_t*>(a.out) + to) = u2_t{w[0], w[1]};
+          else
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = w[0];
+        }
       }
       if (a.lse && d0 == 0)
         a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
@@ -663,8 +742,8 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   } else {
     s = scan_items<4>(a, plan, sums);
   }
-  const int64_t all = s.total * a.c.heads;
-  const int64_t n = plan.groups < all ? plan.groups : all;
+  s.total = uniform64(s.total);
+  const int64_t all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
   if (by_item) {
     h = blockIdx.x / plan.items;
     it = blockIdx.x - h * plan.items;
@@ -676,67 +755,79 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
         found[1] = y;
       }
       __syncthreads();
-      before = found[1];
+      before = uniform64(found[1]);
     }
   } else {
     const int64_t g = (int64_t)blockIdx.x + 1;
     if (g >= n) return;
-    const int64_t begin = g * all / n;
-    h = (int)(begin / s.total);
+    const int64_t begin = divide(g * all, n);
+    h = (int)divide(begin, s.total);
     it = 0;
     before = 0;
     if (plan.items > 1) {
       find_item(a, plan, s, begin - h * s.total, found);
-      it = (int)found[0];
-      before = found[1];
+      it = __builtin_amdgcn_readfirstlane((int)found[0]);
+      before = uniform64(found[1]);
     }
     const int64_t first = h * s.total + before;
     // only the boundary behind the item's first range joins it
-    if (first == begin || ((first + 1) * n - 1) / all != g - 1) return;
+    if (first == begin || divide((first + 1) * n - 1, all) != g - 1) return;
   }
   const Item x = item_of(a, plan, it);
   const int end = item_end(a, plan, x);
   const int tiles = tiles_of(plan, end);
   const int64_t first = h * s.total + before;
-  const int g0 = (int)(((first + 1) * n - 1) / all), g1 = (int)(((first + tiles) * n - 1) / all);
+  // the range that holds tile y begins at or before it: g * all / n <= y  <=>  g * all < (y + 1) n
+  const int g0 = (int)divide((first + 1) * n - 1, all), g1 = (int)divide((first + tiles) * n - 1, all);
   if (g0 == g1) return;
 
   const int row = blockIdx.y * 4 + wave, grow = x.row0 + row, rows_all = a.nodes * a.group;
   if (grow >= rows_all) return;
   const float* ml = plan.part + (int64_t)2 * plan.groups * R * D;
-  float top = kStart;
-  for (int g = g0 + lane; g <= g1; g += 64) {
-    const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
-    top = __builtin_fmaxf(top, ml[(slot * R + row) * 2]);
-  }
-  for (int off = 32; off > 0; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
-  constexpr int N = D / 64;
-  float sum = 0.0f, acc[N];
+  constexpr int N = D / 64, FLY = 32 / N;  // values of a lane, loads in flight
+  typedef float vec_t __attribute__((ext_vector_type(N < 2 ? 2 : N)));
+  float top = kStart, sum = 0.0f, acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
   for (int base = g0; base <= g1; base += 64) {
-    float f = 0.0f;
+    // the statistics of up to 64 partial sums, a lane each
+    float m = kStart, l = 0.0f;
     if (base + lane <= g1) {
       const int g = base + lane;
-      const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
-      const float* y = ml + (slot * R + row) * 2;
-      f = __builtin_amdgcn_exp2f(y[0] - top);
-      sum += f * y[1];
+      const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((int64_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
+      m = y.x;
+      l = y.y;
     }
     const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
-    for (int k = 0; k < many; k += 8) {  // eight loads in flight
-      float y[8][N];
+    float f = 0.0f;
+    for (int k = 0; k < many; k += FLY) {
+      float y[FLY][N];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < FLY; ++u) {
         const int g = base + (k + u < many ? k + u : k);
-        const int64_t slot = 2 * g + (g == g0 ? 1 : 0);
-        const float* from = plan.part + (slot * R + row) * D + N * lane;
+        const float* from = plan.part + ((int64_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane;
+        if constexpr (N == 1) {
+          y[u][0] = *from;
+        } else {
+          const vec_t v = *reinterpret_cast<const vec_t*>(from);
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[u][i] = from[i];
+          for (int i = 0; i < N; ++i) y[u][i] = v[i];
+        }
+      }
+      if (k == 0) {  // their weights, while the first sums arrive
+        float high = m;
+        for (int off = 32; off > 0; off >>= 1) high = __builtin_fmaxf(high, __shfl_xor(high, off));
+        high = __builtin_fmaxf(high, top);
+        const float old = __builtin_amdgcn_exp2f(top - high);
+        f = __builtin_amdgcn_exp2f(m - high);
+        sum = sum * old + f * l;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] *= old;
+        top = high;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float w = k + u < many ? __shfl(f, k + u) : 0.0f;
+      for (int u = 0; u < FLY; ++u) {
+        const float w = k + u < many ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), k + u < many ? k + u : 0)) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += w * y[u][i];
       }
@@ -745,11 +836,11 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   const int node = grow / a.group;
   const bool live = node < x.count && sum > 0.0f;
-  const float f = live ? *a.v_scale / sum : 0.0f;
+  const float scale = live ? *a.v_scale / sum : 0.0f;
   const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float y = live ? acc[i] * f : 0.0f;
+    const float y = live ? acc[i] * scale : 0.0f;
     if constexpr (F32) static_cast<float*>(a.out)[orow * D + N * lane + i] = y;
     else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
   }
