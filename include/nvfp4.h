@@ -420,7 +420,8 @@ int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int
                                            int64_t W, nvfp4_dtype dt);
 
 /* Attention of a step's nodes over the cache, the nodes' own keys and values
- * included (append them first).  Query head h reads KV head h / (Hq / H).
+ * included (append them first).  Query head h reads KV head h / (Hq / H); a KV
+ * head has at most 256 query heads.
  *   q        [B * M] rows of Hq * D values in dt, device.
  *   sm_scale finite factor of the scores (1 / sqrt(D) in most models).
  *   parent   int32 [B][M], device, M <= 64: the drafted trees, as

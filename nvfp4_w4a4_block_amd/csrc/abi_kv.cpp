@@ -14,6 +14,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // tokens a table row covers
 constexpr int64_t kMaxTable = (int64_t)1 << 29;    // entries of a page table
 constexpr int64_t kMaxRows = (int64_t)1 << 24;     // query or key rows of one call
 constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxGroup = 256;                 // query heads of a KV head
 constexpr int64_t kMaxEntries = 1024;              // sequences of one fork or resize
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -70,7 +71,7 @@ bool stride_ok(int64_t stride, int64_t row, nvfp4_dtype dt) {
 }
 
 bool attention_shape_ok(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t W) {
-  if (H < 1 || H > kMaxHeads || Hq < 1 || Hq > 65535 || Hq % H != 0) return false;
+  if (H < 1 || H > kMaxHeads || Hq < 1 || Hq % H != 0 || Hq / H > kMaxGroup) return false;
   if (!page_size_ok(page_size) || (D != 64 && D != 128 && D != 256)) return false;
   return table_ok(B, W, page_size) && nodes_ok(B, M);
 }

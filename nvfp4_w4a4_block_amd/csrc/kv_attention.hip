@@ -50,14 +50,21 @@ constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
 constexpr float kMost = 32768.0f;      // a lane's eight p sum up to no more, so each fits f16
 
 struct Plan {
-  int items;      // per KV head: sequences * row tiles
-  int row_items;  // items of a sequence
-  int rows;       // rows of an item
-  int tile;       // tokens of a key tile
-  int groups;     // workgroups that share the list; 0: one per item, nothing is cut
-  int64_t cap;    // tokens a table row covers
-  float* part;    // [2 * groups][rows][dim], then [2 * groups][rows][2]
+  int items;       // per KV head: sequences * row tiles
+  int row_items;   // items of a sequence
+  int rows;        // rows of an item
+  int tile;        // tokens of a key tile
+  int groups;      // workgroups that share the list; 0: one per item, nothing is cut
+  int cap;         // tokens a table row covers
+  uint32_t magic;  // ceil(2^32 / group), 0 for a group of one
+  float* part;     // [2 * groups][rows][dim], then [2 * groups][rows][2]
 };
+
+// Node of a row.  The quotient is exact while row * group < 2^32: a group has
+// at most 256 heads and a step 65535 nodes.
+__device__ __forceinline__ int node_of(const Plan& p, int row) {
+  return p.magic ? (int)__umulhi((uint32_t)row, p.magic) : row;
+}
 
 // Committed length (negative: unused), nodes and first row of an item.
 struct Item {
@@ -68,7 +75,8 @@ __device__ __forceinline__ Item item_of(const KvAttentionArgs& a, const Plan& p,
   Item x;
   x.b = p.row_items == 1 ? it : it / p.row_items;
   x.row0 = (it - x.b * p.row_items) * p.rows;
-  x.len = a.c.lens[x.b];
+  const int len = a.c.lens[x.b];
+  x.len = len < (1 << 30) ? len : 1 << 30;  // no table covers more
   int n = a.counts ? a.counts[x.b] : a.nodes;
   n = n < a.nodes ? n : a.nodes;
   x.count = n > 0 && x.len >= 0 ? n : 0;
@@ -80,14 +88,16 @@ __device__ __forceinline__ int item_end(const KvAttentionArgs& a, const Plan& p,
   if (x.row0 >= x.count * a.group) return 0;
   int last = x.count;
   if (!a.parent) {
-    const int n = (x.row0 + p.rows - 1) / a.group + 1;
+    const int n = node_of(p, x.row0 + p.rows - 1) + 1;
     last = n < last ? n : last;
   }
-  const int64_t end = (int64_t)x.len + last;
-  return (int)(end < p.cap ? end : p.cap);
+  const int end = x.len + last;
+  return end < p.cap ? end : p.cap;
 }
 
-__device__ __forceinline__ int tiles_of(const Plan& p, int end) { return end > p.tile ? (end + p.tile - 1) / p.tile : 1; }
+__device__ __forceinline__ int tiles_of(const Plan& p, int end) {
+  return end > p.tile ? (int)((uint32_t)(end + p.tile - 1) >> (31 - __clz(p.tile))) : 1;
+}
 
 __device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& p, int it) {
   return tiles_of(p, item_end(a, p, item_of(a, p, it)));
@@ -96,23 +106,22 @@ __device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& 
 // Sum of the items' tiles and this thread's exclusive part of it; every thread
 // of the workgroup calls it.  Thread t has the items [t * per, (t + 1) * per).
 struct Scan {
-  int per;
-  int64_t before, total;
+  int per, before, total;
 };
 
 template <int WAVES>
-__device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int64_t* sums) {
+__device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan& p, int* sums) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   Scan s;
   s.per = (p.items + 64 * WAVES - 1) / (64 * WAVES);
-  int64_t mine = 0;
+  int mine = 0;
   for (int i = 0; i < s.per; ++i) {
     const int it = t * s.per + i;
     if (it < p.items) mine += item_tiles(a, p, it);
   }
-  int64_t v = mine;
+  int v = mine;
   for (int off = 1; off < 64; off <<= 1) {
-    const int64_t o = __shfl_up(v, off);
+    const int o = __shfl_up(v, off);
     v += lane >= off ? o : 0;
   }
   if (lane == 63) sums[wave] = v;
@@ -120,30 +129,35 @@ __device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan&
   s.total = 0;
   s.before = v - mine;
   for (int w = 0; w < WAVES; ++w) {
-    const int64_t x = sums[w];
+    const int x = sums[w];
     s.before += w < wave ? x : 0;
     s.total += x;
   }
+  s.total = __builtin_amdgcn_readfirstlane(s.total);
   return s;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
+// floor(x / y) for x < 2^53: the rounded quotient is at most one too large.
+__device__ __forceinline__ int divide(uint64_t x, uint32_t y) {
+  const uint32_t q = (uint32_t)((double)x / (double)y);
+  return __builtin_amdgcn_readfirstlane((int)(x < (uint64_t)q * y ? q - 1 : q));
 }
 
-// x / y of non-negative numbers, in 32 bits where they fit (a 64-bit division
-// takes hundreds of instructions).
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-  return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+// The list of all heads' items, tile by tile: range g of n begins at tile
+// floor(g * all / n), so that ranges and equal items stay aligned.
+__device__ __forceinline__ int range_begin(int g, int all, int n) { return divide((uint64_t)g * (uint32_t)all, n); }
+
+// The range that holds tile y: the last that begins at or before it, g * all <
+// (y + 1) * n.
+__device__ __forceinline__ int range_of(int y, int all, int n) {
+  return divide((uint64_t)(uint32_t)(y + 1) * (uint32_t)n - 1, all);
 }
 
 // The item with tile `at` of one head's list: found[0] the item, found[1] the
 // tiles of the list before it.
-__device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, const Scan& s, int64_t at,
-                                          int64_t* found) {
+__device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, const Scan& s, int at, int* found) {
   const int t = threadIdx.x;
-  int64_t x = s.before;
+  int x = s.before;
   for (int i = 0; i < s.per && x <= at; ++i) {
     const int it = t * s.per + i;
     if (it >= p.items) break;
@@ -313,7 +327,7 @@ struct Smem {
   float m[kWaves][16 * RT], l[kWaves][16 * RT];
   uint64_t line[16 * RG * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
   uint64_t tree[64];            // ancestors of the nodes
-  int64_t sums[kWaves], found[2];
+  int sums[kWaves], found[2];
 };
 
 template <int RT, int NT>
@@ -358,24 +372,45 @@ __device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyT
 }
 
 // Scores of tokens that a row does not see become -infinity, and the values of
-// tokens that nobody sees, which may be anything, zero.
+// tokens that nobody sees, which may be anything, zero.  The lane's four tokens
+// of block kb are the nodes u .. u + 3 (negative: committed tokens).
 template <int NR, int D, int RT, int RG, bool F32>
 __device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT, RG, F32>& sm, KeyTile<D>& kt,
-                                     int r0, f4_t (&z)[2][RT], int key0, int len, int limit, const Blocks& here) {
+                                     int r0, f4_t (&z)[2][RT], int key0, const Item& x, const Blocks& here) {
   const int lane = fresh_thread() & 63, j = lane & 15, q4 = lane >> 4;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int pos = key0 + 16 * (e >> 2) + 4 * q4 + (e & 3), u = pos - len;
-    const bool there = here.there[e >> 2] && pos < limit;
+  for (int kb = 0; kb < 2; ++kb) {
+    const int u = key0 + 16 * kb + 4 * q4 - x.len;
+    int have = here.there[kb] ? x.count - u : 0;  // how many of the four anybody sees
+    have = have < 0 ? 0 : have < 4 ? have : 4;
+    const uint32_t some = (1u << have) - 1;
 #pragma unroll
-    for (int n = 0; n < D / 64; ++n) kt.v[e].w[n] = there ? kt.v[e].w[n] : 0u;
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)some, e, 1);
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) kt.v[4 * kb + e].w[n] &= keep;
+    }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const uint64_t line = sm.line[16 * (r0 + r) + j];
-      const bool node = a.parent ? (line >> (u & 63)) & 1 : u <= (int)line;
-      z[e >> 2][r][e & 3] = there && (u < 0 || node) ? z[e >> 2][r][e & 3] : -__builtin_inff();
+      uint32_t seen;  // of the four: bits 0 .. 3
+      if (a.parent) {
+        const uint32_t ahead = u < 0 ? (uint32_t)(line << (-u & 3)) | ((1u << (-u & 3)) - 1) : (uint32_t)(line >> (u & 63));
+        seen = u < -3 ? 15u : u < 64 ? ahead : 0u;
+      } else {
+        int n = (int)line + 1 - u;  // nodes 0 .. the row's own
+        n = n < 0 ? 0 : n < 4 ? n : 4;
+        seen = (1u << n) - 1;
+      }
+      seen &= some;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)seen, e, 1);
+        const uint32_t bits = __float_as_uint(z[kb][r][e]);
+        z[kb][r][e] = __uint_as_float((bits & keep) | (0xFF800000u & ~keep));
+      }
+      fence();
     }
-    fence();
   }
 }
 
@@ -465,8 +500,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
   const float vs = *a.v_scale;
 
   // This workgroup's range of the list.
-  int h, it;
-  int64_t at, left;  // first tile within the item, tiles to do
+  int h, it, at, left;  // head, item, first tile within it, tiles to do
   int group = 0;
   if (plan.groups == 0) {
     h = blockIdx.x / plan.items;
@@ -475,24 +509,20 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     left = item_tiles(a, plan, it);
   } else {
     Scan s;
-    if (plan.items == 1) {
-      s.total = item_tiles(a, plan, 0);
-    } else {
-      s = scan_items<kWaves>(a, plan, sm.sums);
-    }
-    s.total = uniform64(s.total);
-    const int64_t all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
+    if (plan.items == 1) s.total = item_tiles(a, plan, 0);
+    else s = scan_items<kWaves>(a, plan, sm.sums);
+    const int all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
     group = blockIdx.x;
     if (group >= n) return;
-    const int64_t begin = divide(group * all, n), end = divide((group + 1) * all, n);
-    h = (int)divide(begin, s.total);
+    const int begin = range_begin(group, all, n);
+    left = range_begin(group + 1, all, n) - begin;
+    h = divide((uint32_t)begin, s.total);
     at = begin - h * s.total;
-    left = end - begin;
     it = 0;
     if (plan.items > 1) {
       find_item(a, plan, s, at, sm.found);
-      it = __builtin_amdgcn_readfirstlane((int)sm.found[0]);
-      at -= uniform64(sm.found[1]);
+      it = __builtin_amdgcn_readfirstlane(sm.found[0]);
+      at -= __builtin_amdgcn_readfirstlane(sm.found[1]);
     }
   }
 
@@ -500,9 +530,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     const Item x = item_of(a, plan, it);
     const int end = item_end(a, plan, x);
     const int tiles = tiles_of(plan, end);
-    const int t0 = (int)at;
-    const int t1 = (int)(at + left < tiles ? at + left : tiles);
-    const int limit = x.len + x.count;                    // the first token nobody sees
+    const int t0 = at, t1 = at + left < tiles ? at + left : tiles;
     const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
 
     // The item's row tiles in use are shared out evenly over the row groups.
@@ -520,9 +548,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       const int s = f % KS;
       int row = x.row0 + 16 * (f / KS) + j;
       row = row < rows_all ? row : rows_all - 1;
-      const int node = row / a.group;
+      const int node = node_of(plan, row);
       const int64_t off = ((int64_t)x.b * a.nodes + node) * a.q_stride +
-                          (int64_t)(h * a.group + (row - node * a.group)) * D + 16 * q4 + 64 * (s >> 1) + 8 * (s & 1);
+                          (h * a.group + (row - node * a.group)) * D + 16 * q4 + 64 * (s >> 1) + 8 * (s & 1);
       const u4_t* from = reinterpret_cast<const u4_t*>(static_cast<const char*>(a.q) + off * (F32 ? 4 : 2));
 #pragma unroll
       for (int v = 0; v < NV; ++v) raw[i][v] = from[v];
@@ -570,7 +598,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     if (t < R) {
       int row = x.row0 + t;
       row = row < rows_all ? row : rows_all - 1;
-      const int node = row / a.group;
+      const int node = node_of(plan, row);
       sm.line[t] = a.parent ? sm.tree[node] : (uint64_t)node;
     }
     __syncthreads();
@@ -603,7 +631,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         load_keys<D>(a, next, more, kt);
         entries = fetch_entries(a, pages, key0 + 2 * TILE);
         if (key0 + 32 > clear || !here.there[0] || !here.there[1])
-          mask<NR>(a, sm, kt, r0, z, key0, x.len, limit, here);
+          mask<NR>(a, sm, kt, r0, z, key0, x, here);
+        if (tile == t0) raise<NR>(z, acc, c);
         h8_t ph[RT], pl[F32 ? RT : 1];
         float sum[RT];
         weigh<NR, F32>(z, acc, c, ph, pl, sum);
@@ -647,23 +676,27 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         sm.l[wave][16 * r + je] = l;
       }
     }
-#pragma unroll
+    constexpr int THREADS = 64 * KW, PER = 16 * D / THREADS;  // of a row tile, values of a thread
+    constexpr int VEC = PER < 4 ? PER : 4, LANES = D / PER;   // values side by side, threads of a row
+    typedef float vec_t __attribute__((ext_vector_type(VEC)));
+    const int rg = te / THREADS, row16 = te % THREADS / LANES, d0 = VEC * (te % LANES);
+    const int first = rg * used / RG, tiles_here = (rg + 1) * used / RG - first;
+#pragma nounroll
     for (int r = 0; r < RT; ++r) {
       lds_barrier();
-      if (r < mine) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int y = 0; y < RT; ++y) {
+        if (y != r || r >= mine) continue;
 #pragma unroll
-        for (int n = 0; n < NT; n += 4)
-          *reinterpret_cast<f4_t*>(&sm.o[wave][je][NT * (4 * qe + e) + n]) =
-              f4_t{acc.o[r][n][e], acc.o[r][n + 1][e], acc.o[r][n + 2][e], acc.o[r][n + 3][e]};
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int n = 0; n < NT; n += 4)
+            *reinterpret_cast<f4_t*>(&sm.o[wave][je][NT * (4 * qe + e) + n]) =
+                f4_t{acc.o[y][n][e], acc.o[y][n + 1][e], acc.o[y][n + 2][e], acc.o[y][n + 3][e]};
       }
       lds_barrier();
-      constexpr int THREADS = 64 * KW, PER = 16 * D / THREADS;  // of a row tile, values of a thread
-      constexpr int VEC = PER < 4 ? PER : 4, LANES = D / PER;   // values side by side, threads of a row
-      typedef float vec_t __attribute__((ext_vector_type(VEC)));
-      const int rg = te / THREADS, row16 = te % THREADS / LANES, d0 = VEC * (te % LANES);
-      const int first = rg * used / RG, row = 16 * (first + r) + row16, grow = x.row0 + row;
+      const int row = 16 * (first + r) + row16, grow = x.row0 + row;
+      if (r >= tiles_here || grow >= rows_all) continue;
       float mw[KW], top = kStart, sum = 0.0f;
       vec_t y[PER / VEC];
 #pragma unroll
@@ -681,17 +714,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         for (int n = 0; n < PER / VEC; ++n)
           y[n] += f * *reinterpret_cast<const vec_t*>(&sm.o[rg * KW + w][row16][d0 + VEC * LANES * n]);
       }
-      if (grow >= rows_all || first + r >= (rg + 1) * used / RG) continue;
       if (!whole) {
-        float* to = plan.part + ((int64_t)slot * R + row) * D + d0;
+        const uint32_t at_row = (uint32_t)slot * R + row;
+        float* to = plan.part + (uint64_t)at_row * D + d0;
 #pragma unroll
         for (int n = 0; n < PER / VEC; ++n) *reinterpret_cast<vec_t*>(to + VEC * LANES * n) = y[n];
         if (d0 == 0)
-          *reinterpret_cast<f2_t*>(plan.part + (int64_t)2 * plan.groups * R * D + ((int64_t)slot * R + row) * 2) =
-              f2_t{top, sum};
+          *reinterpret_cast<f2_t*>(plan.part + (uint64_t)2 * plan.groups * R * D + (uint64_t)at_row * 2) = f2_t{top, sum};
         continue;
       }
-      const int node = grow / a.group;
+      const int node = node_of(plan, grow);
       const bool live = node < x.count && sum > 0.0f;
       const float f = live ? vs / sum : 0.0f;
       const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group +
@@ -703,14 +735,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         if constexpr (F32) {
           *reinterpret_cast<vec_t*>(static_cast<float*>(a.out) + to) = out;
         } else {
-          uint32_t w[VEC / 2];
-#pragma unroll
-          for (int i = 0; i < VEC; i += 2)
-            w[i / 2] = (uint32_t)f32_to_bf16_rne(out[i]) | ((uint32_t)f32_to_bf16_rne(out[i + 1]) << 16);
-          if constexpr (VEC == 4)
-            *reinterpret_cast<u2_t*>(static_cast<uint16_t*>(a.out) + to) = u2_t{w[0], w[1]};
-          else
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = w[0];
+          typedef __bf16 half_t __attribute__((ext_vector_type(VEC)));
+          *reinterpret_cast<half_t*>(static_cast<uint16_t*>(a.out) + to) = __builtin_convertvector(out, half_t);
         }
       }
       if (a.lse && d0 == 0)
@@ -727,63 +753,51 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
   }
 }
 
-// Joins the partial sums of the items that a range boundary cut: block (item
-// or boundary, four rows), a wave a row.
-template <int D, bool F32>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan, int by_item) {
+// Joins the partial sums of the items that a range boundary cut: block (item,
+// or boundary, whichever are fewer; four rows), a wave a row.
+template <int D, bool F32, bool BY_ITEM>
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan) {
   const int R = plan.rows;
-  __shared__ int64_t sums[4], found[2];
+  __shared__ int sums[4], found[2];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  int h, it;
-  int64_t before;  // tiles of the head's list before the item
+  int h, it = 0, before = 0;  // before: tiles of the head's list before the item
   Scan s;
-  if (plan.items == 1) {
-    s.total = item_tiles(a, plan, 0);
-  } else {
-    s = scan_items<4>(a, plan, sums);
-  }
-  s.total = uniform64(s.total);
-  const int64_t all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
-  if (by_item) {
+  if (plan.items == 1) s.total = item_tiles(a, plan, 0);
+  else s = scan_items<4>(a, plan, sums);
+  const int all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
+  int boundary = 0;
+  if constexpr (BY_ITEM) {
     h = blockIdx.x / plan.items;
     it = blockIdx.x - h * plan.items;
-    before = 0;
     if (plan.items > 1) {
       if (it / s.per == t) {
-        int64_t y = s.before;
+        int y = s.before;
         for (int i = t * s.per; i < it; ++i) y += item_tiles(a, plan, i);
         found[1] = y;
       }
       __syncthreads();
-      before = uniform64(found[1]);
+      before = __builtin_amdgcn_readfirstlane(found[1]);
     }
   } else {
-    const int64_t g = (int64_t)blockIdx.x + 1;
-    if (g >= n) return;
-    const int64_t begin = divide(g * all, n);
-    h = (int)divide(begin, s.total);
-    it = 0;
-    before = 0;
+    boundary = blockIdx.x + 1;
+    if (boundary >= n) return;
+    const int begin = range_begin(boundary, all, n);
+    h = divide((uint32_t)begin, s.total);
     if (plan.items > 1) {
       find_item(a, plan, s, begin - h * s.total, found);
-      it = __builtin_amdgcn_readfirstlane((int)found[0]);
-      before = uniform64(found[1]);
+      it = __builtin_amdgcn_readfirstlane(found[0]);
+      before = __builtin_amdgcn_readfirstlane(found[1]);
     }
-    const int64_t first = h * s.total + before;
-    // only the boundary behind the item's first range joins it
-    if (first == begin || divide((first + 1) * n - 1, all) != g - 1) return;
   }
   const Item x = item_of(a, plan, it);
-  const int end = item_end(a, plan, x);
-  const int tiles = tiles_of(plan, end);
-  const int64_t first = h * s.total + before;
-  // the range that holds tile y begins at or before it: g * all / n <= y  <=>  g * all < (y + 1) n
-  const int g0 = (int)divide((first + 1) * n - 1, all), g1 = (int)divide((first + tiles) * n - 1, all);
-  if (g0 == g1) return;
+  const int tiles = tiles_of(plan, item_end(a, plan, x)), first = h * s.total + before;
+  const int g0 = range_of(first, all, n), g1 = range_of(first + tiles - 1, all, n);
+  // the boundary behind the item's first range joins it, if that range does not hold the item
+  if (g0 == g1 || (!BY_ITEM && g0 != boundary - 1)) return;
 
   const int row = blockIdx.y * 4 + wave, grow = x.row0 + row, rows_all = a.nodes * a.group;
   if (grow >= rows_all) return;
-  const float* ml = plan.part + (int64_t)2 * plan.groups * R * D;
+  const float* ml = plan.part + (uint64_t)2 * plan.groups * R * D;
   constexpr int N = D / 64, FLY = 32 / N;  // values of a lane, loads in flight
   typedef float vec_t __attribute__((ext_vector_type(N < 2 ? 2 : N)));
   float top = kStart, sum = 0.0f, acc[N];
@@ -794,7 +808,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     float m = kStart, l = 0.0f;
     if (base + lane <= g1) {
       const int g = base + lane;
-      const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((int64_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
+      const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
       m = y.x;
       l = y.y;
     }
@@ -805,7 +819,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
 #pragma unroll
       for (int u = 0; u < FLY; ++u) {
         const int g = base + (k + u < many ? k + u : k);
-        const float* from = plan.part + ((int64_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane;
+        const float* from = plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane;
         if constexpr (N == 1) {
           y[u][0] = *from;
         } else {
@@ -834,7 +848,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     }
   }
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  const int node = grow / a.group;
+  const int node = node_of(plan, grow);
   const bool live = node < x.count && sum > 0.0f;
   const float scale = live ? *a.v_scale / sum : 0.0f;
   const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
@@ -884,10 +898,12 @@ Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
   p.items = a.c.seqs * p.row_items;
   p.rows = 16 * *rt * *rg;
   p.tile = 32 * kWaves / *rg;
-  p.cap = (int64_t)a.c.width << a.c.page_shift;
-  const int64_t tiles = (p.cap + p.tile - 1) / p.tile, most = (int64_t)p.items * a.c.heads * tiles;
+  p.cap = a.c.width << a.c.page_shift;
+  p.magic = a.group == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
+  const int64_t tiles = ((int64_t)p.cap + p.tile - 1) / p.tile, most = (int64_t)p.items * a.c.heads * tiles;
   const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt, !a.bf16);
-  p.groups = tiles == 1 ? 0 : (int)(groups < most ? groups : most);
+  // nothing to cut, or more tiles than the ranges' 32 bits count
+  p.groups = tiles == 1 || most >= ((int64_t)1 << 31) ? 0 : (int)(groups < most ? groups : most);
   *bytes = (int64_t)2 * p.groups * p.rows * (a.c.dim + 2) * 4;
   p.part = nullptr;
   return p;
@@ -899,9 +915,10 @@ hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t strea
   kv_attention_kernel<D, RT, RG, F32><<<(unsigned)(p.groups ? p.groups : items), 64 * kWaves, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups < 2) return e;
-  const int by_item = items < p.groups ? 1 : 0;
-  kv_attention_join_kernel<D, F32><<<dim3((unsigned)(by_item ? items : p.groups - 1), p.rows / 4), 256, 0, stream>>>(
-      a, p, by_item);
+  if (items < p.groups)
+    kv_attention_join_kernel<D, F32, true><<<dim3((unsigned)items, p.rows / 4), 256, 0, stream>>>(a, p);
+  else
+    kv_attention_join_kernel<D, F32, false><<<dim3(p.groups - 1, p.rows / 4), 256, 0, stream>>>(a, p);
   return hipGetLastError();
 }
 

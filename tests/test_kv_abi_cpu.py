@@ -45,7 +45,7 @@ def test_append_refuses_shapes(lib, bad):
     assert lib.nvfp4_kv_append(*changed(APPEND, **bad)) == B.NVFP4_ERR_SHAPE
 
 
-@pytest.mark.parametrize("bad", SHAPES + [dict(B=-1), dict(M=65), dict(Hq=6), dict(Hq=0), dict(qs=504), dict(qs=516),
+@pytest.mark.parametrize("bad", SHAPES + [dict(B=-1), dict(M=65), dict(Hq=6), dict(Hq=0), dict(Hq=4 * 257, qs=4 * 257 * 64), dict(qs=504), dict(qs=516),
                                           dict(sm=float("inf")), dict(sm=float("nan")), dict(wsb=-1),
                                           dict(parent=None, B=4096, M=8192)])
 def test_attention_refuses_shapes(lib, bad):
