@@ -54,6 +54,7 @@ struct Plan {
   int row_items;   // items of a sequence
   int rows;        // rows of an item
   int tile;        // tokens of a key tile
+  int start;       // what an item's set-up and join cost, in tiles
   int groups;      // workgroups that share the list; 0: one per item, nothing is cut
   int cap;         // tokens a table row covers
   uint32_t magic;  // ceil(2^32 / group), 0 for a group of one
@@ -99,11 +100,12 @@ __device__ __forceinline__ int tiles_of(const Plan& p, int end) {
   return end > p.tile ? (int)((uint32_t)(end + p.tile - 1) >> (31 - __clz(p.tile))) : 1;
 }
 
-__device__ __forceinline__ int item_tiles(const KvAttentionArgs& a, const Plan& p, int it) {
-  return tiles_of(p, item_end(a, p, item_of(a, p, it)));
+// An item's length in the list: its tiles behind `start` places for its set-up.
+__device__ __forceinline__ int item_places(const KvAttentionArgs& a, const Plan& p, int it) {
+  return p.start + tiles_of(p, item_end(a, p, item_of(a, p, it)));
 }
 
-// Sum of the items' tiles and this thread's exclusive part of it; every thread
+// Sum of the items' places and this thread's exclusive part of it; every thread
 // of the workgroup calls it.  Thread t has the items [t * per, (t + 1) * per).
 struct Scan {
   int per, before, total;
@@ -117,7 +119,7 @@ __device__ __forceinline__ Scan scan_items(const KvAttentionArgs& a, const Plan&
   int mine = 0;
   for (int i = 0; i < s.per; ++i) {
     const int it = t * s.per + i;
-    if (it < p.items) mine += item_tiles(a, p, it);
+    if (it < p.items) mine += item_places(a, p, it);
   }
   int v = mine;
   for (int off = 1; off < 64; off <<= 1) {
@@ -143,25 +145,25 @@ __device__ __forceinline__ int divide(uint64_t x, uint32_t y) {
   return __builtin_amdgcn_readfirstlane((int)(x < (uint64_t)q * y ? q - 1 : q));
 }
 
-// The list of all heads' items, tile by tile: range g of n begins at tile
+// The list of all heads' items, place by place: range g of n begins at place
 // floor(g * all / n), so that ranges and equal items stay aligned.
 __device__ __forceinline__ int range_begin(int g, int all, int n) { return divide((uint64_t)g * (uint32_t)all, n); }
 
-// The range that holds tile y: the last that begins at or before it, g * all <
+// The range that holds place y: the last that begins at or before it, g * all <
 // (y + 1) * n.
 __device__ __forceinline__ int range_of(int y, int all, int n) {
   return divide((uint64_t)(uint32_t)(y + 1) * (uint32_t)n - 1, all);
 }
 
-// The item with tile `at` of one head's list: found[0] the item, found[1] the
-// tiles of the list before it.
+// The item with place `at` of one head's list: found[0] the item, found[1] the
+// places of the list before it.
 __device__ __forceinline__ void find_item(const KvAttentionArgs& a, const Plan& p, const Scan& s, int at, int* found) {
   const int t = threadIdx.x;
   int x = s.before;
   for (int i = 0; i < s.per && x <= at; ++i) {
     const int it = t * s.per + i;
     if (it >= p.items) break;
-    const int n = item_tiles(a, p, it);
+    const int n = item_places(a, p, it);
     if (at < x + n) {
       found[0] = it;
       found[1] = x;
@@ -326,7 +328,6 @@ struct Smem {
   };
   float m[kWaves][16 * RT], l[kWaves][16 * RT];
   uint64_t line[16 * RG * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
-  uint64_t tree[64];            // ancestors of the nodes
   int sums[kWaves], found[2];
 };
 
@@ -500,16 +501,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
   const float vs = *a.v_scale;
 
   // This workgroup's range of the list.
-  int h, it, at, left;  // head, item, first tile within it, tiles to do
+  int h, it, at, left;  // head, item, first place within it, places to do
   int group = 0;
   if (plan.groups == 0) {
     h = blockIdx.x / plan.items;
     it = blockIdx.x - h * plan.items;
     at = 0;
-    left = item_tiles(a, plan, it);
+    left = item_places(a, plan, it);
   } else {
     Scan s;
-    if (plan.items == 1) s.total = item_tiles(a, plan, 0);
+    if (plan.items == 1) s.total = item_places(a, plan, 0);
     else s = scan_items<kWaves>(a, plan, sm.sums);
     const int all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
     group = blockIdx.x;
@@ -526,12 +527,17 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     }
   }
 
+  bool first_item = true;
   while (left > 0) {
     const Item x = item_of(a, plan, it);
     const int end = item_end(a, plan, x);
     const int tiles = tiles_of(plan, end);
-    const int t0 = at, t1 = at + left < tiles ? at + left : tiles;
-    const int clear = x.len < end ? x.len : end;          // tokens before it are seen by every row
+    const int past = at + left - plan.start;
+    const int t0 = at > plan.start ? at - plan.start : 0, t1 = past < tiles ? past : tiles;
+    if (t1 <= t0) break;  // the range ends in the item's set-up
+    // Tokens before it are seen by every row: the committed ones, and in a chain the first row's.
+    int clear = x.len + (a.parent ? 0 : node_of(plan, x.row0) + 1);
+    clear = clear < end ? clear : end;
 
     // The item's row tiles in use are shared out evenly over the row groups.
     int used = (rows_all - x.row0 + 15) / 16;
@@ -566,8 +572,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 
     int par = -1;
     if (a.parent && wave == 0 && lane < a.nodes) par = a.parent[(int64_t)x.b * a.nodes + lane];
-    __syncthreads();  // the last item's sums have been read
-    if (a.parent && wave == 0) sm.tree[lane] = ancestors_of_wave(par);
+    if (!first_item) __syncthreads();  // the last item's sums have been read
+    first_item = false;
+    if (wave == 0) {
+      const uint64_t tree = a.parent ? ancestors_of_wave(par) : 0;
+#pragma unroll
+      for (int i = 0; i < (R + 63) / 64; ++i) {
+        int row = x.row0 + 64 * i + lane;
+        row = row < rows_all ? row : rows_all - 1;
+        const int node = node_of(plan, row);
+        const uint64_t bits = __shfl(tree, node & 63);
+        if (64 * i + lane < R) sm.line[64 * i + lane] = a.parent ? bits : (uint64_t)node;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < PER_WAVE; ++i) {
       const int f = i * kWaves + wave;
@@ -593,13 +610,6 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         if (flip) w ^= 0x80008000u;
         sm.q[0][r][s][lane] = __builtin_bit_cast(bf8_t, w);
       }
-    }
-    __syncthreads();
-    if (t < R) {
-      int row = x.row0 + t;
-      row = row < rows_all ? row : rows_all - 1;
-      const int node = node_of(plan, row);
-      sm.line[t] = a.parent ? sm.tree[node] : (uint64_t)node;
     }
     __syncthreads();
 
@@ -744,7 +754,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     }
 
     // The next item of the list.
-    left -= t1 - t0;
+    left -= plan.start + tiles - at;
     at = 0;
     if (++it == plan.items) {
       it = 0;
@@ -760,9 +770,9 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   const int R = plan.rows;
   __shared__ int sums[4], found[2];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  int h, it = 0, before = 0;  // before: tiles of the head's list before the item
+  int h, it = 0, before = 0;  // before: places of the head's list before the item
   Scan s;
-  if (plan.items == 1) s.total = item_tiles(a, plan, 0);
+  if (plan.items == 1) s.total = item_places(a, plan, 0);
   else s = scan_items<4>(a, plan, sums);
   const int all = s.total * a.c.heads, n = plan.groups < all ? plan.groups : all;
   int boundary = 0;
@@ -772,7 +782,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     if (plan.items > 1) {
       if (it / s.per == t) {
         int y = s.before;
-        for (int i = t * s.per; i < it; ++i) y += item_tiles(a, plan, i);
+        for (int i = t * s.per; i < it; ++i) y += item_places(a, plan, i);
         found[1] = y;
       }
       __syncthreads();
@@ -790,7 +800,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     }
   }
   const Item x = item_of(a, plan, it);
-  const int tiles = tiles_of(plan, item_end(a, plan, x)), first = h * s.total + before;
+  const int tiles = tiles_of(plan, item_end(a, plan, x)), first = h * s.total + before + plan.start;
   const int g0 = range_of(first, all, n), g1 = range_of(first + tiles - 1, all, n);
   // the boundary behind the item's first range joins it, if that range does not hold the item
   if (g0 == g1 || (!BY_ITEM && g0 != boundary - 1)) return;
@@ -798,11 +808,10 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   const int row = blockIdx.y * 4 + wave, grow = x.row0 + row, rows_all = a.nodes * a.group;
   if (grow >= rows_all) return;
   const float* ml = plan.part + (uint64_t)2 * plan.groups * R * D;
-  constexpr int N = D / 64, FLY = 32 / N;  // values of a lane, loads in flight
-  typedef float vec_t __attribute__((ext_vector_type(N < 2 ? 2 : N)));
-  float top = kStart, sum = 0.0f, acc[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  constexpr int N = D / 64;  // values of a lane
+  typedef float vec_t __attribute__((ext_vector_type(N)));
+  float top = kStart, sum = 0.0f;
+  vec_t acc = (vec_t)0.0f;
   for (int base = g0; base <= g1; base += 64) {
     // the statistics of up to 64 partial sums, a lane each
     float m = kStart, l = 0.0f;
@@ -814,38 +823,36 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     }
     const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
     float f = 0.0f;
-    for (int k = 0; k < many; k += FLY) {
-      float y[FLY][N];
+    // `fly` sums at a time; their weights are worked out while the first ones arrive
+    auto add = [&](auto fly, int k) {
+      constexpr int FLY = decltype(fly)::value;
+      vec_t y[FLY];
 #pragma unroll
       for (int u = 0; u < FLY; ++u) {
         const int g = base + (k + u < many ? k + u : k);
-        const float* from = plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane;
-        if constexpr (N == 1) {
-          y[u][0] = *from;
-        } else {
-          const vec_t v = *reinterpret_cast<const vec_t*>(from);
-#pragma unroll
-          for (int i = 0; i < N; ++i) y[u][i] = v[i];
-        }
+        y[u] = *reinterpret_cast<const vec_t*>(
+            plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane);
       }
-      if (k == 0) {  // their weights, while the first sums arrive
+      if (k == 0) {
         float high = m;
         for (int off = 32; off > 0; off >>= 1) high = __builtin_fmaxf(high, __shfl_xor(high, off));
         high = __builtin_fmaxf(high, top);
         const float old = __builtin_amdgcn_exp2f(top - high);
         f = __builtin_amdgcn_exp2f(m - high);
         sum = sum * old + f * l;
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] *= old;
+        acc *= old;
         top = high;
       }
 #pragma unroll
       for (int u = 0; u < FLY; ++u) {
-        const float w = k + u < many ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), k + u < many ? k + u : 0)) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += w * y[u][i];
+        const int from = k + u < many ? k + u : 0;
+        const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), from));
+        acc += (k + u < many ? w : 0.0f) * y[u];
       }
-    }
+    };
+    int k = 0;
+    for (; k + 16 <= many; k += 16) add(std::integral_constant<int, 16>{}, k);
+    for (; k < many; k += 4) add(std::integral_constant<int, 4>{}, k);
   }
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   const int node = node_of(plan, grow);
@@ -890,6 +897,9 @@ void row_split(const KvAttentionArgs& a, int* rt, int* rg, int* row_items) {
   *rt = (all + *row_items * *rg - 1) / (*row_items * *rg);
 }
 
+// Sequences of up to kWhole tiles are not split: the join costs more.
+constexpr int kWhole = 4, kStartCost = 2;
+
 int groups_per_cu(int dim, int rt, bool f32) { return waves_per_simd(dim, rt, f32) * 4 / kWaves; }
 
 Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
@@ -900,10 +910,12 @@ Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
   p.tile = 32 * kWaves / *rg;
   p.cap = a.c.width << a.c.page_shift;
   p.magic = a.group == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
-  const int64_t tiles = ((int64_t)p.cap + p.tile - 1) / p.tile, most = (int64_t)p.items * a.c.heads * tiles;
+  p.start = kStartCost;
+  const int64_t tiles = ((int64_t)p.cap + p.tile - 1) / p.tile;
+  const int64_t most = (int64_t)p.items * a.c.heads * (tiles + p.start);
   const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt, !a.bf16);
-  // nothing to cut, or more tiles than the ranges' 32 bits count
-  p.groups = tiles == 1 || most >= ((int64_t)1 << 31) ? 0 : (int)(groups < most ? groups : most);
+  // too short to cut, or more places than 32 bits count
+  p.groups = tiles <= kWhole || most >= ((int64_t)1 << 31) ? 0 : (int)(groups < most ? groups : most);
   *bytes = (int64_t)2 * p.groups * p.rows * (a.c.dim + 2) * 4;
   p.part = nullptr;
   return p;
