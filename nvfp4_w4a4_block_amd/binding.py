@@ -510,23 +510,24 @@ def _call(dev: torch.device, where: str, fn, *args) -> None:
         raise NVFP4Error(status, where)
 
 
-def _ints(dev: torch.device, **ts: torch.Tensor) -> None:
-    for name, t in ts.items():
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+def _ints(dev: torch.device, names: str, *ts: torch.Tensor) -> None:
+    for t in ts:
+        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{names} must be contiguous int32 tensors on {dev}")
 
 
-def _kv_scale(dev: torch.device, **ts: torch.Tensor) -> None:
-    for name, t in ts.items():
-        if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
-            raise ValueError(f"{name} must be a float32 tensor of one element on {dev}")
+def _kv_scale(dev: torch.device, *ts: torch.Tensor) -> None:
+    for t in ts:
+        if t.dtype is not torch.float32 or t.numel() != 1 or t.device != dev:
+            raise ValueError(f"k_scale and v_scale must be float32 tensors of one element on {dev}")
 
 
-def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[torch.device, int, int]:
+def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[torch.device, torch.Size, int, int]:
     """Checks a pair of page tensors of `dim` dimensions (same shape and strides, whole pages);
-    returns their device and the bytes from a layer to the next and from a page to the next."""
+    returns their device and shape and the bytes from a layer to the next and from a page to the next."""
     dev = k_pages.device
-    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8 or dev.type != "cuda" or v_pages.device != dev:
+    if k_pages.dtype is not torch.uint8 or v_pages.dtype is not torch.uint8 or dev.type != "cuda" or \
+            v_pages.device != dev:
         raise ValueError("pages must be uint8 tensors on one GPU")
     st, shape = k_pages.stride(), k_pages.shape
     if len(shape) != dim or shape != v_pages.shape or st != v_pages.stride():
@@ -535,16 +536,16 @@ def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[t
     P, H, page, D = shape[-4:]
     if (st[-1] != 1 and D > 1) or (st[-2] != D and page > 1) or (st[-3] != page * D and H > 1):
         raise ValueError("a page must be contiguous [H, page_size, D]")
-    return dev, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
+    return dev, shape, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
 
 
-def _kv_rows(x: torch.Tensor, dev: torch.device, name: str) -> int:
-    """x [B, M, heads, D] whose rows are contiguous; returns the values from a row to the next."""
-    B, M, H, D = x.shape
-    sb, sm, sh, sd = x.stride()
+def _kv_rows(x: torch.Tensor, shape: torch.Size, dev: torch.device, name: str) -> int:
+    """x of shape [B, M, heads, D] whose rows are contiguous; returns the values from a row to the next."""
     if x.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if x.numel() == 0:
+    B, M, H, D = shape
+    sb, sm, sh, sd = x.stride()
+    if B == 0 or M == 0:
         return H * D
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the rows of {name} must be contiguous [heads, D]")
@@ -559,21 +560,21 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_s
                     counts: Optional[torch.Tensor] = None) -> None:
     """Writes k and v [B, M, H, D] (float32/bfloat16; rows may be column ranges of a wider tensor) as
     E4M3 bytes at tokens lens[b] .. lens[b] + M - 1 (counts[b] of them) of the sequences' pages."""
-    dev, _, page_stride = _kv_pages(k_pages, v_pages, 4)
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    dev, (P, Hp, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    shape, entries = k.shape, table.shape
+    if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must be [B, M, H, D] of one dtype")
-    B, M, H, D = k.shape
-    P, Hp, page, Dp = k_pages.shape
-    if (H, D) != (Hp, Dp) or table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+    B, M, H, D = shape
+    if H != Hp or D != Dp or len(entries) != 2 or entries[0] != B or lens.shape != (B,):
         raise ValueError("k, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
-    _ints(dev, table=table, lens=lens)
+    _ints(dev, "table and lens", table, lens)
     if counts is not None:
-        _ints(dev, counts=counts)
+        _ints(dev, "counts", counts)
         if counts.shape != (B,):
             raise ValueError("counts must be [B]")
-    _kv_scale(dev, k_scale=k_scale, v_scale=v_scale)
-    _call(dev, "nvfp4_kv_append", load().nvfp4_kv_append, B, M, H, D, page, P, table.shape[1], k.data_ptr(),
-          v.data_ptr(), _dt(k.dtype), _kv_rows(k, dev, "k"), _kv_rows(v, dev, "v"), k_scale.data_ptr(),
+    _kv_scale(dev, k_scale, v_scale)
+    _call(dev, "nvfp4_kv_append", load().nvfp4_kv_append, B, M, H, D, page, P, entries[1], k.data_ptr(),
+          v.data_ptr(), _dt(k.dtype), _kv_rows(k, shape, dev, "k"), _kv_rows(v, shape, dev, "v"), k_scale.data_ptr(),
           v_scale.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_stride, table.data_ptr(),
           lens.data_ptr(), counts.data_ptr() if counts is not None else None)
 
@@ -587,28 +588,28 @@ def nvfp4_kv_attention(q: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Te
     the nodes' own keys and values already stand behind lens[b].  parent int32 [B, M]: drafted trees (M <=
     64); None: a chain.  sm_scale defaults to 1/sqrt(D).  Returns out [B, M, Hq, D] of q's dtype, or
     (out, lse float32 [B, M, Hq]) with want_lse.  workspace: uint8 scratch; None allocates it."""
-    dev, _, page_stride = _kv_pages(k_pages, v_pages, 4)
-    if q.dim() != 4:
+    dev, (P, H, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    shape, entries = q.shape, table.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, M, Hq, D]")
-    B, M, Hq, D = q.shape
-    P, H, page, Dp = k_pages.shape
-    if D != Dp or H < 1 or Hq % H or table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+    B, M, Hq, D = shape
+    if D != Dp or H < 1 or Hq % H or len(entries) != 2 or entries[0] != B or lens.shape != (B,):
         raise ValueError("q, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
-    _ints(dev, table=table, lens=lens)
+    _ints(dev, "table and lens", table, lens)
     if parent is not None:
-        _ints(dev, parent=parent)
+        _ints(dev, "parent", parent)
         if parent.shape != (B, M):
             raise ValueError("parent must be [B, M]")
     if counts is not None:
-        _ints(dev, counts=counts)
+        _ints(dev, "counts", counts)
         if counts.shape != (B,):
             raise ValueError("counts must be [B]")
-    _kv_scale(dev, k_scale=k_scale, v_scale=v_scale)
-    stride = _kv_rows(q, dev, "q")
-    dt, W = _dt(q.dtype), table.shape[1]
+    _kv_scale(dev, k_scale, v_scale)
+    stride = _kv_rows(q, shape, dev, "q")
+    dt, W = _dt(q.dtype), entries[1]
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+    elif out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous [B, M, Hq, D] of q's dtype on its GPU")
     lse = torch.empty((B, M, Hq), dtype=torch.float32, device=dev) if want_lse else None
     lib = load()
@@ -636,20 +637,19 @@ def nvfp4_kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.
     """Moves the accepted path of each sequence's tree to the front in all layers of pages [L, P, H,
     page_size, D]; result int32 [B, 3 + M]: rows of nvfp4_tree_accept / nvfp4_tree_verify.  Returns
     new_lens int32 [B] = lens + 1 + accepted (a tensor of its own: lens is not changed)."""
-    dev, layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
-    L, P, H, page, D = k_pages.shape
-    if table.dim() != 2 or result.dim() != 2 or lens.shape != (table.shape[0],) or \
-            result.shape[0] != table.shape[0]:
+    dev, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    entries, paths = table.shape, result.shape
+    if len(entries) != 2 or len(paths) != 2 or lens.shape != entries[:1] or paths[0] != entries[0]:
         raise ValueError("table [B, W], lens [B] and result [B, 3 + M] do not fit together")
-    B, W = table.shape
-    _ints(dev, table=table, lens=lens, result=result)
+    B, W = entries
+    _ints(dev, "table, lens and result", table, lens, result)
     if new_lens is None:
         new_lens = torch.empty_like(lens)
     else:
-        _ints(dev, new_lens=new_lens)
+        _ints(dev, "new_lens", new_lens)
         if new_lens.shape != lens.shape:
             raise ValueError("new_lens must be [B]")
-    _call(dev, "nvfp4_kv_compact", load().nvfp4_kv_compact, L, B, result.shape[1] - 3, H, D, page, P, W,
+    _call(dev, "nvfp4_kv_compact", load().nvfp4_kv_compact, L, B, paths[1] - 3, H, D, page, P, W,
           k_pages.data_ptr(), v_pages.data_ptr(), layer_stride, page_stride, table.data_ptr(),
           lens.data_ptr(), result.data_ptr(), new_lens.data_ptr())
     return new_lens
@@ -668,7 +668,7 @@ def _pool(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list
     dev = table.device
     if dev.type != "cuda":
         raise ValueError("the page pool must be on a GPU")
-    _ints(dev, table=table, held=held, refs=refs, free_list=free_list)
+    _ints(dev, "table, held, refs and free_list", table, held, refs, free_list)
     if table.dim() != 2 or held.shape != (table.shape[0],) or refs.dim() != 1 or \
             free_list.shape != (refs.shape[0] + 1,):
         raise ValueError("table [S, W], held [S], refs [P] and free_list [1 + P] do not fit together")
@@ -681,13 +681,13 @@ def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor,
     """Lets each sequence of seqs int32 [n] hold the pages of tokens int32 [n] tokens (0 frees it).
     Returns shortage int32 [1]: 0, or how many pages were missing (then nothing is changed)."""
     dev = _pool(table, held, refs, free_list)
-    _ints(dev, seqs=seqs, tokens=tokens)
+    _ints(dev, "seqs and tokens", seqs, tokens)
     if seqs.dim() != 1 or tokens.shape != seqs.shape:
         raise ValueError("seqs and tokens must be [n]")
     if shortage is None:
         shortage = torch.empty((1,), dtype=torch.int32, device=dev)
     else:
-        _ints(dev, shortage=shortage)
+        _ints(dev, "shortage", shortage)
         if shortage.numel() != 1:
             raise ValueError("shortage must have one element")
     S, W = table.shape
@@ -704,20 +704,19 @@ def nvfp4_kv_fork(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, f
     shared, a partial one is copied in all layers of pages [L, P, H, page_size, D], what dst held is
     given up.  Returns shortage as nvfp4_kv_resize."""
     dev = _pool(table, held, refs, free_list)
-    on, layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
-    if on != dev or k_pages.shape[1] != refs.shape[0]:
+    on, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    if on != dev or P != refs.shape[0]:
         raise ValueError("pages must be [L, P, H, page_size, D] of the pool's P pages, on its GPU")
-    _ints(dev, src=src, dst=dst, tokens=tokens)
+    _ints(dev, "src, dst and tokens", src, dst, tokens)
     if src.dim() != 1 or dst.shape != src.shape or tokens.shape != src.shape:
         raise ValueError("src, dst and tokens must be [n]")
     if shortage is None:
         shortage = torch.empty((1,), dtype=torch.int32, device=dev)
     else:
-        _ints(dev, shortage=shortage)
+        _ints(dev, "shortage", shortage)
         if shortage.numel() != 1:
             raise ValueError("shortage must have one element")
     S, W = table.shape
-    L, P, H, page, D = k_pages.shape
     n = src.shape[0]
     moves = torch.empty((3 * n,), dtype=torch.int32, device=dev)
     _call(dev, "nvfp4_kv_fork", load().nvfp4_kv_fork, n, S, W, P, page, table.data_ptr(), held.data_ptr(),

@@ -10,20 +10,25 @@
 // round trip and can be captured in a graph.
 //
 // One workgroup does the bookkeeping: every phase is a loop over the flattened
-// (entry, page) list with the running offsets of the entries in LDS, and the
-// phases are separated by barriers.  Nothing depends on the order in which the
-// atomics land: the counts are sums, and a page that falls to zero goes back
-// on the list at the rank of its first occurrence, which the occurrences agree
-// on by an atomic minimum in the page's own count (zero at that point) that is
-// reset afterwards.  Bound by the latency of its dependent accesses.
+// (entry, page) list with the running offsets of the entries in LDS, four places
+// a thread (their loads overlap), and the phases are separated by barriers.
+// What bounds it is the one compute unit's rate of accesses to the counts, which
+// lie at random; a given-up page costs one of them, the atomic that takes its
+// holder off.  The one that takes the last holder off pushes the page, so the
+// place of a page in the list must not depend on the order in which the atomics
+// land: only where a call itself gives up a page more than once could it, and
+// there the occurrences settle on the first by an atomic minimum in the page's
+// own count, which is zero by then and is reset afterwards.
 #include "device_common.h"
 #include "launch.h"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kClaim = 1 << 30;  // claims lie below any count: occurrence - kClaim
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kEach = 4;                  // places of a thread: 64 apart, 256 a wave
+constexpr int kStep = kThreads * kEach;
+constexpr int kClaim = 1 << 30;           // claims lie below any count: place - kClaim
 
 __device__ __forceinline__ int load_agent(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -32,28 +37,40 @@ __device__ __forceinline__ void store_agent(int32_t* p, int v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Inclusive sum over the workgroup; `sums` has one word per wave.
-__device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
+// Exclusive sums over the workgroup of N values a thread, and their totals.
+template <int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*sums)[N]) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int mine[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine[i] = v[i];
   for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off);
-    v += lane >= off ? o : 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int o = __shfl_up(v[i], off);
+      v[i] += lane >= off ? o : 0;
+    }
   }
-  if (lane == 63) sums[wave] = v;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 63) sums[wave][i] = v[i];
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kThreads / 64; ++w) {
-    const int s = sums[w];
-    before += w < wave ? s : 0;
-    all += s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int s = sums[w][i];
+      before += w < wave ? s : 0;
+      all += s;
+    }
+    total[i] = all;
+    v[i] += before - mine[i];
   }
-  __syncthreads();
-  *total = all;
-  return v + before;
 }
 
-// Entry of flattened index x: the last e with start[e] <= x among those that
-// have a page (start is the exclusive running sum of n entries).
+// Entry of flattened place x: the last e with start[e] <= x, which has a page
+// (start is the exclusive running sum of n entries, x is below the total).
 __device__ __forceinline__ int entry_of(const int* start, int n, int x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -69,48 +86,47 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
   __shared__ int src[kThreads], dst[kThreads];           // sequences (dst: the one that changes)
   __shared__ int first[kThreads];                        // resize: first page to take or give back
   __shared__ int take_at[kThreads], drop_at[kThreads], share_at[kThreads];  // running offsets
-  __shared__ int sums[kThreads / 64];
-  const int t = threadIdx.x, n = a.n, W = a.width, P = a.pages;
+  __shared__ int sums[kWaves][3], counts[2][kWaves], flags[2];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = a.n, W = a.width, P = a.pages;
   const int page = 1 << a.page_shift;
 
   // The entries, and which of them count.
   const bool in = t < n;
   const int d = in ? a.dst[t] : -1, tok = in ? a.tokens[t] : -1, s = FORK && in ? a.src[t] : -1;
+  int F = a.free_list[0];
+  F = F < 0 ? 0 : F < P ? F : P;
   dst[t] = d;
   src[t] = s;
-  __syncthreads();
+  if (t < 2) flags[t] = 0;
   bool ok = in && d >= 0 && d < a.seqs && tok >= 0 && (!FORK || (s >= 0 && s < a.seqs));
-  for (int j = 0; j < n && ok; ++j) {
-    if (j < t && dst[j] == d) ok = false;
-    if (FORK && dst[j] == s) ok = false;
+  int have = ok ? a.held[d] : 0, of = FORK && ok ? a.held[s] : 0;
+  __syncthreads();
+  if (64 * wave < n) {
+    bool again = false;
+    for (int j = 0; j < n; j += 8) {  // places behind the last entry hold -1
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int other = dst[j + i];
+        again |= (j + i < t && other == d) || (FORK && other == s);
+      }
+    }
+    ok = ok && !again;
   }
-  int have = 0;
-  if (ok) {
-    have = a.held[d];
-    have = have < 0 ? 0 : have < W ? have : W;
-  }
+  have = !ok || have < 0 ? 0 : have < W ? have : W;
+  of = of < 0 ? 0 : of < W ? of : W;
   const int full = ok ? tok >> a.page_shift : 0;                    // whole pages
   const int part = ok ? tok & (page - 1) : 0;                       // tokens in a partial one
   const int need = full + (part > 0);
-  if (FORK) {
-    if (ok) {
-      int of = a.held[s];
-      of = of < 0 ? 0 : of < W ? of : W;
-      ok = need <= of;
-    }
-  } else {
-    ok = ok && need <= W;
-  }
+  ok = ok && need <= (FORK ? of : W);
   const int take = !ok ? 0 : FORK ? (part > 0) : need > have ? need - have : 0;
   const int drop = !ok ? 0 : FORK ? have : have > need ? have - need : 0;
-  const int share = FORK && ok ? full : 0;
-  int takes, drops, shares = 0;
-  take_at[t] = block_scan(take, sums, &takes) - take;
-  drop_at[t] = block_scan(drop, sums, &drops) - drop;
-  if (FORK) share_at[t] = block_scan(share, sums, &shares) - share;
+  int at3[3] = {take, drop, FORK && ok ? full : 0}, total3[3];
+  block_scan<3>(at3, total3, sums);
+  const int takes = total3[0], drops = total3[1], shares = total3[2];
+  take_at[t] = at3[0];
+  drop_at[t] = at3[1];
+  share_at[t] = at3[2];
   first[t] = FORK ? 0 : need < have ? need : have;
-  int F = a.free_list[0];
-  F = F < 0 ? 0 : F < P ? F : P;
   __syncthreads();
 
   if (takes > F) {  // all or nothing
@@ -120,10 +136,11 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
   }
 
   // Pages taken off the list, and shared ones.
+  const int mine = 256 * wave + lane;  // a thread's places of a step: mine + 64 i
   int fresh = -1;
   if (FORK) {
     if (take) {
-      fresh = a.free_list[F - take_at[t]];
+      fresh = a.free_list[F - at3[0]];
       if (fresh >= 0 && fresh < P) store_agent(a.refs + fresh, 1);
     }
     if (in) {
@@ -131,65 +148,156 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
       a.moves[3 * t + 1] = fresh;
       a.moves[3 * t + 2] = part;
     }
-    for (int x = t; x < shares; x += kThreads) {
-      const int e = entry_of(share_at, n, x);
-      const int p = a.table[(int64_t)src[e] * W + (x - share_at[e])];
-      if (p >= 0 && p < P) atomicAdd(a.refs + p, 1);
+    for (int x = mine; x < shares; x += kStep) {
+      int p[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        p[i] = -1;
+        if (y < shares) {
+          const int e = entry_of(share_at, n, y);
+          p[i] = a.table[(int64_t)src[e] * W + (y - share_at[e])];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (p[i] >= 0 && p[i] < P) atomicAdd(a.refs + p[i], 1);
     }
   } else {
-    for (int x = t; x < takes; x += kThreads) {
-      const int e = entry_of(take_at, n, x);
-      const int p = a.free_list[F - x];
-      a.table[(int64_t)dst[e] * W + first[e] + (x - take_at[e])] = p;
-      if (p >= 0 && p < P) store_agent(a.refs + p, 1);
+    for (int x = mine; x < takes; x += kStep) {
+      int p[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) p[i] = x + 64 * i < takes ? a.free_list[F - x - 64 * i] : -1;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        if (y >= takes) break;
+        const int e = entry_of(take_at, n, y);
+        a.table[(int64_t)dst[e] * W + first[e] + (y - take_at[e])] = p[i];
+        if (p[i] >= 0 && p[i] < P) store_agent(a.refs + p[i], 1);
+      }
     }
   }
   __syncthreads();
 
-  // Pages given up: one holder less each, then the claims of those at zero.
-  for (int x = t; x < drops; x += kThreads) {
-    const int e = entry_of(drop_at, n, x);
-    const int p = a.table[(int64_t)dst[e] * W + first[e] + (x - drop_at[e])];
-    if (p >= 0 && p < P) atomicSub(a.refs + p, 1);
-  }
-  __syncthreads();
-  for (int x = t; x < drops; x += kThreads) {
-    const int e = entry_of(drop_at, n, x);
-    const int p = a.table[(int64_t)dst[e] * W + first[e] + (x - drop_at[e])];
-    if (p >= 0 && p < P) {
-      const int r = load_agent(a.refs + p);
-      if (r == 0 || r < -(kClaim >> 1)) atomicMin(a.refs + p, x - kClaim);
+  // Pages given up: one holder less each.  An entry of the table that did not
+  // take the last holder off is kept as -2 - page meanwhile.
+  auto place = [&](int y) {
+    const int e = entry_of(drop_at, n, y);
+    return a.table + (int64_t)dst[e] * W + first[e] + (y - drop_at[e]);
+  };
+  for (int x = mine; x < drops; x += kStep) {
+    int32_t* at[kEach];
+    int p[kEach], old[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      p[i] = -1;
+      if (x + 64 * i < drops) {
+        at[i] = place(x + 64 * i);
+        p[i] = *at[i];
+        if (p[i] < 0 || p[i] >= P) {
+          p[i] = -1;
+          *at[i] = -1;
+        }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) old[i] = p[i] >= 0 ? atomicSub(a.refs + p[i], 1) : 1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (old[i] != 1) {
+        *at[i] = -2 - p[i];
+        flags[0] = 1;
+      }
   }
   __syncthreads();
+  // A page that has no holder left although this place did not take the last
+  // one off is given up twice: its places claim it.
+  if (flags[0]) {
+    for (int x = mine; x < drops; x += kStep) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        if (y >= drops) break;
+        const int p = -2 - *place(y);
+        if (p < 0) continue;
+        const int r = load_agent(a.refs + p);
+        if (r == 0 || r < -(kClaim >> 1)) {
+          flags[1] = 1;
+          atomicMin(a.refs + p, y - kClaim);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const bool twice = flags[1] != 0;
+  if (twice) {
+    for (int x = mine; x < drops; x += kStep) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        if (y >= drops) break;
+        const int p = *place(y);
+        if (p >= 0) atomicMin(a.refs + p, y - kClaim);
+      }
+    }
+    __syncthreads();
+  }
   const int top = F - takes;
   int back = 0;
-  for (int x0 = 0; x0 < drops; x0 += kThreads) {
-    const int x = x0 + t;
-    int p = -1;
-    bool mine = false;
-    if (x < drops) {
-      const int e = entry_of(drop_at, n, x);
-      int32_t* at = a.table + (int64_t)dst[e] * W + first[e] + (x - drop_at[e]);
-      p = *at;
-      mine = p >= 0 && p < P && load_agent(a.refs + p) == x - kClaim;
-      *at = -1;
+  for (int x0 = 0, turn = 0; x0 < drops; x0 += kStep, turn ^= 1) {
+    int p[kEach];
+    uint64_t own[kEach];
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int y = x0 + mine + 64 * i;
+      bool push = false;
+      p[i] = -1;
+      if (y < drops) {
+        int32_t* at = place(y);
+        const int v = *at;
+        p[i] = v < -1 ? -2 - v : v;
+        push = twice ? p[i] >= 0 && load_agent(a.refs + p[i]) == y - kClaim : v >= 0;
+        *at = -1;
+      }
+      own[i] = __ballot(push);
+      many += __popcll(own[i]);
     }
-    int all;
-    const int rank = back + block_scan(mine ? 1 : 0, sums, &all);
-    if (mine) {
-      store_agent(a.refs + p, 0);
-      if (top + rank <= P) a.free_list[top + rank] = p;
+    if (lane == 0) counts[turn][wave] = many;
+    __syncthreads();
+    int rank = back;
+    for (int w = 0; w < kWaves; ++w) {
+      const int c = counts[turn][w];
+      rank += w < wave ? c : 0;
+      back += c;
     }
-    back += all;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if ((own[i] >> lane) & 1) {
+        const int r = top + rank + 1 + __popcll(own[i] & ((1ull << lane) - 1));
+        if (r <= P) a.free_list[r] = p[i];
+        if (twice) store_agent(a.refs + p[i], 0);
+      }
+      rank += __popcll(own[i]);
+    }
   }
   __syncthreads();
 
   if (FORK) {
-    for (int x = t; x < shares; x += kThreads) {
-      const int e = entry_of(share_at, n, x);
-      const int j = x - share_at[e];
-      a.table[(int64_t)dst[e] * W + j] = a.table[(int64_t)src[e] * W + j];
+    for (int x = mine; x < shares; x += kStep) {
+      int p[kEach], e[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        e[i] = y < shares ? entry_of(share_at, n, y) : 0;
+        p[i] = y < shares ? a.table[(int64_t)src[e[i]] * W + (y - share_at[e[i]])] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int y = x + 64 * i;
+        if (y < shares) a.table[(int64_t)dst[e[i]] * W + (y - share_at[e[i]])] = p[i];
+      }
     }
     if (take) a.table[(int64_t)d * W + full] = fresh;
   }
