@@ -430,7 +430,7 @@ int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int
  *            [0, v) is a root.  NULL: the nodes are a chain of any length
  *            (M = 1: the next token; a long chain: a suffix prefill), node v
  *            sees the committed tokens and nodes 0 .. v.
- *   out      [B][M][Hq][D] in dt:  sum_t p_t * v_hat_t, p the softmax of
+ *   out      [B][M][Hq][D] in dt, not overlapping q:  sum_t p_t * v_hat_t, p the softmax of
  *            sm_scale * q . k_hat_t over the tokens the node sees, k_hat and
  *            v_hat the decoded cache.
  *   lse      optional out [B][M][Hq] fp32: the logarithm of the softmax's sum.

@@ -120,7 +120,7 @@ int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int
   a.nodes = (int)M;
   a.group = (int)(Hq / H);
   a.bf16 = dt == NVFP4_BF16;
-  return nvfp4::kv_attention_workspace_bytes(a);
+  return nvfp4::kv_attention_supported(a) ? nvfp4::kv_attention_workspace_bytes(a) : 0;
 }
 
 nvfp4_status nvfp4_kv_attention(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t P,
@@ -159,6 +159,11 @@ nvfp4_status nvfp4_kv_attention(int64_t B, int64_t M, int64_t Hq, int64_t H, int
   a.lse = lse;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
+  if (!nvfp4::kv_attention_supported(a)) return NVFP4_ERR_SHAPE;
+  // several workgroups read a row of q that one of them writes
+  const uintptr_t size = a.bf16 ? 2 : 4, q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+  const uintptr_t q1 = q0 + ((B * M - 1) * q_stride + Hq * D) * size, o1 = o0 + B * M * Hq * D * size;
+  if (q0 < o1 && o0 < q1) return NVFP4_ERR_SHAPE;
   return from_hip(nvfp4::launch_kv_attention(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -167,7 +172,7 @@ nvfp4_status nvfp4_kv_compact(int64_t L, int64_t B, int64_t M, int64_t H, int64_
                               int64_t page_stride, const int32_t* table, const int32_t* lens, const int32_t* result,
                               int32_t* new_lens, void* stream) {
   if (!pages_ok(L, P, H, page_size, D, layer_stride, page_stride) || L < 1 || !table_ok(B, W, page_size) || M < 1 ||
-      M > 64 || B * L * H >= kMaxInt / 2)
+      M > 64 || B * L * H >= kMaxInt / 128)
     return NVFP4_ERR_SHAPE;
   if (B == 0) return NVFP4_OK;
   if (!k_pages || !v_pages || !table || !lens || !result || !new_lens) return NVFP4_ERR_NULL;

@@ -10,7 +10,8 @@
 // Mathematics.  For a row (node v, query head) z_t = c * sum_d q_d k_td in
 // exponent units of 2 (c = sm_scale * k_scale * log2 e), p_t = 2^(z_t - m), out
 // = v_scale * sum_t p_t v_t / sum_t p_t.  Any m gives the same quotient, so m
-// follows the running maximum lazily: p is held as 2^(z - m + 7), and only when
+// follows the running maximum lazily: p is held as 2^(z + lift), lift = 7 - m (one
+// rounded number, which the sums are scaled by exactly), and only when
 // the sum of a lane's eight p, which the softmax needs anyway, exceeds 2^15 (a
 // score is 5 to 8 above m, or more) does m move up to the maximum, the sums are
 // rescaled and the eight are taken again.  So p stays inside f16's range, normal
@@ -45,8 +46,8 @@ typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;              // waves of a workgroup
-constexpr float kStart = -1e30f;       // running maximum before the first score
-constexpr float kLift = 7.0f;          // p is held as 2^(z - m + kLift)
+constexpr float kStart = 1e30f;        // lift before the first score
+constexpr float kLift = 7.0f;          // lift is kLift less the running maximum
 constexpr float kMost = 32768.0f;      // a lane's eight p sum up to no more, so each fits f16
 
 struct Plan {
@@ -326,7 +327,7 @@ struct Smem {
                                            // + e of row lane % 16
     float o[kWaves][16][D + 4];            // one row tile of the waves' sums (rows padded by 16 bytes)
   };
-  float m[kWaves][16 * RT], l[kWaves][16 * RT];
+  float lift[kWaves][16 * RT], l[kWaves][16 * RT];
   uint64_t line[16 * RG * RT];       // what a row sees of the nodes: bits (trees), or its node (chains)
   int sums[kWaves], found[2];
 };
@@ -334,7 +335,7 @@ struct Smem {
 template <int RT, int NT>
 struct Sums {
   f4_t o[RT][NT];
-  float m[RT], l[RT];
+  float lift[RT], l[RT];
 };
 
 // Barrier for what is passed through LDS: unlike __syncthreads it does not wait
@@ -426,9 +427,9 @@ __device__ __forceinline__ void raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc,
                                               __builtin_fmaxf(z[1][r][2], z[1][r][3]))) * c;
     x = __builtin_fmaxf(x, __shfl_xor(x, 16));
     x = __builtin_fmaxf(x, __shfl_xor(x, 32));
-    x = __builtin_fmaxf(acc.m[r], x);
-    const float f = __builtin_amdgcn_exp2f(acc.m[r] - x);
-    acc.m[r] = x;
+    x = __builtin_fminf(acc.lift[r], kLift - x);
+    const float f = __builtin_amdgcn_exp2f(x - acc.lift[r]);
+    acc.lift[r] = x;
     acc.l[r] *= f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc.o[r][n] *= f;
@@ -442,7 +443,7 @@ __device__ __forceinline__ void weigh(const f4_t (&z)[2][RT], const Sums<RT, NT>
                                       h8_t (&pl)[F32 ? RT : 1], float (&sum)[RT]) {
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    const float lift = kLift - acc.m[r];
+    const float lift = acc.lift[r];
     float p[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e >> 2][r][e & 3], c, lift));
@@ -616,7 +617,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
     Sums<RT, NT> acc;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      acc.m[r] = kStart;
+      acc.lift[r] = kStart;
       acc.l[r] = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc.o[r][n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -682,7 +683,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       l += __shfl_xor(l, 16);
       l += __shfl_xor(l, 32);
       if (qe == 0) {
-        sm.m[wave][16 * r + je] = acc.m[r];
+        sm.lift[wave][16 * r + je] = acc.lift[r];
         sm.l[wave][16 * r + je] = l;
       }
     }
@@ -707,18 +708,18 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
       lds_barrier();
       const int row = 16 * (first + r) + row16, grow = x.row0 + row;
       if (r >= tiles_here || grow >= rows_all) continue;
-      float mw[KW], top = kStart, sum = 0.0f;
+      float lifts[KW], low = kStart, sum = 0.0f;
       vec_t y[PER / VEC];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        mw[w] = sm.m[rg * KW + w][16 * r + row16];
-        top = __builtin_fmaxf(top, mw[w]);
+        lifts[w] = sm.lift[rg * KW + w][16 * r + row16];
+        low = __builtin_fminf(low, lifts[w]);
       }
 #pragma unroll
       for (int n = 0; n < PER / VEC; ++n) y[n] = 0.0f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const float f = __builtin_amdgcn_exp2f(mw[w] - top);
+        const float f = __builtin_amdgcn_exp2f(low - lifts[w]);
         sum += f * sm.l[rg * KW + w][16 * r + row16];
 #pragma unroll
         for (int n = 0; n < PER / VEC; ++n)
@@ -730,7 +731,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 #pragma unroll
         for (int n = 0; n < PER / VEC; ++n) *reinterpret_cast<vec_t*>(to + VEC * LANES * n) = y[n];
         if (d0 == 0)
-          *reinterpret_cast<f2_t*>(plan.part + (uint64_t)2 * plan.groups * R * D + (uint64_t)at_row * 2) = f2_t{top, sum};
+          *reinterpret_cast<f2_t*>(plan.part + (uint64_t)2 * plan.groups * R * D + (uint64_t)at_row * 2) = f2_t{low, sum};
         continue;
       }
       const int node = node_of(plan, grow);
@@ -750,7 +751,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         }
       }
       if (a.lse && d0 == 0)
-        a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
+        a.lse[orow] = live ? (__builtin_log2f(sum) - low) * 0.69314718055994530942f : -__builtin_inff();
     }
 
     // The next item of the list.
@@ -810,15 +811,15 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   const float* ml = plan.part + (uint64_t)2 * plan.groups * R * D;
   constexpr int N = D / 64;  // values of a lane
   typedef float vec_t __attribute__((ext_vector_type(N)));
-  float top = kStart, sum = 0.0f;
+  float low = kStart, sum = 0.0f;
   vec_t acc = (vec_t)0.0f;
   for (int base = g0; base <= g1; base += 64) {
     // the statistics of up to 64 partial sums, a lane each
-    float m = kStart, l = 0.0f;
+    float lift = kStart, l = 0.0f;
     if (base + lane <= g1) {
       const int g = base + lane;
       const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
-      m = y.x;
+      lift = y.x;
       l = y.y;
     }
     const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
@@ -834,14 +835,14 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
             plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane);
       }
       if (k == 0) {
-        float high = m;
-        for (int off = 32; off > 0; off >>= 1) high = __builtin_fmaxf(high, __shfl_xor(high, off));
-        high = __builtin_fmaxf(high, top);
-        const float old = __builtin_amdgcn_exp2f(top - high);
-        f = __builtin_amdgcn_exp2f(m - high);
+        float lowest = lift;
+        for (int off = 32; off > 0; off >>= 1) lowest = __builtin_fminf(lowest, __shfl_xor(lowest, off));
+        lowest = __builtin_fminf(lowest, low);
+        const float old = __builtin_amdgcn_exp2f(lowest - low);
+        f = __builtin_amdgcn_exp2f(lowest - lift);
         sum = sum * old + f * l;
         acc *= old;
-        top = high;
+        low = lowest;
       }
 #pragma unroll
       for (int u = 0; u < FLY; ++u) {
@@ -866,7 +867,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
   }
   if (a.lse && lane == 0)
-    a.lse[orow] = live ? (__builtin_log2f(sum) + (top - kLift)) * 0.69314718055994530942f : -__builtin_inff();
+    a.lse[orow] = live ? (__builtin_log2f(sum) - low) * 0.69314718055994530942f : -__builtin_inff();
 }
 
 int compute_units() {
@@ -955,6 +956,12 @@ hipError_t launch_dim(const KvAttentionArgs& a, const Plan& p, int rt, int rg, h
 }
 
 }  // namespace
+
+bool kv_attention_supported(const KvAttentionArgs& a) {
+  int rt, rg, row_items;
+  row_split(a, &rt, &rg, &row_items);
+  return (int64_t)a.c.seqs * row_items * a.c.heads * 64 * kWaves < ((int64_t)1 << 32);  // threads of a launch
+}
 
 int64_t kv_attention_workspace_bytes(const KvAttentionArgs& a) {
   int rt, rg;

@@ -14,6 +14,8 @@
 namespace nvfp4 {
 namespace {
 
+constexpr int kMaxTokens = 1 << 30;  // no table covers more
+
 // Address of a token's row of one head, or NULL when the position lies outside
 // the table or its page id outside the cache.
 __device__ __forceinline__ uint8_t* token_row(uint8_t* base, const KvCache& c, int seq, int head, int pos) {
@@ -39,8 +41,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, uint32_t
   const int b = (int)(row / (uint32_t)a.nodes), v = (int)(row - (uint32_t)b * a.nodes);
   const int len = c.lens[b];
   const int count = a.counts ? a.counts[b] : a.nodes;
-  if (len < 0 || v >= count) return;
-  const int e = (int)chunk << 4, head = e / c.dim, d = e - head * c.dim;
+  if (len < 0 || len > kMaxTokens || v >= count) return;
+  const int e = (int)chunk << 4, head = e >> (31 - __clz(c.dim)), d = e & (c.dim - 1);
   uint8_t* to = token_row(is_v ? c.v : c.k, c, b, head, len + v);
   if (!to) return;
   const float s = is_v ? *a.v_scale : *a.k_scale;
@@ -91,8 +93,8 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(KvCompactArgs a, uint32
   const int len = c.lens[b];
   int moves = res[1];
   moves = moves < 0 ? 0 : moves < a.nodes ? moves : a.nodes - 1;
-  if (x == 0 && lane == 0) a.new_lens[b] = len < 0 ? len : len + 1 + moves;
-  if (len < 0) return;
+  if (x == 0 && lane == 0) a.new_lens[b] = len < 0 || len > kMaxTokens ? len : len + 1 + moves;
+  if (len < 0 || len > kMaxTokens) return;
   uint8_t* base = ((hv & 1) ? c.v : c.k) + layer * c.layer_stride;
   const int per = c.dim >> 4;  // 16-byte chunks of a row
   for (int r = 0; r < moves * per; r += 64) {

@@ -141,6 +141,7 @@ struct KvPoolArgs {
 
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
 hipError_t launch_kv_compact(const KvCompactArgs& a, hipStream_t stream);
+bool kv_attention_supported(const KvAttentionArgs& a);  // one launch holds its items
 int64_t kv_attention_workspace_bytes(const KvAttentionArgs& a);
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t stream);
 hipError_t launch_kv_resize(const KvPoolArgs& a, hipStream_t stream);

@@ -292,6 +292,13 @@ def test_attention_of_a_suffix_over_a_long_prefix():
     c.check(c.gpu())
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_attention_of_large_scores(dtype):
+    """Scores of some thousands: the exponent's offset rounds, and every partial sum by its own."""
+    c = Case(dtype, [1500, 700], 5, 2, 3, 64, 32, True, seed=19, gain=600.0)
+    c.check(c.gpu())
+
+
 @pytest.mark.parametrize("sm", [0.0, -0.3, 2.0])
 def test_attention_scales(sm):
     c = Case(FP, [150, 20], 4, 2, 2, 64, 16, True, seed=9, gain=1.0)

@@ -25,7 +25,7 @@ def changed(args, **new):
 
 APPEND = dict(B=2, M=3, H=4, D=64, page=16, P=8, W=5, k=A, v=A, dt=B.NVFP4_BF16, ks=256, vs=256, k_scale=A, v_scale=A,
               kp=A, vp=A, stride=4 * 16 * 64, table=A, lens=A, counts=None, stream=None)
-ATTEND = dict(B=2, M=3, Hq=8, H=4, D=64, page=16, P=8, W=5, q=A, dt=B.NVFP4_BF16, qs=512, sm=0.125, k_scale=A,
+ATTEND = dict(B=2, M=3, Hq=8, H=4, D=64, page=16, P=8, W=5, q=16 * A, dt=B.NVFP4_BF16, qs=512, sm=0.125, k_scale=A,
               v_scale=A, kp=A, vp=A, stride=4 * 16 * 64, table=A, lens=A, parent=A, counts=None, out=A, lse=A, ws=None,
               wsb=0, stream=None)
 COMPACT = dict(L=2, B=2, M=3, H=4, D=64, page=16, P=8, W=5, kp=A, vp=A, layer=8 * 4096, stride=4096, table=A, lens=A,
@@ -46,14 +46,15 @@ def test_append_refuses_shapes(lib, bad):
 
 
 @pytest.mark.parametrize("bad", SHAPES + [dict(B=-1), dict(M=65), dict(Hq=6), dict(Hq=0), dict(Hq=4 * 257, qs=4 * 257 * 64), dict(qs=504), dict(qs=516),
-                                          dict(sm=float("inf")), dict(sm=float("nan")), dict(wsb=-1),
+                                          dict(sm=float("inf")), dict(sm=float("nan")), dict(wsb=-1), dict(out=16 * A), dict(out=16 * A + 6000), dict(q=A),
+                                          dict(B=65535, H=1024, Hq=1024, M=1, qs=65536, stride=1 << 20),
                                           dict(parent=None, B=4096, M=8192)])
 def test_attention_refuses_shapes(lib, bad):
     assert lib.nvfp4_kv_attention(*changed(ATTEND, **bad)) == B.NVFP4_ERR_SHAPE
 
 
 @pytest.mark.parametrize("bad", SHAPES + [dict(L=0), dict(L=4097), dict(B=-1), dict(M=0), dict(M=65), dict(layer=-16),
-                                          dict(layer=8), dict(new=A), dict(new=A + 4), dict(new=A - 4)])
+                                          dict(layer=8), dict(B=4096, L=4096, H=1), dict(new=A), dict(new=A + 4), dict(new=A - 4)])
 def test_compact_refuses_shapes(lib, bad):
     assert lib.nvfp4_kv_compact(*changed(COMPACT, **bad)) == B.NVFP4_ERR_SHAPE
 
