@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "launch.h"
+#include "kv_launch.h"
 
 namespace {
 

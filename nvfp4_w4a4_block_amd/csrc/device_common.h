@@ -44,23 +44,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
   return __builtin_amdgcn_cvt_f32_fp8(byte, 0);
 }
 
-// Four values -> four E4M3 bytes (value i in byte i) with the hardware
-// conversion after clamping to +-448.  On gfx950 this equals
-// e4m3_from_nonneg of the magnitude with the sign bit kept for every finite
-// input (checked on 50M inputs: every E4M3 midpoint and its float32
-// neighbours, subnormals, signed zeros and saturating values): round to
-// nearest even, and the clamp supplies the saturation that the conversion
-// alone would turn into NaN.
-__device__ __forceinline__ uint32_t encode4_e4m3(float a, float b, float c, float d) {
-  const float lo = -448.0f, hi = 448.0f;
-  a = __builtin_fminf(__builtin_fmaxf(a, lo), hi);
-  b = __builtin_fminf(__builtin_fmaxf(b, lo), hi);
-  c = __builtin_fminf(__builtin_fmaxf(c, lo), hi);
-  d = __builtin_fminf(__builtin_fmaxf(d, lo), hi);
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-}
-
 // fp32 -> E2M1 code, round to nearest even, saturating at 6; sign bit taken
 // from the input's sign bit.  Decision points are the midpoints between the
 // magnitudes {0, .5, 1, 1.5, 2, 3, 4, 6}; a midpoint goes to the even code.

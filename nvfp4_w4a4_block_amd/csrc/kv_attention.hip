@@ -37,7 +37,7 @@
 #include <type_traits>
 
 #include "device_common.h"
-#include "launch.h"
+#include "kv_launch.h"
 
 namespace nvfp4 {
 namespace {

@@ -23,6 +23,22 @@ __device__ __forceinline__ uint32_t encode_e4m3_signed(float y) {
   return e4m3_from_nonneg(__builtin_fabsf(y)) | ((__float_as_uint(y) >> 24) & 0x80u);
 }
 
+// Four values -> four E4M3 bytes (value i in byte i) with the hardware
+// conversion after clamping to +-448.  On gfx950 this equals
+// encode_e4m3_signed for every finite input (checked on 50M inputs: every
+// E4M3 midpoint and its float32 neighbours, subnormals, signed zeros and
+// saturating values): round to nearest even, and the clamp supplies the
+// saturation that the conversion alone would turn into NaN.
+__device__ __forceinline__ uint32_t encode4_e4m3(float a, float b, float c, float d) {
+  const float lo = -448.0f, hi = 448.0f;
+  a = __builtin_fminf(__builtin_fmaxf(a, lo), hi);
+  b = __builtin_fminf(__builtin_fmaxf(b, lo), hi);
+  c = __builtin_fminf(__builtin_fmaxf(c, lo), hi);
+  d = __builtin_fminf(__builtin_fmaxf(d, lo), hi);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
 template <bool BF16>
 __device__ __forceinline__ void load16(const void* x, int64_t c, float* v) {
   if constexpr (BF16) {

@@ -9,7 +9,7 @@
 // path is accepted moves the path's tokens to the front (kv_compact_kernel).
 #pragma clang fp contract(off)
 #include "device_common.h"
-#include "launch.h"
+#include "kv_launch.h"
 
 namespace nvfp4 {
 namespace {
@@ -25,6 +25,18 @@ __device__ __forceinline__ uint8_t* token_row(uint8_t* base, const KvCache& c, i
   if (page < 0 || page >= c.pages) return nullptr;
   const int slot = pos & ((1 << c.page_shift) - 1);
   return base + page * c.page_stride + (((int64_t)head << c.page_shift) + slot) * c.dim;
+}
+
+// Four values -> four E4M3 bytes: the hardware conversion rounds to nearest
+// even, and the clamp to +-448 gives the codec's saturation.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const float lo = -kE4M3Max, hi = kE4M3Max;
+  a = __builtin_fminf(__builtin_fmaxf(a, lo), hi);
+  b = __builtin_fminf(__builtin_fmaxf(b, lo), hi);
+  c = __builtin_fminf(__builtin_fmaxf(c, lo), hi);
+  d = __builtin_fminf(__builtin_fmaxf(d, lo), hi);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 // q = E4M3(x * (1 / s)) of every node's keys and values, 16 elements per
@@ -71,7 +83,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, uint32_t
   u4_t w;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    w[j] = encode4_e4m3(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
+    w[j] = e4m3x4(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
   *reinterpret_cast<u4_t*>(to + d) = w;
 }
 

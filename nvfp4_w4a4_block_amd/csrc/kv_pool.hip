@@ -20,7 +20,7 @@
 // there the occurrences settle on the first by an atomic minimum in the page's
 // own count, which is zero by then and is reset afterwards.
 #include "device_common.h"
-#include "launch.h"
+#include "kv_launch.h"
 
 namespace nvfp4 {
 namespace {
