@@ -351,12 +351,24 @@ __device__ __forceinline__ void lds_barrier() {
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // Scores of a wave's 32 tokens against its row tiles r0 .. r0 + RT - 1: their
-// sum over the 32 values of step s.
+// sum over the 32 values of step s.  Where they fit (kAhead), the query operands
+// of step s are in `ahead`, and those of the next one are fetched to it before
+// the products (3% of a step: the LDS latency shows otherwise).
+template <int RT, bool F32>
+constexpr bool kAhead = !F32 && RT <= 4;
+
 template <int NR, int D, int RT, int RG, bool F32>
 __device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyTile<D>& kt, int r0, int s,
-                                      f4_t (&z)[2][RT]) {
+                                      bf8_t (&ahead)[RT], f4_t (&z)[2][RT]) {
   const int lane = threadIdx.x & 63;
-  bf8_t kop[2];
+  bf8_t kop[2], now[RT];
+  if constexpr (kAhead<RT, F32>) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      now[r] = ahead[r];
+      if (s + 1 < D / 32) ahead[r] = sm.q[0][r0 + r][s + 1][lane];
+    }
+  }
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     const u4_t w = kt.k[kb][s >> 1];
@@ -366,10 +378,10 @@ __device__ __forceinline__ void score(const Smem<D, RT, RG, F32>& sm, const KeyT
   for (int n = F32 ? 2 : 0; n >= 0; --n)  // small parts first
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const bf8_t qop = sm.q[n][r0 + r][s][lane];
+      if constexpr (!kAhead<RT, F32>) now[r] = sm.q[n][r0 + r][s][lane];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
-        z[kb][r] = mfma_bf16(kop[kb], qop, s == 0 && n == (F32 ? 2 : 0) ? f4_t{0.0f, 0.0f, 0.0f, 0.0f} : z[kb][r]);
+        z[kb][r] = mfma_bf16(kop[kb], now[r], s == 0 && n == (F32 ? 2 : 0) ? f4_t{0.0f, 0.0f, 0.0f, 0.0f} : z[kb][r]);
     }
 }
 
@@ -633,9 +645,14 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         else __builtin_amdgcn_s_setprio(0);
         asm volatile("" ::: "memory");  // the queries are read again from LDS: kept in registers they would spill
         f4_t z[2][RT];
+        bf8_t ahead[RT];
+        if constexpr (kAhead<RT, F32>) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) ahead[r] = sm.q[0][r0 + r][0][threadIdx.x & 63];
+        }
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          score<NR>(sm, kt, r0, s, z);
+          score<NR>(sm, kt, r0, s, ahead, z);
           fence();
         }
         const Blocks next = find_blocks(a, entries, h, key0 + TILE);
