@@ -442,7 +442,8 @@ int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int
  * zeros and lse = -infinity.  Scores, softmax statistics and sums are fp32; in
  * bf16 calls the probabilities are rounded to f16 (11 bits) for the product
  * with the values, in fp32 calls they keep 22 bits.  Cache bytes that no row
- * sees may hold anything, NaN codes included, behind a sequence's last node. */
+ * sees may hold anything; a NaN code, or a NaN in a query, reaches the rows that
+ * see it and no other. */
 nvfp4_status nvfp4_kv_attention(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t P,
                                 int64_t W, const void* q, nvfp4_dtype dt, int64_t q_stride, float sm_scale,
                                 const float* k_scale, const float* v_scale, const uint8_t* k_pages,

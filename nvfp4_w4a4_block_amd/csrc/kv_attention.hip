@@ -428,6 +428,49 @@ __device__ __forceinline__ void mask(const KvAttentionArgs& a, const Smem<D, RT,
   }
 }
 
+// NaN codes among the values of a masked tile reach the rows that see their
+// tokens and no other (0 * NaN would): they are taken out of the values, and the
+// sums that one belongs to are set to NaN, found by the product of the codes' places with
+// what the rows see.
+template <int NR, int D, int RT>
+__device__ __forceinline__ void spread_nans(KeyTile<D>& kt, const f4_t (&z)[2][RT], Sums<RT, D / 16>& acc) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) any |= (kt.v[e].w[n] & 0x7F7F7F7Fu) + 0x01010101u;
+  if (!__any((any & 0x80808080u) != 0)) return;
+#pragma unroll
+  for (int n = 0; n < D / 64; ++n) {
+    uint32_t one[8];  // E4M3 ones in the codes' places
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t nan = ((kt.v[e].w[n] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+      one[e] = nan >> 2 | nan >> 3 | nan >> 4;
+      kt.v[e].w[n] &= ~(nan | (nan - (nan >> 7)));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t pair[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        pair[e] = __builtin_amdgcn_perm(one[2 * e + 1], one[2 * e], u < 2 ? 0x05010400u : 0x07030602u);
+      const h8_t places = u & 1 ? to_f16x8<true>(pair) : to_f16x8<false>(pair);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        h8_t seen;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) seen[e] = z[e >> 2][r][e & 3] == -__builtin_inff() ? (_Float16)0.0f : (_Float16)1.0f;
+        const f4_t hits = mfma16x16x32(places, seen, f4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc.o[r][4 * n + u][e] = hits[e] > 0.0f ? __builtin_nanf("") : acc.o[r][4 * n + u][e];
+        fence();
+      }
+    }
+  }
+}
+
 // Moves the running maxima to the largest score so far.
 template <int NR, int RT, int NT>
 __device__ __forceinline__ void raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc, float c) {
@@ -655,11 +698,13 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
           score<NR>(sm, kt, r0, s, ahead, z);
           fence();
         }
+        if (key0 + 32 > clear || !here.there[0] || !here.there[1]) {
+          mask<NR>(a, sm, kt, r0, z, key0, x, here);
+          spread_nans<NR>(kt, z, acc);
+        }
         const Blocks next = find_blocks(a, entries, h, key0 + TILE);
         load_keys<D>(a, next, more, kt);
         entries = fetch_entries(a, pages, key0 + 2 * TILE);
-        if (key0 + 32 > clear || !here.there[0] || !here.there[1])
-          mask<NR>(a, sm, kt, r0, z, key0, x, here);
         if (tile == t0) raise<NR>(z, acc, c);
         h8_t ph[RT], pl[F32 ? RT : 1];
         float sum[RT];
@@ -752,7 +797,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
         continue;
       }
       const int node = node_of(plan, grow);
-      const bool live = node < x.count && sum > 0.0f;
+      const bool live = node < x.count && sum != 0.0f;
       const float f = live ? vs / sum : 0.0f;
       const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group +
                            (grow - node * a.group);
@@ -874,7 +919,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   }
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   const int node = node_of(plan, grow);
-  const bool live = node < x.count && sum > 0.0f;
+  const bool live = node < x.count && sum != 0.0f;
   const float scale = live ? *a.v_scale / sum : 0.0f;
   const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
 #pragma unroll

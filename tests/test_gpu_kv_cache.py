@@ -601,3 +601,38 @@ def test_empty_calls():
     t = B.kv_pool(2, 2, 2, DEV)
     assert int(B.nvfp4_kv_resize(*t, 16, none, none)) == 0
     assert int(B.nvfp4_kv_fork(*t, pages[None], pages[None].clone(), none, none, none)) == 0
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (256, BF), (128, FP)])
+def test_nan_codes_reach_only_the_rows_that_see_them(D, dtype, tree):
+    """A NaN among a node's values spoils one dimension, in the rows of its descendants; one among its
+    keys, and one in a query, spoil whole rows.  The other rows are as they were without them."""
+    c = Case(dtype, [70, 300], 12, 2, 3, D, 32, tree=tree, seed=D + tree)
+    clean_out, clean_lse = (x.cpu().numpy() for x in (lambda r: (r[0].float(), r[1]))(c.gpu()))
+    line = np.tri(12, dtype=bool) if not tree else C.ancestors(c.parent[1])
+
+    def at(t):
+        return c.table[1, t // 32], t % 32
+
+    node_v, node_k = 5, 9
+    p, s = at(300 + node_v)
+    c.v[p, 1, s, 7] = 0xFF
+    c.v[p, 1, s, D - 1] = 0x7F
+    p, s = at(300 + node_k)
+    c.k[p, 0, s, 3] = 0x7F
+    q = c.q.clone()
+    q[0, 4, 2, 1] = float("nan")
+    out, lse = c.gpu(q=q)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    want_out, want_lse = clean_out.copy(), clean_lse.copy()
+    for v in range(12):
+        if line[v, node_v]:
+            want_out[1, v, 3:, [7, D - 1]] = np.nan
+        if line[v, node_k]:
+            want_out[1, v, :3] = np.nan
+            want_lse[1, v, :3] = np.nan
+    want_out[0, 4, 2] = np.nan
+    want_lse[0, 4, 2] = np.nan
+    np.testing.assert_array_equal(out, want_out)
+    np.testing.assert_array_equal(lse, want_lse)
