@@ -387,7 +387,9 @@ nvfp4_status nvfp4_tree_verify(int64_t M, int64_t K, int64_t N,
  *   Shapes: D 64, 128 or 256; page_size a power of two, 16 .. 1024; 1 <= H <=
  *   1024; B <= 65535; W * page_size <= 2^30 and B * W <= 2^29; M <= 65535 and
  *   B * M <= 2^24; 1 <= P < 2^31 pages; page_stride a multiple of 16, at least
- *   H * page_size * D and below 2^31.  layer_stride a multiple of 16.
+ *   H * page_size * D and below 2^31.  layer_stride a multiple of 16; layers do
+ *   not overlap: they lie behind each other, or side by side within a page's
+ *   stride.
  *   What the device arrays hold is checked on the device: a token whose
  *   position lies outside the table, or whose page id lies outside [0, P), is
  *   not written, not read and not attended.
@@ -406,7 +408,8 @@ nvfp4_status nvfp4_tree_verify(int64_t M, int64_t K, int64_t N,
  *            nvfp4_kv_fp8_encode with that scale.
  * Node v of sequence b is written at token lens[b] + v of one layer's pages;
  * lens is not changed.  Two sequences that share a page must not both append
- * to it (nvfp4_kv_fork gives each its own partial page). */
+ * to it, nor both compact in it (nvfp4_kv_fork gives each its own partial
+ * page).  Both refuse k_pages = v_pages. */
 nvfp4_status nvfp4_kv_append(int64_t B, int64_t M, int64_t H, int64_t D, int64_t page_size, int64_t P, int64_t W,
                              const void* k, const void* v, nvfp4_dtype dt, int64_t k_stride, int64_t v_stride,
                              const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,

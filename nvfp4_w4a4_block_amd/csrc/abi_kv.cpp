@@ -30,12 +30,16 @@ int shift_of(int64_t n) {
 }
 
 // The cache's geometry: heads, page size, head dimension, pages, strides (bytes).
+// Layers lie behind each other, or side by side within the pages' stride.
 bool pages_ok(int64_t L, int64_t P, int64_t H, int64_t page_size, int64_t D, int64_t layer_stride,
               int64_t page_stride) {
   if (L < 0 || L > 4096 || P < 1 || P >= kMaxInt || H < 1 || H > kMaxHeads) return false;
   if (!page_size_ok(page_size) || (D != 64 && D != 128 && D != 256)) return false;
   if (page_stride < H * page_size * D || page_stride >= kMaxInt || page_stride % 16 != 0) return false;
-  return layer_stride >= 0 && layer_stride < ((int64_t)1 << 46) && layer_stride % 16 == 0;
+  if (layer_stride < 0 || layer_stride >= ((int64_t)1 << 46) || layer_stride % 16 != 0) return false;
+  const int64_t bytes = H * page_size * D;
+  return L <= 1 || layer_stride >= (P - 1) * page_stride + bytes ||
+         (layer_stride >= bytes && page_stride >= (L - 1) * layer_stride + bytes);
 }
 
 bool table_ok(int64_t B, int64_t W, int64_t page_size) {
@@ -98,6 +102,7 @@ nvfp4_status nvfp4_kv_append(int64_t B, int64_t M, int64_t H, int64_t D, int64_t
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;
+  if (k_pages == v_pages) return NVFP4_ERR_SHAPE;  // two writers of a row
   nvfp4::KvAppendArgs a;
   a.c = cache_of(1, P, H, page_size, D, k_pages, v_pages, 0, page_stride, B, W, table, lens);
   a.nodes = (int)M;
@@ -180,6 +185,7 @@ nvfp4_status nvfp4_kv_compact(int64_t L, int64_t B, int64_t M, int64_t H, int64_
       !aligned(result, 4) || !aligned(new_lens, 4))
     return NVFP4_ERR_ALIGN;
   if (lens < new_lens + B && new_lens < lens + B) return NVFP4_ERR_SHAPE;  // every workgroup reads lens
+  if (k_pages == v_pages) return NVFP4_ERR_SHAPE;  // two waves would move a row
   nvfp4::KvCompactArgs a;
   a.c = cache_of(L, P, H, page_size, D, k_pages, v_pages, layer_stride, page_stride, B, W, table, lens);
   a.nodes = (int)M;

@@ -636,3 +636,81 @@ def test_nan_codes_reach_only_the_rows_that_see_them(D, dtype, tree):
     want_lse[0, 4, 2] = np.nan
     np.testing.assert_array_equal(out, want_out)
     np.testing.assert_array_equal(lse, want_lse)
+
+
+def many_rows(D, dtype, most):
+    return [pytest.param(D, dtype, n, id=f"{D}-{'bf16' if dtype == BF else 'f32'}-{n}") for n in most]
+
+
+@pytest.mark.parametrize("D,dtype,tiles", many_rows(64, BF, [2, 5, 6, 7, 11, 13, 24, 25]) +
+                         many_rows(128, BF, [2, 3, 4, 5, 8, 9, 16, 17]) + many_rows(256, BF, [1, 2, 3, 4, 5, 8, 9]) +
+                         many_rows(64, FP, [1, 2, 3, 5, 8, 9]) + many_rows(128, FP, [2, 4, 7, 9]) +
+                         many_rows(256, FP, [1, 2, 3, 4, 5]))
+def test_attention_of_every_number_of_row_tiles(D, dtype, tiles):
+    """Rows (3 query heads a KV head) that fill `tiles` tiles of 16, over sequences that are cut."""
+    M = (16 * tiles - 1) // 3
+    c = Case(dtype, [1150 - M, 40], M, 1, 3, D, 64, seed=D + tiles, width=20)
+    c.check(c.gpu())
+
+
+class Shared(Case):
+    """Sequences whose tables name random pages of one small pool."""
+
+    def __init__(self, dtype, lens, M, H, G, D, page, width, pages, seed, counts=None):
+        rng = np.random.default_rng(seed)
+        self.lens, self.counts, self.M, self.parent, self.dtype, self.D = lens, counts, M, None, dtype, D
+        self.table = rng.integers(0, pages, (len(lens), width)).astype(np.int32)
+        self.k, self.v = (KV.encode(rng.standard_normal((pages, H, page, D)).astype(np.float32), s) for s in (KS, VS))
+        self.q, self.qf = dtype_values(rng.standard_normal((len(lens), M, H * G, D)), dtype)
+
+
+@pytest.mark.parametrize("dtype,B_,M,H", [(BF, 600, 1, 1), (FP, 350, 1, 2), (BF, 1100, 1, 1)])
+def test_attention_of_more_sequences_than_workgroups(dtype, B_, M, H):
+    """Ranges that hold several sequences, cut at places of their set-up as well, unused rows among them."""
+    lens = np.random.default_rng(B_).integers(-60, 1290 - M, B_)
+    c = Shared(dtype, lens, M, H, 2, 64, 64, 21, 50, B_)
+    c.check(c.gpu())
+
+
+@pytest.mark.parametrize("tree", [True, False])
+def test_attention_of_nodes_behind_the_table(tree):
+    """Nodes whose tokens have no place see the tokens that have one."""
+    c = Case(BF, [60, 3000], 9, 2, 2, 64, 16, tree, seed=23)
+    c.table = np.ascontiguousarray(c.table[:, :4])
+    c.lens = np.array([60, 64])
+    c.check(c.gpu())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, give what they give alone."""
+    cases = [Case(BF, [5000], 16, 2, 5, 128, 64, True, seed=24), Case(BF, [900, 2500, 40], 5, 2, 4, 64, 32, seed=25)]
+    alone = [c.gpu() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(cases[i].gpu())
+    torch.cuda.synchronize()
+    for i, want in enumerate(alone):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_forks_of_one_sequence_and_pages_given_up_twice():
+    """One source named many times; then its copies, which share every whole page, are freed in one call."""
+    pool = C.Pool(12, 8, 60)
+    pool.resize(16, [0, 1], [100, 40])
+    t = pool_tensors(pool)
+    start = np.random.default_rng(26).integers(0, 256, (2, 3, 60, 2, 16, 64), dtype=np.uint8)
+    pages = torch.from_numpy(start).to(DEV)
+    src, dst, tokens = [0] * 9, [2, 3, 4, 5, 6, 7, 8, 9, 1], [100, 96, 95, 1, 16, 0, 81, 100, 33]
+    short, moves = pool.fork(16, src, dst, tokens)
+    assert int(B.nvfp4_kv_fork(*t, pages[0], pages[1], ints(src), ints(dst), ints(tokens))) == short == 0
+    check_pool(t, pool)
+    np.testing.assert_array_equal(pages.cpu().numpy(), np.stack([C.copy_slots(x, moves) for x in start]))
+    seqs = [9, 3, 0, 0, 8, 2, 1, 6]
+    assert pool.resize(16, seqs, [0] * 8) == 0
+    assert int(B.nvfp4_kv_resize(*t, 16, ints(seqs), ints([0] * 8))) == 0
+    check_pool(t, pool)

@@ -83,6 +83,23 @@ def test_null_and_misaligned_pointers(lib, call, args, optional):
         assert getattr(lib, call)(*changed(args, **{name: value + 2})) == B.NVFP4_ERR_ALIGN, name
 
 
+@pytest.mark.parametrize("call,args", [("nvfp4_kv_compact", COMPACT), ("nvfp4_kv_fork", FORK)])
+def test_layers_that_overlap_are_refused(lib, call, args):
+    for bad in (dict(layer=0), dict(layer=4096), dict(layer=8 * 4096 - 16), dict(layer=4096, stride=2 * 4096 - 16),
+                dict(layer=4080, stride=3 * 4096)):
+        assert getattr(lib, call)(*changed(args, **bad)) == B.NVFP4_ERR_SHAPE, bad
+    for good in (dict(layer=8 * 4096 - 4096), dict(layer=4096, stride=2 * 4096), dict(layer=2 * 4096, stride=3 * 4096),
+                 dict(L=1, layer=0)):  # past the shapes: the missing table is what is refused
+        if good.get("layer") == 7 * 4096:
+            good["P"] = 7
+        assert getattr(lib, call)(*changed(args, **good, table=None)) == B.NVFP4_ERR_NULL, good
+
+
+def test_one_array_for_keys_and_values_is_not_written(lib):
+    assert lib.nvfp4_kv_append(*changed(APPEND, v=A + 64)) == B.NVFP4_ERR_SHAPE
+    assert lib.nvfp4_kv_compact(*changed(COMPACT)) == B.NVFP4_ERR_SHAPE
+
+
 def test_dtypes_and_workspace(lib):
     assert lib.nvfp4_kv_append(*changed(APPEND, dt=2)) == B.NVFP4_ERR_DTYPE
     assert lib.nvfp4_kv_attention(*changed(ATTEND, dt=-1)) == B.NVFP4_ERR_DTYPE
