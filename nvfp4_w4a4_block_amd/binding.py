@@ -498,36 +498,41 @@ def nvfp4_stream_read(a: torch.Tensor, b: torch.Tensor, sink: Optional[torch.Ten
 
 # Paged FP8 KV cache.  Pages are uint8 [P, H, page_size, D] per layer ([L, P, H, page_size, D] for
 # all layers), tables int32 [B, W], lengths int32 [B]; include/nvfp4.h states the layout.
+# A small call is bound by its host time (an append: 4 us for the launch, 5 for what is here), so the
+# checks compare device indices and bound names.
 
-def _call(dev: torch.device, where: str, fn, *args) -> None:
-    """Calls fn(*args, stream) with `dev` current and its current stream."""
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, _stream(dev))
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(on: int, where: str, fn, *args) -> None:
+    """Calls fn(*args, stream) with GPU `on` current and its current stream."""
+    if on == _current_device() and _raw_stream is not None:
+        status = fn(*args, _raw_stream(on))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
+        with torch.cuda.device(on):
+            status = fn(*args, torch.cuda.current_stream(on).cuda_stream)
     if status != NVFP4_OK:
         raise NVFP4Error(status, where)
 
 
-def _ints(dev: torch.device, names: str, *ts: torch.Tensor) -> None:
+def _ints(on: int, names: str, *ts: torch.Tensor) -> None:
     for t in ts:
-        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{names} must be contiguous int32 tensors on {dev}")
+        if t.dtype is not _I32 or t.get_device() != on or not t.is_contiguous():
+            raise ValueError(f"{names} must be contiguous int32 tensors on cuda:{on}")
 
 
-def _kv_scale(dev: torch.device, *ts: torch.Tensor) -> None:
-    for t in ts:
-        if t.dtype is not torch.float32 or t.numel() != 1 or t.device != dev:
-            raise ValueError(f"k_scale and v_scale must be float32 tensors of one element on {dev}")
+def _kv_scale(on: int, k_scale: torch.Tensor, v_scale: torch.Tensor) -> None:
+    if k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.get_device() != on or \
+            v_scale.get_device() != on or k_scale.numel() != 1 or v_scale.numel() != 1:
+        raise ValueError(f"k_scale and v_scale must be float32 tensors of one element on cuda:{on}")
 
 
-def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[torch.device, torch.Size, int, int]:
+def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[int, torch.Size, int, int]:
     """Checks a pair of page tensors of `dim` dimensions (same shape and strides, whole pages);
-    returns their device and shape and the bytes from a layer to the next and from a page to the next."""
-    dev = k_pages.device
-    if k_pages.dtype is not torch.uint8 or v_pages.dtype is not torch.uint8 or dev.type != "cuda" or \
-            v_pages.device != dev:
+    returns their GPU and shape and the bytes from a layer to the next and from a page to the next."""
+    on = k_pages.get_device()
+    if k_pages.dtype is not _U8 or v_pages.dtype is not _U8 or on < 0 or v_pages.get_device() != on:
         raise ValueError("pages must be uint8 tensors on one GPU")
     st, shape = k_pages.stride(), k_pages.shape
     if len(shape) != dim or shape != v_pages.shape or st != v_pages.stride():
@@ -536,13 +541,13 @@ def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[t
     P, H, page, D = shape[-4:]
     if (st[-1] != 1 and D > 1) or (st[-2] != D and page > 1) or (st[-3] != page * D and H > 1):
         raise ValueError("a page must be contiguous [H, page_size, D]")
-    return dev, shape, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
+    return on, shape, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
 
 
-def _kv_rows(x: torch.Tensor, shape: torch.Size, dev: torch.device, name: str) -> int:
+def _kv_rows(x: torch.Tensor, shape: torch.Size, on: int, name: str) -> int:
     """x of shape [B, M, heads, D] whose rows are contiguous; returns the values from a row to the next."""
-    if x.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if x.get_device() != on:
+        raise ValueError(f"{name} must be on cuda:{on}")
     B, M, H, D = shape
     sb, sm, sh, sd = x.stride()
     if B == 0 or M == 0:
@@ -560,21 +565,21 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_s
                     counts: Optional[torch.Tensor] = None) -> None:
     """Writes k and v [B, M, H, D] (float32/bfloat16; rows may be column ranges of a wider tensor) as
     E4M3 bytes at tokens lens[b] .. lens[b] + M - 1 (counts[b] of them) of the sequences' pages."""
-    dev, (P, Hp, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    on, (P, Hp, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
     shape, entries = k.shape, table.shape
     if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must be [B, M, H, D] of one dtype")
     B, M, H, D = shape
     if H != Hp or D != Dp or len(entries) != 2 or entries[0] != B or lens.shape != (B,):
         raise ValueError("k, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
-    _ints(dev, "table and lens", table, lens)
+    _ints(on, "table and lens", table, lens)
     if counts is not None:
-        _ints(dev, "counts", counts)
+        _ints(on, "counts", counts)
         if counts.shape != (B,):
             raise ValueError("counts must be [B]")
-    _kv_scale(dev, k_scale, v_scale)
-    _call(dev, "nvfp4_kv_append", load().nvfp4_kv_append, B, M, H, D, page, P, entries[1], k.data_ptr(),
-          v.data_ptr(), _dt(k.dtype), _kv_rows(k, shape, dev, "k"), _kv_rows(v, shape, dev, "v"), k_scale.data_ptr(),
+    _kv_scale(on, k_scale, v_scale)
+    _call(on, "nvfp4_kv_append", load().nvfp4_kv_append, B, M, H, D, page, P, entries[1], k.data_ptr(),
+          v.data_ptr(), _dt(k.dtype), _kv_rows(k, shape, on, "k"), _kv_rows(v, shape, on, "v"), k_scale.data_ptr(),
           v_scale.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_stride, table.data_ptr(),
           lens.data_ptr(), counts.data_ptr() if counts is not None else None)
 
@@ -588,41 +593,41 @@ def nvfp4_kv_attention(q: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Te
     the nodes' own keys and values already stand behind lens[b].  parent int32 [B, M]: drafted trees (M <=
     64); None: a chain.  sm_scale defaults to 1/sqrt(D).  Returns out [B, M, Hq, D] of q's dtype, or
     (out, lse float32 [B, M, Hq]) with want_lse.  workspace: uint8 scratch; None allocates it."""
-    dev, (P, H, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    on, (P, H, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
     shape, entries = q.shape, table.shape
     if len(shape) != 4:
         raise ValueError("q must be [B, M, Hq, D]")
     B, M, Hq, D = shape
     if D != Dp or H < 1 or Hq % H or len(entries) != 2 or entries[0] != B or lens.shape != (B,):
         raise ValueError("q, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
-    _ints(dev, "table and lens", table, lens)
+    _ints(on, "table and lens", table, lens)
     if parent is not None:
-        _ints(dev, "parent", parent)
+        _ints(on, "parent", parent)
         if parent.shape != (B, M):
             raise ValueError("parent must be [B, M]")
     if counts is not None:
-        _ints(dev, "counts", counts)
+        _ints(on, "counts", counts)
         if counts.shape != (B,):
             raise ValueError("counts must be [B]")
-    _kv_scale(dev, k_scale, v_scale)
-    stride = _kv_rows(q, shape, dev, "q")
+    _kv_scale(on, k_scale, v_scale)
+    stride = _kv_rows(q, shape, on, "q")
     dt, W = _dt(q.dtype), entries[1]
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+    elif out.shape != shape or out.dtype != q.dtype or out.get_device() != on or not out.is_contiguous():
         raise ValueError("out must be a contiguous [B, M, Hq, D] of q's dtype on its GPU")
-    lse = torch.empty((B, M, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    lse = k_scale.new_empty((B, M, Hq)) if want_lse else None
     lib = load()
     if workspace is None:
-        if dev.index == torch.cuda.current_device():
+        if on == _current_device():
             need = lib.nvfp4_kv_attention_workspace_bytes(B, M, Hq, H, D, page, W, dt)
         else:
-            with torch.cuda.device(dev):
+            with torch.cuda.device(on):
                 need = lib.nvfp4_kv_attention_workspace_bytes(B, M, Hq, H, D, page, W, dt)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        workspace = k_pages.new_empty((need,)) if need else None
+    elif workspace.dtype is not _U8 or workspace.get_device() != on or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
-    _call(dev, "nvfp4_kv_attention", lib.nvfp4_kv_attention, B, M, Hq, H, D, page, P, W, q.data_ptr(), dt, stride,
+    _call(on, "nvfp4_kv_attention", lib.nvfp4_kv_attention, B, M, Hq, H, D, page, P, W, q.data_ptr(), dt, stride,
           1.0 / math.sqrt(D) if sm_scale is None else sm_scale, k_scale.data_ptr(), v_scale.data_ptr(),
           k_pages.data_ptr(), v_pages.data_ptr(), page_stride, table.data_ptr(), lens.data_ptr(),
           parent.data_ptr() if parent is not None else None, counts.data_ptr() if counts is not None else None,
@@ -637,19 +642,19 @@ def nvfp4_kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.
     """Moves the accepted path of each sequence's tree to the front in all layers of pages [L, P, H,
     page_size, D]; result int32 [B, 3 + M]: rows of nvfp4_tree_accept / nvfp4_tree_verify.  Returns
     new_lens int32 [B] = lens + 1 + accepted (a tensor of its own: lens is not changed)."""
-    dev, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    on, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
     entries, paths = table.shape, result.shape
     if len(entries) != 2 or len(paths) != 2 or lens.shape != entries[:1] or paths[0] != entries[0]:
         raise ValueError("table [B, W], lens [B] and result [B, 3 + M] do not fit together")
     B, W = entries
-    _ints(dev, "table, lens and result", table, lens, result)
+    _ints(on, "table, lens and result", table, lens, result)
     if new_lens is None:
         new_lens = torch.empty_like(lens)
     else:
-        _ints(dev, "new_lens", new_lens)
+        _ints(on, "new_lens", new_lens)
         if new_lens.shape != lens.shape:
             raise ValueError("new_lens must be [B]")
-    _call(dev, "nvfp4_kv_compact", load().nvfp4_kv_compact, L, B, paths[1] - 3, H, D, page, P, W,
+    _call(on, "nvfp4_kv_compact", load().nvfp4_kv_compact, L, B, paths[1] - 3, H, D, page, P, W,
           k_pages.data_ptr(), v_pages.data_ptr(), layer_stride, page_stride, table.data_ptr(),
           lens.data_ptr(), result.data_ptr(), new_lens.data_ptr())
     return new_lens
@@ -664,15 +669,25 @@ def kv_pool(seqs: int, width: int, pages: int, dev) -> Tuple[torch.Tensor, torch
     return table, held, refs, torch.arange(pages, -1, -1, dtype=torch.int32, device=dev)
 
 
-def _pool(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor) -> torch.device:
-    dev = table.device
-    if dev.type != "cuda":
+def _pool(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor,
+          free_list: torch.Tensor) -> Tuple[int, int, int, int]:
+    """Checks a pool; returns its GPU, sequences, width and pages."""
+    on, shape, seqs, pages = table.get_device(), table.shape, held.shape, refs.shape
+    if on < 0:
         raise ValueError("the page pool must be on a GPU")
-    _ints(dev, "table, held, refs and free_list", table, held, refs, free_list)
-    if table.dim() != 2 or held.shape != (table.shape[0],) or refs.dim() != 1 or \
-            free_list.shape != (refs.shape[0] + 1,):
+    _ints(on, "table, held, refs and free_list", table, held, refs, free_list)
+    if len(shape) != 2 or seqs != shape[:1] or len(pages) != 1 or free_list.shape != (pages[0] + 1,):
         raise ValueError("table [S, W], held [S], refs [P] and free_list [1 + P] do not fit together")
-    return dev
+    return on, shape[0], shape[1], pages[0]
+
+
+def _shortage(on: int, shortage: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
+    if shortage is None:
+        return like.new_empty((1,))
+    _ints(on, "shortage", shortage)
+    if shortage.numel() != 1:
+        raise ValueError("shortage must have one element")
+    return shortage
 
 
 def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor,
@@ -680,18 +695,13 @@ def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor,
                     shortage: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Lets each sequence of seqs int32 [n] hold the pages of tokens int32 [n] tokens (0 frees it).
     Returns shortage int32 [1]: 0, or how many pages were missing (then nothing is changed)."""
-    dev = _pool(table, held, refs, free_list)
-    _ints(dev, "seqs and tokens", seqs, tokens)
-    if seqs.dim() != 1 or tokens.shape != seqs.shape:
+    on, S, W, P = _pool(table, held, refs, free_list)
+    _ints(on, "seqs and tokens", seqs, tokens)
+    entries = seqs.shape
+    if len(entries) != 1 or tokens.shape != entries:
         raise ValueError("seqs and tokens must be [n]")
-    if shortage is None:
-        shortage = torch.empty((1,), dtype=torch.int32, device=dev)
-    else:
-        _ints(dev, "shortage", shortage)
-        if shortage.numel() != 1:
-            raise ValueError("shortage must have one element")
-    S, W = table.shape
-    _call(dev, "nvfp4_kv_resize", load().nvfp4_kv_resize, seqs.shape[0], S, W, refs.shape[0], page_size,
+    shortage = _shortage(on, shortage, table)
+    _call(on, "nvfp4_kv_resize", load().nvfp4_kv_resize, entries[0], S, W, P, page_size,
           table.data_ptr(), held.data_ptr(), refs.data_ptr(), free_list.data_ptr(), seqs.data_ptr(),
           tokens.data_ptr(), shortage.data_ptr())
     return shortage
@@ -703,23 +713,18 @@ def nvfp4_kv_fork(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, f
     """Sequence dst[i] becomes the first tokens[i] tokens of src[i] (int32 [n] each): whole pages are
     shared, a partial one is copied in all layers of pages [L, P, H, page_size, D], what dst held is
     given up.  Returns shortage as nvfp4_kv_resize."""
-    dev = _pool(table, held, refs, free_list)
-    on, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
-    if on != dev or P != refs.shape[0]:
+    on, S, W, pages = _pool(table, held, refs, free_list)
+    at, (L, P, H, page, D), layer_stride, page_stride = _kv_pages(k_pages, v_pages, 5)
+    if at != on or P != pages:
         raise ValueError("pages must be [L, P, H, page_size, D] of the pool's P pages, on its GPU")
-    _ints(dev, "src, dst and tokens", src, dst, tokens)
-    if src.dim() != 1 or dst.shape != src.shape or tokens.shape != src.shape:
+    _ints(on, "src, dst and tokens", src, dst, tokens)
+    entries = src.shape
+    if len(entries) != 1 or dst.shape != entries or tokens.shape != entries:
         raise ValueError("src, dst and tokens must be [n]")
-    if shortage is None:
-        shortage = torch.empty((1,), dtype=torch.int32, device=dev)
-    else:
-        _ints(dev, "shortage", shortage)
-        if shortage.numel() != 1:
-            raise ValueError("shortage must have one element")
-    S, W = table.shape
-    n = src.shape[0]
-    moves = torch.empty((3 * n,), dtype=torch.int32, device=dev)
-    _call(dev, "nvfp4_kv_fork", load().nvfp4_kv_fork, n, S, W, P, page, table.data_ptr(), held.data_ptr(),
+    shortage = _shortage(on, shortage, table)
+    n = entries[0]
+    moves = table.new_empty((3 * n,))
+    _call(on, "nvfp4_kv_fork", load().nvfp4_kv_fork, n, S, W, P, page, table.data_ptr(), held.data_ptr(),
           refs.data_ptr(), free_list.data_ptr(), src.data_ptr(), dst.data_ptr(), tokens.data_ptr(),
           shortage.data_ptr(), moves.data_ptr(), L, H, D, k_pages.data_ptr(), v_pages.data_ptr(), layer_stride,
           page_stride)
