@@ -827,7 +827,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_at
 }
 
 // Joins the partial sums of the items that a range boundary cut: block (item,
-// or boundary, whichever are fewer; four rows), a wave a row.
+// or boundary, whichever are fewer; four rows, and every fourth of gridDim.y
+// further ones), a wave a row.
 template <int D, bool F32, bool BY_ITEM>
 __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan) {
   const int R = plan.rows;
@@ -868,68 +869,70 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
   // the boundary behind the item's first range joins it, if that range does not hold the item
   if (g0 == g1 || (!BY_ITEM && g0 != boundary - 1)) return;
 
-  const int row = blockIdx.y * 4 + wave, grow = x.row0 + row, rows_all = a.nodes * a.group;
-  if (grow >= rows_all) return;
+  const int rows_all = a.nodes * a.group;
   const float* ml = plan.part + (uint64_t)2 * plan.groups * R * D;
   constexpr int N = D / 64;  // values of a lane
   typedef float vec_t __attribute__((ext_vector_type(N)));
-  float low = kStart, sum = 0.0f;
-  vec_t acc = (vec_t)0.0f;
-  for (int base = g0; base <= g1; base += 64) {
-    // the statistics of up to 64 partial sums, a lane each
-    float lift = kStart, l = 0.0f;
-    if (base + lane <= g1) {
-      const int g = base + lane;
-      const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
-      lift = y.x;
-      l = y.y;
+  for (int row = blockIdx.y * 4 + wave; row < R && x.row0 + row < rows_all; row += 4 * gridDim.y) {
+    const int grow = x.row0 + row;
+    float low = kStart, sum = 0.0f;
+    vec_t acc = (vec_t)0.0f;
+    for (int base = g0; base <= g1; base += 64) {
+      // the statistics of up to 64 partial sums, a lane each
+      float lift = kStart, l = 0.0f;
+      if (base + lane <= g1) {
+        const int g = base + lane;
+        const f2_t y = *reinterpret_cast<const f2_t*>(ml + ((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * 2);
+        lift = y.x;
+        l = y.y;
+      }
+      const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
+      float f = 0.0f;
+      // `fly` sums at a time; their weights are worked out while the first ones arrive
+      auto add = [&](auto fly, int k) {
+        constexpr int FLY = decltype(fly)::value;
+        vec_t y[FLY];
+#pragma unroll
+        for (int u = 0; u < FLY; ++u) {
+          const int g = base + (k + u < many ? k + u : k);
+          y[u] = *reinterpret_cast<const vec_t*>(
+              plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane);
+        }
+        if (k == 0) {
+          float lowest = lift;
+          for (int off = 32; off > 0; off >>= 1) lowest = __builtin_fminf(lowest, __shfl_xor(lowest, off));
+          lowest = __builtin_fminf(lowest, low);
+          const float old = __builtin_amdgcn_exp2f(lowest - low);
+          f = __builtin_amdgcn_exp2f(lowest - lift);
+          sum = sum * old + f * l;
+          acc *= old;
+          low = lowest;
+        }
+#pragma unroll
+        for (int u = 0; u < FLY; ++u) {
+          const int from = k + u < many ? k + u : 0;
+          const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), from));
+          acc += (k + u < many ? w : 0.0f) * y[u];
+        }
+      };
+      int k = 0;
+      for (; k + 16 <= many; k += 16) add(std::integral_constant<int, 16>{}, k);
+      for (; k < many; k += 4) add(std::integral_constant<int, 4>{}, k);
     }
-    const int many = g1 - base + 1 < 64 ? g1 - base + 1 : 64;
-    float f = 0.0f;
-    // `fly` sums at a time; their weights are worked out while the first ones arrive
-    auto add = [&](auto fly, int k) {
-      constexpr int FLY = decltype(fly)::value;
-      vec_t y[FLY];
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    const int node = node_of(plan, grow);
+    const bool live = node < x.count && sum != 0.0f;
+    const float scale = live ? *a.v_scale / sum : 0.0f;
+    const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
 #pragma unroll
-      for (int u = 0; u < FLY; ++u) {
-        const int g = base + (k + u < many ? k + u : k);
-        y[u] = *reinterpret_cast<const vec_t*>(
-            plan.part + (uint64_t)((uint32_t)(2 * g + (g == g0 ? 1 : 0)) * R + row) * D + N * lane);
-      }
-      if (k == 0) {
-        float lowest = lift;
-        for (int off = 32; off > 0; off >>= 1) lowest = __builtin_fminf(lowest, __shfl_xor(lowest, off));
-        lowest = __builtin_fminf(lowest, low);
-        const float old = __builtin_amdgcn_exp2f(lowest - low);
-        f = __builtin_amdgcn_exp2f(lowest - lift);
-        sum = sum * old + f * l;
-        acc *= old;
-        low = lowest;
-      }
-#pragma unroll
-      for (int u = 0; u < FLY; ++u) {
-        const int from = k + u < many ? k + u : 0;
-        const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), from));
-        acc += (k + u < many ? w : 0.0f) * y[u];
-      }
-    };
-    int k = 0;
-    for (; k + 16 <= many; k += 16) add(std::integral_constant<int, 16>{}, k);
-    for (; k < many; k += 4) add(std::integral_constant<int, 4>{}, k);
+    for (int i = 0; i < N; ++i) {
+      const float y = live ? acc[i] * scale : 0.0f;
+      if constexpr (F32) static_cast<float*>(a.out)[orow * D + N * lane + i] = y;
+      else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
+    }
+    if (a.lse && lane == 0)
+      a.lse[orow] = live ? (__builtin_log2f(sum) - low) * 0.69314718055994530942f : -__builtin_inff();
   }
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  const int node = node_of(plan, grow);
-  const bool live = node < x.count && sum != 0.0f;
-  const float scale = live ? *a.v_scale / sum : 0.0f;
-  const int64_t orow = ((int64_t)x.b * a.nodes + node) * (a.c.heads * a.group) + h * a.group + (grow - node * a.group);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = live ? acc[i] * scale : 0.0f;
-    if constexpr (F32) static_cast<float*>(a.out)[orow * D + N * lane + i] = y;
-    else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
-  }
-  if (a.lse && lane == 0)
-    a.lse[orow] = live ? (__builtin_log2f(sum) - low) * 0.69314718055994530942f : -__builtin_inff();
 }
 
 int compute_units() {
@@ -990,10 +993,11 @@ hipError_t launch_one(const KvAttentionArgs& a, const Plan& p, hipStream_t strea
   kv_attention_kernel<D, RT, RG, F32><<<(unsigned)(p.groups ? p.groups : items), 64 * kWaves, 0, stream>>>(a, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups < 2) return e;
-  if (items < p.groups)
-    kv_attention_join_kernel<D, F32, true><<<dim3((unsigned)items, p.rows / 4), 256, 0, stream>>>(a, p);
-  else
-    kv_attention_join_kernel<D, F32, false><<<dim3(p.groups - 1, p.rows / 4), 256, 0, stream>>>(a, p);
+  // more workgroups than the chip holds at once would find their item anew for each four rows
+  const int joins = items < p.groups ? (int)items : p.groups - 1;
+  const int many = (8 * compute_units() + joins - 1) / joins, y = many < p.rows / 4 ? many : p.rows / 4;
+  if (items < p.groups) kv_attention_join_kernel<D, F32, true><<<dim3(joins, y), 256, 0, stream>>>(a, p);
+  else kv_attention_join_kernel<D, F32, false><<<dim3(joins, y), 256, 0, stream>>>(a, p);
   return hipGetLastError();
 }
 
