@@ -18,14 +18,24 @@
 // down to 2^-21 of the largest, and no maximum is taken in an ordinary step.
 //
 // Work.  The rows that share a KV head (nodes x group) are packed into tiles
-// of 16; an item is RT row tiles of one (sequence, KV head).  A key tile is 128
-// tokens; the four waves of a workgroup take 32 of them each and hold all the
-// item's rows, so every cache byte is loaded and converted by one wave, once,
-// straight from memory to registers, and the loop has no barrier.  The tiles of
-// all items form one list, cut into equal ranges over a fixed grid: long and
-// short sequences of a batch share the chip evenly, and a range that cuts an
-// item leaves a partial sum (at most two per workgroup) that a second kernel
-// joins.
+// of 16.  A workgroup has 8 waves in RG groups of rows; a wave holds up to RT row
+// tiles and takes 32 tokens of a key tile of 32 * 8 / RG, which it loads straight
+// from memory to registers and converts itself, so the loop has no barrier.  An
+// item is RG * RT row tiles of one (sequence, KV head); RG is 1 where all rows
+// fit, so that every cache byte is read once, and a byte is otherwise converted RG
+// times.  The items of all heads, each a set-up cost and its key tiles, form one
+// list that is cut into equal ranges over a fixed grid: long and short sequences
+// of a batch share the chip evenly, and a range that cuts an item leaves a partial
+// sum (at most two per workgroup) that a second kernel joins.
+//
+// Bounds.  One query per KV head and long sequences: the cache's bytes (64 x 8000
+// tokens, 8 heads of 128: 1.05 GB in 182 us, 5.8 TB/s).  Many rows: the vector and
+// the matrix instructions, whose times add up here (512 nodes x 40 heads of 128
+// after 23040 tokens: 245 us of 260 in this kernel, 0.98 PFLOP/s with the second
+// kernel's 16 us; matrix units 48% busy, vector instructions 60%).  One tree or a
+// few sequences: the set-up (4.5 us until the first product), 1 us per row tile
+// to join the waves, and the second kernel (16 nodes x 40 heads after 23552
+// tokens: 23 + 5 us, of which the cache's 48 MB are 10).
 //
 // Operands.  Scores are computed transposed (A = keys, B = queries), 16x16x32
 // bf16: E4M3 is exact in bf16, and so is a bf16 query.  The result has a
@@ -539,13 +549,15 @@ __device__ __forceinline__ void accumulate(const KeyTile<D>& kt, int n, const h8
   }
 }
 
-// Waves per SIMD that the registers are limited for (256 at two: the matrix
-// instructions then keep their sums in ordinary registers).
-constexpr int waves_per_simd(int dim, int rt, bool f32) { return rt * dim <= 128 && !f32 ? 4 : 2; }
+// One workgroup a CU, two waves a SIMD: with up to 256 registers the matrix
+// instructions keep their sums in ordinary ones.  The kernels of one row tile fit
+// in half, but two workgroups a CU are slower (64 x 8000 tokens, 8 queries a head:
+// 194 us against 191; 16 trees of 16 over 8000: 60.9 against 57.8).
+constexpr int kWavesPerSimd = 2;
 
 template <int D, int RT, int RG, bool F32>
-__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT, F32)) void kv_attention_kernel(KvAttentionArgs a,
-                                                                                              Plan plan) {
+__global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kernel(KvAttentionArgs a,
+                                                                                          Plan plan) {
   constexpr int R = 16 * RT * RG, KS = D / 32, NT = D / 16, KW = kWaves / RG, TILE = 32 * KW;
   __shared__ Smem<D, RT, RG, F32> sm;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -947,26 +959,39 @@ int compute_units() {
   return cus[dev];
 }
 
-// A wave holds up to `most` row tiles (a tile's sums take D / 4 registers); the
-// waves of a workgroup are shared out over 1, 2 or 4 groups of rows, the fewest
-// that hold all rows, and only rows beyond that take a further item, which
-// reads the cache again.
+// A wave holds up to `most` row tiles (a tile's sums take D / 4 registers; fewer
+// convert each byte for fewer rows: with 3, 4 and 1 for dimensions 128, 64 and 256
+// a 512-node suffix takes 297 us instead of 275, 32 trees of 96 rows of 256 379
+// instead of 265).  More rows than that take
+//   up to 2 `most`: two groups of rows in a workgroup, which share the key tile
+//     (32 trees of 80 rows after 8000 tokens of 8 x 128: 150 us; as two items, each
+//     of which reads the cache, 203; one tree after 23552 27.6 and 28.1);
+//   up to 4 `most`: further items, as long as the cache that is read again is one
+//     that the Infinity Cache holds (one tree of 96 rows after 8000 tokens of 4 x
+//     256, 16 MB: 25.9 us; as four groups, whose partial sums have four times the
+//     rows, 31.8; 32 of those trees, 524 MB: 292 and 265);
+//   beyond: four groups and further items (1024-token prompt 58 us; one group 62).
 constexpr int most_row_tiles(int dim, bool f32) {
   return f32 ? (dim == 256 ? 1 : 2) : dim == 64 ? 6 : dim == 128 ? 4 : 2;
 }
 
+constexpr int64_t kCached = 256ll << 20;
+
 void row_split(const KvAttentionArgs& a, int* rt, int* rg, int* row_items) {
   const int most = most_row_tiles(a.c.dim, !a.bf16);
   const int all = (int)(((int64_t)a.nodes * a.group + 15) / 16);
-  *rg = all <= most ? 1 : all <= 2 * most ? 2 : 4;
+  const int64_t cache = 2 * ((int64_t)a.c.seqs * a.c.heads * a.c.dim) * ((int64_t)a.c.width << a.c.page_shift);
+  *rg = all <= most ? 1 : all <= 2 * most ? 2 : all <= 4 * most && cache <= kCached ? 1 : 4;
   *row_items = (all + *rg * most - 1) / (*rg * most);
   *rt = (all + *row_items * *rg - 1) / (*row_items * *rg);
 }
 
-// Sequences of up to kWhole tiles are not split: the join costs more.
+// Where no sequence can have more than kWhole tiles, none is split: the second
+// kernel costs more (one token after 511, 8 heads of 128: 9.9 us split, 7.6 us
+// whole).  An item's set-up counts as kStartCost tiles; with 0, 2, 4 and 8 of them
+// 16 ragged fp32 trees take 24.0, 20.7, 21.2 and 22.4 us, 32 ragged sequences of
+// one bf16 token 62.6, 62.3, 64 and 68.8 us.
 constexpr int kWhole = 4, kStartCost = 2;
-
-int groups_per_cu(int dim, int rt, bool f32) { return waves_per_simd(dim, rt, f32) * 4 / kWaves; }
 
 Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
   Plan p;
@@ -979,7 +1004,7 @@ Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {
   p.start = kStartCost;
   const int64_t tiles = ((int64_t)p.cap + p.tile - 1) / p.tile;
   const int64_t most = (int64_t)p.items * a.c.heads * (tiles + p.start);
-  const int64_t groups = (int64_t)compute_units() * groups_per_cu(a.c.dim, *rt, !a.bf16);
+  const int64_t groups = (int64_t)compute_units() * (4 * kWavesPerSimd / kWaves);
   // too short to cut, or more places than 32 bits count
   p.groups = tiles <= kWhole || most >= ((int64_t)1 << 31) ? 0 : (int)(groups < most ? groups : most);
   *bytes = (int64_t)2 * p.groups * p.rows * (a.c.dim + 2) * 4;

@@ -714,3 +714,12 @@ def test_forks_of_one_sequence_and_pages_given_up_twice():
     assert pool.resize(16, seqs, [0] * 8) == 0
     assert int(B.nvfp4_kv_resize(*t, 16, ints(seqs), ints([0] * 8))) == 0
     check_pool(t, pool)
+
+
+@pytest.mark.parametrize("D,dtype,tiles", many_rows(64, BF, [13, 24]) + many_rows(128, BF, [9, 13, 16]) +
+                         many_rows(256, BF, [5, 8]) + many_rows(64, FP, [5, 8]) + many_rows(256, FP, [3, 4]))
+def test_attention_of_many_rows_under_a_wide_table(D, dtype, tiles):
+    """A table that covers a cache of more than 256 MB, of which the sequences use little."""
+    M = (16 * tiles - 1) // 3
+    c = Case(dtype, [1150 - M, 40], M, 1, 3, D, 64, seed=D + tiles, width=(1 << 30) // (2 * 2 * D * 64))
+    c.check(c.gpu())
