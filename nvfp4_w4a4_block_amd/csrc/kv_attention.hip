@@ -943,7 +943,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
     for (int i = 0; i < N; ++i) {
       const float y = live ? acc[i] * scale : 0.0f;
       if constexpr (F32) static_cast<float*>(a.out)[orow * D + N * lane + i] = y;
-      else static_cast<uint16_t*>(a.out)[orow * D + N * lane + i] = f32_to_bf16_rne(y);
+      else static_cast<__bf16*>(a.out)[orow * D + N * lane + i] = (__bf16)y;  // nearest even, NaN stays NaN
     }
     if (a.lse && lane == 0)
       a.lse[orow] = live ? (__builtin_log2f(sum) - low) * 0.69314718055994530942f : -__builtin_inff();

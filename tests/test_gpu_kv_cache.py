@@ -723,3 +723,23 @@ def test_attention_of_many_rows_under_a_wide_table(D, dtype, tiles):
     M = (16 * tiles - 1) // 3
     c = Case(dtype, [1150 - M, 40], M, 1, 3, D, 64, seed=D + tiles, width=(1 << 30) // (2 * 2 * D * 64))
     c.check(c.gpu())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_nans_reach_their_rows_through_split_sequences(dtype):
+    """NaN codes in a long prefix (every row sees them) and in one node, and a NaN with payload in a query."""
+    c = Case(dtype, [3000, 2000], 5, 2, 2, 128, 64, tree=False, seed=41)
+    clean_out, clean_lse = [x.float().cpu().numpy() for x in c.gpu()]
+    p, s = c.table[0, 1700 // 64], 1700 % 64
+    c.v[p, 0, s, 100] = 0x7F
+    p, s = c.table[1, 2003 // 64], 2003 % 64
+    c.k[p, 1, s, 127] = 0xFF
+    q = c.q.clone()
+    raw = q.view(torch.int16 if dtype == BF else torch.int32)
+    raw[0, 2, 3, 5] = 0x7FFF if dtype == BF else 0x7FFFFFFF
+    out, lse = [x.float().cpu().numpy() for x in c.gpu(q=q)]
+    clean_out[0, :, :2, 100] = np.nan
+    clean_out[1, 3:, 2:], clean_lse[1, 3:, 2:] = np.nan, np.nan
+    clean_out[0, 2, 3], clean_lse[0, 2, 3] = np.nan, np.nan
+    np.testing.assert_array_equal(out, clean_out)
+    np.testing.assert_array_equal(lse, clean_lse)
