@@ -56,7 +56,7 @@ typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;              // waves of a workgroup
-constexpr float kStart = 1e30f;        // lift before the first score
+constexpr float kStart = 1e38f;        // lift before the first score
 constexpr float kLift = 7.0f;          // lift is kLift less the running maximum
 constexpr float kMost = 32768.0f;      // a lane's eight p sum up to no more, so each fits f16
 

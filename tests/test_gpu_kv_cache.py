@@ -743,3 +743,16 @@ def test_nans_reach_their_rows_through_split_sequences(dtype):
     clean_out[0, 2, 3], clean_lse[0, 2, 3] = np.nan, np.nan
     np.testing.assert_array_equal(out, clean_out)
     np.testing.assert_array_equal(lse, clean_lse)
+
+
+def test_attention_of_scores_far_below_zero():
+    """All scores near -2.6e32: the offset follows them, the weights are those of their differences."""
+    c = Case(BF, [40], 2, 1, 2, 64, 16, seed=43)
+    c.k[:] = np.where((c.k & 0x7F) == 0x7F, c.k, 0x40)             # every seen key the same: equal scores
+    c.q, c.qf = dtype_values(np.full(c.qf.shape, -2.0 ** 110), BF)  # z = -64 * 2 * 0.0123 * 2^110 / 8
+    out, lse = c.gpu()
+    ref, ref_lse, size = C.attention(c.qf, c.k, c.v, KS, VS, c.table, c.lens)
+    # equal scores give equal weights exactly; what is left are the f16 weights, the sums and the result's rounding
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 100 * 2.0 ** -24) * size
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() / ref_lse - 1) <= 200 * 2.0 ** -24).all()
