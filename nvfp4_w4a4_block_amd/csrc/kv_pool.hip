@@ -10,8 +10,10 @@
 // round trip and can be captured in a graph.
 //
 // One workgroup does the bookkeeping: every phase is a loop over the flattened
-// (entry, page) list with the running offsets of the entries in LDS, four places
-// a thread (their loads overlap), and the phases are separated by barriers.
+// (entry, page) list with the running offsets of the entries in LDS, one place a
+// thread and turn, and the phases are separated by barriers.  (Four places, whose
+// loads overlap, cost the usual call more than they gave the largest: 33 forks
+// 25.9 us against 22.7, 20 sequences to 23552 tokens and back 41.1 against 41.5.)
 // What bounds it is the one compute unit's rate of accesses to the counts, which
 // lie at random; a given-up page costs one of them, the atomic that takes its
 // holder off.  The one that takes the last holder off pushes the page, so the
@@ -19,7 +21,7 @@
 // land: only where a call itself gives up a page more than once could it, and
 // there the occurrences settle on the first by an atomic minimum in the page's
 // count, which is zero by then and is reset afterwards.  A step of one sequence
-// takes 5.0 us, of which the launch is about 2; 20 sequences to 23552 tokens (7360
+// takes 4.5 us, of which the launch is about 2; 20 sequences to 23552 tokens (7360
 // pages) 16, all of them back 25.  Several workgroups would need a launch, or a
 // wait for one another, between the phases.
 #include "device_common.h"
@@ -29,8 +31,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kEach = 4;                  // places of a thread: 64 apart, 256 a wave
-constexpr int kStep = kThreads * kEach;
 constexpr int kClaim = 1 << 30;           // claims lie below any count: place - kClaim
 
 __device__ __forceinline__ int load_agent(const int32_t* p) {
@@ -139,7 +139,6 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
   }
 
   // Pages taken off the list, and shared ones.
-  const int mine = 256 * wave + lane;  // a thread's places of a step: mine + 64 i
   int fresh = -1;
   if (FORK) {
     if (take) {
@@ -151,34 +150,16 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
       a.moves[3 * t + 1] = fresh;
       a.moves[3 * t + 2] = part;
     }
-    for (int x = mine; x < shares; x += kStep) {
-      int p[kEach];
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        p[i] = -1;
-        if (y < shares) {
-          const int e = entry_of(share_at, n, y);
-          p[i] = a.table[(int64_t)src[e] * W + (y - share_at[e])];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (p[i] >= 0 && p[i] < P) atomicAdd(a.refs + p[i], 1);
+    for (int x = t; x < shares; x += kThreads) {
+      const int e = entry_of(share_at, n, x);
+      const int p = a.table[(int64_t)src[e] * W + (x - share_at[e])];
+      if (p >= 0 && p < P) atomicAdd(a.refs + p, 1);
     }
   } else {
-    for (int x = mine; x < takes; x += kStep) {
-      int p[kEach];
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) p[i] = x + 64 * i < takes ? a.free_list[F - x - 64 * i] : -1;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        if (y >= takes) break;
-        const int e = entry_of(take_at, n, y);
-        a.table[(int64_t)dst[e] * W + first[e] + (y - take_at[e])] = p[i];
-        if (p[i] >= 0 && p[i] < P) store_agent(a.refs + p[i], 1);
-      }
+    for (int x = t; x < takes; x += kThreads) {
+      const int p = a.free_list[F - x], e = entry_of(take_at, n, x);
+      a.table[(int64_t)dst[e] * W + first[e] + (x - take_at[e])] = p;
+      if (p >= 0 && p < P) store_agent(a.refs + p, 1);
     }
   }
   __syncthreads();
@@ -189,85 +170,54 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
     const int e = entry_of(drop_at, n, y);
     return a.table + (int64_t)dst[e] * W + first[e] + (y - drop_at[e]);
   };
-  for (int x = mine; x < drops; x += kStep) {
-    int32_t* at[kEach];
-    int p[kEach], old[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      p[i] = -1;
-      if (x + 64 * i < drops) {
-        at[i] = place(x + 64 * i);
-        p[i] = *at[i];
-        if (p[i] < 0 || p[i] >= P) {
-          p[i] = -1;
-          *at[i] = -1;
-        }
-      }
+  for (int x = t; x < drops; x += kThreads) {
+    int32_t* at = place(x);
+    const int p = *at;
+    if (p < 0 || p >= P) {
+      *at = -1;
+    } else if (atomicSub(a.refs + p, 1) != 1) {
+      *at = -2 - p;
+      flags[0] = 1;
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) old[i] = p[i] >= 0 ? atomicSub(a.refs + p[i], 1) : 1;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (old[i] != 1) {
-        *at[i] = -2 - p[i];
-        flags[0] = 1;
-      }
   }
   __syncthreads();
   // A page that has no holder left although this place did not take the last
   // one off is given up twice: its places claim it.
   if (flags[0]) {
-    for (int x = mine; x < drops; x += kStep) {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        if (y >= drops) break;
-        const int p = -2 - *place(y);
-        if (p < 0) continue;
-        const int r = load_agent(a.refs + p);
-        if (r == 0 || r < -(kClaim >> 1)) {
-          flags[1] = 1;
-          atomicMin(a.refs + p, y - kClaim);
-        }
+    for (int x = t; x < drops; x += kThreads) {
+      const int p = -2 - *place(x);
+      if (p < 0) continue;
+      const int r = load_agent(a.refs + p);
+      if (r == 0 || r < -(kClaim >> 1)) {
+        flags[1] = 1;
+        atomicMin(a.refs + p, x - kClaim);
       }
     }
     __syncthreads();
   }
   const bool twice = flags[1] != 0;
   if (twice) {
-    for (int x = mine; x < drops; x += kStep) {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        if (y >= drops) break;
-        const int p = *place(y);
-        if (p >= 0) atomicMin(a.refs + p, y - kClaim);
-      }
+    for (int x = t; x < drops; x += kThreads) {
+      const int p = *place(x);
+      if (p >= 0) atomicMin(a.refs + p, x - kClaim);
     }
     __syncthreads();
   }
   const int top = F - takes;
   int back = 0;
-  for (int x0 = 0, turn = 0; x0 < drops; x0 += kStep, turn ^= 1) {
-    int p[kEach];
-    uint64_t own[kEach];
-    int many = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int y = x0 + mine + 64 * i;
-      bool push = false;
-      p[i] = -1;
-      if (y < drops) {
-        int32_t* at = place(y);
-        const int v = *at;
-        p[i] = v < -1 ? -2 - v : v;
-        push = twice ? p[i] >= 0 && load_agent(a.refs + p[i]) == y - kClaim : v >= 0;
-        *at = -1;
-      }
-      own[i] = __ballot(push);
-      many += __popcll(own[i]);
+  for (int x0 = 0, turn = 0; x0 < drops; x0 += kThreads, turn ^= 1) {
+    const int x = x0 + t;
+    bool push = false;
+    int p = -1;
+    if (x < drops) {
+      int32_t* at = place(x);
+      const int v = *at;
+      p = v < -1 ? -2 - v : v;
+      push = twice ? p >= 0 && load_agent(a.refs + p) == x - kClaim : v >= 0;
+      *at = -1;
     }
-    if (lane == 0) counts[turn][wave] = many;
+    const uint64_t own = __ballot(push);
+    if (lane == 0) counts[turn][wave] = __popcll(own);
     __syncthreads();
     int rank = back;
     for (int w = 0; w < kWaves; ++w) {
@@ -275,32 +225,18 @@ __global__ __launch_bounds__(kThreads) void kv_pool_kernel(KvPoolArgs a) {
       rank += w < wave ? c : 0;
       back += c;
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if ((own[i] >> lane) & 1) {
-        const int r = top + rank + 1 + __popcll(own[i] & ((1ull << lane) - 1));
-        if (r <= P) a.free_list[r] = p[i];
-        if (twice) store_agent(a.refs + p[i], 0);
-      }
-      rank += __popcll(own[i]);
+    if (push) {
+      const int r = top + rank + 1 + __popcll(own & ((1ull << lane) - 1));
+      if (r <= P) a.free_list[r] = p;
+      if (twice) store_agent(a.refs + p, 0);
     }
   }
   __syncthreads();
 
   if (FORK) {
-    for (int x = mine; x < shares; x += kStep) {
-      int p[kEach], e[kEach];
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        e[i] = y < shares ? entry_of(share_at, n, y) : 0;
-        p[i] = y < shares ? a.table[(int64_t)src[e[i]] * W + (y - share_at[e[i]])] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int y = x + 64 * i;
-        if (y < shares) a.table[(int64_t)dst[e[i]] * W + (y - share_at[e[i]])] = p[i];
-      }
+    for (int x = t; x < shares; x += kThreads) {
+      const int e = entry_of(share_at, n, x), at = x - share_at[e];
+      a.table[(int64_t)dst[e] * W + at] = a.table[(int64_t)src[e] * W + at];
     }
     if (take) a.table[(int64_t)d * W + full] = fresh;
   }
