@@ -534,11 +534,15 @@ def _kv_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, dim: int) -> Tuple[i
     on = k_pages.get_device()
     if k_pages.dtype is not _U8 or v_pages.dtype is not _U8 or on < 0 or v_pages.get_device() != on:
         raise ValueError("pages must be uint8 tensors on one GPU")
-    st, shape = k_pages.stride(), k_pages.shape
-    if len(shape) != dim or shape != v_pages.shape or st != v_pages.stride():
+    shape = k_pages.shape
+    dense = k_pages.is_contiguous() and v_pages.is_contiguous()
+    if len(shape) != dim or shape != v_pages.shape or not (dense or k_pages.stride() == v_pages.stride()):
         raise ValueError("k_pages and v_pages must have the same shape "
                          + ("[L, P, H, page_size, D]" if dim == 5 else "[P, H, page_size, D]") + " and strides")
     P, H, page, D = shape[-4:]
+    if dense:
+        return on, shape, P * H * page * D if dim == 5 and shape[0] > 1 else 0, H * page * D
+    st = k_pages.stride()
     if (st[-1] != 1 and D > 1) or (st[-2] != D and page > 1) or (st[-3] != page * D and H > 1):
         raise ValueError("a page must be contiguous [H, page_size, D]")
     return on, shape, st[0] if dim == 5 and shape[0] > 1 else 0, st[-4] if P > 1 else H * page * D
@@ -549,9 +553,9 @@ def _kv_rows(x: torch.Tensor, shape: torch.Size, on: int, name: str) -> int:
     if x.get_device() != on:
         raise ValueError(f"{name} must be on cuda:{on}")
     B, M, H, D = shape
-    sb, sm, sh, sd = x.stride()
-    if B == 0 or M == 0:
+    if x.is_contiguous():
         return H * D
+    sb, sm, sh, sd = x.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the rows of {name} must be contiguous [heads, D]")
     row = sm if M > 1 else sb if B > 1 else H * D

@@ -31,7 +31,7 @@
 // Bounds.  One query per KV head and long sequences: the cache's bytes (64 x 8000
 // tokens, 8 heads of 128: 1.05 GB in 182 us, 5.8 TB/s).  Many rows: the vector and
 // the matrix instructions, whose times add up here (512 nodes x 40 heads of 128
-// after 23040 tokens: 257 us with the second kernel's 16, 0.95 PFLOP/s; matrix
+// after 23040 tokens: 249 us with the second kernel's 16, 0.98 PFLOP/s; matrix
 // units 48% busy, vector instructions 60%).  One tree or a
 // few sequences: the set-up (4.5 us until the first product), 1 us per row tile
 // to join the waves, and the second kernel (16 nodes x 40 heads after 23552
