@@ -54,7 +54,8 @@
  *     NULL pointers, then alignment.
  *   - Results are bit-identical from run to run (fixed reduction orders, no
  *     floating-point atomics on results).
- *   - Non-finite inputs are outside the contract.
+ *   - Non-finite inputs are outside the contract, but where a call states what
+ *     becomes of them (the FP8 KV cache).
  *   - Calls are re-entrant; calls on different streams may run concurrently
  *     as long as they do not write the same buffers.
  */
@@ -314,8 +315,9 @@ nvfp4_status nvfp4_quantize_gemm_dynamic(int64_t M, int64_t K, int64_t N,
  *          calibration sets s = amax / 448).
  *   q      out: [n] E4M3FN bytes.
  * Per element, in correctly rounded fp32: inv = (s == 0) ? 0 : 1 / s,
- * y = x * inv, q = E4M3(y) rounded to nearest even, saturating at +-448, with
- * the sign bit of y.  n < 2^40; x and q 16-byte aligned.
+ * y = x * inv, q = E4M3(y) rounded to nearest even, saturating at +-448
+ * (infinities too), with the sign bit of y; a NaN y gives a NaN code (0x7F or
+ * 0xFF), which the decoder turns into NaN.  n < 2^40; x and q 16-byte aligned.
  * Cites: the page section "Using NVFP4 quantization to accelerate
  * Qwen3.6-27B inference" (the KV cache is FP8). */
 nvfp4_status nvfp4_kv_fp8_encode(const void* x, nvfp4_dtype x_dt, int64_t n, const float* scale, uint8_t* q,
@@ -405,7 +407,7 @@ nvfp4_status nvfp4_tree_verify(int64_t M, int64_t K, int64_t N,
 /* Writes a step's keys and values into the cache.
  *   k, v     [B * M] rows of H * D values in dt, device.
  *   k_scale, v_scale  device floats; the bytes are those of
- *            nvfp4_kv_fp8_encode with that scale.
+ *            nvfp4_kv_fp8_encode with that scale, NaN codes included.
  * Node v of sequence b is written at token lens[b] + v of one layer's pages;
  * lens is not changed.  Two sequences that share a page must not both append
  * to it, nor both compact in it (nvfp4_kv_fork gives each its own partial

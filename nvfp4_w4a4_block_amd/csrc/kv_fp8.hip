@@ -6,38 +6,19 @@
 // NVFP4 weights and activations.  Here: E4M3FN with one static fp32 decode
 // scale s per tensor.  Encode: inv = fl32(1/s) (0 when s == 0), y =
 // fl32(x * inv), code = E4M3 of y rounded to nearest even, saturating at 448,
-// sign bit of y.  Decode: fl32(e4m3(code) * s), as fp32 or rounded to bf16.
+// sign bit of y; a NaN y gives a NaN code.  Decode: fl32(e4m3(code) * s), as
+// fp32 or rounded to bf16.
 // Both kernels stream: 16 elements per thread per chunk, a few chunks' loads
 // in flight per thread, a guarded tail for n % 16.  The streams are read once:
 // their loads carry the non-temporal hint (measured 7% faster encode, 12%
 // faster decode; the same hint on the stores made the decode slower).
 #pragma clang fp contract(off)
 #include "device_common.h"
+#include "kv_codec.h"
 #include "launch.h"
 
 namespace nvfp4 {
 namespace {
-
-
-__device__ __forceinline__ uint32_t encode_e4m3_signed(float y) {
-  return e4m3_from_nonneg(__builtin_fabsf(y)) | ((__float_as_uint(y) >> 24) & 0x80u);
-}
-
-// Four values -> four E4M3 bytes (value i in byte i) with the hardware
-// conversion after clamping to +-448.  On gfx950 this equals
-// encode_e4m3_signed for every finite input (checked on 50M inputs: every
-// E4M3 midpoint and its float32 neighbours, subnormals, signed zeros and
-// saturating values): round to nearest even, and the clamp supplies the
-// saturation that the conversion alone would turn into NaN.
-__device__ __forceinline__ uint32_t encode4_e4m3(float a, float b, float c, float d) {
-  const float lo = -448.0f, hi = 448.0f;
-  a = __builtin_fminf(__builtin_fmaxf(a, lo), hi);
-  b = __builtin_fminf(__builtin_fmaxf(b, lo), hi);
-  c = __builtin_fminf(__builtin_fmaxf(c, lo), hi);
-  d = __builtin_fminf(__builtin_fmaxf(d, lo), hi);
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-}
 
 template <bool BF16>
 __device__ __forceinline__ void load16(const void* x, int64_t c, float* v) {
@@ -85,13 +66,13 @@ __global__ __launch_bounds__(256) void kv_encode_kernel(const void* x, int64_t n
         u4_t w;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = encode4_e4m3(v[u][4 * j] * inv, v[u][4 * j + 1] * inv, v[u][4 * j + 2] * inv, v[u][4 * j + 3] * inv);
+          w[j] = e4m3x4(v[u][4 * j] * inv, v[u][4 * j + 1] * inv, v[u][4 * j + 2] * inv, v[u][4 * j + 3] * inv);
         reinterpret_cast<u4_t*>(q)[c0 + u * T] = w;
       }
     }
   }
   const int64_t i = 16 * chunks + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // tail (< 16 elements)
-  if (blockIdx.x == 0 && i < n) q[i] = (uint8_t)encode_e4m3_signed(load1<BF16>(x, i) * inv);
+  if (blockIdx.x == 0 && i < n) q[i] = (uint8_t)e4m3x4(load1<BF16>(x, i) * inv, 0.0f, 0.0f, 0.0f);
 }
 
 template <bool BF16>

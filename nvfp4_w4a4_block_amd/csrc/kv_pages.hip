@@ -9,6 +9,7 @@
 // path is accepted moves the path's tokens to the front (kv_compact_kernel).
 #pragma clang fp contract(off)
 #include "device_common.h"
+#include "kv_codec.h"
 #include "kv_launch.h"
 
 namespace nvfp4 {
@@ -25,18 +26,6 @@ __device__ __forceinline__ uint8_t* token_row(uint8_t* base, const KvCache& c, i
   if (page < 0 || page >= c.pages) return nullptr;
   const int slot = pos & ((1 << c.page_shift) - 1);
   return base + page * c.page_stride + (((int64_t)head << c.page_shift) + slot) * c.dim;
-}
-
-// Four values -> four E4M3 bytes: the hardware conversion rounds to nearest
-// even, and the clamp to +-448 gives the codec's saturation.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const float lo = -kE4M3Max, hi = kE4M3Max;
-  a = __builtin_fminf(__builtin_fmaxf(a, lo), hi);
-  b = __builtin_fminf(__builtin_fmaxf(b, lo), hi);
-  c = __builtin_fminf(__builtin_fmaxf(c, lo), hi);
-  d = __builtin_fminf(__builtin_fmaxf(d, lo), hi);
-  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 // q = E4M3(x * (1 / s)) of every node's keys and values, 16 elements per

@@ -10,8 +10,8 @@ here is the plainest one, in the same style as the NVFP4 quantizer of this packa
 * one static, calibrated fp32 decode scale s per KV tensor, supplied by the caller (a calibration
   sets s = fl32(amax / 448) so the largest cached value lands on the largest code);
 * encode, per element in correctly rounded float32:  inv = (s == 0) ? 0 : fl32(1 / s),
-  y = fl32(x * inv),  q = E4M3(y) rounded to nearest even, saturating at +-448, with the sign
-  bit of y (so -0 encodes to 0x80);
+  y = fl32(x * inv),  q = E4M3(y) rounded to nearest even, saturating at +-448 (infinities too),
+  with the sign bit of y (so -0 encodes to 0x80); a NaN y gives a NaN code (0x7F or 0xFF: here 0x7F);
 * decode: x_hat = fl32(e4m3(q) * s) as float32, optionally rounded to bfloat16 (nearest even).
 
 Pinned by tests/test_oracle_kvfp8.py: hand-worked elements (tests/golden/kv_fp8_cases.txt), exact
@@ -38,10 +38,12 @@ def encode(x, s) -> np.ndarray:
     """float32 (or bf16-valued) x -> E4M3FN bytes with decode scale s."""
     x = np.asarray(x, dtype=np.float32)
     s = np.float32(s)
-    inv = np.float32(0) if s == 0 else np.float32(np.float32(1) / s)
     with np.errstate(over="ignore"):
+        inv = np.float32(0) if s == 0 else np.float32(np.float32(1) / s)
+    with np.errstate(over="ignore", invalid="ignore"):
         y = (x * inv).astype(np.float32)       # one correctly rounded float32 product
-    return F.encode_e4m3(y)
+    nan = np.isnan(y)
+    return np.where(nan, np.uint8(0x7F), F.encode_e4m3(np.where(nan, np.float32(0), y)))
 
 
 def decode_f32(q, s) -> np.ndarray:

@@ -756,3 +756,35 @@ def test_attention_of_scores_far_below_zero():
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 100 * 2.0 ** -24) * size
     assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
     assert (np.abs(lse.double().cpu().numpy() / ref_lse - 1) <= 200 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_appended_nans_reach_the_rows_that_see_them(dtype):
+    """NaN, infinities and scales that make NaN: append stores the codec's bytes, and attention carries a
+    NaN key or value to the nodes that see it and to no other."""
+    rng = np.random.default_rng(51)
+    M, H, G, D, page = 6, 2, 2, 64, 16
+    c = Case(dtype, [20], M, H, G, D, page, seed=51)
+    x, xf = dtype_values(rng.standard_normal((2, 1, M, H, D)), dtype)
+    x[0, 0, 4, 1, 9], xf[0, 0, 4, 1, 9] = float("nan"), np.nan    # a key of node 4
+    x[1, 0, 2, 0, 3], xf[1, 0, 2, 0, 3] = float("nan"), np.nan    # a value of node 2
+    x[1, 0, 1, 1, 5], xf[1, 0, 1, 1, 5] = float("inf"), np.inf
+    x[0, 0, 0, 0, 7], xf[0, 0, 0, 0, 7] = float("-inf"), -np.inf
+    table, lens = ints(c.table), ints(c.lens)
+    for ks, vs in ((KS, VS), (np.float32(0), VS), (KS, np.float32(1e-39))):
+        pages = [torch.from_numpy(p).to(DEV) for p in (c.k, c.v)]
+        B.nvfp4_kv_append(x[0], x[1], U.scalar(ks), U.scalar(vs), *pages, table, lens)
+        for got, x1, s, p in zip(pages, xf, (ks, vs), (c.k, c.v)):
+            with np.errstate(invalid="ignore"):
+                want = C.append(x1, s, p, c.table, c.lens)
+            got = got.cpu().numpy()
+            nan = (want & 0x7F) == 0x7F
+            np.testing.assert_array_equal((got & 0x7F) == 0x7F, nan)
+            np.testing.assert_array_equal(got[~nan], want[~nan])
+    pages = [torch.from_numpy(p).to(DEV) for p in (c.k, c.v)]
+    B.nvfp4_kv_append(x[0], x[1], U.scalar(KS), U.scalar(VS), *pages, table, lens)
+    out = B.nvfp4_kv_attention(c.q, U.scalar(KS), U.scalar(VS), *pages, table, lens).float().cpu().numpy()
+    want = np.zeros((1, M, H * G, D), dtype=bool)
+    want[0, 4:, G:] = True        # head 1, from node 4 on
+    want[0, 2:, :G, 3] = True     # head 0, one dimension, from node 2 on
+    np.testing.assert_array_equal(np.isnan(out), want)

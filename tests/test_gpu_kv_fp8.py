@@ -74,3 +74,26 @@ def test_full_layer_kv():
     bits = WL.make_kv()
     x = WL.bf16_bits_to_f32(bits).reshape(-1)
     check(x, KV.calibrated_scale(x), torch.bfloat16)
+
+
+@pytest.mark.parametrize("n", [5, 16, 37, 4096 * 16 + 3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_keeps_its_place_and_infinity_saturates(n, dtype):
+    """A NaN product gets a NaN code, in whole chunks of 16 and in the tail; +-inf goes to +-448."""
+    x = np.linspace(-3, 3, n).astype(np.float32)
+    x = WL.bf16_bits_to_f32(KV.f32_to_bf16_bits(x))
+    x[1::7], x[2::7], x[3::7] = np.inf, -np.inf, -np.nan
+    x[[0, n - 1]] = np.nan
+    t = torch.from_numpy(x).to(dtype).cuda()
+    for s in (0.25, 0.0, 1e-39, np.nan):  # 1 / 1e-39 overflows: 0 * inf; a zero scale: inf * 0
+        s = np.float32(s)
+        got = U.host(B.nvfp4_kv_fp8_encode(t, U.scalar(s))).reshape(-1)
+        want = KV.encode(x, s)
+        nan = (want & 0x7F) == 0x7F
+        assert nan[[0, n - 1]].all()
+        np.testing.assert_array_equal((got & 0x7F) == 0x7F, nan)
+        np.testing.assert_array_equal(got[~nan], want[~nan])
+        q = B.nvfp4_kv_fp8_encode(t, U.scalar(s))
+        for out in (torch.float32, torch.bfloat16):
+            back = B.nvfp4_kv_fp8_decode(q, U.scalar(np.float32(1)), out)
+            np.testing.assert_array_equal(np.isnan(back.float().cpu().numpy().reshape(-1)), nan)

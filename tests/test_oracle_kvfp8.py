@@ -72,3 +72,15 @@ def test_bf16_rounding_matches_torch():
 def test_calibrated_scale():
     assert KV.calibrated_scale(np.array([0.0, -896.0, 3.0])) == np.float32(2.0)
     assert KV.calibrated_scale(np.zeros(4)) == 0
+
+
+def test_nan_gets_a_nan_code_and_infinity_saturates():
+    x = np.array([np.nan, 1.0, np.inf, -np.inf, 0.0, -np.nan], dtype=np.float32)
+    with np.errstate(invalid="ignore"):
+        assert (KV.encode(x, np.float32(1)) & 0x7F).tolist() == [0x7F, 0x38, 0x7E, 0x7E, 0, 0x7F]
+        assert (KV.encode(x, np.float32(0)) & 0x7F).tolist() == [0x7F, 0, 0x7F, 0x7F, 0, 0x7F]      # inf * 0
+        assert (KV.encode(x, np.float32(1e-39)) & 0x7F).tolist() == [0x7F, 0x7E, 0x7E, 0x7E, 0x7F, 0x7F]  # 0 * inf
+        assert ((KV.encode(x, np.float32(np.nan)) & 0x7F) == 0x7F).all()
+    assert KV.encode(x[2:4], np.float32(1)).tolist() == [0x7E, 0xFE]
+    got = KV.decode_f32(KV.encode(x[[0, 5]], np.float32(1)), np.float32(2))
+    assert np.isnan(got).all()
