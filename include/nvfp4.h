@@ -448,7 +448,9 @@ int64_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t M, int64_t Hq, int
  * bf16 calls the probabilities are rounded to f16 (11 bits) for the product
  * with the values, in fp32 calls they keep 22 bits.  Cache bytes that no row
  * sees may hold anything; a NaN code, or a NaN in a query, reaches the rows that
- * see it and no other. */
+ * see it and no other.  A k_scale that is NaN, infinite or so large that
+ * sm_scale * k_scale / ln 2 overflows gives NaN (out and lse) in every row that sees
+ * something; a NaN v_scale gives NaN in their out. */
 nvfp4_status nvfp4_kv_attention(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t P,
                                 int64_t W, const void* q, nvfp4_dtype dt, int64_t q_stride, float sm_scale,
                                 const float* k_scale, const float* v_scale, const uint8_t* k_pages,

@@ -584,7 +584,10 @@ __global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kerne
   const int kw = wave % KW;  // which 32 tokens of a tile
   const int rows_all = a.nodes * a.group;
   const float c0 = a.sm_scale * *a.k_scale * 1.44269504088896340736f;
-  const float c = __builtin_fmaxf(__builtin_fabsf(c0), 1.17549435e-38f);  // not 0: a masked score stays -infinity
+  // not 0, infinite or NaN: a masked score stays -infinity.  Where k_scale gives none, the sums of the rows that
+  // see something (theirs are not 0) become NaN.
+  const float c = __builtin_isfinite(c0) ? __builtin_fmaxf(__builtin_fabsf(c0), 1.17549435e-38f) : 1.0f;
+  const float spoil = __builtin_isfinite(c0) ? 0.0f : __builtin_nanf("");
   const bool flip = c0 < 0.0f;
   const float vs = *a.v_scale;
 
@@ -819,6 +822,7 @@ __global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kerne
         for (int n = 0; n < PER / VEC; ++n)
           y[n] += f * *reinterpret_cast<const vec_t*>(&sm.o[rg * KW + w][row16][d0 + VEC * LANES * n]);
       }
+      sum = sum == 0.0f ? 0.0f : sum + spoil;
       if (!whole) {
         const uint32_t at_row = (uint32_t)slot * R + row;
         float* to = plan.part + (uint64_t)at_row * D + d0;

@@ -788,3 +788,32 @@ def test_appended_nans_reach_the_rows_that_see_them(dtype):
     want[0, 4:, G:] = True        # head 1, from node 4 on
     want[0, 2:, :G, 3] = True     # head 0, one dimension, from node 2 on
     np.testing.assert_array_equal(np.isnan(out), want)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("split", [True, False])
+def test_scales_that_are_no_number_reach_every_row_that_sees_something(dtype, split, bad):
+    """A NaN or infinite k_scale: NaN out and lse.  A NaN v_scale: NaN out, lse as it was.  Rows that see
+    nothing (an unused sequence, nodes behind counts, a table without pages) stay zero and -infinity."""
+    c = Case(dtype, [2500, 40, -1, 30], 5, 2, 3, 64, 32, tree=True, counts=[5, 3, 5, 5], seed=53)
+    c.table[3] = -1
+    pages = [torch.from_numpy(x).to(DEV) for x in (c.k, c.v)]
+
+    def call(ks, vs):
+        ws = None if split else torch.empty(0, dtype=torch.uint8, device=DEV)
+        out, lse = B.nvfp4_kv_attention(c.q, U.scalar(np.float32(ks)), U.scalar(np.float32(vs)), *pages, ints(c.table),
+                                        ints(c.lens), parent=ints(c.parent), counts=ints(c.counts), want_lse=True,
+                                        workspace=ws)
+        return out.float().cpu().numpy(), lse.cpu().numpy()
+
+    clean = call(KS, VS)
+    sees = np.isfinite(clean[1])
+    assert sees[0].all() and sees[1, :3].all() and not sees[1, 3:].any() and not sees[2:].any()
+    out, lse = call(bad, VS)
+    assert np.isnan(out[sees]).all() and np.isnan(lse[sees]).all()
+    assert not out[~sees].any() and np.isneginf(lse[~sees]).all()
+    if np.isnan(bad):
+        out, lse = call(KS, bad)
+        assert np.isnan(out[sees]).all() and not out[~sees].any()
+        np.testing.assert_array_equal(lse, clean[1])
