@@ -15,7 +15,10 @@
 // the sum of a lane's eight p, which the softmax needs anyway, exceeds 2^15 (a
 // score is 5 to 8 above m, or more) does m move up to the maximum, the sums are
 // rescaled and the eight are taken again.  So p stays inside f16's range, normal
-// down to 2^-21 of the largest, and no maximum is taken in an ordinary step.
+// down to 2^-21 of the largest, and no maximum is taken in an ordinary step.  z +
+// lift is one fused operation, c * s unrounded, while lift holds m rounded: past
+// 2^24 that alone would move p by more than f16 has room for, so from there on z is
+// rounded as well, and the largest p is 1 to 2^8 whatever the scores are.
 //
 // Work.  The rows that share a KV head (nodes x group) are packed into tiles
 // of 16.  A workgroup has 8 waves in RG groups of rows; a wave holds up to RT row
@@ -58,6 +61,7 @@ typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 8;              // waves of a workgroup
 constexpr float kStart = 1e38f;        // lift before the first score
 constexpr float kLift = 7.0f;          // lift is kLift less the running maximum
+constexpr float kFar = 16777216.0f;    // a lift past it may be off by more than a half (2^24)
 constexpr float kMost = 32768.0f;      // a lane's eight p sum up to no more, so each fits f16
 
 struct Plan {
@@ -376,6 +380,11 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// A value that is alike in all lanes, without a vector register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // Nothing is moved across: without it the compiler converts all operands early
 // and runs out of registers.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
@@ -501,9 +510,21 @@ __device__ __forceinline__ void spread_nans(KeyTile<D>& kt, const f4_t (&z)[2][R
   }
 }
 
-// Moves the running maxima to the largest score so far.
+// Scores in exponent units, rounded (a masked one stays -infinity).
+template <int NR, int RT>
+__device__ __forceinline__ void scale(f4_t (&z)[2][RT], float c) {
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    z[0][r] *= c;
+    z[1][r] *= c;
+  }
+}
+
+// Moves the running maxima to the largest score so far; whether one of them is
+// past kFar now.
 template <int NR, int RT, int NT>
-__device__ __forceinline__ void raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc, float c) {
+__device__ __forceinline__ bool raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc, float c) {
+  bool far = false;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     float x = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(z[0][r][0], z[0][r][1]),
@@ -516,10 +537,12 @@ __device__ __forceinline__ void raise(const f4_t (&z)[2][RT], Sums<RT, NT>& acc,
     const float f = __builtin_amdgcn_exp2f(x - acc.lift[r]);
     acc.lift[r] = x;
     acc.l[r] *= f;
+    far |= __builtin_fabsf(x) > kFar && x != kStart;
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc.o[r][n] *= f;
     fence();
   }
+  return __any(far);
 }
 
 // Softmax of the scores; the lane's sums of p, by row tile, in `sum`.
@@ -715,6 +738,8 @@ __global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kerne
     // NR: the row tiles that the wave works on.
     auto walk = [&](auto nr) {
       constexpr int NR = decltype(nr)::value;
+      float cz = uniform(c);      // the factor that the scores have left
+      bool far = false;
       for (int tile = t0; tile < t1; ++tile) {
         const uint32_t more = tile + 1 < t1 ? ~0u : 0u;
         // A SIMD's two waves take turns to go first: left alone the older one does, and the younger one
@@ -740,17 +765,25 @@ __global__ __launch_bounds__(64 * kWaves, kWavesPerSimd) void kv_attention_kerne
         const Blocks next = find_blocks(a, entries, h, key0 + TILE);
         load_keys<D>(a, next, more, kt);
         entries = fetch_entries(a, pages, key0 + 2 * TILE);
-        if (tile == t0) raise<NR>(z, acc, c);
+        // Moves the maxima.  From the first one past kFar on the scores are rounded as the maxima are.
+        auto up = [&] {
+          if (!raise<NR>(z, acc, cz) || far) return;
+          scale<NR>(z, cz);
+          cz = 1.0f;
+          far = true;
+        };
+        if (far) scale<NR>(z, uniform(c));
+        if (tile == t0) up();
         h8_t ph[RT], pl[F32 ? RT : 1];
         float sum[RT];
-        weigh<NR, F32>(z, acc, c, ph, pl, sum);
+        weigh<NR, F32>(z, acc, cz, ph, pl, sum);
         float most = sum[0];
 #pragma unroll
         for (int r = 1; r < NR; ++r) most = __builtin_fmaxf(most, sum[r]);
         fence();
         if (__any(most > kMost)) {
-          raise<NR>(z, acc, c);
-          weigh<NR, F32>(z, acc, c, ph, pl, sum);
+          up();
+          weigh<NR, F32>(z, acc, cz, ph, pl, sum);
           fence();
         }
 #pragma unroll

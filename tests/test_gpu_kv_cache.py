@@ -817,3 +817,68 @@ def test_scales_that_are_no_number_reach_every_row_that_sees_something(dtype, sp
         out, lse = call(KS, bad)
         assert np.isnan(out[sees]).all() and not out[~sees].any()
         np.testing.assert_array_equal(lse, clean[1])
+
+
+def far_check(c, got, rows, sm):
+    """Rows [B, M] whose best key leads by more than the scores' rounding can hide: its value is the
+    result.  The bound: a score is off by ez (module docstring) and, on the way to the exponent, by 8 u of
+    itself; beyond that and 200 powers of two nothing else weighs in fp32.  The one weight is rounded (2^-11,
+    2^-22), then a few products."""
+    out, lse = (x.double().cpu().numpy() for x in got)
+    ref, ref_lse, _ = C.attention(c.qf, c.k, c.v, KS, VS, c.table, c.lens, c.parent, c.counts, sm)
+    u, B_, M = 2.0 ** -24, len(c.lens), c.M
+    H, page, D = c.k.shape[1:]
+    G = c.qf.shape[2] // H
+    half = torch.finfo(c.dtype).eps / 2
+    rp = 2.0 ** -11 if c.dtype == BF else 2.0 ** -22
+    for b in range(B_):
+        n = int(c.lens[b]) + M
+        at = [(int(c.table[b, t // page]), t % page) for t in range(n)]
+        line = np.tri(M, dtype=bool) if c.parent is None else C.ancestors(c.parent[b])
+        for j in range(H * G):
+            k = C.F.decode_e4m3(np.array([c.k[p, j // G, s] for p, s in at])) * float(KS)
+            for v in np.nonzero(rows[b])[0]:
+                see = np.concatenate([np.ones(n - M, dtype=bool), line[v]])
+                q = c.qf[b, v, j].astype(np.float64)
+                z = abs(sm) * (k[see] @ q) * np.sign(sm)
+                ez = (D + 12) * u * abs(sm) * (np.abs(k[see]) @ np.abs(q)).max() + 8 * u * np.abs(z).max()
+                second, first = np.sort(z)[-2:]
+                assert first - second > 2 * ez + 200, "the case does not say which key wins"
+                assert (np.abs(out[b, v, j] - ref[b, v, j]) <= (half + rp + 16 * u) * np.abs(ref[b, v, j])).all()
+                assert abs(lse[b, v, j] - ref_lse[b, v, j]) <= ez + 8 * u * abs(ref_lse[b, v, j])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sm", [1e8, -3e9, 7e13, 1.1e30])
+def test_attention_of_scores_past_the_exponents_precision(dtype, D, sm):
+    """Scores from 1e9 to 1e31, of either sign: one key takes all, and its value comes out."""
+    c = Case(dtype, [1500, 30], 5, 2, 3, D, 32, tree=True, seed=57 + D)
+    every = np.ones((2, 5), dtype=bool)
+    far_check(c, c.gpu(sm_scale=sm), every, float(np.float32(sm)))
+    far_check(c, c.gpu(sm_scale=sm, workspace=torch.empty(0, dtype=torch.uint8, device=DEV)), every,
+              float(np.float32(sm)))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_far_scores_beside_ordinary_ones(dtype, sign):
+    """Nodes whose queries are 1e9 times as large share their row tiles with ordinary ones, and the keys of
+    the first 1,400 tokens are zero: their rows' scores move from 0 to +-1e10 in the middle of the walk."""
+    c = Case(dtype, [1500, 40], 6, 1, 2, 64, 32, seed=61)
+    for t in range(1400):
+        c.k[c.table[0, t // 32], :, t % 32] = 0
+    q = c.qf.copy()
+    q[:, 1::2] *= sign * 1e9
+    c.q, c.qf = dtype_values(q, dtype)
+    got = c.gpu()
+    rows = np.zeros((2, 6), dtype=bool)
+    rows[:, 1::2] = True
+    far_check(c, got, rows, 1 / 8.0)
+    near = Case.__new__(Case)
+    near.__dict__.update(c.__dict__)
+    for b in range(2):  # the ordinary rows by themselves, under the usual bound
+        for v in range(0, 6, 2):
+            near.qf, near.M = c.qf[b:b + 1, v:v + 1], 1
+            near.lens, near.table = np.array([c.lens[b] + v]), c.table[b:b + 1]
+            near.check([x[b:b + 1, v:v + 1] for x in got])
