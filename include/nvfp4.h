@@ -409,9 +409,10 @@ nvfp4_status nvfp4_tree_verify(int64_t M, int64_t K, int64_t N,
  *   k_scale, v_scale  device floats; the bytes are those of
  *            nvfp4_kv_fp8_encode with that scale, NaN codes included.
  * Node v of sequence b is written at token lens[b] + v of one layer's pages;
- * lens is not changed.  Two sequences that share a page must not both append
- * to it, nor both compact in it (nvfp4_kv_fork gives each its own partial
- * page).  Both refuse k_pages = v_pages. */
+ * lens is not changed.  A page that more than one sequence holds must not be
+ * written by any of them, neither here nor by nvfp4_kv_compact: neither looks
+ * at the holder counts (see the page pool below for how a sequence comes to its
+ * own page).  Both refuse k_pages = v_pages. */
 nvfp4_status nvfp4_kv_append(int64_t B, int64_t M, int64_t H, int64_t D, int64_t page_size, int64_t P, int64_t W,
                              const void* k, const void* v, nvfp4_dtype dt, int64_t k_stride, int64_t v_stride,
                              const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,
@@ -480,6 +481,16 @@ nvfp4_status nvfp4_kv_compact(int64_t L, int64_t B, int64_t M, int64_t H, int64_
  *            ids whose top is free_list[F].
  * An empty pool has table -1, held 0, refs 0 and all P pages on free_list.
  *
+ * Shared pages (refs above 1) are read by all their holders and must not be
+ * written by any, the last one excepted (refs is 1 again).  nvfp4_kv_fork
+ * shares whole pages of committed tokens only, so that what either sequence
+ * appends next lies on pages of its own.  A sequence that is then cut back to a
+ * length inside a shared page, by nvfp4_kv_resize or by a smaller lens alone,
+ * must not be continued where it is: its next token would overwrite the other
+ * holders' committed ones.  Fork it at the new length to an unused sequence,
+ * which gets its own copy of the partial page, go on with that one, and free
+ * the old one (nvfp4_kv_resize to 0 tokens).
+ *
  * nvfp4_kv_resize: sequence seqs[i] holds ceil(tokens[i] / page_size) pages
  * afterwards (n <= 1024 entries): missing pages are popped from free_list in
  * the order of the entries, surplus ones are given up from the back (tokens
@@ -497,8 +508,9 @@ nvfp4_status nvfp4_kv_resize(int64_t n, int64_t S, int64_t W, int64_t P, int64_t
 /* Sequence dst[i] becomes the first tokens[i] tokens of sequence src[i]
  * (n <= 1024 entries): it shares src's whole pages, and a partial last page is
  * copied (the used slots, in all L layers) into a page popped from free_list,
- * in the order of the entries.  What dst held before is given up as in
- * nvfp4_kv_resize.  An entry is passed over if a sequence lies outside [0, S),
+ * in the order of the entries.  tokens[i] must be committed tokens of src, at
+ * most its length: a page that src has yet to fill must not be shared.  What
+ * dst held before is given up as in nvfp4_kv_resize.  An entry is passed over if a sequence lies outside [0, S),
  * an earlier entry has the same dst, its src is any entry's dst, or src holds
  * fewer than tokens[i] tokens' pages.
  *   shortage as above.   moves  workspace of 3 * n int32, device. */

@@ -568,7 +568,8 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_s
                     k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                     counts: Optional[torch.Tensor] = None) -> None:
     """Writes k and v [B, M, H, D] (float32/bfloat16; rows may be column ranges of a wider tensor) as
-    E4M3 bytes at tokens lens[b] .. lens[b] + M - 1 (counts[b] of them) of the sequences' pages."""
+    E4M3 bytes at tokens lens[b] .. lens[b] + M - 1 (counts[b] of them) of the sequences' pages, which
+    must not be shared (refs 1): a sequence cut back into a shared page goes on as a fork of itself."""
     on, (P, Hp, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
     shape, entries = k.shape, table.shape
     if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype:
@@ -697,7 +698,8 @@ def _shortage(on: int, shortage: Optional[torch.Tensor], like: torch.Tensor) -> 
 def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor,
                     page_size: int, seqs: torch.Tensor, tokens: torch.Tensor,
                     shortage: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Lets each sequence of seqs int32 [n] hold the pages of tokens int32 [n] tokens (0 frees it).
+    """Lets each sequence of seqs int32 [n] hold the pages of tokens int32 [n] tokens (0 frees it).  One
+    cut back into a page that others hold too must not be appended to: fork it to an unused one first.
     Returns shortage int32 [1]: 0, or how many pages were missing (then nothing is changed)."""
     on, S, W, P = _pool(table, held, refs, free_list)
     _ints(on, "seqs and tokens", seqs, tokens)
@@ -714,7 +716,7 @@ def nvfp4_kv_resize(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor,
 def nvfp4_kv_fork(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, free_list: torch.Tensor,
                   k_pages: torch.Tensor, v_pages: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
                   tokens: torch.Tensor, shortage: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Sequence dst[i] becomes the first tokens[i] tokens of src[i] (int32 [n] each): whole pages are
+    """Sequence dst[i] becomes the first tokens[i] committed tokens of src[i] (int32 [n] each): whole pages are
     shared, a partial one is copied in all layers of pages [L, P, H, page_size, D], what dst held is
     given up.  Returns shortage as nvfp4_kv_resize."""
     on, S, W, pages = _pool(table, held, refs, free_list)

@@ -135,6 +135,10 @@ class Pool:
         self.refs = np.zeros(pages, dtype=np.int32)
         self.free = list(range(pages - 1, -1, -1))
 
+    def writable(self, seq, page, lo, hi):
+        """Whether tokens lo .. hi - 1 of a sequence lie on pages that no other sequence holds."""
+        return all(self.refs[p] == 1 for p in self.table[seq, lo // page: -(-hi // page)] if p >= 0)
+
     def _give_up(self, pages):
         for p in pages:
             self.refs[p] -= 1

@@ -882,3 +882,49 @@ def test_far_scores_beside_ordinary_ones(dtype, sign):
             near.qf, near.M = c.qf[b:b + 1, v:v + 1], 1
             near.lens, near.table = np.array([c.lens[b] + v]), c.table[b:b + 1]
             near.check([x[b:b + 1, v:v + 1] for x in got])
+
+
+def test_a_sequence_cut_back_into_a_shared_page_goes_on_as_a_fork():
+    """Sequence 0's 96 tokens are shared whole with sequence 1; 0 is cut back to 40, in the middle of a shared
+    page, and goes on as its fork 2: 1 keeps its bytes, and both attend to what is theirs."""
+    rng = np.random.default_rng(71)
+    S, W, P, L, H, G, D, page, M = 3, 8, 30, 2, 2, 3, 64, 16, 12
+    pool, t = C.Pool(S, W, P), list(B.kv_pool(S, W, P, DEV))
+    host = np.zeros((2, L, P, H, page, D), dtype=np.uint8)
+    pages = torch.from_numpy(host).to(DEV)
+
+    def resize(seqs, tokens):
+        assert int(B.nvfp4_kv_resize(*t, page, ints(seqs), ints(tokens))) == pool.resize(page, seqs, tokens) == 0
+        check_pool(t, pool)
+
+    def fork(src, dst, tokens):
+        nonlocal host
+        short, moves = pool.fork(page, [src], [dst], [tokens])
+        assert int(B.nvfp4_kv_fork(*t, pages[0], pages[1], ints([src]), ints([dst]), ints([tokens]))) == short == 0
+        host = np.stack([C.copy_slots(x, moves) for x in host])
+        check_pool(t, pool)
+
+    def append(rows, lens):
+        x, xf = dtype_values(rng.standard_normal((2, S, rows, H, D)), BF)
+        for l in range(L):
+            B.nvfp4_kv_append(x[0], x[1], U.scalar(KS), U.scalar(VS), pages[0, l], pages[1, l], t[0], ints(lens))
+            for kv, s in ((0, KS), (1, VS)):
+                host[kv, l] = C.append(xf[kv], s, host[kv, l], pool.table, np.asarray(lens))
+        np.testing.assert_array_equal(pages.cpu().numpy(), host)
+
+    resize([0], [96])
+    append(96, [0, -1, -1])
+    fork(0, 1, 96)
+    resize([0], [40])
+    assert not pool.writable(0, page, 40, 41)  # its page is sequence 1's, too
+    fork(0, 2, 40)
+    resize([0, 2], [0, 40 + M])
+    assert pool.writable(2, page, 40, 40 + M)
+    before = host[:, :, pool.table[1, :6]].copy()
+    append(M, [-1, -1, 40])
+    np.testing.assert_array_equal(host[:, :, pool.table[1, :6]], before)
+    c = Case.__new__(Case)
+    c.q, c.qf = dtype_values(rng.standard_normal((S, M, H * G, D)), BF)
+    c.k, c.v, c.table, c.lens, c.M, c.D = host[0, 1], host[1, 1], pool.table, np.array([-1, 84, 40]), M, D
+    c.parent, c.counts, c.dtype = None, None, BF
+    c.check(c.gpu())

@@ -115,3 +115,42 @@ def test_fork_shares_whole_pages_and_copies_the_rest():
     assert pool.table[2].tolist() == [0, 1, 3, -1] and pool.refs[:5].tolist() == [2, 2, 1, 1, 0]
     pool.resize(16, [0], [0])
     assert pool.refs[:4].tolist() == [1, 1, 0, 1] and pool.free[-1] == 2
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_only_a_cut_back_leads_onto_a_shared_page_and_a_fork_leads_off_it(seed):
+    """What the header says of shared pages: while sequences grow and are forked from committed tokens, the
+    tokens that any of them writes next lie on pages of its own; one cut back into a shared page would
+    write another's tokens, and its fork does not."""
+    rng = np.random.default_rng(seed)
+    S, W, page = 6, 8, 16
+    pool, lens, cut = C.Pool(S, W, 60), np.zeros(S, dtype=np.int64), 0
+    for _ in range(400):
+        s, d = rng.permutation(S)[:2]
+        what = rng.integers(0, 4)
+        if what <= 1:  # a step: pages for its nodes, the nodes, some of them accepted
+            n = int(min(lens[s] + rng.integers(1, 40), page * W))
+            if pool.resize(page, [s], [n]):
+                continue
+            assert pool.writable(s, page, int(lens[s]), n)
+            lens[s] = rng.integers(lens[s], n + 1)
+        elif what == 2:  # a turn from committed tokens
+            n = int(lens[s] - rng.integers(0, min(lens[s], 20) + 1))
+            if pool.fork(page, [s], [d], [n])[0] == 0:
+                lens[d] = n
+        else:  # a cut back, continued as the header says
+            n = int(rng.integers(0, lens[s] + 1))
+            pool.resize(page, [s], [n])
+            if n % page and not pool.writable(s, page, n, n + 1):
+                cut += 1
+                if pool.fork(page, [s], [d], [n])[0] == 0:
+                    pool.resize(page, [s], [0])
+                    lens[d], lens[s] = n, 0
+                    assert pool.writable(d, page, n, n + 1)
+                else:
+                    pool.resize(page, [s], [0])
+                    lens[s] = 0
+            else:
+                lens[s] = n
+        check_pool(pool)
+    assert cut
