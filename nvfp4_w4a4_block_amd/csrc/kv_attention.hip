@@ -31,14 +31,15 @@
 // of a batch share the chip evenly, and a range that cuts an item leaves a partial
 // sum (at most two per workgroup) that a second kernel joins.
 //
-// Bounds.  One query per KV head and long sequences: the cache's bytes (64 x 8000
-// tokens, 8 heads of 128: 1.05 GB in 182 us, 5.8 TB/s).  Many rows: the vector and
-// the matrix instructions, whose times add up here (512 nodes x 40 heads of 128
-// after 23040 tokens: 249 us with the second kernel's 16, 0.98 PFLOP/s; matrix
-// units 48% busy, vector instructions 60%).  One tree or a
-// few sequences: the set-up (4.5 us until the first product), 1 us per row tile
-// to join the waves, and the second kernel (16 nodes x 40 heads after 23552
-// tokens: 23 + 5 us, of which the cache's 48 MB are 10).
+// Bounds.  Times are those of a call on the device, both kernels, one call after
+// the other in a graph.  One query per KV head and long sequences: the cache's
+// bytes (64 x 8000 tokens, 8 heads of 128, 1.05 GB: 183 us, 5.7 TB/s).  Many rows:
+// the vector and the matrix instructions, whose times add up here (512 nodes x 40
+// heads of 128 after 23040 tokens: 253 to 256 us over five runs, 0.97 PFLOP/s; matrix
+// units 49% busy, vector instructions 61%).  One tree or a few sequences: the set-up
+// (4.5 us until the first product), 1 us per row tile to join the waves, and the
+// second kernel's 4 to 5 (16 nodes x 40 heads after 23552 tokens: 25.9 us, of which
+// the cache's 48 MB are 10).
 //
 // Operands.  Scores are computed transposed (A = keys, B = queries), 16x16x32
 // bf16: E4M3 is exact in bf16, and so is a bf16 query.  The result has a
@@ -46,7 +47,11 @@
 // product (A = values transposed, f16: E4M3 is exact there too), if that
 // product's key order is 4q .. 4q + 3 and 16 + 4q .. for lane group q, which
 // the value loads follow; the 2 x 2 byte transposes are v_perm.  fp32 calls
-// split q into three bf16 parts and p into two f16 parts.
+// split q into three bf16 parts and p into two f16 parts.  bf16 calls round p to
+// f16 for the product (2^-11, an eighth of the result's own half step; the sum that
+// divides takes p as it is): a second part would be another product per value.  It
+// moves 7 to 9% of the results across a rounding border, and their error against
+// 64 bits by 0.2 to 0.6% of itself.
 #include <type_traits>
 
 #include "device_common.h"
@@ -1033,6 +1038,8 @@ int compute_units() {
 //     256, 16 MB: 25.9 us; as four groups, whose partial sums have four times the
 //     rows, 31.8; 32 of those trees, 524 MB: 292 and 265);
 //   beyond: four groups and further items (1024-token prompt 58 us; one group 62).
+// The cache's size is taken from the table's width: the tree of 96 rows under a table
+// of 160000 tokens takes four groups, 31.0 us instead of 23.9 in a graph.
 constexpr int most_row_tiles(int dim, bool f32) {
   return f32 ? (dim == 256 ? 1 : 2) : dim == 64 ? 6 : dim == 128 ? 4 : 2;
 }
@@ -1052,7 +1059,10 @@ void row_split(const KvAttentionArgs& a, int* rt, int* rg, int* row_items) {
 // kernel costs more (one token after 511, 8 heads of 128: 9.9 us split, 7.6 us
 // whole).  An item's set-up counts as kStartCost tiles; with 0, 2, 4 and 8 of them
 // 16 ragged fp32 trees take 24.0, 20.7, 21.2 and 22.4 us, 32 ragged sequences of
-// one bf16 token 62.6, 62.3, 64 and 68.8 us.
+// one bf16 token 62.6, 62.3, 64 and 68.8 us.  Lengths stand on the device, so both
+// this rule and row_split's go by what the table covers: under a table of 23552
+// tokens the first of these calls is split, 9.0 us instead of 6.9 in a graph.  kWhole
+// was measured at two tiles and 8 heads only, its border nowhere.
 constexpr int kWhole = 4, kStartCost = 2;
 
 Plan make_plan(const KvAttentionArgs& a, int* rt, int* rg, int64_t* bytes) {

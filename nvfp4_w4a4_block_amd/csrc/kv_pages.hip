@@ -31,8 +31,8 @@ __device__ __forceinline__ uint8_t* token_row(uint8_t* base, const KvCache& c, i
 // q = E4M3(x * (1 / s)) of every node's keys and values, 16 elements per
 // thread (one 16-byte store; a row never crosses a page), written to the node's
 // slot.  Each element is read and written once: bound by memory for prompts (8188
-// fp32 rows of 8 x 128, K and V, 84 MB: 14.1 us, 5.9 TB/s, part of it from the
-// Infinity Cache), by the launch for a tree (16 bf16 nodes: 3.1 us).
+// fp32 rows of 8 x 128, K and V, 84 MB: 14.3 us, 5.9 TB/s, part of it from the
+// Infinity Cache), by the launch for a tree (16 bf16 nodes: 3.2 us).
 template <bool BF16>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, uint32_t chunks) {
   const KvCache& c = a.c;
