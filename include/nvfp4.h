@@ -520,6 +520,156 @@ nvfp4_status nvfp4_kv_fork(int64_t n, int64_t S, int64_t W, int64_t P, int64_t p
                            uint8_t* k_pages, uint8_t* v_pages, int64_t layer_stride, int64_t page_stride,
                            void* stream);
 
+/* Writes a step's keys and values into the cache as nvfp4_kv_append does, the
+ * keys with rotary positions, and gives the step's queries theirs.
+ *   q        [B * M] rows of Hq * D values in dt, device (Hq >= 1); q_out out
+ *            [B][M][Hq][D] in dt: q itself (contiguous rows: q_stride Hq * D)
+ *            or no part of q, k or v.
+ *   R        the first R of a head's D values are rotated (a multiple of 16, 16
+ *            .. D), the others pass.  Pair j < R / 2 is (x[j], x[j + R / 2]), or
+ *            (x[2 j], x[2 j + 1]) with interleaved != 0.
+ *   inv_freq [R / 2] doubles, device, 8-byte aligned: radians per position of
+ *            each pair (scaled tables of long contexts are the caller's).
+ *   rope_scale  finite factor of the rotated values (1 unless the scaling of a
+ *            long context has one).
+ *   parent   int32 [B][M], device, M <= 64, or NULL: as nvfp4_kv_attention
+ *            takes it.  Node v stands at position lens[b] plus the number of its
+ *            ancestors (NULL: lens[b] + v), and is written at token lens[b] + v.
+ * Pair (x, y) at position p becomes rope_scale * (x cos w - y sin w, y cos w +
+ * x sin w), w = p * inv_freq[j]; the angle is reduced in 64 bits, sine and
+ * cosine are fp32.  A query is rounded to dt; a key goes from fp32 to the
+ * cache's bytes (nvfp4_kv_fp8_encode of the rotated fp32 values).  Query rows
+ * of an unused sequence and behind counts[b] are zero.  The other arguments,
+ * limits and the rule of shared pages are nvfp4_kv_append's.
+ * Cites: the pages "Using tree-based multi-token prediction to accelerate LLM
+ * inference" and "Reusing KV cache across agent turns": nodes of a tree share
+ * positions, a suffix goes on from its prefix. */
+nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t R,
+                                  int64_t page_size, int64_t P, int64_t W, const void* q, const void* k,
+                                  const void* v, nvfp4_dtype dt, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, const double* inv_freq, float rope_scale, int interleaved,
+                                  const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,
+                                  int64_t page_stride, const int32_t* table, const int32_t* lens,
+                                  const int32_t* parent, const int32_t* counts, void* q_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: the layers with a recurrent state of a hybrid model.
+ *
+ * A layer keeps, per sequence and value head, a state S of Dv x Dk fp32 values.
+ * Token t reads and writes it:
+ *     S <- exp(g_t) S;  u_t = beta_t (v_t - S k_t);  S <- S + u_t k_t^T;
+ *     o_t = scale * S q_t
+ * Value head h uses query and key head h / (H / Hk).  With norm_eps >= 0, q and
+ * k are divided by sqrt(their sum of squares + norm_eps) first; negative: they
+ * are used as they are.
+ *   q, k     [B * M] rows of Hk * Dk values in dt, device; v [B * M] rows of
+ *            H * Dv.  q_stride, k_stride, v_stride: values from a row to the
+ *            next (multiples of 16 bytes), as in the paged cache.
+ *   g, beta  [B * M][H] fp32, device: log decay (at most 0 in a layer that
+ *            forgets; -infinity forgets all) and rate.
+ *   states   fp32 [S][H][Dv][Dk], device, 16-byte aligned: S slots.
+ *   src      int32 [B], device: the slot that a sequence starts from, -1: from
+ *            zeros.  A sequence whose src is less than -1 or not below S is not in
+ *            use.
+ *   dst      int32 [B], device: the slot that its last state is written to; one
+ *            outside [0, S): none.  dst[b] may be src[b].  A state is not written
+ *            where dst[b] is the src of another sequence in use or the dst of an
+ *            earlier one, so that no slot is read and written in one call by two.
+ *            A slot kept aside (dst of a call whose src goes on elsewhere) is a
+ *            turn's snapshot, to begin others from.
+ *   counts   int32 [B], device, or NULL: only a sequence's first counts[b] rows
+ *            are tokens (more than M counts as M; none: the state is copied).
+ *   out      [B][M][H][Dv] in dt, not overlapping q, k or v.  Rows that are no
+ *            tokens are zero, and what they hold in q, k, v, g and beta is not
+ *            read.
+ *   Shapes: Dk and Dv 64, 128 or 256; 1 <= H <= 1024, H a multiple of Hk; B and M
+ *   at most 65535, B * M <= 2^24; 1 <= S < 2^31.
+ * States, sums, decays and norms are fp32 (the decays' sums within a block of
+ * tokens 64 bits).  Chains of some length go through the matrix cores block by
+ * block; there every factor of a state is split into f16 parts that keep 22 bits
+ * of it relative to its row's or column's largest value, and in bf16 calls the
+ * factors that reach nothing but out are rounded to f16 (11 bits).  A NaN or an
+ * infinity in a sequence's rows or state may reach all of that sequence's rows
+ * and its new state, and nothing of another sequence.
+ * Cites: the page section "Reusing KV cache across agent turns" (the model is a
+ * hybrid; its recurrent states are kept and restored with the cached pages). */
+
+/* Size in bytes of the workspace with which nvfp4_delta_rule runs long chains
+ * block by block (0 for an invalid call or one that needs none). */
+int64_t nvfp4_delta_rule_workspace_bytes(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv,
+                                         nvfp4_dtype dt);
+
+/* A chain of tokens: one (decoding), a suffix or a prompt.
+ *   workspace  device memory, 16-byte aligned, of workspace_bytes bytes, or
+ *            NULL; with less than nvfp4_delta_rule_workspace_bytes the tokens go
+ *            one after the other (slower, same contract).  It needs no clearing.
+ *            Calls that may overlap need one each. */
+nvfp4_status nvfp4_delta_rule(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, int64_t S,
+                              const void* q, const void* k, const void* v, nvfp4_dtype dt, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const float* g, const float* beta, float scale,
+                              float norm_eps, float* states, const int32_t* src, const int32_t* dst,
+                              const int32_t* counts, void* out, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/* The nodes of drafted trees, M <= 64: a node's state is its parent's one token
+ * on, a root's the sequence's own one token on.  The states are read only.
+ *   parent   int32 [B][M], device: as nvfp4_kv_attention takes it (outside [0,
+ *            v): a root); required.
+ *   keys     out fp32 [B][M][Hk][Dk]: the nodes' keys as used (normalised).
+ *   updates  out fp32 [B][M][H][Dv]: their u.
+ * Both are what nvfp4_delta_commit needs of the step, zero in rows that are no
+ * tokens. */
+nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, int64_t S,
+                              const void* q, const void* k, const void* v, nvfp4_dtype dt, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const float* g, const float* beta, float scale,
+                              float norm_eps, const float* states, const int32_t* src, const int32_t* parent,
+                              const int32_t* counts, void* out, float* keys, float* updates, void* stream);
+
+/* Puts the accepted path of each sequence's tree into its states, in all L
+ * layers: S = the state of src[b] taken through node 0 and the path's nodes, S <-
+ * exp(g_p) S + u_p k_p^T, written to dst[b].
+ *   states   fp32 [L][S][H][Dv][Dk]; keys, updates: [L][B][M] rows as
+ *            nvfp4_delta_tree writes them; g fp32 [L][B][M][H], the layers' log
+ *            decays.
+ *   result   int32 [B][3 + M], device, 1 <= M <= 64: rows as nvfp4_tree_accept
+ *            and nvfp4_tree_verify write them, as nvfp4_kv_compact takes them.  A
+ *            path entry outside [0, M) is passed over.
+ *   src, dst as above, the same slots in every layer.  The decays' sums are 64
+ *            bits, the others fp32. */
+nvfp4_status nvfp4_delta_commit(int64_t L, int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv,
+                                int64_t S, float* states, const float* keys, const float* updates, const float* g,
+                                const int32_t* result, const int32_t* src, const int32_t* dst, void* stream);
+
+/* Size in bytes of nvfp4_token_logprobs's workspace (0 for an invalid or empty
+ * call). */
+int64_t nvfp4_token_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t top, nvfp4_dtype dt);
+
+/* Log probabilities of given tokens under rows of logits, each row's entropy and
+ * its most probable tokens.
+ *   logits   [M] rows of N values in dt, device, aligned to a value; stride:
+ *            values from a row to the next (at least N, any).
+ *   tokens   int32 [M], device.
+ *   top      0 .. 64, at most N.
+ *   logprobs out fp32 [M]: z[token] - log sum exp z; NaN for a token outside
+ *            [0, N).
+ *   entropy  out fp32 [M]: -sum p log p, in nats; a logit of -infinity adds
+ *            nothing.
+ *   top_logprobs, top_tokens  out fp32 and int32 [M][top] (NULL when top is 0):
+ *            the largest logits in descending order, ties to the lowest column,
+ *            -0.0 just below +0.0 (the order of nvfp4_tree_verify's greedy).
+ *   workspace  device memory, 16-byte aligned, at least
+ *            nvfp4_token_logprobs_workspace_bytes; it needs no clearing.  Calls
+ *            that may overlap need one each.
+ * A row that holds a NaN or +infinity, or nothing above -infinity, is no
+ * distribution: its numbers are NaN and its top tokens -1.  Sums are fp32.
+ *   Shapes: M at most 65535, 1 <= N < 2^24.
+ * Cites: the page section "Using NVFP4 quantization to accelerate Qwen3.6-27B
+ * inference" (the LM head, whose logits these are). */
+nvfp4_status nvfp4_token_logprobs(int64_t M, int64_t N, int64_t top, const void* logits, nvfp4_dtype dt,
+                                  int64_t stride, const int32_t* tokens, float* logprobs, float* entropy,
+                                  float* top_logprobs, int32_t* top_tokens, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
 /* Read-only streaming ceiling: reads the a_bytes bytes at a and the b_bytes
  * bytes at b once (16-byte loads, each wave a contiguous span, the loads
  * marked non-temporal); every lane folds the four words of each of its loads

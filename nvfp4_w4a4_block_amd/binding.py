@@ -31,13 +31,14 @@ KERNEL_NAMES = {KERNEL_GEMV_FP4: "gemv_fp4_kernel", KERNEL_GEMV_FLAT: "gemv_flat
                 KERNEL_TILED_PERSISTENT: "gemm_wg_tiled_kernel", KERNEL_TILED: "gemm_tiled_kernel",
                 KERNEL_M16_STREAM: "gemm_m16_stream_kernel"}
 
-EXPORTS = ("nvfp4_abi_version", "nvfp4_act_global_scale", "nvfp4_gemm", "nvfp4_gemm_dispatch", "nvfp4_gemm_ex",
+EXPORTS = ("nvfp4_abi_version", "nvfp4_act_global_scale", "nvfp4_delta_commit", "nvfp4_delta_rule",
+           "nvfp4_delta_rule_workspace_bytes", "nvfp4_delta_tree", "nvfp4_gemm", "nvfp4_gemm_dispatch", "nvfp4_gemm_ex",
            "nvfp4_gemm_quantize_output", "nvfp4_gemm_scratch", "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_ws",
-           "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_kv_compact",
+           "nvfp4_kv_append", "nvfp4_kv_append_rope", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_kv_compact",
            "nvfp4_kv_fork", "nvfp4_kv_fp8_decode", "nvfp4_kv_fp8_encode", "nvfp4_kv_resize",
            "nvfp4_quantize_act",
            "nvfp4_quantize_gemm", "nvfp4_quantize_gemm_dynamic", "nvfp4_quantize_weights", "nvfp4_status_string",
-           "nvfp4_stream_read",
+           "nvfp4_stream_read", "nvfp4_token_logprobs", "nvfp4_token_logprobs_workspace_bytes",
            "nvfp4_tree_accept",
            "nvfp4_tree_verify")
 
@@ -86,7 +87,18 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_kv_compact.argtypes = [i64] * 8 + [p, p, i64, i64, p, p, p, p, p]
     lib.nvfp4_kv_resize.argtypes = [i64] * 5 + [p] * 8
     lib.nvfp4_kv_fork.argtypes = [i64] * 5 + [p] * 9 + [i64] * 3 + [p, p, i64, i64, p]
-    for f in ("nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_compact", "nvfp4_kv_resize", "nvfp4_kv_fork",
+    lib.nvfp4_kv_append_rope.argtypes = [i64] * 9 + [p, p, p, i32, i64, i64, i64, p, f32, i32, p, p, p, p, i64,
+                                                     p, p, p, p, p, p]
+    lib.nvfp4_delta_rule_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.nvfp4_delta_rule_workspace_bytes.restype = i64
+    lib.nvfp4_delta_rule.argtypes = [i64] * 7 + [p, p, p, i32, i64, i64, i64, p, p, f32, f32, p, p, p, p, p, p, i64, p]
+    lib.nvfp4_delta_tree.argtypes = [i64] * 7 + [p, p, p, i32, i64, i64, i64, p, p, f32, f32, p, p, p, p, p, p, p, p]
+    lib.nvfp4_delta_commit.argtypes = [i64] * 8 + [p] * 8
+    lib.nvfp4_token_logprobs_workspace_bytes.argtypes = [i64] * 3 + [i32]
+    lib.nvfp4_token_logprobs_workspace_bytes.restype = i64
+    lib.nvfp4_token_logprobs.argtypes = [i64] * 3 + [p, i32, i64, p, p, p, p, p, p, i64, p]
+    for f in ("nvfp4_kv_append_rope", "nvfp4_delta_rule", "nvfp4_delta_tree", "nvfp4_delta_commit",
+              "nvfp4_token_logprobs", "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_compact", "nvfp4_kv_resize", "nvfp4_kv_fork",
               "nvfp4_quantize_weights", "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_gemm_ws",
               "nvfp4_gemm_scratch",
               "nvfp4_gemm_quantize_output",
@@ -735,3 +747,218 @@ def nvfp4_kv_fork(table: torch.Tensor, held: torch.Tensor, refs: torch.Tensor, f
           shortage.data_ptr(), moves.data_ptr(), L, H, D, k_pages.data_ptr(), v_pages.data_ptr(), layer_stride,
           page_stride)
     return shortage
+
+
+def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained: int = 8192, fast: float = 32.0, slow: float = 1.0,
+                     device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq float64 [rotary / 2] on `device`, rope_scale) for nvfp4_kv_append_rope.  scaling stretches a
+    context of `trained` tokens by `factor`: "none"; "linear" (positions divided by it); "ntk" (a larger base, so
+    that the slowest pair alone is stretched in full); "yarn" (pairs that turn more than `fast` times within the
+    trained length stay, those that turn less than `slow` times are stretched in full, the others by a part
+    between; rotated values times 0.1 ln factor + 1)."""
+    if rotary < 16 or rotary % 16 or base <= 1.0 or factor < 1.0 or trained < 1 or not fast > slow > 0.0:
+        raise ValueError("rotary must be a multiple of 16, base above 1, factor at least 1, fast above slow above 0")
+    if scaling == "ntk":
+        base *= factor ** (rotary / (rotary - 2))
+    elif scaling not in ("none", "linear", "yarn"):
+        raise ValueError("scaling must be none, linear, ntk or yarn")
+    f = float(base) ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        # the pair that turns n times within the trained length; those between are mixed by their index
+        at = [rotary * math.log(trained / (2 * math.pi * n)) / (2 * math.log(base)) for n in (fast, slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary - 1)
+        part = ((torch.arange(rotary // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - part) + f / factor * part
+        scale = 0.1 * math.log(factor) + 1.0
+    return f.to(device), scale
+
+
+def nvfp4_kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
+                         k_scale: torch.Tensor, v_scale: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         table: torch.Tensor, lens: torch.Tensor, parent: Optional[torch.Tensor] = None,
+                         counts: Optional[torch.Tensor] = None, interleaved: bool = False, rope_scale: float = 1.0,
+                         q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """nvfp4_kv_append with rotary positions: keys k [B, M, H, D] are turned on the way into the cache, the
+    queries q [B, M, Hq, D] into q_out (returned; it may be a contiguous q).  inv_freq float64 [R / 2]: radians
+    per position of the first R values' pairs (rope_frequencies).  parent int32 [B, M]: drafted trees, whose
+    nodes stand at lens[b] + depth; None: a chain."""
+    on, (P, Hp, page, Dp), _, page_stride = _kv_pages(k_pages, v_pages, 4)
+    shape, rows, entries = q.shape, k.shape, table.shape
+    if len(shape) != 4 or len(rows) != 4 or rows != v.shape or not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q must be [B, M, Hq, D], k and v [B, M, H, D], all of one dtype")
+    B, M, Hq, D = shape
+    H = rows[2]
+    if rows != (B, M, Hp, Dp) or D != Dp or len(entries) != 2 or entries[0] != B or lens.shape != (B,):
+        raise ValueError("q, k, pages [P, H, page_size, D], table [B, W] and lens [B] do not fit together")
+    _ints(on, "table and lens", table, lens)
+    if parent is not None:
+        _ints(on, "parent", parent)
+        if parent.shape != (B, M):
+            raise ValueError("parent must be [B, M]")
+    if counts is not None:
+        _ints(on, "counts", counts)
+        if counts.shape != (B,):
+            raise ValueError("counts must be [B]")
+    _kv_scale(on, k_scale, v_scale)
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != on or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous float64 [R / 2] on cuda:{on}")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif q_out.shape != shape or q_out.dtype != q.dtype or q_out.get_device() != on or not q_out.is_contiguous():
+        raise ValueError("q_out must be a contiguous [B, M, Hq, D] of q's dtype on its GPU")
+    _call(on, "nvfp4_kv_append_rope", load().nvfp4_kv_append_rope, B, M, Hq, H, D, 2 * inv_freq.shape[0], page, P,
+          entries[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q.dtype), _kv_rows(q, shape, on, "q"),
+          _kv_rows(k, rows, on, "k"), _kv_rows(v, rows, on, "v"), inv_freq.data_ptr(), rope_scale, interleaved,
+          k_scale.data_ptr(), v_scale.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_stride,
+          table.data_ptr(), lens.data_ptr(), parent.data_ptr() if parent is not None else None,
+          counts.data_ptr() if counts is not None else None, q_out.data_ptr())
+    return q_out
+
+
+# Gated delta rule.  States are float32 [S, H, Dv, Dk] per layer ([L, S, H, Dv, Dk] for all layers).
+
+
+def _floats(on: int, shape, name: str, t: torch.Tensor) -> None:
+    if t.dtype is not _F32 or t.get_device() != on or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 {list(shape)} on cuda:{on}")
+
+
+def _delta_rows(q, k, v, g, beta, states, src, counts, out):
+    """Checks a step's rows and slots; returns the GPU, the shape arguments, the rows' arguments and out."""
+    on, rows, values, slots = states.get_device(), k.shape, v.shape, states.shape
+    if on < 0 or states.dtype is not _F32 or len(slots) != 4 or not states.is_contiguous():
+        raise ValueError("states must be a contiguous float32 [S, H, Dv, Dk] on a GPU")
+    if len(rows) != 4 or q.shape != rows or len(values) != 4 or not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q and k must be [B, M, Hk, Dk], v [B, M, H, Dv], all of one dtype")
+    B, M, Hk, Dk = rows
+    S, H, Dv, _ = slots
+    if values != (B, M, H, Dv) or slots[3] != Dk or Hk < 1 or H % Hk or src.shape != (B,):
+        raise ValueError("q, k, v, states [S, H, Dv, Dk] and src [B] do not fit together")
+    _ints(on, "src", src)
+    if counts is not None:
+        _ints(on, "counts", counts)
+        if counts.shape != (B,):
+            raise ValueError("counts must be [B]")
+    _floats(on, (B, M, H), "g", g)
+    _floats(on, (B, M, H), "beta", beta)
+    if out is None:
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+    elif out.shape != values or out.dtype != v.dtype or out.get_device() != on or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [B, M, H, Dv] of v's dtype on its GPU")
+    return on, (B, M, Hk, H, Dk, Dv, S), (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q.dtype), _kv_rows(q, rows, on, "q"), _kv_rows(k, rows, on, "k"),
+        _kv_rows(v, values, on, "v"), g.data_ptr(), beta.data_ptr()), out
+
+
+def nvfp4_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                     states: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                     counts: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     norm_eps: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated delta rule over chains of tokens: q, k [B, M, Hk, Dk] and v [B, M, H, Dv] (float32/bfloat16; rows
+    may be column ranges of a wider tensor), log decays g and rates beta float32 [B, M, H].  Sequence b begins with
+    slot src[b] of states float32 [S, H, Dv, Dk] (-1: with zeros) and leaves its state in slot dst[b] (int32 [B]
+    each).  scale defaults to 1/sqrt(Dk); norm_eps: q and k are normalised with it (None: used as they are).
+    Returns out [B, M, H, Dv] of v's dtype.  workspace: uint8 scratch; None allocates it."""
+    on, dims, rows, out = _delta_rows(q, k, v, g, beta, states, src, counts, out)
+    B, M, Hk, H, Dk, Dv, _ = dims
+    _ints(on, "dst", dst)
+    if dst.shape != (B,):
+        raise ValueError("dst must be [B]")
+    lib = load()
+    if workspace is None:
+        need = lib.nvfp4_delta_rule_workspace_bytes(B, M, Hk, H, Dk, Dv, rows[3])
+        workspace = states.new_empty((need,), dtype=_U8) if need else None
+    elif workspace.dtype is not _U8 or workspace.get_device() != on or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
+    _call(on, "nvfp4_delta_rule", lib.nvfp4_delta_rule, *dims, *rows,
+          1.0 / math.sqrt(Dk) if scale is None else scale, -1.0 if norm_eps is None else norm_eps, states.data_ptr(),
+          src.data_ptr(), dst.data_ptr(), counts.data_ptr() if counts is not None else None, out.data_ptr(),
+          workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0)
+    return out
+
+
+def nvfp4_delta_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                     states: torch.Tensor, src: torch.Tensor, parent: torch.Tensor,
+                     counts: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     norm_eps: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     keys: Optional[torch.Tensor] = None, updates: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The gated delta rule over drafted trees (parent int32 [B, M], M <= 64), which leaves the states as they are.
+    Arguments as nvfp4_delta_rule.  Returns out, and what nvfp4_delta_commit takes: keys float32 [B, M, Hk, Dk] and
+    updates float32 [B, M, H, Dv] (one layer's part of tensors for all layers may be given)."""
+    on, dims, rows, out = _delta_rows(q, k, v, g, beta, states, src, counts, out)
+    B, M, Hk, H, Dk, Dv, _ = dims
+    _ints(on, "parent", parent)
+    if parent.shape != (B, M):
+        raise ValueError("parent must be [B, M]")
+    if keys is None:
+        keys = states.new_empty((B, M, Hk, Dk))
+    else:
+        _floats(on, (B, M, Hk, Dk), "keys", keys)
+    if updates is None:
+        updates = states.new_empty((B, M, H, Dv))
+    else:
+        _floats(on, (B, M, H, Dv), "updates", updates)
+    _call(on, "nvfp4_delta_tree", load().nvfp4_delta_tree, *dims, *rows,
+          1.0 / math.sqrt(Dk) if scale is None else scale, -1.0 if norm_eps is None else norm_eps, states.data_ptr(),
+          src.data_ptr(), parent.data_ptr(), counts.data_ptr() if counts is not None else None, out.data_ptr(),
+          keys.data_ptr(), updates.data_ptr())
+    return out, keys, updates
+
+
+def nvfp4_delta_commit(states: torch.Tensor, keys: torch.Tensor, updates: torch.Tensor, g: torch.Tensor,
+                       result: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Takes each sequence's state through the root and the accepted path of its tree, in all layers: states [L, S,
+    H, Dv, Dk], slot src[b] to slot dst[b]; keys [L, B, M, Hk, Dk] and updates [L, B, M, H, Dv] as nvfp4_delta_tree
+    gives them, g float32 [L, B, M, H] the layers' log decays, result int32 [B, 3 + M]: rows of nvfp4_tree_accept /
+    nvfp4_tree_verify."""
+    on, slots, rows, paths = states.get_device(), states.shape, keys.shape, result.shape
+    if on < 0 or states.dtype is not _F32 or len(slots) != 5 or not states.is_contiguous():
+        raise ValueError("states must be a contiguous float32 [L, S, H, Dv, Dk] on a GPU")
+    if len(rows) != 5 or len(paths) != 2:
+        raise ValueError("keys must be [L, B, M, Hk, Dk] and result [B, 3 + M]")
+    L, S, H, Dv, Dk = slots
+    B, M, Hk = rows[1:4]
+    if paths != (B, 3 + M) or Hk < 1 or H % Hk or src.shape != (B,) or dst.shape != (B,):
+        raise ValueError("states, keys, result [B, 3 + M], src [B] and dst [B] do not fit together")
+    _floats(on, (L, B, M, Hk, Dk), "keys", keys)
+    _floats(on, (L, B, M, H, Dv), "updates", updates)
+    _floats(on, (L, B, M, H), "g", g)
+    _ints(on, "result, src and dst", result, src, dst)
+    _call(on, "nvfp4_delta_commit", load().nvfp4_delta_commit, L, B, M, Hk, H, Dk, Dv, S, states.data_ptr(),
+          keys.data_ptr(), updates.data_ptr(), g.data_ptr(), result.data_ptr(), src.data_ptr(), dst.data_ptr())
+
+
+def nvfp4_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
+                         workspace: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Under the rows of logits [M, N] (float32/bfloat16; rows may be spaced): the log probabilities of tokens int32
+    [M], the entropies, and the `top` most probable tokens with their log probabilities, in descending order:
+    (float32 [M], float32 [M], float32 [M, top], int32 [M, top]).  workspace: uint8 scratch; None allocates it."""
+    on, shape = logits.get_device(), logits.shape
+    if on < 0 or len(shape) != 2 or (logits.stride(1) != 1 and shape[1] > 1):
+        raise ValueError("logits must be [M, N] on a GPU, rows contiguous")
+    M, N = shape
+    _ints(on, "tokens", tokens)
+    if tokens.shape != (M,):
+        raise ValueError("tokens must be [M]")
+    dt = _dt(logits.dtype)
+    numbers = torch.empty((2, M), dtype=_F32, device=logits.device)
+    best = torch.empty((M, top), dtype=_F32, device=logits.device)
+    ids = tokens.new_empty((M, top))
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty((lib.nvfp4_token_logprobs_workspace_bytes(M, N, top, dt),), dtype=_U8,
+                                device=logits.device)
+    elif workspace.dtype is not _U8 or workspace.get_device() != on or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
+    _call(on, "nvfp4_token_logprobs", lib.nvfp4_token_logprobs, M, N, top, logits.data_ptr(), dt,
+          logits.stride(0) if M > 1 else N, tokens.data_ptr(), numbers[0].data_ptr(),
+          numbers[1].data_ptr(), best.data_ptr(), ids.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return numbers[0], numbers[1], best, ids

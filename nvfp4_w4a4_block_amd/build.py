@@ -34,11 +34,15 @@ SOURCES = {
     "kv_pages.hip": [],
     "kv_pool.hip": [],
     "kv_attention.hip": [],
+    "kv_rope.hip": [],
+    "delta.hip": [],
+    "logprobs.hip": [],
     "gemm_tiled.hip": [],
     "stream.hip": [],
     "scratch.hip": [],
     "abi.cpp": [],
     "abi_kv.cpp": [],
+    "abi_hybrid.cpp": [],
 }
 
 COMMON = [

@@ -1,0 +1,323 @@
+// Gated delta rule, token by token: decoding steps, drafted trees, and the
+// accepted path of a tree put into the states.
+//
+// The model of the page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic
+// Benchmark 6.4x Faster on Jetson AGX Thor" is a hybrid whose recurrent states are
+// kept and restored with the cached attention pages (section "Reusing KV cache
+// across agent turns").
+//
+// Mathematics.  Per value head, S [dv][dk] in fp32: S <- e^g S, u = beta (v - S k),
+// S <- S + u k^T, o = scale S q.  Rows of S are independent of each other, so a
+// wave that holds some of them whole needs nothing from any other.
+#include "delta_common.h"
+#include "kv_tree.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kTile = 8;  // tokens whose q and k stand in LDS
+
+// One row of q or k (DK values) as used, by a whole wave: normalised, times scale.
+template <int DK, bool BF16>
+__device__ __forceinline__ void stage_row(const void* rows, int64_t at, float eps, float scale, float* to) {
+  const int lane = threadIdx.x & 63;
+  f4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (lane < DK / 4) x = load4<BF16>(rows, at + 4 * lane);
+  if (eps >= 0.0f)
+    scale *= 1.0f / __builtin_sqrtf(sum_of_wave(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]) + eps);
+  if (lane < DK / 4) *reinterpret_cast<f4_t*>(to + 4 * lane) = x * scale;
+}
+
+template <int DK, int COLS>
+__device__ __forceinline__ void dots(const StateTile<DK, COLS>& x, const float* row, float (&sum)[COLS]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  f4_t acc[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) acc[c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < DK / 16; ++t) {
+    const f4_t r = *reinterpret_cast<const f4_t*>(row + 16 * t + 4 * g);
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) acc[c] += x.s[c][t] * r;
+  }
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) sum[c] = sum_of_groups((acc[c][0] + acc[c][1]) + (acc[c][2] + acc[c][3]));
+}
+
+// A chain, one token after the other.  grid (dv / (64 COLS), heads, seqs).
+template <int DK, int COLS, bool BF16>
+__global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
+  __shared__ float rows[2][kTile][DK];  // k, q
+  const int b = blockIdx.z, h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15;
+  const int kh = h / (a.heads / a.key_heads), row0 = (blockIdx.x * kWaves + wave) * 16 * COLS;
+  const int src = a.src[b];
+  const bool used = delta_used(src, a.slots);
+  const int count = used ? delta_count(a.counts, a.nodes, b) : 0;
+  const int64_t state_size = (int64_t)a.dv * DK;
+  StateTile<DK, COLS> x;
+  if (used && src >= 0) load_state<DK, COLS>(a.states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
+  else zero_state<DK, COLS>(x);
+  const int64_t first = (int64_t)b * a.nodes;
+  for (int t0 = 0; t0 < count; t0 += kTile) {
+    const int n = count - t0 < kTile ? count - t0 : kTile;
+    __syncthreads();
+    for (int i = wave; i < 2 * n; i += kWaves) {
+      const int t = i >> 1;
+      if (i & 1) stage_row<DK, BF16>(a.q, (first + t0 + t) * a.q_stride + kh * DK, a.norm_eps, a.scale, rows[1][t]);
+      else stage_row<DK, BF16>(a.k, (first + t0 + t) * a.k_stride + kh * DK, a.norm_eps, 1.0f, rows[0][t]);
+    }
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      const int64_t r = first + t0 + t;
+      const float decay = expf(a.g[r * a.heads + h]), beta = a.beta[r * a.heads + h];
+      float v[COLS], sk[COLS], o[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const int64_t at = r * a.v_stride + h * a.dv + row0 + 16 * c + j;
+        if constexpr (BF16) v[c] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
+        else v[c] = static_cast<const float*>(a.v)[at];
+      }
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+#pragma unroll
+        for (int e = 0; e < DK / 16; ++e) x.s[c][e] *= decay;
+      dots<DK, COLS>(x, rows[0][t], sk);
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) sk[c] = beta * (v[c] - sk[c]);
+#pragma unroll
+      for (int e = 0; e < DK / 16; ++e) {
+        const f4_t k = *reinterpret_cast<const f4_t*>(&rows[0][t][16 * e + 4 * (lane >> 4)]);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) x.s[c][e] += sk[c] * k;
+      }
+      dots<DK, COLS>(x, rows[1][t], o);
+      if (lane < 16)
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+          store1<BF16>(a.out, (r * a.heads + h) * a.dv + row0 + 16 * c + j, o[c]);
+    }
+  }
+  for (int t = count; t < a.nodes; ++t)
+    if (lane < 16)
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+        store1<BF16>(a.out, ((first + t) * a.heads + h) * a.dv + row0 + 16 * c + j, 0.0f);
+  if (!used) return;
+  const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
+  if (to >= 0) store_state<DK, COLS>(a.states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
+}
+
+// Drafted trees.  With the sums G of the decays along each node's line,
+//   u_v = beta_v (v_v - e^G_v S k_v - sum_a e^(G_v - G_a) (k_a . k_v) u_a),
+//   o_v = scale (e^G_v S q_v + sum_a e^(G_v - G_a) (k_a . q_v) u_a),
+// a the ancestors of v (and v itself in o).  grid (dv / 64, heads, seqs).
+template <int DK, bool BF16>
+__global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
+  __shared__ float rows[2][DK];      // k_v, q_v
+  __shared__ float near[2][64];      // e^(G_v - G_a) k_a . (k_v, q_v)
+  __shared__ float u[64][64];        // nodes x rows of S
+  __shared__ uint64_t lines[64];
+  __shared__ float length[64];       // the factor that normalises k_a
+  const int b = blockIdx.z, h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15;
+  const int kh = h / (a.heads / a.key_heads), col = 16 * wave + j, row = blockIdx.x * 64 + col;
+  const int src = a.src[b];
+  const bool used = delta_used(src, a.slots);
+  const int count = used ? delta_count(a.counts, a.nodes, b) : 0;
+  const int64_t first = (int64_t)b * a.nodes;
+  StateTile<DK, 1> x;
+  if (used && src >= 0)
+    load_state<DK, 1>(a.states + (((int64_t)src * a.heads + h) * a.dv + blockIdx.x * 64 + 16 * wave) * DK, x);
+  else zero_state<DK, 1>(x);
+  if (wave == 0) lines[lane] = ancestors_of_wave(lane < count ? a.parent[first + lane] : -1);
+  for (int v = 0; v < count; ++v) {
+    const int64_t r = first + v;
+    __syncthreads();
+    if (wave == 0) stage_row<DK, BF16>(a.k, r * a.k_stride + kh * DK, a.norm_eps, 1.0f, rows[0]);
+    if (wave == 1) stage_row<DK, BF16>(a.q, r * a.q_stride + kh * DK, a.norm_eps, a.scale, rows[1]);
+    if (wave == 2) {
+      float s = 1.0f;
+      if (a.norm_eps >= 0.0f) {
+        f4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (lane < DK / 4) y = load4<BF16>(a.k, r * a.k_stride + kh * DK + 4 * lane);
+        s = 1.0f / __builtin_sqrtf(sum_of_wave(y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3]) + a.norm_eps);
+      }
+      if (lane == 0) length[v] = s;
+    }
+    __syncthreads();
+    const uint64_t line = lines[v];
+    for (int n = wave; n <= v; n += kWaves) {
+      if (!((line >> n) & 1)) continue;
+      double far = 0.0;  // the decays between n and v
+      for (int i = n + 1; i <= v; ++i)
+        if (((line >> i) & 1)) far += (double)a.g[(first + i) * a.heads + h];
+      float kk = 0.0f, qk = 0.0f;
+      if (lane < DK / 4) {
+        const f4_t y = load4<BF16>(a.k, (first + n) * a.k_stride + kh * DK + 4 * lane) * length[n];
+        const f4_t k = *reinterpret_cast<const f4_t*>(&rows[0][4 * lane]);
+        const f4_t q = *reinterpret_cast<const f4_t*>(&rows[1][4 * lane]);
+        kk = y[0] * k[0] + y[1] * k[1] + y[2] * k[2] + y[3] * k[3];
+        qk = y[0] * q[0] + y[1] * q[1] + y[2] * q[2] + y[3] * q[3];
+      }
+      kk = sum_of_wave(kk);
+      qk = sum_of_wave(qk);
+      const float decay = expf((float)far);
+      if (lane == 0) {
+        near[0][n] = decay * kk;
+        near[1][n] = decay * qk;
+      }
+    }
+    __syncthreads();
+    float sk[1], sq[1];
+    dots<DK, 1>(x, rows[0], sk);
+    dots<DK, 1>(x, rows[1], sq);
+    double all = 0.0;
+    for (int i = 0; i <= v; ++i)
+      if ((line >> i) & 1) all += (double)a.g[(first + i) * a.heads + h];
+    const float into = expf((float)all), beta = a.beta[r * a.heads + h];
+    const int64_t at = r * a.v_stride + h * a.dv + row;
+    float value;
+    if constexpr (BF16) value = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
+    else value = static_cast<const float*>(a.v)[at];
+    float w = value - into * sk[0], o = into * sq[0];
+    for (int n = 0; n < v; ++n)
+      if ((line >> n) & 1) {
+        w -= near[0][n] * u[n][col];
+        o += near[1][n] * u[n][col];
+      }
+    w *= beta;
+    o += near[1][v] * w;
+    if (lane < 16) {
+      u[v][col] = w;
+      a.updates[(r * a.heads + h) * a.dv + row] = w;
+      store1<BF16>(a.out, (r * a.heads + h) * a.dv + row, o);
+    }
+    if (blockIdx.x == 0 && h % (a.heads / a.key_heads) == 0)
+      for (int i = threadIdx.x; i < DK; i += 64 * kWaves) a.keys[(r * a.key_heads + kh) * DK + i] = rows[0][i];
+  }
+  for (int v = count; v < a.nodes; ++v) {
+    const int64_t r = first + v;
+    if (lane < 16) {
+      a.updates[(r * a.heads + h) * a.dv + row] = 0.0f;
+      store1<BF16>(a.out, (r * a.heads + h) * a.dv + row, 0.0f);
+    }
+    if (blockIdx.x == 0 && h % (a.heads / a.key_heads) == 0)
+      for (int i = threadIdx.x; i < DK; i += 64 * kWaves) a.keys[(r * a.key_heads + kh) * DK + i] = 0.0f;
+  }
+}
+
+// The accepted path of a tree into one state: e^G_end S + sum_i e^(G_end - G_i)
+// u_i k_i^T over the root and the path, the sums of the decays behind each node in
+// 64 bits.  A wave holds COLS * 16 rows of the state and takes the keys from LDS.
+// grid (layers * dv / (64 COLS), heads, seqs).
+template <int DK, int COLS>
+__global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitArgs a) {
+  __shared__ float keys[kTile][DK];
+  const int b = blockIdx.z, h = blockIdx.y, parts = a.dv / (64 * COLS), layer = blockIdx.x / parts;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int src = a.src[b];
+  if (!delta_used(src, a.slots)) return;
+  const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
+  if (to < 0) return;
+  const int kh = h / (a.heads / a.key_heads);
+  const int row0 = ((blockIdx.x - layer * parts) * kWaves + wave) * 16 * COLS;
+  const int64_t state_size = (int64_t)a.dv * DK;
+  float* states = a.states + (int64_t)layer * a.slots * a.heads * state_size;
+  StateTile<DK, COLS> x;
+  if (src >= 0) load_state<DK, COLS>(states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
+  else zero_state<DK, COLS>(x);
+  // lane i: node i of the path (the root first), its decay and what follows it
+  const int32_t* res = a.result + (int64_t)b * (3 + a.nodes);
+  int n = res[1] + 1;
+  n = n < 1 ? 1 : n < a.nodes ? n : a.nodes;
+  int node = lane == 0 ? 0 : lane < n ? res[2 + lane] : -1;
+  if (node >= a.nodes) node = -1;
+  const int64_t first = ((int64_t)layer * a.seqs + b) * a.nodes;
+  const double decay = node >= 0 ? (double)a.g[(first + node) * a.heads + h] : 0.0;
+  double after = 0.0;  // sum of the decays behind this node
+  {
+    double s = decay;
+    for (int off = 1; off < 64; off <<= 1) {
+      const double o = __shfl_down(s, off);
+      s += lane + off < 64 ? o : 0.0;
+    }
+    const double all = __shfl(s, 0);
+    const double o = __shfl_down(s, 1);
+    after = lane < 63 ? o : 0.0;
+    const float f = expf((float)all);
+#pragma unroll
+    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t) x.s[c][t] *= f;
+  }
+  const float weight = node >= 0 ? expf((float)after) : 0.0f;
+  for (int t0 = 0; t0 < n; t0 += kTile) {
+    const int m = n - t0 < kTile ? n - t0 : kTile;
+    __syncthreads();
+    for (int i = wave; i < m; i += kWaves) {
+      const int v = __builtin_amdgcn_readlane(node, t0 + i);
+      if (v >= 0 && lane < DK / 4)
+        *reinterpret_cast<f4_t*>(&keys[i][4 * lane]) =
+            load4<false>(a.keys, ((first + v) * a.key_heads + kh) * DK + 4 * lane);
+    }
+    __syncthreads();
+    for (int i = 0; i < m; ++i) {
+      const int v = __builtin_amdgcn_readlane(node, t0 + i);
+      if (v < 0) continue;
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), t0 + i));
+      float u[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+        u[c] = w * a.updates[((first + v) * a.heads + h) * a.dv + row0 + 16 * c + j];
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t) {
+        const f4_t k = *reinterpret_cast<const f4_t*>(&keys[i][16 * t + 4 * g]);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) x.s[c][t] += u[c] * k;
+      }
+    }
+  }
+  store_state<DK, COLS>(states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
+}
+
+template <int DK, bool BF16>
+void step(const DeltaArgs& a, hipStream_t stream) {
+  delta_step_kernel<DK, 1, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+}
+
+template <int DK, bool BF16>
+void tree(const DeltaArgs& a, hipStream_t stream) {
+  delta_tree_kernel<DK, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+}
+
+template <int DK>
+void commit(const DeltaCommitArgs& a, hipStream_t stream) {
+  delta_commit_kernel<DK, 1><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+}
+
+}  // namespace
+
+int64_t delta_rule_workspace_bytes(const DeltaArgs&) { return 0; }
+
+hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
+  if (a.dk == 64) a.bf16 ? step<64, true>(a, stream) : step<64, false>(a, stream);
+  else if (a.dk == 128) a.bf16 ? step<128, true>(a, stream) : step<128, false>(a, stream);
+  else a.bf16 ? step<256, true>(a, stream) : step<256, false>(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_tree(const DeltaArgs& a, hipStream_t stream) {
+  if (a.dk == 64) a.bf16 ? tree<64, true>(a, stream) : tree<64, false>(a, stream);
+  else if (a.dk == 128) a.bf16 ? tree<128, true>(a, stream) : tree<128, false>(a, stream);
+  else a.bf16 ? tree<256, true>(a, stream) : tree<256, false>(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_commit(const DeltaCommitArgs& a, hipStream_t stream) {
+  if (a.dk == 64) commit<64>(a, stream);
+  else if (a.dk == 128) commit<128>(a, stream);
+  else commit<256>(a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,98 @@
+// Device-side helpers of the gated delta rule's kernels.
+#pragma once
+
+#include "device_common.h"
+#include "hybrid_launch.h"
+
+namespace nvfp4 {
+
+// Four values of a row of q, k or v from value `at` on, at a multiple of four.
+template <bool BF16>
+__device__ __forceinline__ f4_t load4(const void* rows, int64_t at) {
+  if constexpr (BF16) {
+    const u2_t w = *reinterpret_cast<const u2_t*>(static_cast<const uint16_t*>(rows) + at);
+    return f4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                __uint_as_float(w.y & 0xFFFF0000u)};
+  } else {
+    return *reinterpret_cast<const f4_t*>(static_cast<const float*>(rows) + at);
+  }
+}
+
+// One value to out, rounded to nearest even; NaN stays NaN.
+template <bool BF16>
+__device__ __forceinline__ void store1(void* out, int64_t at, float x) {
+  if constexpr (BF16) static_cast<__bf16*>(out)[at] = (__bf16)x;
+  else static_cast<float*>(out)[at] = x;
+}
+
+__device__ __forceinline__ float sum_of_wave(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  return x;
+}
+
+// Sum over the four 16-lane groups of a wave, in all of them.
+__device__ __forceinline__ float sum_of_groups(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// Tokens of a sequence; 0 where it is not in use.
+__device__ __forceinline__ bool delta_used(int src, int slots) { return src >= -1 && src < slots; }
+
+__device__ __forceinline__ int delta_count(const int32_t* counts, int nodes, int b) {
+  const int n = counts ? counts[b] : nodes;
+  return n < 0 ? 0 : n < nodes ? n : nodes;
+}
+
+// The slot that sequence b's state goes to, -1: none.  It must be in range, the
+// src of no other sequence in use and the dst of no earlier one.  Every lane of
+// the wave calls it.
+__device__ __forceinline__ int delta_dst(const int32_t* src, const int32_t* dst, int seqs, int slots, int b) {
+  const int to = dst[b];
+  if (to < 0 || to >= slots) return -1;
+  bool taken = false;
+  for (int i = threadIdx.x & 63; i < seqs; i += 64) {
+    const int s = src[i];
+    taken |= i != b && delta_used(s, slots) && (s == to || (i < b && dst[i] == to));
+  }
+  return __any(taken) ? -1 : to;
+}
+
+// A wave's share of a state: 16 * COLS of its dv rows, all DK of their values.
+// Lane j + 16 g holds values 16 t + 4 g .. + 3 of row 16 c + j, which is also how
+// a 16x16 matrix product leaves its result (row index 16 t + 4 g + e, column j).
+template <int DK, int COLS>
+struct StateTile {
+  f4_t s[COLS][DK / 16];
+};
+
+template <int DK, int COLS>
+__device__ __forceinline__ void load_state(const float* state, StateTile<DK, COLS>& x) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int c = 0; c < COLS; ++c)
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+      x.s[c][t] = *reinterpret_cast<const f4_t*>(state + (16 * c + j) * DK + 16 * t + 4 * g);
+}
+
+template <int DK, int COLS>
+__device__ __forceinline__ void store_state(float* state, const StateTile<DK, COLS>& x) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int c = 0; c < COLS; ++c)
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+      *reinterpret_cast<f4_t*>(state + (16 * c + j) * DK + 16 * t + 4 * g) = x.s[c][t];
+}
+
+template <int DK, int COLS>
+__device__ __forceinline__ void zero_state(StateTile<DK, COLS>& x) {
+#pragma unroll
+  for (int c = 0; c < COLS; ++c)
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t) x.s[c][t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+}  // namespace nvfp4

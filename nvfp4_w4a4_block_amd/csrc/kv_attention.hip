@@ -56,6 +56,7 @@
 
 #include "device_common.h"
 #include "kv_launch.h"
+#include "kv_tree.h"
 
 namespace nvfp4 {
 namespace {
@@ -211,25 +212,6 @@ __device__ __forceinline__ Place find_item(const KvAttentionArgs& a, const Plan&
   }
   __syncthreads();
   return {__builtin_amdgcn_readfirstlane(found[0]), __builtin_amdgcn_readfirstlane(found[1])};
-}
-
-// Ancestor-or-self bits of node v of a tree of at most 64 nodes, lane = node:
-// parent pointers doubled six times.  A parent outside [0, v) makes v a root.
-__device__ __forceinline__ uint64_t ancestors_of_wave(int par) {
-  const int lane = threadIdx.x & 63;
-  uint64_t mask = 1ull << lane;
-  int p = par >= 0 && par < lane ? par : -1;
-#pragma unroll
-  for (int s = 0; s < 6; ++s) {
-    const int at = p < 0 ? lane : p;
-    const uint64_t up = __shfl(mask, at);
-    const int pp = __shfl(p, at);
-    if (p >= 0) {
-      mask |= up;
-      p = pp;
-    }
-  }
-  return mask;
 }
 
 // The thread's index, computed anew where it is called: what derives from it is
