@@ -547,7 +547,7 @@ nvfp4_status nvfp4_kv_fork(int64_t n, int64_t S, int64_t W, int64_t P, int64_t p
 nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t R,
                                   int64_t page_size, int64_t P, int64_t W, const void* q, const void* k,
                                   const void* v, nvfp4_dtype dt, int64_t q_stride, int64_t k_stride,
-                                  int64_t v_stride, const double* inv_freq, float rope_scale, int interleaved,
+                                  int64_t v_stride, const double* inv_freq, double rope_scale, int interleaved,
                                   const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,
                                   int64_t page_stride, const int32_t* table, const int32_t* lens,
                                   const int32_t* parent, const int32_t* counts, void* q_out, void* stream);

@@ -87,7 +87,7 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_kv_compact.argtypes = [i64] * 8 + [p, p, i64, i64, p, p, p, p, p]
     lib.nvfp4_kv_resize.argtypes = [i64] * 5 + [p] * 8
     lib.nvfp4_kv_fork.argtypes = [i64] * 5 + [p] * 9 + [i64] * 3 + [p, p, i64, i64, p]
-    lib.nvfp4_kv_append_rope.argtypes = [i64] * 9 + [p, p, p, i32, i64, i64, i64, p, f32, i32, p, p, p, p, i64,
+    lib.nvfp4_kv_append_rope.argtypes = [i64] * 9 + [p, p, p, i32, i64, i64, i64, p, ctypes.c_double, i32, p, p, p, p, i64,
                                                      p, p, p, p, p, p]
     lib.nvfp4_delta_rule_workspace_bytes.argtypes = [i64] * 6 + [i32]
     lib.nvfp4_delta_rule_workspace_bytes.restype = i64

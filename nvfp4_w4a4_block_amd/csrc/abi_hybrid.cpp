@@ -21,7 +21,7 @@ bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0;
 bool dtype_ok(int dt) { return dt == NVFP4_F32 || dt == NVFP4_BF16; }
 nvfp4_status from_hip(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP; }
 bool dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
-bool finite(float x) { return x > -__builtin_inff() && x < __builtin_inff(); }
+bool is_finite(double x) { return x > -__builtin_inf() && x < __builtin_inf(); }
 int64_t size_of(nvfp4_dtype dt) { return dt == NVFP4_BF16 ? 2 : 4; }
 
 bool rows_ok(int64_t B, int64_t M) {
@@ -96,7 +96,7 @@ nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, cons
 bool delta_values_ok(int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, nvfp4_dtype dt, int64_t q_stride,
                      int64_t k_stride, int64_t v_stride, float scale, float norm_eps) {
   return stride_ok(q_stride, Hk * Dk, dt) && stride_ok(k_stride, Hk * Dk, dt) && stride_ok(v_stride, H * Dv, dt) &&
-         finite(scale) && finite(norm_eps);
+         is_finite(scale) && is_finite(norm_eps);
 }
 
 }  // namespace
@@ -106,7 +106,7 @@ extern "C" {
 nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, int64_t R,
                                   int64_t page_size, int64_t P, int64_t W, const void* q, const void* k,
                                   const void* v, nvfp4_dtype dt, int64_t q_stride, int64_t k_stride,
-                                  int64_t v_stride, const double* inv_freq, float rope_scale, int interleaved,
+                                  int64_t v_stride, const double* inv_freq, double rope_scale, int interleaved,
                                   const float* k_scale, const float* v_scale, uint8_t* k_pages, uint8_t* v_pages,
                                   int64_t page_stride, const int32_t* table, const int32_t* lens,
                                   const int32_t* parent, const int32_t* counts, void* q_out, void* stream) {
@@ -116,7 +116,7 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
       P >= kMaxInt || W < 1 || W > kMaxTokens / page_size || (B > 0 && W > kMaxTable / B) ||
       page_stride < H * page_size * D || page_stride >= kMaxInt || page_stride % 16 != 0 ||
       !stride_ok(q_stride, Hq * D, dt) || !stride_ok(k_stride, H * D, dt) || !stride_ok(v_stride, H * D, dt) ||
-      !finite(rope_scale) || (parent && M > 64))
+      !is_finite(rope_scale) || (parent && M > 64))
     return NVFP4_ERR_SHAPE;
   if (B == 0 || M == 0) return NVFP4_OK;
   if (!q || !k || !v || !inv_freq || !k_scale || !v_scale || !k_pages || !v_pages || !table || !lens || !q_out)

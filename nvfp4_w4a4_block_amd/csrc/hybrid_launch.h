@@ -18,7 +18,7 @@ struct KvRopeArgs {
   int rotary;  // values of a head that turn
   bool interleaved;
   const double* inv_freq;  // [rotary / 2] radians per position
-  float rope_scale;
+  double rope_scale;
   const int32_t* parent;  // optional [seqs][nodes]
   void* q_out;            // [seqs][nodes][q_heads][dim]
 };

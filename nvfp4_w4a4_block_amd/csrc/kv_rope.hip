@@ -11,7 +11,8 @@
 // scaled cosine and sine of p * inv_freq.  The angle in turns, p * inv_freq / 2 pi,
 // is a product of 64 bits whose whole part is dropped there: at position 2^30 it is
 // off by 2^-24 turns at most, where 32 bits would keep nothing of it.  What is
-// left, at most half a turn, is rounded to fp32 (2^-26 turns).
+// left goes to sine and cosine in 64 bits, too (14 multiply-adds), which are rounded
+// to fp32 once, with the factor in them.
 //
 // Bounds.  Every value is read and written once: memory for prompts, the launch
 // for a tree.  A workgroup takes the tokens of one sequence from `first` on, works
@@ -68,6 +69,29 @@ __device__ __forceinline__ u2_t codes8(const float (&x)[8], float inv) {
               e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv)};
 }
 
+// Cosine and sine of x turns, |x| <= 1/2: the series of both within an eighth of a
+// turn (what is left out is below 7e-12), exchanged and signed by the quarter.
+__device__ __forceinline__ void turn(double x, double& c, double& s) {
+  const double quarter = __builtin_rint(4.0 * x);
+  const double r = (x - 0.25 * quarter) * 6.283185307179586477, z = r * r;
+  double si = -1.0 / 39916800.0, co = 1.0 / 479001600.0;
+  si = __builtin_fma(si, z, 1.0 / 362880.0);
+  si = __builtin_fma(si, z, -1.0 / 5040.0);
+  si = __builtin_fma(si, z, 1.0 / 120.0);
+  si = __builtin_fma(si, z, -1.0 / 6.0);
+  si = __builtin_fma(si * z, r, r);
+  co = __builtin_fma(co, z, -1.0 / 3628800.0);
+  co = __builtin_fma(co, z, 1.0 / 40320.0);
+  co = __builtin_fma(co, z, -1.0 / 720.0);
+  co = __builtin_fma(co, z, 1.0 / 24.0);
+  co = __builtin_fma(co, z, -0.5);
+  co = __builtin_fma(co, z, 1.0);
+  const int k = (int)quarter & 3;
+  const double a = (k & 1) ? si : co, b = (k & 1) ? co : si;
+  c = (k == 1 || k == 2) ? -a : a;
+  s = (k & 2) ? -b : b;
+}
+
 // grid (ceil(nodes / span), seqs, parts): part p of the parts takes every
 // parts-th of the tokens' units of 16 values.
 template <bool BF16, bool INTERLEAVED>
@@ -105,11 +129,10 @@ __global__ __launch_bounds__(256) void kv_append_rope_kernel(KvRopeArgs a, int s
     const int t = i / half, j = i - t * half;
     const int64_t pos = (int64_t)len + (a.parent ? depths[first + t] : first + t);
     const double turns = (double)pos * (a.inv_freq[j] * 0.15915494309189533577);
-    const float f = (float)(turns - __builtin_rint(turns));
-    float s, co;
-    sincospif(2.0f * f, &s, &co);
-    cs[t][0][j] = co * a.rope_scale;
-    cs[t][1][j] = s * a.rope_scale;
+    double co, si;
+    turn(turns - __builtin_rint(turns), co, si);
+    cs[t][0][j] = (float)(co * a.rope_scale);
+    cs[t][1][j] = (float)(si * a.rope_scale);
   }
   __syncthreads();
   const int per = c.dim >> 4, heads = a.q_heads + 2 * c.heads, turning = a.rotary >> 4;

@@ -537,8 +537,8 @@ def check_logprobs(z, tokens, top, got):
         span = min(104.0, float(live.max() - live.min()))
         # every e^(z - m): z - m is rounded once, e^x by 2^-23; sums as the docstring has them
         rel = (span + 2) * 2.0 ** -23 + (N / 64 + 64) * 2.0 ** -24
-        total = np.exp(-abs(b[0])) if top else 1.0  # 1 / (1 + a)
-        small = 1.0 - total if top else 1.0  # log1p(a) is off by rel a / (1 + a) at most
+        # log1p(a) is off by rel a / (1 + a) at most, and a / (1 + a) = 1 - e^(the best's log p)
+        small = -np.expm1(b[0]) if top else 1.0
         assert abs(ent[i] - e) <= 2 * rel * (e + small) + 2.0 ** -22 * e + 1e-37, (i, ent[i], e)
         for x, y in [(lp[i], a)] + list(zip(best[i], b)):
             if not np.isfinite(y):
