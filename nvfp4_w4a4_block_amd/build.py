@@ -36,6 +36,7 @@ SOURCES = {
     "kv_attention.hip": [],
     "kv_rope.hip": [],
     "delta.hip": [],
+    "delta_chunk.hip": [],
     "logprobs.hip": [],
     "gemm_tiled.hip": [],
     "stream.hip": [],

@@ -297,9 +297,15 @@ void commit(const DeltaCommitArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t delta_rule_workspace_bytes(const DeltaArgs&) { return 0; }
+int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {
+  return delta_chunked(a) ? delta_chunk_workspace_bytes(a) : 0;
+}
 
 hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
+  if (delta_chunked(a) && a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
+    launch_delta_chunks(a, stream);
+    return hipGetLastError();
+  }
   if (a.dk == 64) a.bf16 ? step<64, true>(a, stream) : step<64, false>(a, stream);
   else if (a.dk == 128) a.bf16 ? step<128, true>(a, stream) : step<128, false>(a, stream);
   else a.bf16 ? step<256, true>(a, stream) : step<256, false>(a, stream);

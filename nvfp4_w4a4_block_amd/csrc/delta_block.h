@@ -1,0 +1,421 @@
+// The gated delta rule for a block of tokens at once, on the matrix cores.
+//
+// Mathematics.  In a block that begins with state S, with G_i the sums of the log
+// decays up to token i (along its line in a tree),
+//   u_i + beta_i sum_j e^(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - e^G_i S k_i),
+// j the tokens before i (its ancestors): (I + A) u = diag(beta) r with A strictly
+// lower triangular.  Once T = (I + A)^-1 diag(beta) is known, a block is five matrix
+// products: r = v - e^G (K S), u = T r, o = e^G (Q S) + P u with P_ij = e^(G_i - G_j)
+// q_i . k_j, and S <- e^G_end S + K^T diag(e^(G_end - G)) u.  T and P need neither S
+// nor v: they are prepared for all blocks at once, and what one block waits for in
+// the one before it are the five products alone.
+//
+// Operands.  A 16x16x32 f16 product wants 8 values of its inner dimension a lane.
+// With the inner order 32 s + 4 g .. + 3, 32 s + 16 + 4 g .. + 3 for lane group g, a
+// result (rows 4 g .. 4 g + 3 of a tile, one column a lane) is an operand as it
+// stands.  So S, r and u stay in the registers of the wave whose columns they are,
+// and everything prepared is stored in operand order: one 16-byte load a lane.
+//
+// Accuracy.  Every factor on the way to a state keeps 22 bits: two f16 parts (rounded
+// to nearest, the second the rest of the first), of which the product of the two
+// second ones is left out, 2^-22.  A bf16 row of k is exact in one part.  f16's range
+// is 2^40: rows of k, q, T and P are scaled by a power of two to a largest value of 1
+// to 2, columns of r by one to 8 to 16, and a column of S, with what is added to it, by
+// one to 32 to 64, so that 64 products fit (values 2^-30 below a row's or column's
+// largest lose bits: as fp32 sums would). In bf16 calls what reaches out alone (S
+// and Q in Q S, P and u in P u) is rounded to f16, an eighth of out's own step.
+#pragma once
+
+#include "delta_common.h"
+
+namespace nvfp4 {
+
+typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 64;  // tokens of a block
+
+__device__ __forceinline__ f4_t scale4(f4_t x, int e) {
+  return f4_t{__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e), __builtin_amdgcn_ldexpf(x[2], e),
+              __builtin_amdgcn_ldexpf(x[3], e)};
+}
+
+__device__ __forceinline__ float max4(float m, f4_t x) {
+  m = fmaxf(fmaxf(m, fabsf(x[0])), fabsf(x[1]));
+  return fmaxf(fmaxf(m, fabsf(x[2])), fabsf(x[3]));
+}
+
+// Over the four lane groups, in all of them.
+__device__ __forceinline__ float max_of_groups(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// floor(log2 x) of x > 0; 0 of 0.
+__device__ __forceinline__ int exponent_of(float x) {
+  return x > 0.0f ? (int)((__float_as_uint(x) >> 23) & 255) - 127 : 0;
+}
+
+__device__ __forceinline__ h4_t to_half(f4_t x) { return __builtin_convertvector(x, h4_t); }
+__device__ __forceinline__ f4_t rest_of(f4_t x, h4_t hi) { return x - __builtin_convertvector(hi, f4_t); }
+__device__ __forceinline__ h8_t join8(h4_t a, h4_t b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// Two result tiles as the operand of a product over their rows.
+__device__ __forceinline__ h8_t operand_hi(f4_t a, f4_t b) { return join8(to_half(a), to_half(b)); }
+
+__device__ __forceinline__ void operand_parts(f4_t a, f4_t b, h8_t& hi, h8_t& lo) {
+  const h4_t p = to_half(a), q = to_half(b);
+  hi = join8(p, q);
+  lo = join8(to_half(rest_of(a, p)), to_half(rest_of(b, q)));
+}
+
+// What is prepared of a block, in units of an operand of one lane (16 bytes).  PARTS:
+// f16 parts of rows of k and q, and of P.
+template <int DK, bool BF16, int NT>
+struct BlockOps {
+  static constexpr int kParts = BF16 ? 1 : 2;
+  static constexpr int kSteps = DK / 32;                 // inner steps over dk
+  static constexpr int kTokenSteps = (NT + 1) / 2;       // over tokens
+  static constexpr int kLower = NT == 1 ? 1 : NT == 2 ? 2 : NT == 3 ? 4 : 6;  // of lower triangular rows
+  static constexpr int kRows = NT * kSteps * 64;         // K or Q, one part
+  static constexpr int kCols = DK / 16 * kTokenSteps * 64;  // K transposed, one part
+  static constexpr int kKey = 0, kQuery = kParts * kRows, kKeyT = 2 * kParts * kRows;
+  static constexpr int kKeyUnits = kKeyT + kParts * kCols;  // of a key head
+  static constexpr int kT = 0, kP = 2 * kLower * 64, kFactors = kP + kParts * kLower * 64;
+  static constexpr int kHeadUnits = kFactors + 4 * 4 * NT + 1;  // of a value head: factors [4][16 NT], then e^G_end
+  // steps of the rows of tile rt begin at this one
+  static __device__ constexpr int lower(int rt) { return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? 2 : 4; }
+};
+
+// Factors of a block's rows.
+enum { kFactorR, kFactorX, kFactorQ, kFactorP };
+
+template <int DK, bool BF16, int NT>
+struct BlockShared {
+  static constexpr int kPitch = 16 * NT + 4;
+  h8_t key[BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows];
+  float a[16 * NT][kPitch];  // A, then T
+  float p[16 * NT][kPitch];  // P
+  double decay[64];          // G
+  uint64_t line[64];         // trees: ancestors and self
+  float beta[64], key_factor[64], query_factor[64];
+  int t_exponent[64];
+};
+
+// A tile's 16 rows of k or q as an operand: lane j + 16 g has its values of row j.
+// Returns the factor that makes the stored row the row as used.
+template <int DK, bool BF16>
+__device__ __forceinline__ float row_operand(const void* rows, int64_t at, bool there, float eps,
+                                             h8_t (&op)[BF16 ? 1 : 2][DK / 32]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  f4_t x[DK / 32][2];
+  float m = 0.0f;
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[s][h] = there ? load4<BF16>(rows, at + 32 * s + 16 * h + 4 * g) : f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      m = max4(m, x[s][h]);
+    }
+  const int e = exponent_of(max_of_groups(m));
+  float ss = 0.0f;
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[s][h] = scale4(x[s][h], -e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = __builtin_fmaf(x[s][h][i], x[s][h][i], ss);
+    }
+    if constexpr (BF16) op[0][s] = operand_hi(x[s][0], x[s][1]);
+    else operand_parts(x[s][0], x[s][1], op[0][s], op[1][s]);
+  }
+  if (!there) return 0.0f;
+  if (eps < 0.0f) return __builtin_amdgcn_ldexpf(1.0f, e);
+  const double square = (double)sum_of_groups(ss) + __builtin_amdgcn_ldexp((double)eps, -2 * e);
+  return (float)(1.0 / __builtin_sqrt(square));
+}
+
+// a b^T of two tiles' rows, with `parts` as above: 16x16.
+template <int STEPS, int PARTS>
+__device__ __forceinline__ f4_t rows_product(const h8_t (&a)[PARTS][STEPS], const h8_t* b, int pitch) {
+  f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const h8_t hi = b[s * 64 + lane];
+    acc = mfma16x16x32(a[0][s], hi, acc);
+    if constexpr (PARTS == 2) {
+      acc = mfma16x16x32(a[0][s], b[pitch + s * 64 + lane], acc);
+      acc = mfma16x16x32(a[1][s], hi, acc);
+    }
+  }
+  return acc;
+}
+
+// c + a b of 16x16 blocks in fp32, a in LDS with `pitch`, b as a result stands.
+__device__ __forceinline__ f4_t block_product(const float* a, int pitch, f4_t b, f4_t c) {
+  const int lane = threadIdx.x & 63;
+  const f4_t x = *reinterpret_cast<const f4_t*>(a + (lane & 15) * pitch + 4 * (lane >> 4));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ f4_t load_block(const float* a, int pitch) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  return f4_t{a[(4 * g) * pitch + j], a[(4 * g + 1) * pitch + j], a[(4 * g + 2) * pitch + j], a[(4 * g + 3) * pitch + j]};
+}
+
+__device__ __forceinline__ void store_block(float* a, int pitch, f4_t x) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[(4 * g + i) * pitch + j] = x[i];
+}
+
+// (I + A)^-1 of a 16x16 block in place, by substitution, a column a lane.
+__device__ __forceinline__ void invert_block(float* a, int pitch) {
+  const int j = threadIdx.x & 15;
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float sum = i == j ? 1.0f : 0.0f;
+#pragma unroll
+    for (int m4 = 0; m4 < (i + 3) / 4; ++m4) {
+      const f4_t r = *reinterpret_cast<const f4_t*>(a + i * pitch + 4 * m4);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        if (4 * m4 + m < i) sum = __builtin_fmaf(-r[m], x[4 * m4 + m], sum);
+    }
+    x[i] = sum;
+  }
+  if ((threadIdx.x & 63) < 16)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i * pitch + j] = x[i];
+}
+
+// The largest magnitude of a row of operands to 1 .. 2; returns its exponent.
+template <int PARTS>
+__device__ __forceinline__ int store_rows(const f4_t (&x)[2][2], int steps, h8_t* to, int pitch) {
+  const int lane = threadIdx.x & 63;
+  float m = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (s < steps) m = max4(max4(m, x[s][0]), x[s][1]);
+  const int e = exponent_of(max_of_groups(m));
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (s >= steps) continue;
+    const f4_t p = scale4(x[s][0], -e), q = scale4(x[s][1], -e);
+    if constexpr (PARTS == 1) {
+      to[s * 64 + lane] = operand_hi(p, q);
+    } else {
+      h8_t hi, lo;
+      operand_parts(p, q, hi, lo);
+      to[s * 64 + lane] = hi;
+      to[pitch + s * 64 + lane] = lo;
+    }
+  }
+  return e;
+}
+
+// Prepares the n tokens from row `first` on of value head h (key head kh), n <= 16 NT,
+// by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
+// head's part (NULL: not wanted), head_to: the value head's.
+template <int DK, bool BF16, int NT, bool TREE>
+__device__ __forceinline__ void prepare_block(const DeltaArgs& a, int b, int64_t first, int n, int h, int kh,
+                                              BlockShared<DK, BF16, NT>& sh, h8_t* key_to, h8_t* head_to) {
+  typedef BlockOps<DK, BF16, NT> Ops;
+  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT>::kPitch;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
+  const bool works = w < NT;
+  const int64_t row = first + 16 * w + j;
+  const bool there = works && 16 * w + j < n;
+  h8_t key[P][Ops::kSteps], query[P][Ops::kSteps];
+  if (works) {
+    const float kf = row_operand<DK, BF16>(a.k, row * a.k_stride + (int64_t)kh * DK, there, a.norm_eps, key);
+    const float qf = row_operand<DK, BF16>(a.q, row * a.q_stride + (int64_t)kh * DK, there, a.norm_eps, query);
+    if (g == 0) {
+      sh.key_factor[16 * w + j] = kf;
+      sh.query_factor[16 * w + j] = qf * a.scale;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int s = 0; s < Ops::kSteps; ++s) {
+        const int at = p * Ops::kRows + (w * Ops::kSteps + s) * 64 + lane;
+        sh.key[at] = key[p][s];
+        if (key_to) {
+          key_to[Ops::kKey + at] = key[p][s];
+          key_to[Ops::kQuery + at] = query[p][s];
+        }
+      }
+  }
+  if (w == 0) {
+    float gl = lane < n ? a.g[(first + lane) * a.heads + h] : 0.0f;
+    sh.beta[lane] = lane < n ? a.beta[(first + lane) * a.heads + h] : 0.0f;
+    gl = gl < -1e4f ? -1e4f : gl;  // e^-1e4 is 0, and differences of sums stay finite
+    double sum = gl;
+    if constexpr (TREE) {
+      const int par = lane < n ? a.parent[first + lane] : -1;
+      uint64_t mask = 1ull << lane;
+      int up = par >= 0 && par < lane ? par : -1;
+#pragma unroll
+      for (int s = 0; s < 6; ++s) {  // pointers doubled
+        const int at = up < 0 ? lane : up;
+        const uint64_t m = __shfl(mask, at);
+        const double d = __shfl(sum, at);
+        const int u = __shfl(up, at);
+        if (up >= 0) {
+          mask |= m;
+          sum += d;
+          up = u;
+        }
+      }
+      sh.line[lane] = mask;
+    } else {
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(sum, off);
+        sum += lane >= off ? o : 0.0;
+      }
+    }
+    sh.decay[lane] = sum;
+  }
+  __syncthreads();
+  if (works) {
+    double gi[4];
+    float bi[4], ki[4], qi[4];
+    uint64_t line[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * w + 4 * g + e;
+      gi[e] = sh.decay[i];
+      bi[e] = sh.beta[i];
+      ki[e] = sh.key_factor[i];
+      qi[e] = sh.query_factor[i];
+      line[e] = TREE ? sh.line[i] : 0;
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      if (c > w) {
+        if (c == w + 1 && (w & 1) == 0) {  // the other half of a step over tokens
+          store_block(&sh.a[16 * w][16 * c], pitch, f4_t{0.0f, 0.0f, 0.0f, 0.0f});
+          store_block(&sh.p[16 * w][16 * c], pitch, f4_t{0.0f, 0.0f, 0.0f, 0.0f});
+        }
+        continue;
+      }
+      const h8_t* kc = sh.key + c * Ops::kSteps * 64;
+      f4_t kk = rows_product<Ops::kSteps, P>(key, kc, Ops::kRows);
+      f4_t qk = rows_product<Ops::kSteps, P>(query, kc, Ops::kRows);
+      const int col = 16 * c + j;
+      const double gj = sh.decay[col];
+      const float kj = sh.key_factor[col];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * w + 4 * g + e;
+        const bool seen = TREE ? ((line[e] >> col) & 1) != 0 : col <= i;
+        const float d = expf((float)(gi[e] - gj)) * kj;
+        kk[e] = seen && col < i ? bi[e] * ki[e] * d * kk[e] : 0.0f;
+        qk[e] = seen ? qi[e] * d * qk[e] : 0.0f;
+      }
+      store_block(&sh.a[16 * w][16 * c], pitch, kk);
+      store_block(&sh.p[16 * w][16 * c], pitch, qk);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    invert_block(&sh.a[16 * w][16 * w], pitch);
+  }
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (NT >= 2) {
+    __syncthreads();
+    if (w < NT / 2) {  // -T_11 A_10 T_00 of each pair of tiles
+      float* at = &sh.a[32 * w + 16][32 * w];
+      const f4_t y = block_product(at, pitch, load_block(&sh.a[32 * w][32 * w], pitch), zero);
+      store_block(at, pitch, -block_product(at + 16, pitch, y, zero));
+    }
+  }
+  if constexpr (NT >= 3) {
+    __syncthreads();
+    // rows of tile r, columns of tile c: -sum_m T_rm (A_m0 T_0c + A_m1 T_1c)
+    const int c = w & 1, r = 2 + (w >> 1);
+    f4_t z = zero;
+    if (works && r < NT) {
+      const f4_t t0 = load_block(&sh.a[0][16 * c], pitch), t1 = load_block(&sh.a[16][16 * c], pitch);
+#pragma unroll
+      for (int m = 2; m < NT; ++m) {
+        if (m > r) continue;
+        f4_t y = block_product(&sh.a[16 * m][16], pitch, t1, zero);
+        if (c == 0) y = block_product(&sh.a[16 * m][0], pitch, t0, y);
+        z = block_product(&sh.a[16 * r][16 * m], pitch, y, z);
+      }
+    }
+    __syncthreads();
+    if (works && r < NT) store_block(&sh.a[16 * r][16 * c], pitch, -z);
+  }
+  __syncthreads();
+  float* factors = reinterpret_cast<float*>(head_to + Ops::kFactors);
+  const int steps = w / 2 + 1;
+  if (works) {
+    f4_t x[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int col = 32 * s + 16 * half + 4 * g;
+        if (s >= steps || col >= 16 * NT) {
+          x[s][half] = zero;
+          continue;
+        }
+        x[s][half] = *reinterpret_cast<const f4_t*>(&sh.a[16 * w + j][col]) * *reinterpret_cast<const f4_t*>(&sh.beta[col]);
+      }
+    const int e = store_rows<2>(x, steps, head_to + Ops::kT + Ops::lower(w) * 64, Ops::kLower * 64);
+    if (g == 0) sh.t_exponent[16 * w + j] = e;
+  }
+  __syncthreads();
+  if (works) {
+    f4_t x[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int col = 32 * s + 16 * half + 4 * g;
+        if (s >= steps || col >= 16 * NT) {
+          x[s][half] = zero;
+          continue;
+        }
+        const f4_t y = *reinterpret_cast<const f4_t*>(&sh.p[16 * w + j][col]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[s][half][i] = __builtin_amdgcn_ldexpf(y[i], sh.t_exponent[col + i]);
+      }
+    const int e = store_rows<P>(x, steps, head_to + Ops::kP + Ops::lower(w) * 64, Ops::kLower * 64);
+    if (g == 0) {
+      const int i = 16 * w + j;
+      const double at = sh.decay[i], end = sh.decay[16 * NT - 1];
+      const float into = expf((float)at), kf = sh.key_factor[i];
+      factors[kFactorR * 16 * NT + i] = -into * kf;
+      factors[kFactorX * 16 * NT + i] = __builtin_amdgcn_ldexpf(kf * expf((float)(end - at)), sh.t_exponent[i]);
+      factors[kFactorQ * 16 * NT + i] = into * sh.query_factor[i];
+      factors[kFactorP * 16 * NT + i] = __builtin_amdgcn_ldexpf(1.0f, e);
+      if (i == 0) factors[4 * 16 * NT] = expf((float)end);
+    }
+    if (key_to && !TREE) {
+      // K transposed: lane j + 16 g has tokens 32 s + 4 g .., 32 s + 16 + 4 g .. of value 16 t + j
+      const _Float16* from = reinterpret_cast<const _Float16*>(sh.key);
+#pragma unroll 1
+      for (int u = w; u < P * (DK / 16) * Ops::kTokenSteps; u += NT) {
+        const int part = u / ((DK / 16) * Ops::kTokenSteps), v = u - part * ((DK / 16) * Ops::kTokenSteps);
+        const int t = v / Ops::kTokenSteps, s = v - t * Ops::kTokenSteps;
+        h8_t x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rt = 2 * s + (i >> 2), tok = 4 * g + (i & 3);
+          const int unit = part * Ops::kRows + (rt * Ops::kSteps + (t >> 1)) * 64 + tok + 16 * (j >> 2);
+          x[i] = rt < NT ? from[unit * 8 + 4 * (t & 1) + (j & 3)] : (_Float16)0.0f;
+        }
+        key_to[Ops::kKeyT + part * Ops::kCols + v * 64 + lane] = x;
+      }
+    }
+  }
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,286 @@
+// Gated delta rule over chains of some length, 64 tokens at a time.
+//
+// The page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic Benchmark 6.4x
+// Faster on Jetson AGX Thor" prefills only the new suffix of a turn and goes on from
+// the recurrent state that was kept (section "Reusing KV cache across agent turns").
+//
+// delta_block.h has the mathematics.  delta_prepare_kernel makes the blocks' T, P and
+// operands, all blocks at once; delta_scan_kernel walks each sequence, a wave with
+// its 16 columns of the state in registers, without any exchange between waves.
+#include "delta_block.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kTiles = kChunk / 16;
+constexpr int kScanWaves = 2;
+
+// Blocks c0 .. c1 - 1 of every sequence; what is prepared of them, and the states
+// between two such rounds.
+struct Round {
+  int c0, c1, last;
+  h8_t *keys, *heads;  // [seqs][c1 - c0][key_heads or heads][units]
+  float* carry;        // [seqs][heads][dv][dk]
+};
+
+// grid (heads, c1 - c0, seqs).
+template <int DK, bool BF16>
+__global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a, Round r) {
+  typedef BlockOps<DK, BF16, kTiles> Ops;
+  __shared__ BlockShared<DK, BF16, kTiles> sh;
+  const int h = blockIdx.x, b = blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
+  const int count = delta_used(a.src[b], a.slots) ? delta_count(a.counts, a.nodes, b) : 0;
+  if (t0 >= count) return;
+  const int n = count - t0 < kChunk ? count - t0 : kChunk;
+  const int64_t block = (int64_t)b * (r.c1 - r.c0) + blockIdx.y;
+  const int kh = h / group;
+  h8_t* key_to = h % group == 0 ? r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits : nullptr;
+  prepare_block<DK, BF16, kTiles, false>(a, b, (int64_t)b * a.nodes + t0, n, h, kh, sh, key_to,
+                                         r.heads + (block * a.heads + h) * Ops::kHeadUnits);
+}
+
+// A chunk's values of a wave's columns, as results stand.
+template <bool BF16>
+__device__ __forceinline__ void load_values(const DeltaArgs& a, int64_t first, int n, int64_t at, f4_t (&v)[kTiles]) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * t + 4 * g + e;
+      float x = 0.0f;
+      if (i < n) {
+        const int64_t from = (first + i) * a.v_stride + at;
+        if constexpr (BF16) x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[from] << 16);
+        else x = static_cast<const float*>(a.v)[from];
+      }
+      v[t][e] = x;
+    }
+}
+
+// grid (heads, dv / (16 kScanWaves), seqs): a wave has 16 columns.
+template <int DK, bool BF16>
+__global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a, Round r) {
+  typedef BlockOps<DK, BF16, kTiles> Ops;
+  constexpr int P = Ops::kParts, KT = DK / 16;
+  const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int col0 = (blockIdx.y * kScanWaves + (threadIdx.x >> 6)) * 16, kh = h / (a.heads / a.key_heads);
+  const int src = a.src[b];
+  if (!delta_used(src, a.slots)) {
+    if (r.c0 == 0)
+      for (int t = 0; t < a.nodes; ++t)
+        if (lane < 16) store1<BF16>(a.out, (((int64_t)b * a.nodes + t) * a.heads + h) * a.dv + col0 + j, 0.0f);
+    return;
+  }
+  const int count = delta_count(a.counts, a.nodes, b);
+  const int64_t first = (int64_t)b * a.nodes, state_size = (int64_t)a.dv * DK;
+  float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
+  StateTile<DK, 1> st;
+  if (r.c0 > 0) load_state<DK, 1>(carry, st);
+  else if (src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + (int64_t)col0 * DK, st);
+  else zero_state<DK, 1>(st);
+  f4_t(&s)[KT] = st.s[0];
+  // s holds S times 2^es
+  int es = 0;
+  if (r.c0 * kChunk < count) {
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
+    es = 5 - exponent_of(max_of_groups(m));
+#pragma unroll
+    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
+  }
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t value_at = (int64_t)h * a.dv + col0 + j;
+  for (int c = r.c0; c < r.c1 && c * kChunk < count; ++c) {
+    const int t0 = c * kChunk, n = count - t0 < kChunk ? count - t0 : kChunk;
+    const int64_t block = (int64_t)b * (r.c1 - r.c0) + c - r.c0;
+    const h8_t* key = r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits + lane;
+    const h8_t* head = r.heads + (block * a.heads + h) * Ops::kHeadUnits;
+    const float* factors = reinterpret_cast<const float*>(head + Ops::kFactors);
+    const auto factor = [&](int which, int t) {
+      return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
+    };
+    head += lane;
+    f4_t v[kTiles];
+    load_values<BF16>(a, first + t0, n, value_at, v);
+    // K S and Q S
+    f4_t ks[kTiles], qs[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) ks[t] = qs[t] = zero;
+#pragma unroll
+    for (int x = 0; x < Ops::kSteps; ++x) {
+      h8_t hi, lo;
+      operand_parts(s[2 * x], s[2 * x + 1], hi, lo);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const int at = (t * Ops::kSteps + x) * 64;
+        const h8_t k = key[Ops::kKey + at], q = key[Ops::kQuery + at];
+        ks[t] = mfma16x16x32(k, hi, ks[t]);
+        ks[t] = mfma16x16x32(k, lo, ks[t]);
+        qs[t] = mfma16x16x32(q, hi, qs[t]);
+        if constexpr (P == 2) {
+          ks[t] = mfma16x16x32(key[Ops::kKey + Ops::kRows + at], hi, ks[t]);
+          qs[t] = mfma16x16x32(q, lo, qs[t]);
+          qs[t] = mfma16x16x32(key[Ops::kQuery + Ops::kRows + at], hi, qs[t]);
+        }
+      }
+    }
+    // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
+      m = max4(m, v[t]);
+    }
+    const int er = 3 - exponent_of(max_of_groups(m));
+    f4_t w[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) w[t] = zero;
+#pragma unroll
+    for (int x = 0; x < Ops::kTokenSteps; ++x) {
+      h8_t hi, lo;
+      operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
+#pragma unroll
+      for (int t = 2 * x; t < kTiles; ++t) {
+        const int at = Ops::kT + (Ops::lower(t) + x) * 64;
+        const h8_t th = head[at], tl = head[at + Ops::kLower * 64];
+        w[t] = mfma16x16x32(th, hi, w[t]);
+        w[t] = mfma16x16x32(th, lo, w[t]);
+        w[t] = mfma16x16x32(tl, hi, w[t]);
+      }
+    }
+    // P u
+    f4_t pu[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) pu[t] = zero;
+#pragma unroll
+    for (int x = 0; x < Ops::kTokenSteps; ++x) {
+      h8_t hi, lo;
+      if constexpr (P == 1) hi = operand_hi(w[2 * x], w[2 * x + 1]);
+      else operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
+#pragma unroll
+      for (int t = 2 * x; t < kTiles; ++t) {
+        const int at = Ops::kP + (Ops::lower(t) + x) * 64;
+        const h8_t p = head[at];
+        pu[t] = mfma16x16x32(p, hi, pu[t]);
+        if constexpr (P == 2) {
+          pu[t] = mfma16x16x32(p, lo, pu[t]);
+          pu[t] = mfma16x16x32(head[at + Ops::kLower * 64], hi, pu[t]);
+        }
+      }
+    }
+    // X = diag(e^(G_end - G)) u, and S <- e^G_end S + K^T X
+    const float end = factors[4 * kChunk];
+    float mx = 0.0f, ms = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      w[t] *= factor(kFactorX, t);
+      mx = max4(mx, w[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) ms = max4(ms, s[t]);
+    const int before = es;
+    {
+      const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
+      es = 5 - exponent_of(max_of_groups(most));
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, es - before);
+#pragma unroll
+    for (int x = 0; x < Ops::kTokenSteps; ++x) {
+      h8_t hi, lo;
+      operand_parts(scale4(w[2 * x], es - er), scale4(w[2 * x + 1], es - er), hi, lo);
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const int at = Ops::kKeyT + (t * Ops::kTokenSteps + x) * 64;
+        const h8_t k = key[at];
+        s[t] = mfma16x16x32(k, hi, s[t]);
+        s[t] = mfma16x16x32(k, lo, s[t]);
+        if constexpr (P == 2) s[t] = mfma16x16x32(key[at + Ops::kCols], hi, s[t]);
+      }
+    }
+    // o
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t);
+      const f4_t y = scale4(qs[t], -before), z = scale4(pu[t], -er);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * t + 4 * g + e;
+        if (i < n)
+          store1<BF16>(a.out, (first + t0 + i) * a.heads * a.dv + value_at, __builtin_fmaf(fq[e], y[e], fp[e] * z[e]));
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
+  if (!r.last) {
+    store_state<DK, 1>(carry, st);
+    return;
+  }
+  for (int t = count; t < a.nodes; ++t)
+    if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
+  const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
+  if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + (int64_t)col0 * DK, st);
+}
+
+// Bytes of a block of every sequence, and blocks of a round: what is prepared of them
+// stays within 128 MB, half the Infinity Cache.
+template <int DK, bool BF16>
+int64_t block_bytes(const DeltaArgs& a) {
+  typedef BlockOps<DK, BF16, kTiles> Ops;
+  return (int64_t)a.seqs * 16 * ((int64_t)a.key_heads * Ops::kKeyUnits + (int64_t)a.heads * Ops::kHeadUnits);
+}
+
+int64_t block_bytes(const DeltaArgs& a) {
+  if (a.dk == 64) return a.bf16 ? block_bytes<64, true>(a) : block_bytes<64, false>(a);
+  if (a.dk == 128) return a.bf16 ? block_bytes<128, true>(a) : block_bytes<128, false>(a);
+  return a.bf16 ? block_bytes<256, true>(a) : block_bytes<256, false>(a);
+}
+
+constexpr int64_t kRoundBytes = (int64_t)128 << 20;
+
+int round_blocks(const DeltaArgs& a) {
+  const int all = (a.nodes + kChunk - 1) / kChunk;
+  const int64_t fit = kRoundBytes / block_bytes(a);
+  return fit < 1 ? 1 : fit < all ? (int)fit : all;
+}
+
+int64_t carry_bytes(const DeltaArgs& a) {
+  const int all = (a.nodes + kChunk - 1) / kChunk;
+  return round_blocks(a) < all ? (int64_t)a.seqs * a.heads * a.dv * a.dk * 4 : 0;
+}
+
+template <int DK, bool BF16>
+void run(const DeltaArgs& a, hipStream_t stream) {
+  typedef BlockOps<DK, BF16, kTiles> Ops;
+  const int all = (a.nodes + kChunk - 1) / kChunk, step = round_blocks(a);
+  Round r = {};
+  r.carry = static_cast<float*>(a.workspace);
+  r.keys = reinterpret_cast<h8_t*>(static_cast<char*>(a.workspace) + carry_bytes(a));
+  r.heads = r.keys + (int64_t)a.seqs * step * a.key_heads * Ops::kKeyUnits;
+  for (int c = 0; c < all; c += step) {
+    r.c0 = c;
+    r.c1 = c + step < all ? c + step : all;
+    r.last = r.c1 == all;
+    delta_prepare_kernel<DK, BF16><<<dim3(a.heads, r.c1 - r.c0, a.seqs), 64 * kTiles, 0, stream>>>(a, r);
+    delta_scan_kernel<DK, BF16><<<dim3(a.heads, a.dv / (16 * kScanWaves), a.seqs), 64 * kScanWaves, 0, stream>>>(a, r);
+  }
+}
+
+}  // namespace
+
+bool delta_chunked(const DeltaArgs& a) { return a.nodes > 16; }
+
+int64_t delta_chunk_workspace_bytes(const DeltaArgs& a) { return carry_bytes(a) + round_blocks(a) * block_bytes(a); }
+
+void launch_delta_chunks(const DeltaArgs& a, hipStream_t stream) {
+  if (a.dk == 64) a.bf16 ? run<64, true>(a, stream) : run<64, false>(a, stream);
+  else if (a.dk == 128) a.bf16 ? run<128, true>(a, stream) : run<128, false>(a, stream);
+  else a.bf16 ? run<256, true>(a, stream) : run<256, false>(a, stream);
+}
+
+}  // namespace nvfp4
