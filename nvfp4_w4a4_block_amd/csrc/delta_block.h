@@ -81,7 +81,8 @@ struct BlockOps {
   static constexpr int kKey = 0, kQuery = kParts * kRows, kKeyT = 2 * kParts * kRows;
   static constexpr int kKeyUnits = kKeyT + kParts * kCols;  // of a key head
   static constexpr int kT = 0, kP = 2 * kLower * 64, kFactors = kP + kParts * kLower * 64;
-  static constexpr int kHeadUnits = kFactors + 4 * 4 * NT + 1;  // of a value head: factors [4][16 NT], then e^G_end
+  // of a value head: factors [4][16 NT], then e^G_end; whole loads of a wave
+  static constexpr int kHeadUnits = (kFactors + 4 * 4 * NT + 1 + 63) / 64 * 64;
   // steps of the rows of tile rt begin at this one
   static __device__ constexpr int lower(int rt) { return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? 2 : 4; }
 };

@@ -13,7 +13,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kTiles = kChunk / 16;
-constexpr int kScanWaves = 2;
 
 // Blocks c0 .. c1 - 1 of every sequence; what is prepared of them, and the states
 // between two such rounds.
@@ -39,32 +38,49 @@ __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a,
                                          r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
 
-// A chunk's values of a wave's columns, as results stand.
+// A block's values of a wave's columns as they come, where results stand; rows behind
+// the n-th are the last one again (their rate is 0, and so is what they add).
 template <bool BF16>
-__device__ __forceinline__ void load_values(const DeltaArgs& a, int64_t first, int n, int64_t at, f4_t (&v)[kTiles]) {
+struct Values {
+  uint32_t x[kTiles][4];
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load_values(const DeltaArgs& a, int64_t first, int n, int64_t at, Values<BF16>& v) {
   const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * t + 4 * g + e;
-      float x = 0.0f;
-      if (i < n) {
-        const int64_t from = (first + i) * a.v_stride + at;
-        if constexpr (BF16) x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[from] << 16);
-        else x = static_cast<const float*>(a.v)[from];
-      }
-      v[t][e] = x;
+      const int64_t from = (first + (i < n ? i : n - 1)) * a.v_stride + at;
+      if constexpr (BF16) v.x[t][e] = static_cast<const uint16_t*>(a.v)[from];
+      else v.x[t][e] = static_cast<const uint32_t*>(a.v)[from];
     }
 }
 
-// grid (heads, dv / (16 kScanWaves), seqs): a wave has 16 columns.
-template <int DK, bool BF16>
-__global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a, Round r) {
+#define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(uintptr_t)(p))
+#define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(uintptr_t)(p))
+
+// `units` operands of a lane (a multiple of 64) from memory to LDS, by the waves in
+// turn; nobody waits here.
+template <int WAVES>
+__device__ __forceinline__ void stage(const h8_t* from, h8_t* to, int units) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int i = wave; i < units / 64; i += WAVES)
+    __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from + 64 * i + lane), LDS_PTR(to + 64 * i), 16, 0, 0);
+}
+
+// grid (heads, dv / (16 WAVES), seqs): a wave has 16 columns.  BUFFERS: of a block's
+// operands in LDS; 2: those of the next block come while one is worked on; 0: they are
+// read where they are.
+template <int DK, bool BF16, int WAVES, int BUFFERS>
+__global__ __launch_bounds__(64 * WAVES, 1) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  constexpr int P = Ops::kParts, KT = DK / 16;
+  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kKeyUnits + Ops::kHeadUnits;
+  __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
   const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int col0 = (blockIdx.y * kScanWaves + (threadIdx.x >> 6)) * 16, kh = h / (a.heads / a.key_heads);
+  const int col0 = (blockIdx.y * WAVES + (threadIdx.x >> 6)) * 16, kh = h / (a.heads / a.key_heads);
   const int src = a.src[b];
   if (!delta_used(src, a.slots)) {
     if (r.c0 == 0)
@@ -73,7 +89,27 @@ __global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a
     return;
   }
   const int count = delta_count(a.counts, a.nodes, b);
+  const int end_block = (count + kChunk - 1) / kChunk < r.c1 ? (count + kChunk - 1) / kChunk : r.c1;
   const int64_t first = (int64_t)b * a.nodes, state_size = (int64_t)a.dv * DK;
+  const int64_t value_at = (int64_t)h * a.dv + col0 + j;
+  const auto keys_of = [&](int c) {
+    return r.keys + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.key_heads + kh) * Ops::kKeyUnits;
+  };
+  const auto heads_of = [&](int c) {
+    return r.heads + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.heads + h) * Ops::kHeadUnits;
+  };
+  const auto fetch = [&](int c) {
+    if constexpr (BUFFERS > 0) {
+      h8_t* to = ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0];
+      stage<WAVES>(keys_of(c), to, Ops::kKeyUnits);
+      stage<WAVES>(heads_of(c), to + Ops::kKeyUnits, Ops::kHeadUnits);
+    }
+  };
+  Values<BF16> next;
+  if (r.c0 < end_block) {
+    fetch(r.c0);
+    load_values<BF16>(a, first + r.c0 * kChunk, count - r.c0 * kChunk, value_at, next);
+  }
   float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
   StateTile<DK, 1> st;
   if (r.c0 > 0) load_state<DK, 1>(carry, st);
@@ -82,7 +118,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a
   f4_t(&s)[KT] = st.s[0];
   // s holds S times 2^es
   int es = 0;
-  if (r.c0 * kChunk < count) {
+  if (r.c0 < end_block) {
     float m = 0.0f;
 #pragma unroll
     for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
@@ -91,19 +127,37 @@ __global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a
     for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
   }
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t value_at = (int64_t)h * a.dv + col0 + j;
-  for (int c = r.c0; c < r.c1 && c * kChunk < count; ++c) {
-    const int t0 = c * kChunk, n = count - t0 < kChunk ? count - t0 : kChunk;
-    const int64_t block = (int64_t)b * (r.c1 - r.c0) + c - r.c0;
-    const h8_t* key = r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits + lane;
-    const h8_t* head = r.heads + (block * a.heads + h) * Ops::kHeadUnits;
-    const float* factors = reinterpret_cast<const float*>(head + Ops::kFactors);
+  f4_t o[kTiles];
+  const auto store_out = [&](int c) {
+    const bool whole = (c + 1) * kChunk <= count;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = c * kChunk + 16 * t + 4 * g + e;
+        if (whole || i < count) store1<BF16>(a.out, (first + i) * a.heads * a.dv + value_at, o[t][e]);
+      }
+  };
+  for (int c = r.c0; c < end_block; ++c) {
+    f4_t v[kTiles];
+    // the block's operands and values are here, and nobody reads the last one's any more
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[t][e] = __uint_as_float(BF16 ? next.x[t][e] << 16 : next.x[t][e]);
+    if (c + 1 < end_block) {
+      if constexpr (BUFFERS == 2) fetch(c + 1);
+      load_values<BF16>(a, first + (c + 1) * kChunk, count - (c + 1) * kChunk, value_at, next);
+    }
+    if (c > r.c0) store_out(c - 1);  // now, so that the next wait finds it done
+    const h8_t* key = (BUFFERS ? ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0] : keys_of(c)) + lane;
+    const h8_t* head = BUFFERS ? key + Ops::kKeyUnits : heads_of(c) + lane;
+    const float* factors = reinterpret_cast<const float*>(head - lane + Ops::kFactors);
     const auto factor = [&](int which, int t) {
       return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
     };
-    head += lane;
-    f4_t v[kTiles];
-    load_values<BF16>(a, first + t0, n, value_at, v);
     // K S and Q S
     f4_t ks[kTiles], qs[kTiles];
 #pragma unroll
@@ -208,13 +262,14 @@ __global__ __launch_bounds__(64 * kScanWaves) void delta_scan_kernel(DeltaArgs a
       const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t);
       const f4_t y = scale4(qs[t], -before), z = scale4(pu[t], -er);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * t + 4 * g + e;
-        if (i < n)
-          store1<BF16>(a.out, (first + t0 + i) * a.heads * a.dv + value_at, __builtin_fmaf(fq[e], y[e], fp[e] * z[e]));
-      }
+      for (int e = 0; e < 4; ++e) o[t][e] = __builtin_fmaf(fq[e], y[e], fp[e] * z[e]);
+    }
+    if constexpr (BUFFERS == 1) {
+      __syncthreads();
+      if (c + 1 < end_block) fetch(c + 1);
     }
   }
+  if (r.c0 < end_block) store_out(end_block - 1);
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
   if (!r.last) {
@@ -254,6 +309,15 @@ int64_t carry_bytes(const DeltaArgs& a) {
   return round_blocks(a) < all ? (int64_t)a.seqs * a.heads * a.dv * a.dk * 4 : 0;
 }
 
+constexpr int kLds = 160 * 1024;
+
+template <int DK, bool BF16>
+void scan(const DeltaArgs& a, const Round& r, hipStream_t stream) {
+  typedef BlockOps<DK, BF16, kTiles> Ops;
+  constexpr int bytes = 16 * (Ops::kKeyUnits + Ops::kHeadUnits), buffers = 2 * bytes <= kLds ? 2 : bytes <= kLds ? 1 : 0;
+  delta_scan_kernel<DK, BF16, 2, buffers><<<dim3(a.heads, a.dv / 32, a.seqs), 128, 0, stream>>>(a, r);
+}
+
 template <int DK, bool BF16>
 void run(const DeltaArgs& a, hipStream_t stream) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
@@ -267,7 +331,7 @@ void run(const DeltaArgs& a, hipStream_t stream) {
     r.c1 = c + step < all ? c + step : all;
     r.last = r.c1 == all;
     delta_prepare_kernel<DK, BF16><<<dim3(a.heads, r.c1 - r.c0, a.seqs), 64 * kTiles, 0, stream>>>(a, r);
-    delta_scan_kernel<DK, BF16><<<dim3(a.heads, a.dv / (16 * kScanWaves), a.seqs), 64 * kScanWaves, 0, stream>>>(a, r);
+    scan<DK, BF16>(a, r, stream);
   }
 }
 
