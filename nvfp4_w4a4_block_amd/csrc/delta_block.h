@@ -78,11 +78,13 @@ struct BlockOps {
   static constexpr int kLower = NT == 1 ? 1 : NT == 2 ? 2 : NT == 3 ? 4 : 6;  // of lower triangular rows
   static constexpr int kRows = NT * kSteps * 64;         // K or Q, one part
   static constexpr int kCols = DK / 16 * kTokenSteps * 64;  // K transposed, one part
-  static constexpr int kKey = 0, kQuery = kParts * kRows, kKeyT = 2 * kParts * kRows;
-  static constexpr int kKeyUnits = kKeyT + kParts * kCols;  // of a key head
-  static constexpr int kT = 0, kP = 2 * kLower * 64, kFactors = kP + kParts * kLower * 64;
-  // of a value head: factors [4][16 NT], then e^G_end; whole loads of a wave
-  static constexpr int kHeadUnits = (kFactors + 4 * 4 * NT + 1 + 63) / 64 * 64;
+  // of a key head: K and its transpose, what a scan's states need, before Q
+  static constexpr int kKey = 0, kKeyT = kParts * kRows, kQuery = kKeyT + kParts * kCols;
+  static constexpr int kKeyUnits = kQuery + kParts * kRows;
+  // of a value head: T, the factors [4][16 NT] with e^G_end behind them, before P
+  static constexpr int kT = 0, kFactors = 2 * kLower * 64;
+  static constexpr int kP = (kFactors + 4 * 4 * NT + 1 + 63) / 64 * 64;
+  static constexpr int kHeadUnits = kP + kParts * kLower * 64;
   // steps of the rows of tile rt begin at this one
   static __device__ constexpr int lower(int rt) { return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? 2 : 4; }
 };

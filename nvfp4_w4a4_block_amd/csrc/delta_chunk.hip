@@ -62,71 +62,229 @@ __device__ __forceinline__ void load_values(const DeltaArgs& a, int64_t first, i
 #define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(uintptr_t)(p))
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(uintptr_t)(p))
 
-// `units` operands of a lane (a multiple of 64) from memory to LDS, by the waves in
+// `units` operands of a lane (a multiple of 64) from memory to LDS, by WAVES waves in
 // turn; nobody waits here.
 template <int WAVES>
-__device__ __forceinline__ void stage(const h8_t* from, h8_t* to, int units) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ void stage(const h8_t* from, h8_t* to, int units, int wave) {
+  const int lane = threadIdx.x & 63;
   for (int i = wave; i < units / 64; i += WAVES)
     __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from + 64 * i + lane), LDS_PTR(to + 64 * i), 16, 0, 0);
 }
 
-// grid (heads, dv / (16 WAVES), seqs): a wave has 16 columns.  BUFFERS: of a block's
-// operands in LDS; 2: those of the next block come while one is worked on; 0: they are
-// read where they are.
-template <int DK, bool BF16, int WAVES, int BUFFERS>
-__global__ __launch_bounds__(64 * WAVES, 1) void delta_scan_kernel(DeltaArgs a, Round r) {
+// Every wave's LDS work is done and seen by all; memory is not waited for.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// What a state's wave leaves for the wave of its outputs.
+template <int DK, bool BF16>
+struct Handed {
+  h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
+  h8_t w[BF16 ? 1 : 2][2][64];        // u
+  int es[64], er[64];                 // their exponents
+};
+
+// grid (heads, dv / (16 SLABS), seqs).  Of 2 SLABS waves the first half have 16 columns
+// of the state each: r, u and the new state, one block after the other.  The second
+// half makes the outputs of the same columns, of which no state waits, and fetches the
+// next block's operands.  BUFFERS: blocks whose K, K^T, T and factors are in LDS; 2:
+// those of the next block come while one is worked on; 0: they are read where they
+// are.
+template <int DK, bool BF16, int SLABS, int BUFFERS>
+__global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kKeyUnits + Ops::kHeadUnits;
+  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
+  __shared__ Handed<DK, BF16> handed[SLABS];
   const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int col0 = (blockIdx.y * WAVES + (threadIdx.x >> 6)) * 16, kh = h / (a.heads / a.key_heads);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slab = wave & (SLABS - 1);
+  const int col0 = (blockIdx.y * SLABS + slab) * 16, kh = h / (a.heads / a.key_heads);
+  const bool states = wave < SLABS;
   const int src = a.src[b];
+  const int64_t first = (int64_t)b * a.nodes, state_size = (int64_t)a.dv * DK;
+  const int64_t value_at = (int64_t)h * a.dv + col0 + j;
   if (!delta_used(src, a.slots)) {
-    if (r.c0 == 0)
+    if (r.c0 == 0 && !states)
       for (int t = 0; t < a.nodes; ++t)
-        if (lane < 16) store1<BF16>(a.out, (((int64_t)b * a.nodes + t) * a.heads + h) * a.dv + col0 + j, 0.0f);
+        if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
     return;
   }
   const int count = delta_count(a.counts, a.nodes, b);
   const int end_block = (count + kChunk - 1) / kChunk < r.c1 ? (count + kChunk - 1) / kChunk : r.c1;
-  const int64_t first = (int64_t)b * a.nodes, state_size = (int64_t)a.dv * DK;
-  const int64_t value_at = (int64_t)h * a.dv + col0 + j;
   const auto keys_of = [&](int c) {
     return r.keys + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.key_heads + kh) * Ops::kKeyUnits;
   };
   const auto heads_of = [&](int c) {
     return r.heads + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.heads + h) * Ops::kHeadUnits;
   };
+  const auto buffer_of = [&](int c) { return ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0]; };
+  const auto key_ops = [&](int c) { return (BUFFERS ? buffer_of(c) : keys_of(c)) + lane; };
+  const auto head_ops = [&](int c) { return BUFFERS ? buffer_of(c) + Ops::kQuery : heads_of(c); };
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  Handed<DK, BF16>& hand = handed[slab];
+  if (states) {
+    Values<BF16> next;
+    if (r.c0 < end_block) load_values<BF16>(a, first + r.c0 * kChunk, count - r.c0 * kChunk, value_at, next);
+    float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
+    StateTile<DK, 1> st;
+    if (r.c0 > 0) load_state<DK, 1>(carry, st);
+    else if (src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + (int64_t)col0 * DK, st);
+    else zero_state<DK, 1>(st);
+    f4_t(&s)[KT] = st.s[0];
+    // s holds S times 2^es
+    int es = 0;
+    if (r.c0 < end_block) {
+      float m = 0.0f;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
+      es = 5 - exponent_of(max_of_groups(m));
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
+    }
+    for (int c = r.c0; c < end_block; ++c) {
+      lds_barrier();  // the block's operands are here
+      const h8_t* key = key_ops(c);
+      const h8_t* head = head_ops(c) + lane;
+      const float* factors = reinterpret_cast<const float*>(head - lane + Ops::kFactors);
+      const auto factor = [&](int which, int t) {
+        return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
+      };
+      f4_t v[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[t][e] = __uint_as_float(BF16 ? next.x[t][e] << 16 : next.x[t][e]);
+      if (c + 1 < end_block) load_values<BF16>(a, first + (c + 1) * kChunk, count - (c + 1) * kChunk, value_at, next);
+      // K S
+      f4_t ks[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) ks[t] = zero;
+#pragma unroll
+      for (int x = 0; x < Ops::kSteps; ++x) {
+        h8_t hi, lo;
+        operand_parts(s[2 * x], s[2 * x + 1], hi, lo);
+        hand.s[0][x][lane] = hi;
+        if constexpr (P == 2) hand.s[1][x][lane] = lo;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const int at = Ops::kKey + (t * Ops::kSteps + x) * 64;
+          const h8_t k = key[at];
+          ks[t] = mfma16x16x32(k, hi, ks[t]);
+          ks[t] = mfma16x16x32(k, lo, ks[t]);
+          if constexpr (P == 2) ks[t] = mfma16x16x32(key[at + Ops::kRows], hi, ks[t]);
+        }
+      }
+      hand.es[lane] = es;
+      lds_barrier();  // S is handed over
+      // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
+      float m = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
+        m = max4(m, v[t]);
+      }
+      const int er = 3 - exponent_of(max_of_groups(m));
+      f4_t w[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) w[t] = zero;
+#pragma unroll
+      for (int x = 0; x < Ops::kTokenSteps; ++x) {
+        h8_t hi, lo;
+        operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
+#pragma unroll
+        for (int t = 2 * x; t < kTiles; ++t) {
+          const int at = Ops::kT + (Ops::lower(t) + x) * 64;
+          const h8_t th = head[at], tl = head[at + Ops::kLower * 64];
+          w[t] = mfma16x16x32(th, hi, w[t]);
+          w[t] = mfma16x16x32(th, lo, w[t]);
+          w[t] = mfma16x16x32(tl, hi, w[t]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (P == 1) {
+          hand.w[0][x][lane] = operand_hi(w[2 * x], w[2 * x + 1]);
+        } else {
+          h8_t hi, lo;
+          operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
+          hand.w[0][x][lane] = hi;
+          hand.w[1][x][lane] = lo;
+        }
+      }
+      hand.er[lane] = er;
+      lds_barrier();  // u is handed over
+      // X = diag(e^(G_end - G)) u, and S <- e^G_end S + K^T X
+      const float end = factors[4 * kChunk];
+      float mx = 0.0f, ms = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        w[t] *= factor(kFactorX, t);
+        mx = max4(mx, w[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) ms = max4(ms, s[t]);
+      const int before = es;
+      {
+        const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
+        es = 5 - exponent_of(max_of_groups(most));
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, es - before);
+#pragma unroll
+      for (int x = 0; x < Ops::kTokenSteps; ++x) {
+        h8_t hi, lo;
+        operand_parts(scale4(w[2 * x], es - er), scale4(w[2 * x + 1], es - er), hi, lo);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const int at = Ops::kKeyT + (t * Ops::kTokenSteps + x) * 64;
+          const h8_t k = key[at];
+          s[t] = mfma16x16x32(k, hi, s[t]);
+          s[t] = mfma16x16x32(k, lo, s[t]);
+          if constexpr (P == 2) s[t] = mfma16x16x32(key[at + Ops::kCols], hi, s[t]);
+        }
+      }
+      if constexpr (BUFFERS == 1) lds_barrier();  // the operands have been read
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
+    if (!r.last) {
+      store_state<DK, 1>(carry, st);
+      return;
+    }
+    const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
+    if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + (int64_t)col0 * DK, st);
+    return;
+  }
   const auto fetch = [&](int c) {
     if constexpr (BUFFERS > 0) {
-      h8_t* to = ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0];
-      stage<WAVES>(keys_of(c), to, Ops::kKeyUnits);
-      stage<WAVES>(heads_of(c), to + Ops::kKeyUnits, Ops::kHeadUnits);
+      stage<SLABS>(keys_of(c), buffer_of(c), Ops::kQuery, slab);
+      stage<SLABS>(heads_of(c), buffer_of(c) + Ops::kQuery, Ops::kP, slab);
     }
   };
-  Values<BF16> next;
-  if (r.c0 < end_block) {
-    fetch(r.c0);
-    load_values<BF16>(a, first + r.c0 * kChunk, count - r.c0 * kChunk, value_at, next);
-  }
-  float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
-  StateTile<DK, 1> st;
-  if (r.c0 > 0) load_state<DK, 1>(carry, st);
-  else if (src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + (int64_t)col0 * DK, st);
-  else zero_state<DK, 1>(st);
-  f4_t(&s)[KT] = st.s[0];
-  // s holds S times 2^es
-  int es = 0;
-  if (r.c0 < end_block) {
-    float m = 0.0f;
+  // Q and P are this wave's alone: straight to registers, Q where it fits
+  constexpr bool hold = P * Ops::kSteps <= 8;
+  h8_t q[P][kTiles][hold ? Ops::kSteps : 1], p[P][Ops::kLower];
+  const auto load_q = [&](int c) {
+    if constexpr (!hold) return;
+    const h8_t* from = keys_of(c) + Ops::kQuery + lane;
 #pragma unroll
-    for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
-    es = 5 - exponent_of(max_of_groups(m));
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
-  }
-  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int x = 0; x < (hold ? Ops::kSteps : 1); ++x) q[i][t][x] = from[i * Ops::kRows + (t * Ops::kSteps + x) * 64];
+  };
+  const auto load_p = [&](int c) {
+    const h8_t* from = heads_of(c) + Ops::kP + lane;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int x = 0; x < Ops::kLower; ++x) p[i][x] = from[(i * Ops::kLower + x) * 64];
+  };
   f4_t o[kTiles];
   const auto store_out = [&](int c) {
     const bool whole = (c + 1) * kChunk <= count;
@@ -138,148 +296,74 @@ __global__ __launch_bounds__(64 * WAVES, 1) void delta_scan_kernel(DeltaArgs a, 
         if (whole || i < count) store1<BF16>(a.out, (first + i) * a.heads * a.dv + value_at, o[t][e]);
       }
   };
+  if (r.c0 < end_block) {
+    fetch(r.c0);
+    load_q(r.c0);
+    load_p(r.c0);
+  }
   for (int c = r.c0; c < end_block; ++c) {
-    f4_t v[kTiles];
-    // the block's operands and values are here, and nobody reads the last one's any more
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-    __syncthreads();
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the operands is in LDS
+    lds_barrier();
+    if (BUFFERS == 2 && c + 1 < end_block) fetch(c + 1);
+    if (c > r.c0) store_out(c - 1);
+    const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
+    lds_barrier();  // S is handed over
+    f4_t y[kTiles];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[t][e] = __uint_as_float(BF16 ? next.x[t][e] << 16 : next.x[t][e]);
-    if (c + 1 < end_block) {
-      if constexpr (BUFFERS == 2) fetch(c + 1);
-      load_values<BF16>(a, first + (c + 1) * kChunk, count - (c + 1) * kChunk, value_at, next);
-    }
-    if (c > r.c0) store_out(c - 1);  // now, so that the next wait finds it done
-    const h8_t* key = (BUFFERS ? ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0] : keys_of(c)) + lane;
-    const h8_t* head = BUFFERS ? key + Ops::kKeyUnits : heads_of(c) + lane;
-    const float* factors = reinterpret_cast<const float*>(head - lane + Ops::kFactors);
-    const auto factor = [&](int which, int t) {
-      return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
-    };
-    // K S and Q S
-    f4_t ks[kTiles], qs[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) ks[t] = qs[t] = zero;
+    for (int t = 0; t < kTiles; ++t) y[t] = zero;
 #pragma unroll
     for (int x = 0; x < Ops::kSteps; ++x) {
-      h8_t hi, lo;
-      operand_parts(s[2 * x], s[2 * x + 1], hi, lo);
+      const h8_t hi = hand.s[0][x][lane];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        const int at = (t * Ops::kSteps + x) * 64;
-        const h8_t k = key[Ops::kKey + at], q = key[Ops::kQuery + at];
-        ks[t] = mfma16x16x32(k, hi, ks[t]);
-        ks[t] = mfma16x16x32(k, lo, ks[t]);
-        qs[t] = mfma16x16x32(q, hi, qs[t]);
+        const h8_t* in_place = keys_of(c) + Ops::kQuery + (t * Ops::kSteps + x) * 64 + lane;
+        const h8_t q0 = hold ? q[0][t][hold ? x : 0] : in_place[0];
+        y[t] = mfma16x16x32(q0, hi, y[t]);
         if constexpr (P == 2) {
-          ks[t] = mfma16x16x32(key[Ops::kKey + Ops::kRows + at], hi, ks[t]);
-          qs[t] = mfma16x16x32(q, lo, qs[t]);
-          qs[t] = mfma16x16x32(key[Ops::kQuery + Ops::kRows + at], hi, qs[t]);
+          const h8_t q1 = hold ? q[1][t][hold ? x : 0] : in_place[Ops::kRows];
+          y[t] = mfma16x16x32(q0, hand.s[1][x][lane], y[t]);
+          y[t] = mfma16x16x32(q1, hi, y[t]);
         }
       }
     }
-    // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
-    float m = 0.0f;
+    const int es = hand.es[lane];
+    if (c + 1 < end_block) load_q(c + 1);
+    lds_barrier();  // u is handed over
+    const int er = hand.er[lane];
+    f4_t z[kTiles];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
-      m = max4(m, v[t]);
-    }
-    const int er = 3 - exponent_of(max_of_groups(m));
-    f4_t w[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) w[t] = zero;
+    for (int t = 0; t < kTiles; ++t) z[t] = zero;
 #pragma unroll
     for (int x = 0; x < Ops::kTokenSteps; ++x) {
-      h8_t hi, lo;
-      operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
+      const h8_t hi = hand.w[0][x][lane];
 #pragma unroll
       for (int t = 2 * x; t < kTiles; ++t) {
-        const int at = Ops::kT + (Ops::lower(t) + x) * 64;
-        const h8_t th = head[at], tl = head[at + Ops::kLower * 64];
-        w[t] = mfma16x16x32(th, hi, w[t]);
-        w[t] = mfma16x16x32(th, lo, w[t]);
-        w[t] = mfma16x16x32(tl, hi, w[t]);
-      }
-    }
-    // P u
-    f4_t pu[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) pu[t] = zero;
-#pragma unroll
-    for (int x = 0; x < Ops::kTokenSteps; ++x) {
-      h8_t hi, lo;
-      if constexpr (P == 1) hi = operand_hi(w[2 * x], w[2 * x + 1]);
-      else operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
-#pragma unroll
-      for (int t = 2 * x; t < kTiles; ++t) {
-        const int at = Ops::kP + (Ops::lower(t) + x) * 64;
-        const h8_t p = head[at];
-        pu[t] = mfma16x16x32(p, hi, pu[t]);
+        const int at = Ops::lower(t) + x;
+        z[t] = mfma16x16x32(p[0][at], hi, z[t]);
         if constexpr (P == 2) {
-          pu[t] = mfma16x16x32(p, lo, pu[t]);
-          pu[t] = mfma16x16x32(head[at + Ops::kLower * 64], hi, pu[t]);
+          z[t] = mfma16x16x32(p[0][at], hand.w[1][x][lane], z[t]);
+          z[t] = mfma16x16x32(p[1][at], hi, z[t]);
         }
       }
     }
-    // X = diag(e^(G_end - G)) u, and S <- e^G_end S + K^T X
-    const float end = factors[4 * kChunk];
-    float mx = 0.0f, ms = 0.0f;
+    if (c + 1 < end_block) load_p(c + 1);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      w[t] *= factor(kFactorX, t);
-      mx = max4(mx, w[t]);
-    }
+      const f4_t fq = *reinterpret_cast<const f4_t*>(factors + kFactorQ * kChunk + 16 * t + 4 * g);
+      const f4_t fp = *reinterpret_cast<const f4_t*>(factors + kFactorP * kChunk + 16 * t + 4 * g);
+      const f4_t qs = scale4(y[t], -es), pu = scale4(z[t], -er);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) ms = max4(ms, s[t]);
-    const int before = es;
-    {
-      const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
-      es = 5 - exponent_of(max_of_groups(most));
-    }
-#pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, es - before);
-#pragma unroll
-    for (int x = 0; x < Ops::kTokenSteps; ++x) {
-      h8_t hi, lo;
-      operand_parts(scale4(w[2 * x], es - er), scale4(w[2 * x + 1], es - er), hi, lo);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        const int at = Ops::kKeyT + (t * Ops::kTokenSteps + x) * 64;
-        const h8_t k = key[at];
-        s[t] = mfma16x16x32(k, hi, s[t]);
-        s[t] = mfma16x16x32(k, lo, s[t]);
-        if constexpr (P == 2) s[t] = mfma16x16x32(key[at + Ops::kCols], hi, s[t]);
-      }
-    }
-    // o
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t);
-      const f4_t y = scale4(qs[t], -before), z = scale4(pu[t], -er);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = __builtin_fmaf(fq[e], y[e], fp[e] * z[e]);
+      for (int e = 0; e < 4; ++e) o[t][e] = __builtin_fmaf(fq[e], qs[e], fp[e] * pu[e]);
     }
     if constexpr (BUFFERS == 1) {
-      __syncthreads();
+      lds_barrier();
       if (c + 1 < end_block) fetch(c + 1);
     }
   }
   if (r.c0 < end_block) store_out(end_block - 1);
-#pragma unroll
-  for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
-  if (!r.last) {
-    store_state<DK, 1>(carry, st);
-    return;
-  }
+  if (!r.last) return;
   for (int t = count; t < a.nodes; ++t)
     if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
-  const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
-  if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + (int64_t)col0 * DK, st);
 }
 
 // Bytes of a block of every sequence, and blocks of a round: what is prepared of them
@@ -314,8 +398,9 @@ constexpr int kLds = 160 * 1024;
 template <int DK, bool BF16>
 void scan(const DeltaArgs& a, const Round& r, hipStream_t stream) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  constexpr int bytes = 16 * (Ops::kKeyUnits + Ops::kHeadUnits), buffers = 2 * bytes <= kLds ? 2 : bytes <= kLds ? 1 : 0;
-  delta_scan_kernel<DK, BF16, 2, buffers><<<dim3(a.heads, a.dv / 32, a.seqs), 128, 0, stream>>>(a, r);
+  constexpr int slabs = 2, bytes = 16 * (Ops::kQuery + Ops::kP), hand = slabs * (int)sizeof(Handed<DK, BF16>);
+  constexpr int buffers = 2 * bytes + hand <= kLds ? 2 : bytes + hand <= kLds ? 1 : 0;
+  delta_scan_kernel<DK, BF16, slabs, buffers><<<dim3(a.heads, a.dv / (16 * slabs), a.seqs), 128 * slabs, 0, stream>>>(a, r);
 }
 
 template <int DK, bool BF16>
