@@ -98,25 +98,53 @@ struct BlockShared {
   h8_t key[BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows];
   float a[16 * NT][kPitch];  // A, then T
   float p[16 * NT][kPitch];  // P
-  double decay[64];          // G
+  double decay[64];          // G in exponents of 2
   uint64_t line[64];         // trees: ancestors and self
   float beta[64], key_factor[64], query_factor[64];
   int t_exponent[64];
 };
 
-// A tile's 16 rows of k or q as an operand: lane j + 16 g has its values of row j.
-// Returns the factor that makes the stored row the row as used.
+// A row of k or q as it comes: lane j + 16 g has its share of row j of a tile.
 template <int DK, bool BF16>
-__device__ __forceinline__ float row_operand(const void* rows, int64_t at, bool there, float eps,
-                                             h8_t (&op)[BF16 ? 1 : 2][DK / 32]) {
+struct RawRow {
+  u4_t x[DK / 32][BF16 ? 1 : 2];  // values 32 s + 4 g .., 32 s + 16 + 4 g ..
+};
+
+template <int DK, bool BF16>
+__device__ __forceinline__ void load_row(const void* rows, int64_t at, RawRow<DK, BF16>& raw) {
   const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+    if constexpr (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(rows) + at + 32 * s + 4 * g;
+      const u2_t lo = *reinterpret_cast<const u2_t*>(p), hi = *reinterpret_cast<const u2_t*>(p + 16);
+      raw.x[s][0] = u4_t{lo.x, lo.y, hi.x, hi.y};
+    } else {
+      const float* p = static_cast<const float*>(rows) + at + 32 * s + 4 * g;
+      raw.x[s][0] = *reinterpret_cast<const u4_t*>(p);
+      raw.x[s][1] = *reinterpret_cast<const u4_t*>(p + 16);
+    }
+  }
+}
+
+// The row as an operand, zeros where it is not there.  Returns the factor that makes
+// the stored row the row as used.
+template <int DK, bool BF16>
+__device__ __forceinline__ float row_operand(const RawRow<DK, BF16>& raw, bool there, float eps,
+                                             h8_t (&op)[BF16 ? 1 : 2][DK / 32]) {
   f4_t x[DK / 32][2];
   float m = 0.0f;
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      x[s][h] = there ? load4<BF16>(rows, at + 32 * s + 16 * h + 4 * g) : f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w;
+        if constexpr (BF16) w = (i & 1) ? raw.x[s][0][2 * h + (i >> 1)] & 0xFFFF0000u : raw.x[s][0][2 * h + (i >> 1)] << 16;
+        else w = raw.x[s][h][i];
+        x[s][h][i] = there ? __uint_as_float(w) : 0.0f;
+      }
       m = max4(m, x[s][h]);
     }
   const int e = exponent_of(max_of_groups(m));
@@ -134,8 +162,13 @@ __device__ __forceinline__ float row_operand(const void* rows, int64_t at, bool 
   }
   if (!there) return 0.0f;
   if (eps < 0.0f) return __builtin_amdgcn_ldexpf(1.0f, e);
-  const double square = (double)sum_of_groups(ss) + __builtin_amdgcn_ldexp((double)eps, -2 * e);
-  return (float)(1.0 / __builtin_sqrt(square));
+  // 1 / sqrt of the scaled row's squares; where eps, scaled alike, is past fp32 it is all
+  const float small = __builtin_amdgcn_ldexpf(eps, -2 * e);
+  const bool all = small > 1e38f;
+  const float square = all ? eps : sum_of_groups(ss) + small;
+  float y = __builtin_amdgcn_rsqf(square);
+  y = square > 0.0f ? __builtin_fmaf(0.5f * y, __builtin_fmaf(-square * y, y, 1.0f), y) : y;
+  return all ? __builtin_amdgcn_ldexpf(y, e) : y;
 }
 
 // a b^T of two tiles' rows, with `parts` as above: 16x16.
@@ -221,22 +254,46 @@ __device__ __forceinline__ int store_rows(const f4_t (&x)[2][2], int steps, h8_t
   return e;
 }
 
-// Prepares the n tokens from row `first` on of value head h (key head kh), n <= 16 NT,
+// What a block is made of, as it comes from memory.
+template <int DK, bool BF16>
+struct BlockRows {
+  RawRow<DK, BF16> k, q;
+  float g, beta;
+  int parent;
+};
+
+// The rows from `first` on, `rows` of which are in memory (at least one): those behind
+// them are the last one again.
+template <int DK, bool BF16, int NT, bool TREE>
+__device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t first, int rows, int h, int kh,
+                                                BlockRows<DK, BF16>& to) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = 16 * w + (lane & 15);
+  if (w >= NT) return;
+  const int64_t row = first + (i < rows ? i : rows - 1), token = first + (lane < rows ? lane : rows - 1);
+  load_row<DK, BF16>(a.k, row * a.k_stride + (int64_t)kh * DK, to.k);
+  load_row<DK, BF16>(a.q, row * a.q_stride + (int64_t)kh * DK, to.q);
+  if (w == 0) {
+    to.g = a.g[token * a.heads + h];
+    to.beta = a.beta[token * a.heads + h];
+    if constexpr (TREE) to.parent = a.parent[token];
+  }
+}
+
+// Prepares the n tokens of a block of value head h, n <= 16 NT, from its rows,
 // by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
 // head's part (NULL: not wanted), head_to: the value head's.
 template <int DK, bool BF16, int NT, bool TREE>
-__device__ __forceinline__ void prepare_block(const DeltaArgs& a, int b, int64_t first, int n, int h, int kh,
+__device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
                                               BlockShared<DK, BF16, NT>& sh, h8_t* key_to, h8_t* head_to) {
   typedef BlockOps<DK, BF16, NT> Ops;
   constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT>::kPitch;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const bool works = w < NT;
-  const int64_t row = first + 16 * w + j;
   const bool there = works && 16 * w + j < n;
   h8_t key[P][Ops::kSteps], query[P][Ops::kSteps];
   if (works) {
-    const float kf = row_operand<DK, BF16>(a.k, row * a.k_stride + (int64_t)kh * DK, there, a.norm_eps, key);
-    const float qf = row_operand<DK, BF16>(a.q, row * a.q_stride + (int64_t)kh * DK, there, a.norm_eps, query);
+    const float kf = row_operand<DK, BF16>(rows.k, there, a.norm_eps, key);
+    const float qf = row_operand<DK, BF16>(rows.q, there, a.norm_eps, query);
     if (g == 0) {
       sh.key_factor[16 * w + j] = kf;
       sh.query_factor[16 * w + j] = qf * a.scale;
@@ -254,12 +311,11 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, int b, int64_t
       }
   }
   if (w == 0) {
-    float gl = lane < n ? a.g[(first + lane) * a.heads + h] : 0.0f;
-    sh.beta[lane] = lane < n ? a.beta[(first + lane) * a.heads + h] : 0.0f;
-    gl = gl < -1e4f ? -1e4f : gl;  // e^-1e4 is 0, and differences of sums stay finite
-    double sum = gl;
+    sh.beta[lane] = lane < n ? rows.beta : 0.0f;
+    const float gl = lane >= n ? 0.0f : rows.g < -1e4f ? -1e4f : rows.g;  // e^-1e4 is 0, and differences stay finite
+    double sum = (double)gl * 1.4426950408889634074;  // exponents of 2
     if constexpr (TREE) {
-      const int par = lane < n ? a.parent[first + lane] : -1;
+      const int par = lane < n ? rows.parent : -1;
       uint64_t mask = 1ull << lane;
       int up = par >= 0 && par < lane ? par : -1;
 #pragma unroll
@@ -317,7 +373,7 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, int b, int64_t
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * w + 4 * g + e;
         const bool seen = TREE ? ((line[e] >> col) & 1) != 0 : col <= i;
-        const float d = expf((float)(gi[e] - gj)) * kj;
+        const float d = __builtin_amdgcn_exp2f((float)(gi[e] - gj)) * kj;
         kk[e] = seen && col < i ? bi[e] * ki[e] * d * kk[e] : 0.0f;
         qk[e] = seen ? qi[e] * d * qk[e] : 0.0f;
       }
@@ -394,12 +450,12 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, int b, int64_t
     if (g == 0) {
       const int i = 16 * w + j;
       const double at = sh.decay[i], end = sh.decay[16 * NT - 1];
-      const float into = expf((float)at), kf = sh.key_factor[i];
+      const float into = __builtin_amdgcn_exp2f((float)at), kf = sh.key_factor[i];
       factors[kFactorR * 16 * NT + i] = -into * kf;
-      factors[kFactorX * 16 * NT + i] = __builtin_amdgcn_ldexpf(kf * expf((float)(end - at)), sh.t_exponent[i]);
+      factors[kFactorX * 16 * NT + i] = __builtin_amdgcn_ldexpf(kf * __builtin_amdgcn_exp2f((float)(end - at)), sh.t_exponent[i]);
       factors[kFactorQ * 16 * NT + i] = into * sh.query_factor[i];
       factors[kFactorP * 16 * NT + i] = __builtin_amdgcn_ldexpf(1.0f, e);
-      if (i == 0) factors[4 * 16 * NT] = expf((float)end);
+      if (i == 0) factors[4 * 16 * NT] = __builtin_amdgcn_exp2f((float)end);
     }
     if (key_to && !TREE) {
       // K transposed: lane j + 16 g has tokens 32 s + 4 g .., 32 s + 16 + 4 g .. of value 16 t + j

@@ -28,14 +28,15 @@ __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a,
   typedef BlockOps<DK, BF16, kTiles> Ops;
   __shared__ BlockShared<DK, BF16, kTiles> sh;
   const int h = blockIdx.x, b = blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
+  const int kh = h / group;
+  BlockRows<DK, BF16> rows;
+  load_block_rows<DK, BF16, kTiles, false>(a, (int64_t)b * a.nodes + t0, a.nodes - t0, h, kh, rows);
   const int count = delta_used(a.src[b], a.slots) ? delta_count(a.counts, a.nodes, b) : 0;
   if (t0 >= count) return;
   const int n = count - t0 < kChunk ? count - t0 : kChunk;
   const int64_t block = (int64_t)b * (r.c1 - r.c0) + blockIdx.y;
-  const int kh = h / group;
   h8_t* key_to = h % group == 0 ? r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits : nullptr;
-  prepare_block<DK, BF16, kTiles, false>(a, b, (int64_t)b * a.nodes + t0, n, h, kh, sh, key_to,
-                                         r.heads + (block * a.heads + h) * Ops::kHeadUnits);
+  prepare_block<DK, BF16, kTiles, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
 
 // A block's values of a wave's columns as they come, where results stand; rows behind
@@ -45,31 +46,35 @@ struct Values {
   uint32_t x[kTiles][4];
 };
 
+// `rows` is the block's first row in memory, `at` the lane's place in it and `stride`
+// a row, in bytes: a whole block's addresses are a number for all lanes and one of the
+// lane's own.
 template <bool BF16>
-__device__ __forceinline__ void load_values(const DeltaArgs& a, int64_t first, int n, int64_t at, Values<BF16>& v) {
+__device__ __forceinline__ void load_values(const char* rows, uint32_t at, uint32_t stride, int n, Values<BF16>& v) {
   const int g = (threadIdx.x & 63) >> 4;
+  const auto load = [](const char* p) -> uint32_t {
+    if constexpr (BF16) return *reinterpret_cast<const uint16_t*>(p);
+    else return *reinterpret_cast<const uint32_t*>(p);
+  };
+  if (n >= kChunk) {
+    const uint32_t mine = at + 4 * g * stride;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.x[t][e] = load(rows + (int64_t)(16 * t + e) * stride + mine);
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * t + 4 * g + e;
-      const int64_t from = (first + (i < n ? i : n - 1)) * a.v_stride + at;
-      if constexpr (BF16) v.x[t][e] = static_cast<const uint16_t*>(a.v)[from];
-      else v.x[t][e] = static_cast<const uint32_t*>(a.v)[from];
+      v.x[t][e] = load(rows + (int64_t)(i < n ? i : n - 1) * stride + at);
     }
 }
 
 #define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(uintptr_t)(p))
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(uintptr_t)(p))
-
-// `units` operands of a lane (a multiple of 64) from memory to LDS, by WAVES waves in
-// turn; nobody waits here.
-template <int WAVES>
-__device__ __forceinline__ void stage(const h8_t* from, h8_t* to, int units, int wave) {
-  const int lane = threadIdx.x & 63;
-  for (int i = wave; i < units / 64; i += WAVES)
-    __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from + 64 * i + lane), LDS_PTR(to + 64 * i), 16, 0, 0);
-}
 
 // Every wave's LDS work is done and seen by all; memory is not waited for.
 __device__ __forceinline__ void lds_barrier() {
@@ -126,7 +131,13 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
   Handed<DK, BF16>& hand = handed[slab];
   if (states) {
     Values<BF16> next;
-    if (r.c0 < end_block) load_values<BF16>(a, first + r.c0 * kChunk, count - r.c0 * kChunk, value_at, next);
+    constexpr int size = BF16 ? 2 : 4;
+    const uint32_t v_row = (uint32_t)a.v_stride * size;
+    const auto load_next = [&](int c) {
+      load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv) * size,
+                        (uint32_t)(col0 + j) * size, v_row, count - c * kChunk, next);
+    };
+    if (r.c0 < end_block) load_next(r.c0);
     float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
     StateTile<DK, 1> st;
     if (r.c0 > 0) load_state<DK, 1>(carry, st);
@@ -156,7 +167,7 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[t][e] = __uint_as_float(BF16 ? next.x[t][e] << 16 : next.x[t][e]);
-      if (c + 1 < end_block) load_values<BF16>(a, first + (c + 1) * kChunk, count - (c + 1) * kChunk, value_at, next);
+      if (c + 1 < end_block) load_next(c + 1);
       // K S
       f4_t ks[kTiles];
 #pragma unroll
@@ -168,13 +179,12 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
         hand.s[0][x][lane] = hi;
         if constexpr (P == 2) hand.s[1][x][lane] = lo;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const int at = Ops::kKey + (t * Ops::kSteps + x) * 64;
-          const h8_t k = key[at];
-          ks[t] = mfma16x16x32(k, hi, ks[t]);
-          ks[t] = mfma16x16x32(k, lo, ks[t]);
-          if constexpr (P == 2) ks[t] = mfma16x16x32(key[at + Ops::kRows], hi, ks[t]);
-        }
+        for (int part = 0; part < P + 1; ++part)
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            const int at = Ops::kKey + (t * Ops::kSteps + x) * 64;
+            ks[t] = mfma16x16x32(key[part == 2 ? at + Ops::kRows : at], part == 1 ? lo : hi, ks[t]);
+          }
       }
       hand.es[lane] = es;
       lds_barrier();  // S is handed over
@@ -196,13 +206,12 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
         h8_t hi, lo;
         operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
 #pragma unroll
-        for (int t = 2 * x; t < kTiles; ++t) {
-          const int at = Ops::kT + (Ops::lower(t) + x) * 64;
-          const h8_t th = head[at], tl = head[at + Ops::kLower * 64];
-          w[t] = mfma16x16x32(th, hi, w[t]);
-          w[t] = mfma16x16x32(th, lo, w[t]);
-          w[t] = mfma16x16x32(tl, hi, w[t]);
-        }
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int t = 2 * x; t < kTiles; ++t) {
+            const int at = Ops::kT + (Ops::lower(t) + x) * 64;
+            w[t] = mfma16x16x32(head[part == 2 ? at + Ops::kLower * 64 : at], part == 1 ? lo : hi, w[t]);
+          }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -232,20 +241,22 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
         const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
         es = 5 - exponent_of(max_of_groups(most));
       }
+      // e^G_end times a power of two, one factor: where it leaves fp32's range S is as nothing
+      // beside X (its largest value is taken to 32 .. 64 after it)
+      const float fade = __builtin_amdgcn_ldexpf(end, es - before);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, es - before);
+      for (int t = 0; t < KT; ++t) s[t] *= fade;
 #pragma unroll
       for (int x = 0; x < Ops::kTokenSteps; ++x) {
         h8_t hi, lo;
         operand_parts(scale4(w[2 * x], es - er), scale4(w[2 * x + 1], es - er), hi, lo);
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const int at = Ops::kKeyT + (t * Ops::kTokenSteps + x) * 64;
-          const h8_t k = key[at];
-          s[t] = mfma16x16x32(k, hi, s[t]);
-          s[t] = mfma16x16x32(k, lo, s[t]);
-          if constexpr (P == 2) s[t] = mfma16x16x32(key[at + Ops::kCols], hi, s[t]);
-        }
+        for (int part = 0; part < P + 1; ++part)
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            const int at = Ops::kKeyT + (t * Ops::kTokenSteps + x) * 64;
+            s[t] = mfma16x16x32(key[part == 2 ? at + Ops::kCols : at], part == 1 ? lo : hi, s[t]);
+          }
       }
       if constexpr (BUFFERS == 1) lds_barrier();  // the operands have been read
     }
@@ -259,11 +270,19 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
     if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + (int64_t)col0 * DK, st);
     return;
   }
-  const auto fetch = [&](int c) {
+  const auto fetch_part = [&](int c, int part) {
     if constexpr (BUFFERS > 0) {
-      stage<SLABS>(keys_of(c), buffer_of(c), Ops::kQuery, slab);
-      stage<SLABS>(heads_of(c), buffer_of(c) + Ops::kQuery, Ops::kP, slab);
+      constexpr int loads = (Ops::kQuery + Ops::kP) / 64, third = (loads + 3 * SLABS - 1) / (3 * SLABS);
+      const h8_t *keys = keys_of(c) + lane, *heads = heads_of(c) + lane - Ops::kQuery;
+      h8_t* to = buffer_of(c);
+#pragma unroll 4
+      for (int i = part * third * SLABS + slab; i < (part + 1) * third * SLABS; i += SLABS)
+        if (i < loads)
+          __builtin_amdgcn_global_load_lds(GLOBAL_PTR((i < Ops::kQuery / 64 ? keys : heads) + 64 * i), LDS_PTR(to + 64 * i), 16, 0, 0);
     }
+  };
+  const auto fetch = [&](int c) {
+    for (int part = 0; part < 3; ++part) fetch_part(c, part);
   };
   // Q and P are this wave's alone: straight to registers, Q where it fits
   constexpr bool hold = P * Ops::kSteps <= 8;
@@ -287,14 +306,27 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
   };
   f4_t o[kTiles];
   const auto store_out = [&](int c) {
-    const bool whole = (c + 1) * kChunk <= count;
+    constexpr int size = BF16 ? 2 : 4;
+    const uint32_t out_row = (uint32_t)(a.heads * a.dv) * size;
+    char* rows = static_cast<char*>(a.out) + ((first + c * kChunk) * a.heads + h) * a.dv * size;
+    const uint32_t mine = (uint32_t)(col0 + j) * size + 4 * g * out_row;
+    const int n = count - c * kChunk;
+    const auto store = [](char* p, float x) {
+      if constexpr (BF16) *reinterpret_cast<__bf16*>(p) = (__bf16)x;
+      else *reinterpret_cast<float*>(p) = x;
+    };
+    if (n >= kChunk) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store(rows + (int64_t)(16 * t + e) * out_row + mine, o[t][e]);
+      return;
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = c * kChunk + 16 * t + 4 * g + e;
-        if (whole || i < count) store1<BF16>(a.out, (first + i) * a.heads * a.dv + value_at, o[t][e]);
-      }
+      for (int e = 0; e < 4; ++e)
+        if (16 * t + 4 * g + e < n) store(rows + (int64_t)(16 * t + e) * out_row + mine, o[t][e]);
   };
   if (r.c0 < end_block) {
     fetch(r.c0);
@@ -304,8 +336,10 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
   for (int c = r.c0; c < end_block; ++c) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the operands is in LDS
     lds_barrier();
-    if (BUFFERS == 2 && c + 1 < end_block) fetch(c + 1);
+    // the next block's operands: a part before each of the block's waits
+    const bool ahead = BUFFERS == 2 && c + 1 < end_block;
     if (c > r.c0) store_out(c - 1);
+    if (ahead) fetch_part(c + 1, 0);
     const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
     lds_barrier();  // S is handed over
     f4_t y[kTiles];
@@ -327,6 +361,7 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
       }
     }
     const int es = hand.es[lane];
+    if (ahead) fetch_part(c + 1, 1);
     if (c + 1 < end_block) load_q(c + 1);
     lds_barrier();  // u is handed over
     const int er = hand.er[lane];
@@ -346,6 +381,7 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
         }
       }
     }
+    if (ahead) fetch_part(c + 1, 2);
     if (c + 1 < end_block) load_p(c + 1);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
