@@ -302,9 +302,7 @@ int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {
 }
 
 hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
-  // a lane's place in a tile of rows is a 32-bit number of bytes there
-  const bool near = a.v_stride < (int64_t)1 << 26;
-  if (delta_chunked(a) && near && a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
+  if (delta_chunked(a) && a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
     launch_delta_chunks(a, stream);
     return hipGetLastError();
   }

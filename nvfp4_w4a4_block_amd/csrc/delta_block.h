@@ -44,10 +44,14 @@ __device__ __forceinline__ float max4(float m, f4_t x) {
   return fmaxf(fmaxf(m, fabsf(x[2])), fabsf(x[3]));
 }
 
-// Over the four lane groups, in all of them.
+// Over the four lane groups, in all of them: rows of lanes exchanged in registers.
 __device__ __forceinline__ float max_of_groups(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
+  const uint32_t a = __float_as_uint(x);
+  const pair_t p = __builtin_bit_cast(pair_t, __builtin_amdgcn_permlane16_swap(a, a, false, false));
+  const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(p.x), __uint_as_float(p.y)));
+  const pair_t q = __builtin_bit_cast(pair_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+  return fmaxf(__uint_as_float(q.x), __uint_as_float(q.y));
 }
 
 // floor(log2 x) of x > 0; 0 of 0.
@@ -56,7 +60,11 @@ __device__ __forceinline__ int exponent_of(float x) {
 }
 
 __device__ __forceinline__ h4_t to_half(f4_t x) { return __builtin_convertvector(x, h4_t); }
-__device__ __forceinline__ f4_t rest_of(f4_t x, h4_t hi) { return x - __builtin_convertvector(hi, f4_t); }
+// x - hi, exact; as a multiply-add it takes hi as it stands, in one instruction
+__device__ __forceinline__ f4_t rest_of(f4_t x, h4_t hi) {
+  return f4_t{__builtin_fmaf((float)hi[0], -1.0f, x[0]), __builtin_fmaf((float)hi[1], -1.0f, x[1]),
+              __builtin_fmaf((float)hi[2], -1.0f, x[2]), __builtin_fmaf((float)hi[3], -1.0f, x[3])};
+}
 __device__ __forceinline__ h8_t join8(h4_t a, h4_t b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 // Two result tiles as the operand of a product over their rows.
@@ -208,22 +216,22 @@ __device__ __forceinline__ void store_block(float* a, int pitch, f4_t x) {
   for (int i = 0; i < 4; ++i) a[(4 * g + i) * pitch + j] = x[i];
 }
 
-// (I + A)^-1 of a 16x16 block in place, by substitution, a column a lane.
+// (I + A)^-1 of a 16x16 block in place, by substitution, a column a lane: each value
+// found is taken off all rows below it, which do not wait for each other.
 __device__ __forceinline__ void invert_block(float* a, int pitch) {
   const int j = threadIdx.x & 15;
+  f4_t r[16][4];
+#pragma unroll
+  for (int i = 1; i < 16; ++i)
+#pragma unroll
+    for (int m = 0; m < (i + 3) / 4; ++m) r[i][m] = *reinterpret_cast<const f4_t*>(a + i * pitch + 4 * m);
   float x[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float sum = i == j ? 1.0f : 0.0f;
+  for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.0f : 0.0f;
 #pragma unroll
-    for (int m4 = 0; m4 < (i + 3) / 4; ++m4) {
-      const f4_t r = *reinterpret_cast<const f4_t*>(a + i * pitch + 4 * m4);
+  for (int m = 0; m < 15; ++m)
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (4 * m4 + m < i) sum = __builtin_fmaf(-r[m], x[4 * m4 + m], sum);
-    }
-    x[i] = sum;
-  }
+    for (int i = m + 1; i < 16; ++i) x[i] = __builtin_fmaf(-r[i][m >> 2][m & 3], x[m], x[i]);
   if ((threadIdx.x & 63) < 16)
 #pragma unroll
     for (int i = 0; i < 16; ++i) a[i * pitch + j] = x[i];

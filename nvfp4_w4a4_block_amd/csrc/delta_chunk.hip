@@ -39,38 +39,29 @@ __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a,
   prepare_block<DK, BF16, kTiles, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
 
-// A block's values of a wave's columns as they come, where results stand; rows behind
-// the n-th are the last one again (their rate is 0, and so is what they add).
+// 64 rows of 16 values, one after the other in LDS; the pitch keeps the four rows that
+// a wave's lane groups read at a time in banks of their own.
 template <bool BF16>
-struct Values {
-  uint32_t x[kTiles][4];
+struct Rows16 {
+  static constexpr int kSize = BF16 ? 2 : 4, kPitch = BF16 ? 48 : 80, kPieces = kSize, kLoads = kSize;
+  char x[kChunk * kPitch];  // a row is kPieces pieces of 16 bytes, a lane has kLoads of them
+  __device__ __forceinline__ char* piece(int u) {
+    const int i = 64 * u + (threadIdx.x & 63);
+    return x + i / kPieces * kPitch + i % kPieces * 16;
+  }
+  __device__ __forceinline__ char* value(int row) { return x + row * kPitch + (threadIdx.x & 15) * kSize; }
 };
 
-// `rows` is the block's first row in memory, `at` the lane's place in it and `stride`
-// a row, in bytes: a whole block's addresses are a number for all lanes and one of the
-// lane's own.
+// A block's values of a wave's columns from memory: rows behind the n-th are the last
+// one again (their rate is 0, and so is what they add).
 template <bool BF16>
-__device__ __forceinline__ void load_values(const char* rows, uint32_t at, uint32_t stride, int n, Values<BF16>& v) {
-  const int g = (threadIdx.x & 63) >> 4;
-  const auto load = [](const char* p) -> uint32_t {
-    if constexpr (BF16) return *reinterpret_cast<const uint16_t*>(p);
-    else return *reinterpret_cast<const uint32_t*>(p);
-  };
-  if (n >= kChunk) {
-    const uint32_t mine = at + 4 * g * stride;
+__device__ __forceinline__ void load_values(const char* rows, int64_t stride, int n, u4_t (&x)[BF16 ? 2 : 4]) {
+  constexpr int pieces = Rows16<BF16>::kPieces;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v.x[t][e] = load(rows + (int64_t)(16 * t + e) * stride + mine);
-    return;
+  for (int u = 0; u < Rows16<BF16>::kLoads; ++u) {
+    const int i = 64 * u + (threadIdx.x & 63), row = i / pieces;
+    x[u] = *reinterpret_cast<const u4_t*>(rows + (row < n ? row : n - 1) * stride + i % pieces * 16);
   }
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * t + 4 * g + e;
-      v.x[t][e] = load(rows + (int64_t)(i < n ? i : n - 1) * stride + at);
-    }
 }
 
 #define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(uintptr_t)(p))
@@ -88,6 +79,7 @@ template <int DK, bool BF16>
 struct Handed {
   h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
   h8_t w[BF16 ? 1 : 2][2][64];        // u
+  Rows16<BF16> v, o;                  // the other way: the block's values; and outputs on their way to memory
   int es[64], er[64];                 // their exponents
 };
 
@@ -98,7 +90,7 @@ struct Handed {
 // those of the next block come while one is worked on; 0: they are read where they
 // are.
 template <int DK, bool BF16, int SLABS, int BUFFERS>
-__global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a, Round r) {
+__global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256))) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
   constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
@@ -130,14 +122,6 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   Handed<DK, BF16>& hand = handed[slab];
   if (states) {
-    Values<BF16> next;
-    constexpr int size = BF16 ? 2 : 4;
-    const uint32_t v_row = (uint32_t)a.v_stride * size;
-    const auto load_next = [&](int c) {
-      load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv) * size,
-                        (uint32_t)(col0 + j) * size, v_row, count - c * kChunk, next);
-    };
-    if (r.c0 < end_block) load_next(r.c0);
     float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
     StateTile<DK, 1> st;
     if (r.c0 > 0) load_state<DK, 1>(carry, st);
@@ -162,12 +146,6 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
       const auto factor = [&](int which, int t) {
         return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
       };
-      f4_t v[kTiles];
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[t][e] = __uint_as_float(BF16 ? next.x[t][e] << 16 : next.x[t][e]);
-      if (c + 1 < end_block) load_next(c + 1);
       // K S
       f4_t ks[kTiles];
 #pragma unroll
@@ -189,9 +167,16 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
       hand.es[lane] = es;
       lds_barrier();  // S is handed over
       // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
+      f4_t v[kTiles];
       float m = 0.0f;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const char* at = hand.v.value(16 * t + 4 * g + e);
+          if constexpr (BF16) v[t][e] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at) << 16);
+          else v[t][e] = *reinterpret_cast<const float*>(at);
+        }
         const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
@@ -304,31 +289,25 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
 #pragma unroll
       for (int x = 0; x < Ops::kLower; ++x) p[i][x] = from[(i * Ops::kLower + x) * 64];
   };
-  f4_t o[kTiles];
+  constexpr int size = BF16 ? 2 : 4;
   const auto store_out = [&](int c) {
-    constexpr int size = BF16 ? 2 : 4;
-    const uint32_t out_row = (uint32_t)(a.heads * a.dv) * size;
-    char* rows = static_cast<char*>(a.out) + ((first + c * kChunk) * a.heads + h) * a.dv * size;
-    const uint32_t mine = (uint32_t)(col0 + j) * size + 4 * g * out_row;
+    const int64_t out_row = (int64_t)a.heads * a.dv * size;
+    char* rows = static_cast<char*>(a.out) + (first + c * kChunk) * out_row + ((int64_t)h * a.dv + col0) * size;
     const int n = count - c * kChunk;
-    const auto store = [](char* p, float x) {
-      if constexpr (BF16) *reinterpret_cast<__bf16*>(p) = (__bf16)x;
-      else *reinterpret_cast<float*>(p) = x;
-    };
-    if (n >= kChunk) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) store(rows + (int64_t)(16 * t + e) * out_row + mine, o[t][e]);
-      return;
+    for (int u = 0; u < Rows16<BF16>::kLoads; ++u) {
+      const int i = 64 * u + lane, row = i / Rows16<BF16>::kPieces;
+      const u4_t x = *reinterpret_cast<const u4_t*>(hand.o.piece(u));
+      if (row < n) *reinterpret_cast<u4_t*>(rows + row * out_row + i % Rows16<BF16>::kPieces * 16) = x;
     }
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * t + 4 * g + e < n) store(rows + (int64_t)(16 * t + e) * out_row + mine, o[t][e]);
+  };
+  u4_t next[Rows16<BF16>::kLoads];
+  const auto load_next = [&](int c) {
+    load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv + col0) * size,
+                      a.v_stride * size, count - c * kChunk, next);
   };
   if (r.c0 < end_block) {
+    load_next(r.c0);
     fetch(r.c0);
     load_q(r.c0);
     load_p(r.c0);
@@ -336,6 +315,8 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
   for (int c = r.c0; c < end_block; ++c) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the operands is in LDS
     lds_barrier();
+#pragma unroll
+    for (int u = 0; u < Rows16<BF16>::kLoads; ++u) *reinterpret_cast<u4_t*>(hand.v.piece(u)) = next[u];
     // the next block's operands: a part before each of the block's waits
     const bool ahead = BUFFERS == 2 && c + 1 < end_block;
     if (c > r.c0) store_out(c - 1);
@@ -362,7 +343,10 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
     }
     const int es = hand.es[lane];
     if (ahead) fetch_part(c + 1, 1);
-    if (c + 1 < end_block) load_q(c + 1);
+    if (c + 1 < end_block) {
+      load_next(c + 1);
+      load_q(c + 1);
+    }
     lds_barrier();  // u is handed over
     const int er = hand.er[lane];
     f4_t z[kTiles];
@@ -389,8 +373,10 @@ __global__ __launch_bounds__(128 * SLABS, 1) void delta_scan_kernel(DeltaArgs a,
       const f4_t fp = *reinterpret_cast<const f4_t*>(factors + kFactorP * kChunk + 16 * t + 4 * g);
       const f4_t qs = scale4(y[t], -es), pu = scale4(z[t], -er);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = __builtin_fmaf(fq[e], qs[e], fp[e] * pu[e]);
+      for (int e = 0; e < 4; ++e)
+        store1<BF16>(hand.o.value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[e], qs[e], fp[e] * pu[e]));
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if constexpr (BUFFERS == 1) {
       lds_barrier();
       if (c + 1 < end_block) fetch(c + 1);
