@@ -83,27 +83,27 @@ struct Handed {
   int es[64], er[64];                 // their exponents
 };
 
-// grid (heads, dv / (16 SLABS), seqs).  Of 2 SLABS waves the first half have 16 columns
-// of the state each: r, u and the new state, one block after the other.  The second
-// half makes the outputs of the same columns, of which no state waits, and fetches the
-// next block's operands.  BUFFERS: blocks whose K, K^T, T and factors are in LDS; 2:
+// grid (heads, dv / (16 SLABS), seqs).  SLABS waves have 16 columns of the state each:
+// r, u and the new state, one block after the other.  SLABS more make the outputs of
+// the same columns, of which no state waits, and one fetches the next block's operands
+// and values, so that none of the others stands in the queue to memory.  BUFFERS: blocks whose K, K^T, T and factors are in LDS; 2:
 // those of the next block come while one is worked on; 0: they are read where they
 // are.
 template <int DK, bool BF16, int SLABS, int BUFFERS>
-__global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256))) void delta_scan_kernel(DeltaArgs a, Round r) {
+__global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
   constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
   __shared__ Handed<DK, BF16> handed[SLABS];
   const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slab = wave & (SLABS - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slab = wave % SLABS;
   const int col0 = (blockIdx.y * SLABS + slab) * 16, kh = h / (a.heads / a.key_heads);
   const bool states = wave < SLABS;
   const int src = a.src[b];
   const int64_t first = (int64_t)b * a.nodes, state_size = (int64_t)a.dv * DK;
   const int64_t value_at = (int64_t)h * a.dv + col0 + j;
   if (!delta_used(src, a.slots)) {
-    if (r.c0 == 0 && !states)
+    if (r.c0 == 0 && states)
       for (int t = 0; t < a.nodes; ++t)
         if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
     return;
@@ -255,20 +255,60 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
     if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + (int64_t)col0 * DK, st);
     return;
   }
-  const auto fetch_part = [&](int c, int part) {
-    if constexpr (BUFFERS > 0) {
-      constexpr int loads = (Ops::kQuery + Ops::kP) / 64, third = (loads + 3 * SLABS - 1) / (3 * SLABS);
-      const h8_t *keys = keys_of(c) + lane, *heads = heads_of(c) + lane - Ops::kQuery;
-      h8_t* to = buffer_of(c);
+  constexpr int size = BF16 ? 2 : 4;
+  if (wave == 2 * SLABS) {
+    const h8_t* heads = nullptr;
+    const auto fetch_part = [&](int c, int part) {
+      if constexpr (BUFFERS > 0) {
+        constexpr int loads = (Ops::kQuery + Ops::kP) / 64, third = (loads + 2) / 3;
+        const h8_t* keys = keys_of(c) + lane;
+        heads = heads_of(c) + lane - Ops::kQuery;
+        h8_t* to = buffer_of(c);
 #pragma unroll 4
-      for (int i = part * third * SLABS + slab; i < (part + 1) * third * SLABS; i += SLABS)
-        if (i < loads)
-          __builtin_amdgcn_global_load_lds(GLOBAL_PTR((i < Ops::kQuery / 64 ? keys : heads) + 64 * i), LDS_PTR(to + 64 * i), 16, 0, 0);
+        for (int i = part * third; i < (part + 1) * third; ++i)
+          if (i < loads)
+            __builtin_amdgcn_global_load_lds(GLOBAL_PTR((i < Ops::kQuery / 64 ? keys : heads) + 64 * i),
+                                             LDS_PTR(to + 64 * i), 16, 0, 0);
+      }
+    };
+    u4_t v[SLABS][Rows16<BF16>::kLoads];
+    const auto load_next = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < SLABS; ++u)
+        load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv +
+                                                           (blockIdx.y * SLABS + u) * 16) * size,
+                          a.v_stride * size, count - c * kChunk, v[u]);
+    };
+    const auto hand_next = [&]() {
+#pragma unroll
+      for (int u = 0; u < SLABS; ++u)
+#pragma unroll
+        for (int i = 0; i < Rows16<BF16>::kLoads; ++i) *reinterpret_cast<u4_t*>(handed[u].v.piece(i)) = v[u][i];
+    };
+    if (r.c0 < end_block) {
+      load_next(r.c0);
+      for (int part = 0; part < 3; ++part) fetch_part(r.c0, part);
+      hand_next();
     }
-  };
-  const auto fetch = [&](int c) {
-    for (int part = 0; part < 3; ++part) fetch_part(c, part);
-  };
+    for (int c = r.c0; c < end_block; ++c) {
+      const bool more = c + 1 < end_block, ahead = BUFFERS == 2 && more;
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the operands are in LDS
+      lds_barrier();
+      if (more) load_next(c + 1);
+      if (ahead) fetch_part(c + 1, 0);
+      lds_barrier();  // S is handed over
+      if (ahead) fetch_part(c + 1, 1);
+      lds_barrier();  // u is handed over, the values have been read
+      if (more) hand_next();
+      if (ahead) fetch_part(c + 1, 2);
+      if constexpr (BUFFERS == 1) {
+        lds_barrier();
+        if (more)
+          for (int part = 0; part < 3; ++part) fetch_part(c + 1, part);
+      }
+    }
+    return;
+  }
   // Q and P are this wave's alone: straight to registers, Q where it fits
   constexpr bool hold = P * Ops::kSteps <= 8;
   h8_t q[P][kTiles][hold ? Ops::kSteps : 1], p[P][Ops::kLower];
@@ -289,7 +329,6 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
 #pragma unroll
       for (int x = 0; x < Ops::kLower; ++x) p[i][x] = from[(i * Ops::kLower + x) * 64];
   };
-  constexpr int size = BF16 ? 2 : 4;
   const auto store_out = [&](int c) {
     const int64_t out_row = (int64_t)a.heads * a.dv * size;
     char* rows = static_cast<char*>(a.out) + (first + c * kChunk) * out_row + ((int64_t)h * a.dv + col0) * size;
@@ -301,26 +340,13 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
       if (row < n) *reinterpret_cast<u4_t*>(rows + row * out_row + i % Rows16<BF16>::kPieces * 16) = x;
     }
   };
-  u4_t next[Rows16<BF16>::kLoads];
-  const auto load_next = [&](int c) {
-    load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv + col0) * size,
-                      a.v_stride * size, count - c * kChunk, next);
-  };
   if (r.c0 < end_block) {
-    load_next(r.c0);
-    fetch(r.c0);
     load_q(r.c0);
     load_p(r.c0);
   }
   for (int c = r.c0; c < end_block; ++c) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the operands is in LDS
     lds_barrier();
-#pragma unroll
-    for (int u = 0; u < Rows16<BF16>::kLoads; ++u) *reinterpret_cast<u4_t*>(hand.v.piece(u)) = next[u];
-    // the next block's operands: a part before each of the block's waits
-    const bool ahead = BUFFERS == 2 && c + 1 < end_block;
     if (c > r.c0) store_out(c - 1);
-    if (ahead) fetch_part(c + 1, 0);
     const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
     lds_barrier();  // S is handed over
     f4_t y[kTiles];
@@ -342,11 +368,7 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
       }
     }
     const int es = hand.es[lane];
-    if (ahead) fetch_part(c + 1, 1);
-    if (c + 1 < end_block) {
-      load_next(c + 1);
-      load_q(c + 1);
-    }
+    if (c + 1 < end_block) load_q(c + 1);
     lds_barrier();  // u is handed over
     const int er = hand.er[lane];
     f4_t z[kTiles];
@@ -365,7 +387,6 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
         }
       }
     }
-    if (ahead) fetch_part(c + 1, 2);
     if (c + 1 < end_block) load_p(c + 1);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -377,10 +398,7 @@ __global__ __launch_bounds__(128 * SLABS, 1) __attribute__((amdgpu_num_vgpr(256)
         store1<BF16>(hand.o.value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[e], qs[e], fp[e] * pu[e]));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if constexpr (BUFFERS == 1) {
-      lds_barrier();
-      if (c + 1 < end_block) fetch(c + 1);
-    }
+    if constexpr (BUFFERS == 1) lds_barrier();
   }
   if (r.c0 < end_block) store_out(end_block - 1);
   if (!r.last) return;
@@ -422,7 +440,8 @@ void scan(const DeltaArgs& a, const Round& r, hipStream_t stream) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
   constexpr int slabs = 2, bytes = 16 * (Ops::kQuery + Ops::kP), hand = slabs * (int)sizeof(Handed<DK, BF16>);
   constexpr int buffers = 2 * bytes + hand <= kLds ? 2 : bytes + hand <= kLds ? 1 : 0;
-  delta_scan_kernel<DK, BF16, slabs, buffers><<<dim3(a.heads, a.dv / (16 * slabs), a.seqs), 128 * slabs, 0, stream>>>(a, r);
+  delta_scan_kernel<DK, BF16, slabs, buffers><<<dim3(a.heads, a.dv / (16 * slabs), a.seqs), 64 * (2 * slabs + 1), 0,
+                                                    stream>>>(a, r);
 }
 
 template <int DK, bool BF16>
