@@ -108,12 +108,14 @@ __global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
   if (to >= 0) store_state<DK, COLS>(a.states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
 }
 
-// Drafted trees.  With the sums G of the decays along each node's line,
+// Drafted trees of more than 48 fp32 nodes with keys of 256, node after node (the others are
+// delta_tree.hip's).  With the sums G of the decays along each node's line,
 //   u_v = beta_v (v_v - e^G_v S k_v - sum_a e^(G_v - G_a) (k_a . k_v) u_a),
 //   o_v = scale (e^G_v S q_v + sum_a e^(G_v - G_a) (k_a . q_v) u_a),
 // a the ancestors of v (and v itself in o).  grid (dv / 64, heads, seqs).
-template <int DK, bool BF16>
 __global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
+  constexpr int DK = 256;
+  constexpr bool BF16 = false;
   __shared__ float rows[2][DK];      // k_v, q_v
   __shared__ float near[2][64];      // e^(G_v - G_a) k_a . (k_v, q_v)
   __shared__ float u[64][64];        // nodes x rows of S
@@ -285,11 +287,6 @@ void step(const DeltaArgs& a, hipStream_t stream) {
   delta_step_kernel<DK, 1, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
 }
 
-template <int DK, bool BF16>
-void tree(const DeltaArgs& a, hipStream_t stream) {
-  delta_tree_kernel<DK, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
-}
-
 template <int DK>
 void commit(const DeltaCommitArgs& a, hipStream_t stream) {
   delta_commit_kernel<DK, 1><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
@@ -313,9 +310,8 @@ hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_delta_tree(const DeltaArgs& a, hipStream_t stream) {
-  if (a.dk == 64) a.bf16 ? tree<64, true>(a, stream) : tree<64, false>(a, stream);
-  else if (a.dk == 128) a.bf16 ? tree<128, true>(a, stream) : tree<128, false>(a, stream);
-  else a.bf16 ? tree<256, true>(a, stream) : tree<256, false>(a, stream);
+  if (delta_tree_in_block(a)) launch_delta_tree_block(a, stream);
+  else delta_tree_kernel<<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
   return hipGetLastError();
 }
 

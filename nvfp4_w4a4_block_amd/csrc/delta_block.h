@@ -100,7 +100,7 @@ struct BlockOps {
 // Factors of a block's rows.
 enum { kFactorR, kFactorX, kFactorQ, kFactorP };
 
-template <int DK, bool BF16, int NT>
+template <int DK, bool BF16, int NT, bool TREE>
 struct BlockShared {
   static constexpr int kPitch = 16 * NT + 4;
   h8_t key[BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows];
@@ -108,6 +108,7 @@ struct BlockShared {
   float p[16 * NT][kPitch];  // P
   double decay[64];          // G in exponents of 2
   uint64_t line[64];         // trees: ancestors and self
+  h8_t query[TREE ? BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows : 1];
   float beta[64], key_factor[64], query_factor[64];
   int t_exponent[64];
 };
@@ -136,10 +137,10 @@ __device__ __forceinline__ void load_row(const void* rows, int64_t at, RawRow<DK
 }
 
 // The row as an operand, zeros where it is not there.  Returns the factor that makes
-// the stored row the row as used.
+// the stored row the row as used; `as_used` (or NULL) is where that goes.
 template <int DK, bool BF16>
 __device__ __forceinline__ float row_operand(const RawRow<DK, BF16>& raw, bool there, float eps,
-                                             h8_t (&op)[BF16 ? 1 : 2][DK / 32]) {
+                                             h8_t (&op)[BF16 ? 1 : 2][DK / 32], float* as_used = nullptr) {
   f4_t x[DK / 32][2];
   float m = 0.0f;
 #pragma unroll
@@ -168,15 +169,26 @@ __device__ __forceinline__ float row_operand(const RawRow<DK, BF16>& raw, bool t
     if constexpr (BF16) op[0][s] = operand_hi(x[s][0], x[s][1]);
     else operand_parts(x[s][0], x[s][1], op[0][s], op[1][s]);
   }
-  if (!there) return 0.0f;
-  if (eps < 0.0f) return __builtin_amdgcn_ldexpf(1.0f, e);
-  // 1 / sqrt of the scaled row's squares; where eps, scaled alike, is past fp32 it is all
-  const float small = __builtin_amdgcn_ldexpf(eps, -2 * e);
-  const bool all = small > 1e38f;
-  const float square = all ? eps : sum_of_groups(ss) + small;
-  float y = __builtin_amdgcn_rsqf(square);
-  y = square > 0.0f ? __builtin_fmaf(0.5f * y, __builtin_fmaf(-square * y, y, 1.0f), y) : y;
-  return all ? __builtin_amdgcn_ldexpf(y, e) : y;
+  float factor = __builtin_amdgcn_ldexpf(1.0f, e);
+  if (eps >= 0.0f) {
+    // 1 / sqrt of the scaled row's squares; where eps, scaled alike, is past fp32 it is all
+    const float small = __builtin_amdgcn_ldexpf(eps, -2 * e);
+    const bool all = small > 1e38f;
+    const float square = all ? eps : sum_of_groups(ss) + small;
+    float y = __builtin_amdgcn_rsqf(square);
+    y = square > 0.0f ? __builtin_fmaf(0.5f * y, __builtin_fmaf(-square * y, y, 1.0f), y) : y;
+    factor = all ? __builtin_amdgcn_ldexpf(y, e) : y;
+  }
+  if (as_used) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<f4_t*>(as_used + 32 * s + 16 * h + 4 * g) =
+            there ? x[s][h] * factor : f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  return there ? factor : 0.0f;
 }
 
 // a b^T of two tiles' rows, with `parts` as above: 16x16.
@@ -289,18 +301,22 @@ __device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t firs
 
 // Prepares the n tokens of a block of value head h, n <= 16 NT, from its rows,
 // by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
-// head's part (NULL: not wanted), head_to: the value head's.
+// head's part (NULL: not wanted; of trees K and Q stay in sh), head_to: the value
+// head's.  Trees: factor X is u's power of two alone, and `keys` (or NULL) the keys'
+// rows as used, `key_row` values apart, for all `nodes` of them.
 template <int DK, bool BF16, int NT, bool TREE>
 __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
-                                              BlockShared<DK, BF16, NT>& sh, h8_t* key_to, h8_t* head_to) {
+                                              BlockShared<DK, BF16, NT, TREE>& sh, h8_t* key_to, h8_t* head_to,
+                                              float* keys = nullptr, int64_t key_row = 0, int nodes = 0) {
   typedef BlockOps<DK, BF16, NT> Ops;
-  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT>::kPitch;
+  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT, TREE>::kPitch;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const bool works = w < NT;
   const bool there = works && 16 * w + j < n;
   h8_t key[P][Ops::kSteps], query[P][Ops::kSteps];
   if (works) {
-    const float kf = row_operand<DK, BF16>(rows.k, there, a.norm_eps, key);
+    float* as_used = TREE && keys && 16 * w + j < nodes ? keys + (16 * w + j) * key_row : nullptr;
+    const float kf = row_operand<DK, BF16>(rows.k, there, a.norm_eps, key, as_used);
     const float qf = row_operand<DK, BF16>(rows.q, there, a.norm_eps, query);
     if (g == 0) {
       sh.key_factor[16 * w + j] = kf;
@@ -312,7 +328,8 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
       for (int s = 0; s < Ops::kSteps; ++s) {
         const int at = p * Ops::kRows + (w * Ops::kSteps + s) * 64 + lane;
         sh.key[at] = key[p][s];
-        if (key_to) {
+        if constexpr (TREE) sh.query[at] = query[p][s];
+        else if (key_to) {
           key_to[Ops::kKey + at] = key[p][s];
           key_to[Ops::kQuery + at] = query[p][s];
         }
@@ -460,7 +477,8 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
       const double at = sh.decay[i], end = sh.decay[16 * NT - 1];
       const float into = __builtin_amdgcn_exp2f((float)at), kf = sh.key_factor[i];
       factors[kFactorR * 16 * NT + i] = -into * kf;
-      factors[kFactorX * 16 * NT + i] = __builtin_amdgcn_ldexpf(kf * __builtin_amdgcn_exp2f((float)(end - at)), sh.t_exponent[i]);
+      factors[kFactorX * 16 * NT + i] =
+          __builtin_amdgcn_ldexpf(TREE ? 1.0f : kf * __builtin_amdgcn_exp2f((float)(end - at)), sh.t_exponent[i]);
       factors[kFactorQ * 16 * NT + i] = into * sh.query_factor[i];
       factors[kFactorP * 16 * NT + i] = __builtin_amdgcn_ldexpf(1.0f, e);
       if (i == 0) factors[4 * 16 * NT] = __builtin_amdgcn_exp2f((float)end);

@@ -26,7 +26,7 @@ struct Round {
 template <int DK, bool BF16>
 __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  __shared__ BlockShared<DK, BF16, kTiles> sh;
+  __shared__ BlockShared<DK, BF16, kTiles, false> sh;
   const int h = blockIdx.x, b = blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
   const int kh = h / group;
   BlockRows<DK, BF16> rows;

@@ -11,6 +11,10 @@ bool delta_chunked(const DeltaArgs& a);
 int64_t delta_chunk_workspace_bytes(const DeltaArgs& a);
 void launch_delta_chunks(const DeltaArgs& a, hipStream_t stream);
 
+// Trees as one block (delta_tree.hip).
+bool delta_tree_in_block(const DeltaArgs& a);
+void launch_delta_tree_block(const DeltaArgs& a, hipStream_t stream);
+
 // Four values of a row of q, k or v from value `at` on, at a multiple of four.
 template <bool BF16>
 __device__ __forceinline__ f4_t load4(const void* rows, int64_t at) {

@@ -1,0 +1,153 @@
+// Gated delta rule over drafted trees of at most 64 nodes, in one launch.
+//
+// The page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic Benchmark 6.4x
+// Faster on Jetson AGX Thor" verifies a tree of drafted tokens in one pass (section
+// "Using tree-based multi-token prediction to accelerate LLM inference").  A tree is a
+// block of delta_block.h whose tokens see their ancestors: one reading of the state
+// serves all nodes, where a state per node would be written and read again.
+//
+// A workgroup has 64 columns of one head's state, a wave 16 of them; its first waves
+// prepare the block (the other workgroups of the head do the same), while all of them
+// wait for their columns.
+#include "delta_block.h"
+
+namespace nvfp4 {
+namespace {
+
+// grid (heads, dv / 64, seqs).
+template <int DK, bool BF16, int NT>
+__global__ __launch_bounds__(256) void delta_tree_block_kernel(DeltaArgs a) {
+  typedef BlockOps<DK, BF16, NT> Ops;
+  constexpr int P = Ops::kParts, KT = DK / 16;
+  __shared__ BlockShared<DK, BF16, NT, true> sh;
+  __shared__ h8_t head[Ops::kHeadUnits];
+  const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int group = a.heads / a.key_heads, kh = h / group, col0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 16;
+  const int64_t first = (int64_t)b * a.nodes, value_at = (int64_t)h * a.dv + col0 + j, row = (int64_t)a.heads * a.dv;
+  BlockRows<DK, BF16> rows;
+  load_block_rows<DK, BF16, NT, true>(a, first, a.nodes, h, kh, rows);
+  const int src = a.src[b];
+  const bool used = delta_used(src, a.slots);
+  const int n = used ? delta_count(a.counts, a.nodes, b) : 0;
+  StateTile<DK, 1> st;
+  if (used && src >= 0) load_state<DK, 1>(a.states + (((int64_t)src * a.heads + h) * a.dv + col0) * DK, st);
+  else zero_state<DK, 1>(st);
+  f4_t(&s)[KT] = st.s[0];
+  uint32_t raw[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * t + 4 * g + e;
+      const int64_t at = (first + (i < a.nodes ? i : a.nodes - 1)) * a.v_stride + value_at;
+      if constexpr (BF16) raw[t][e] = static_cast<const uint16_t*>(a.v)[at];
+      else raw[t][e] = static_cast<const uint32_t*>(a.v)[at];
+    }
+  float* keys = h % group == 0 && blockIdx.y == 0 ? a.keys + (first * a.key_heads + kh) * DK : nullptr;
+  prepare_block<DK, BF16, NT, true>(a, rows, n, sh, nullptr, head, keys, (int64_t)a.key_heads * DK, a.nodes);
+  __syncthreads();
+  float m = 0.0f;
+#pragma unroll
+  for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
+  const int es = 5 - exponent_of(max_of_groups(m));
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f4_t ks[NT], qs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) ks[t] = qs[t] = zero;
+#pragma unroll
+  for (int x = 0; x < Ops::kSteps; ++x) {
+    h8_t hi, lo;
+    operand_parts(scale4(s[2 * x], es), scale4(s[2 * x + 1], es), hi, lo);
+#pragma unroll
+    for (int part = 0; part < P + 1; ++part)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int at = (part == 2 ? Ops::kRows : 0) + (t * Ops::kSteps + x) * 64 + lane;
+        ks[t] = mfma16x16x32(sh.key[at], part == 1 ? lo : hi, ks[t]);
+        if (P == 2 || part == 0) qs[t] = mfma16x16x32(sh.query[at], part == 1 ? lo : hi, qs[t]);
+      }
+  }
+  const float* factors = reinterpret_cast<const float*>(head + Ops::kFactors);
+  const auto factor = [&](int which, int t) {
+    return *reinterpret_cast<const f4_t*>(factors + which * 16 * NT + 16 * t + 4 * g);
+  };
+  f4_t v[NT + (NT & 1)], w[NT + (NT & 1)], pu[NT];
+  m = 0.0f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(BF16 ? raw[t][e] << 16 : raw[t][e]);
+      v[t][e] = 16 * t + 4 * g + e < n ? __builtin_fmaf(f[e], y[e], x) : 0.0f;
+    }
+    m = max4(m, v[t]);
+    w[t] = pu[t] = zero;
+  }
+  if constexpr (NT & 1) v[NT] = w[NT] = zero;
+  const int er = 3 - exponent_of(max_of_groups(m));
+#pragma unroll
+  for (int x = 0; x < Ops::kTokenSteps; ++x) {
+    h8_t hi, lo;
+    operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+#pragma unroll
+      for (int t = 2 * x; t < NT; ++t) {
+        const int at = Ops::kT + (Ops::lower(t) + x) * 64 + (part == 2 ? Ops::kLower * 64 : 0) + lane;
+        w[t] = mfma16x16x32(head[at], part == 1 ? lo : hi, w[t]);
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < Ops::kTokenSteps; ++x) {
+    h8_t hi, lo;
+    if constexpr (P == 1) lo = hi = operand_hi(w[2 * x], w[2 * x + 1]);
+    else operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
+#pragma unroll
+    for (int part = 0; part < (P == 1 ? 1 : 3); ++part)
+#pragma unroll
+      for (int t = 2 * x; t < NT; ++t) {
+        const int at = Ops::kP + (Ops::lower(t) + x) * 64 + (part == 2 ? Ops::kLower * 64 : 0) + lane;
+        pu[t] = mfma16x16x32(head[at], part == 1 ? lo : hi, pu[t]);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t), fx = factor(kFactorX, t);
+    const f4_t y = scale4(qs[t], -es), z = scale4(pu[t], -er), u = scale4(w[t] * fx, -er);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * t + 4 * g + e;
+      if (i >= a.nodes) continue;
+      const bool in = i < n;
+      a.updates[(first + i) * row + value_at] = in ? u[e] : 0.0f;
+      store1<BF16>(a.out, (first + i) * row + value_at, in ? __builtin_fmaf(fq[e], y[e], fp[e] * z[e]) : 0.0f);
+    }
+  }
+}
+
+template <int DK, bool BF16, int NT>
+void run(const DeltaArgs& a, hipStream_t stream) {
+  delta_tree_block_kernel<DK, BF16, NT><<<dim3(a.heads, a.dv / 64, a.seqs), 256, 0, stream>>>(a);
+}
+
+template <int DK, bool BF16>
+void run(const DeltaArgs& a, hipStream_t stream) {
+  if (a.nodes <= 16) run<DK, BF16, 1>(a, stream);
+  else if (a.nodes <= 32) run<DK, BF16, 2>(a, stream);
+  else if (a.nodes <= 48) run<DK, BF16, 3>(a, stream);
+  else if constexpr (DK < 256 || BF16) run<DK, BF16, 4>(a, stream);
+}
+
+}  // namespace
+
+// What the block of 64 fp32 rows of 256 needs is past a CU's LDS.
+bool delta_tree_in_block(const DeltaArgs& a) { return a.dk < 256 || a.bf16 || a.nodes <= 48; }
+
+void launch_delta_tree_block(const DeltaArgs& a, hipStream_t stream) {
+  if (a.dk == 64) a.bf16 ? run<64, true>(a, stream) : run<64, false>(a, stream);
+  else if (a.dk == 128) a.bf16 ? run<128, true>(a, stream) : run<128, false>(a, stream);
+  else a.bf16 ? run<256, true>(a, stream) : run<256, false>(a, stream);
+}
+
+}  // namespace nvfp4
