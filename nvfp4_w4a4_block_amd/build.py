@@ -37,7 +37,7 @@ SOURCES = {
     "kv_rope.hip": [],
     "delta.hip": [],
     "delta_chunk.hip": [],
-    "delta_tree.hip": [],
+    "delta_single.hip": [],
     "logprobs.hip": [],
     "gemm_tiled.hip": [],
     "stream.hip": [],

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
 }
 
 // Drafted trees of more than 48 fp32 nodes with keys of 256, node after node (the others are
-// delta_tree.hip's).  With the sums G of the decays along each node's line,
+// delta_single.hip's).  With the sums G of the decays along each node's line,
 //   u_v = beta_v (v_v - e^G_v S k_v - sum_a e^(G_v - G_a) (k_a . k_v) u_a),
 //   o_v = scale (e^G_v S q_v + sum_a e^(G_v - G_a) (k_a . q_v) u_a),
 // a the ancestors of v (and v itself in o).  grid (dv / 64, heads, seqs).
@@ -294,14 +294,23 @@ void commit(const DeltaCommitArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Up to four tokens go one after the other, up to 64 as one block, more block by block.
+constexpr int kFewTokens = 4;
+
 int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {
-  return delta_chunked(a) ? delta_chunk_workspace_bytes(a) : 0;
+  return a.nodes <= kFewTokens || delta_single_block(a) ? 0 : delta_chunk_workspace_bytes(a);
 }
 
 hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
-  if (delta_chunked(a) && a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
-    launch_delta_chunks(a, stream);
-    return hipGetLastError();
+  if (a.nodes > kFewTokens) {
+    if (delta_single_block(a)) {
+      launch_delta_block(a, stream);
+      return hipGetLastError();
+    }
+    if (a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
+      launch_delta_chunks(a, stream);
+      return hipGetLastError();
+    }
   }
   if (a.dk == 64) a.bf16 ? step<64, true>(a, stream) : step<64, false>(a, stream);
   else if (a.dk == 128) a.bf16 ? step<128, true>(a, stream) : step<128, false>(a, stream);
@@ -310,7 +319,7 @@ hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_delta_tree(const DeltaArgs& a, hipStream_t stream) {
-  if (delta_tree_in_block(a)) launch_delta_tree_block(a, stream);
+  if (delta_single_block(a)) launch_delta_block(a, stream);
   else delta_tree_kernel<<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
   return hipGetLastError();
 }

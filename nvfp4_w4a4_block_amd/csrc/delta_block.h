@@ -100,7 +100,7 @@ struct BlockOps {
 // Factors of a block's rows.
 enum { kFactorR, kFactorX, kFactorQ, kFactorP };
 
-template <int DK, bool BF16, int NT, bool TREE>
+template <int DK, bool BF16, int NT, bool LOCAL>
 struct BlockShared {
   static constexpr int kPitch = 16 * NT + 4;
   h8_t key[BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows];
@@ -108,7 +108,7 @@ struct BlockShared {
   float p[16 * NT][kPitch];  // P
   double decay[64];          // G in exponents of 2
   uint64_t line[64];         // trees: ancestors and self
-  h8_t query[TREE ? BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows : 1];
+  h8_t query[LOCAL ? BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows : 1];
   float beta[64], key_factor[64], query_factor[64];
   int t_exponent[64];
 };
@@ -274,6 +274,23 @@ __device__ __forceinline__ int store_rows(const f4_t (&x)[2][2], int steps, h8_t
   return e;
 }
 
+// An operand of K transposed from K's: lane j + 16 g has tokens 32 s + 4 g .., 32 s +
+// 16 + 4 g .. of value 16 t + j.
+template <int DK, bool BF16, int NT>
+__device__ __forceinline__ h8_t transposed_operand(const h8_t* key, int part, int t, int s) {
+  typedef BlockOps<DK, BF16, NT> Ops;
+  const _Float16* from = reinterpret_cast<const _Float16*>(key);
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  h8_t x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rt = 2 * s + (i >> 2), tok = 4 * g + (i & 3);
+    const int unit = part * Ops::kRows + (rt * Ops::kSteps + (t >> 1)) * 64 + tok + 16 * (j >> 2);
+    x[i] = rt < NT ? from[unit * 8 + 4 * (t & 1) + (j & 3)] : (_Float16)0.0f;
+  }
+  return x;
+}
+
 // What a block is made of, as it comes from memory.
 template <int DK, bool BF16>
 struct BlockRows {
@@ -301,15 +318,15 @@ __device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t firs
 
 // Prepares the n tokens of a block of value head h, n <= 16 NT, from its rows,
 // by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
-// head's part (NULL: not wanted; of trees K and Q stay in sh), head_to: the value
-// head's.  Trees: factor X is u's power of two alone, and `keys` (or NULL) the keys'
+// head's part (NULL: not wanted), head_to: the value head's.  LOCAL: the workgroup
+// goes on with the block itself, K and Q stay in sh.  Trees: factor X is u's power of two alone, and `keys` (or NULL) the keys'
 // rows as used, `key_row` values apart, for all `nodes` of them.
-template <int DK, bool BF16, int NT, bool TREE>
+template <int DK, bool BF16, int NT, bool TREE, bool LOCAL>
 __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
-                                              BlockShared<DK, BF16, NT, TREE>& sh, h8_t* key_to, h8_t* head_to,
+                                              BlockShared<DK, BF16, NT, LOCAL>& sh, h8_t* key_to, h8_t* head_to,
                                               float* keys = nullptr, int64_t key_row = 0, int nodes = 0) {
   typedef BlockOps<DK, BF16, NT> Ops;
-  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT, TREE>::kPitch;
+  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT, LOCAL>::kPitch;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const bool works = w < NT;
   const bool there = works && 16 * w + j < n;
@@ -328,7 +345,7 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
       for (int s = 0; s < Ops::kSteps; ++s) {
         const int at = p * Ops::kRows + (w * Ops::kSteps + s) * 64 + lane;
         sh.key[at] = key[p][s];
-        if constexpr (TREE) sh.query[at] = query[p][s];
+        if constexpr (LOCAL) sh.query[at] = query[p][s];
         else if (key_to) {
           key_to[Ops::kKey + at] = key[p][s];
           key_to[Ops::kQuery + at] = query[p][s];
@@ -483,23 +500,14 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
       factors[kFactorP * 16 * NT + i] = __builtin_amdgcn_ldexpf(1.0f, e);
       if (i == 0) factors[4 * 16 * NT] = __builtin_amdgcn_exp2f((float)end);
     }
-    if (key_to && !TREE) {
-      // K transposed: lane j + 16 g has tokens 32 s + 4 g .., 32 s + 16 + 4 g .. of value 16 t + j
-      const _Float16* from = reinterpret_cast<const _Float16*>(sh.key);
+    if constexpr (!LOCAL)
+      if (key_to)
 #pragma unroll 1
-      for (int u = w; u < P * (DK / 16) * Ops::kTokenSteps; u += NT) {
-        const int part = u / ((DK / 16) * Ops::kTokenSteps), v = u - part * ((DK / 16) * Ops::kTokenSteps);
-        const int t = v / Ops::kTokenSteps, s = v - t * Ops::kTokenSteps;
-        h8_t x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rt = 2 * s + (i >> 2), tok = 4 * g + (i & 3);
-          const int unit = part * Ops::kRows + (rt * Ops::kSteps + (t >> 1)) * 64 + tok + 16 * (j >> 2);
-          x[i] = rt < NT ? from[unit * 8 + 4 * (t & 1) + (j & 3)] : (_Float16)0.0f;
+        for (int u = w; u < P * (DK / 16) * Ops::kTokenSteps; u += NT) {
+          const int part = u / ((DK / 16) * Ops::kTokenSteps), v = u - part * ((DK / 16) * Ops::kTokenSteps);
+          key_to[Ops::kKeyT + part * Ops::kCols + v * 64 + lane] =
+              transposed_operand<DK, BF16, NT>(sh.key, part, v / Ops::kTokenSteps, v % Ops::kTokenSteps);
         }
-        key_to[Ops::kKeyT + part * Ops::kCols + v * 64 + lane] = x;
-      }
-    }
   }
 }
 

@@ -36,7 +36,7 @@ __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a,
   const int n = count - t0 < kChunk ? count - t0 : kChunk;
   const int64_t block = (int64_t)b * (r.c1 - r.c0) + blockIdx.y;
   h8_t* key_to = h % group == 0 ? r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits : nullptr;
-  prepare_block<DK, BF16, kTiles, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
+  prepare_block<DK, BF16, kTiles, false, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
 
 // 64 rows of 16 values, one after the other in LDS; the pitch keeps the four rows that
@@ -226,9 +226,10 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
         es = 5 - exponent_of(max_of_groups(most));
       }
-      // e^G_end times a power of two, one factor: where it leaves fp32's range S is as nothing
-      // beside X (its largest value is taken to 32 .. 64 after it)
-      const float fade = __builtin_amdgcn_ldexpf(end, es - before);
+      // e^G_end times a power of two, one factor: it takes the largest of s, 2^-30 at least
+      // or nothing at all, to 64 at most, so it is past fp32 only where s is nothing
+      float fade = __builtin_amdgcn_ldexpf(end, es - before);
+      fade = fade == __builtin_inff() ? 0.0f : fade;
 #pragma unroll
       for (int t = 0; t < KT; ++t) s[t] *= fade;
 #pragma unroll
@@ -462,8 +463,6 @@ void run(const DeltaArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
-
-bool delta_chunked(const DeltaArgs& a) { return a.nodes > 16; }
 
 int64_t delta_chunk_workspace_bytes(const DeltaArgs& a) { return carry_bytes(a) + round_blocks(a) * block_bytes(a); }
 

@@ -6,14 +6,13 @@
 
 namespace nvfp4 {
 
-// Chains that go block by block, given their workspace (delta_chunk.hip).
-bool delta_chunked(const DeltaArgs& a);
+// Chains block by block, given their workspace (delta_chunk.hip).
 int64_t delta_chunk_workspace_bytes(const DeltaArgs& a);
 void launch_delta_chunks(const DeltaArgs& a, hipStream_t stream);
 
-// Trees as one block (delta_tree.hip).
-bool delta_tree_in_block(const DeltaArgs& a);
-void launch_delta_tree_block(const DeltaArgs& a, hipStream_t stream);
+// Trees (with parents) and chains of one block (delta_single.hip).
+bool delta_single_block(const DeltaArgs& a);
+void launch_delta_block(const DeltaArgs& a, hipStream_t stream);
 
 // Four values of a row of q, k or v from value `at` on, at a multiple of four.
 template <bool BF16>

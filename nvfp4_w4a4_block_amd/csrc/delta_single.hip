@@ -1,10 +1,11 @@
-// Gated delta rule over drafted trees of at most 64 nodes, in one launch.
+// Gated delta rule over drafted trees and chains of at most 64 tokens, in one launch.
 //
 // The page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic Benchmark 6.4x
 // Faster on Jetson AGX Thor" verifies a tree of drafted tokens in one pass (section
 // "Using tree-based multi-token prediction to accelerate LLM inference").  A tree is a
 // block of delta_block.h whose tokens see their ancestors: one reading of the state
-// serves all nodes, where a state per node would be written and read again.
+// serves all nodes, where a state per node would be written and read again.  A short
+// chain is a block that writes the state that follows.
 //
 // A workgroup has 64 columns of one head's state, a wave 16 of them; its first waves
 // prepare the block (the other workgroups of the head do the same), while all of them
@@ -15,8 +16,8 @@ namespace nvfp4 {
 namespace {
 
 // grid (heads, dv / 64, seqs).
-template <int DK, bool BF16, int NT>
-__global__ __launch_bounds__(256) void delta_tree_block_kernel(DeltaArgs a) {
+template <int DK, bool BF16, int NT, bool TREE>
+__global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
   typedef BlockOps<DK, BF16, NT> Ops;
   constexpr int P = Ops::kParts, KT = DK / 16;
   __shared__ BlockShared<DK, BF16, NT, true> sh;
@@ -25,7 +26,7 @@ __global__ __launch_bounds__(256) void delta_tree_block_kernel(DeltaArgs a) {
   const int group = a.heads / a.key_heads, kh = h / group, col0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 16;
   const int64_t first = (int64_t)b * a.nodes, value_at = (int64_t)h * a.dv + col0 + j, row = (int64_t)a.heads * a.dv;
   BlockRows<DK, BF16> rows;
-  load_block_rows<DK, BF16, NT, true>(a, first, a.nodes, h, kh, rows);
+  load_block_rows<DK, BF16, NT, TREE>(a, first, a.nodes, h, kh, rows);
   const int src = a.src[b];
   const bool used = delta_used(src, a.slots);
   const int n = used ? delta_count(a.counts, a.nodes, b) : 0;
@@ -43,13 +44,14 @@ __global__ __launch_bounds__(256) void delta_tree_block_kernel(DeltaArgs a) {
       if constexpr (BF16) raw[t][e] = static_cast<const uint16_t*>(a.v)[at];
       else raw[t][e] = static_cast<const uint32_t*>(a.v)[at];
     }
-  float* keys = h % group == 0 && blockIdx.y == 0 ? a.keys + (first * a.key_heads + kh) * DK : nullptr;
-  prepare_block<DK, BF16, NT, true>(a, rows, n, sh, nullptr, head, keys, (int64_t)a.key_heads * DK, a.nodes);
+  float* keys = TREE && h % group == 0 && blockIdx.y == 0 ? a.keys + (first * a.key_heads + kh) * DK : nullptr;
+  prepare_block<DK, BF16, NT, TREE, true>(a, rows, n, sh, nullptr, head, keys, (int64_t)a.key_heads * DK, a.nodes);
   __syncthreads();
   float m = 0.0f;
 #pragma unroll
   for (int t = 0; t < KT; ++t) m = max4(m, s[t]);
-  const int es = 5 - exponent_of(max_of_groups(m));
+  const float m_state = max_of_groups(m);
+  const int es = 5 - exponent_of(m_state);
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f4_t ks[NT], qs[NT];
 #pragma unroll
@@ -113,22 +115,56 @@ __global__ __launch_bounds__(256) void delta_tree_block_kernel(DeltaArgs a) {
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t), fx = factor(kFactorX, t);
-    const f4_t y = scale4(qs[t], -es), z = scale4(pu[t], -er), u = scale4(w[t] * fx, -er);
+    const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t);
+    const f4_t y = scale4(qs[t], -es), z = scale4(pu[t], -er);
+    w[t] *= factor(kFactorX, t);
+    const f4_t u = scale4(w[t], -er);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * t + 4 * g + e;
       if (i >= a.nodes) continue;
       const bool in = i < n;
-      a.updates[(first + i) * row + value_at] = in ? u[e] : 0.0f;
+      if constexpr (TREE) a.updates[(first + i) * row + value_at] = in ? u[e] : 0.0f;
       store1<BF16>(a.out, (first + i) * row + value_at, in ? __builtin_fmaf(fq[e], y[e], fp[e] * z[e]) : 0.0f);
     }
+  }
+  if constexpr (!TREE) {
+    if (!used) return;
+    const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
+    if (to < 0) return;
+    if (n > 0) {
+      // S <- e^G_end S + K^T X, X = diag(e^(G_end - G)) u
+      const float end = factors[4 * 16 * NT];
+      float mx = 0.0f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mx = max4(mx, w[t]);
+      const int en = 5 - exponent_of(max_of_groups(fmaxf(__builtin_amdgcn_ldexpf(mx, -er), m_state * end)));
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, en);
+#pragma unroll
+      for (int x = 0; x < Ops::kTokenSteps; ++x) {
+        h8_t hi, lo;
+        operand_parts(scale4(w[2 * x], en - er), scale4(w[2 * x + 1], en - er), hi, lo);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const h8_t k = transposed_operand<DK, BF16, NT>(sh.key, 0, t, x);
+          s[t] = mfma16x16x32(k, hi, s[t]);
+          s[t] = mfma16x16x32(k, lo, s[t]);
+          if constexpr (P == 2) s[t] = mfma16x16x32(transposed_operand<DK, BF16, NT>(sh.key, 1, t, x), hi, s[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -en);
+    }
+    store_state<DK, 1>(a.states + (((int64_t)to * a.heads + h) * a.dv + col0) * DK, st);
   }
 }
 
 template <int DK, bool BF16, int NT>
 void run(const DeltaArgs& a, hipStream_t stream) {
-  delta_tree_block_kernel<DK, BF16, NT><<<dim3(a.heads, a.dv / 64, a.seqs), 256, 0, stream>>>(a);
+  const dim3 grid(a.heads, a.dv / 64, a.seqs);
+  if (a.parent) delta_block_kernel<DK, BF16, NT, true><<<grid, 256, 0, stream>>>(a);
+  else delta_block_kernel<DK, BF16, NT, false><<<grid, 256, 0, stream>>>(a);
 }
 
 template <int DK, bool BF16>
@@ -142,9 +178,9 @@ void run(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 
 // What the block of 64 fp32 rows of 256 needs is past a CU's LDS.
-bool delta_tree_in_block(const DeltaArgs& a) { return a.dk < 256 || a.bf16 || a.nodes <= 48; }
+bool delta_single_block(const DeltaArgs& a) { return a.nodes <= (a.dk < 256 || a.bf16 ? 64 : 48); }
 
-void launch_delta_tree_block(const DeltaArgs& a, hipStream_t stream) {
+void launch_delta_block(const DeltaArgs& a, hipStream_t stream) {
   if (a.dk == 64) a.bf16 ? run<64, true>(a, stream) : run<64, false>(a, stream);
   else if (a.dk == 128) a.bf16 ? run<128, true>(a, stream) : run<128, false>(a, stream);
   else a.bf16 ? run<256, true>(a, stream) : run<256, false>(a, stream);
