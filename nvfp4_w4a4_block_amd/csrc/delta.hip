@@ -254,28 +254,34 @@ __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitAr
   }
   const float weight = node >= 0 ? expf((float)after) : 0.0f;
   for (int t0 = 0; t0 < n; t0 += kTile) {
-    const int m = n - t0 < kTile ? n - t0 : kTile;
-    __syncthreads();
-    for (int i = wave; i < m; i += kWaves) {
+    // a tile's u at once, one latency for all; a place without a node adds 0 times 0
+    float u[kTile][COLS];
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
       const int v = __builtin_amdgcn_readlane(node, t0 + i);
-      if (v >= 0 && lane < DK / 4)
-        *reinterpret_cast<f4_t*>(&keys[i][4 * lane]) =
-            load4<false>(a.keys, ((first + v) * a.key_heads + kh) * DK + 4 * lane);
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), t0 + i));
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const float y = a.updates[((first + (v < 0 ? 0 : v)) * a.heads + h) * a.dv + row0 + 16 * c + j];
+        u[i][c] = v < 0 ? 0.0f : w * y;
+      }
     }
     __syncthreads();
-    for (int i = 0; i < m; ++i) {
+    for (int i = wave; i < kTile; i += kWaves) {
       const int v = __builtin_amdgcn_readlane(node, t0 + i);
-      if (v < 0) continue;
-      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), t0 + i));
-      float u[COLS];
+      if (lane < DK / 4)
+        *reinterpret_cast<f4_t*>(&keys[i][4 * lane]) =
+            v < 0 ? f4_t{0.0f, 0.0f, 0.0f, 0.0f} : load4<false>(a.keys, ((first + v) * a.key_heads + kh) * DK + 4 * lane);
+    }
+    __syncthreads();
 #pragma unroll
-      for (int c = 0; c < COLS; ++c)
-        u[c] = w * a.updates[((first + v) * a.heads + h) * a.dv + row0 + 16 * c + j];
+    for (int i = 0; i < kTile; ++i) {
+      if (t0 + i >= n) break;
 #pragma unroll
       for (int t = 0; t < DK / 16; ++t) {
         const f4_t k = *reinterpret_cast<const f4_t*>(&keys[i][16 * t + 4 * g]);
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) x.s[c][t] += u[c] * k;
+        for (int c = 0; c < COLS; ++c) x.s[c][t] += u[i][c] * k;
       }
     }
   }
@@ -289,7 +295,10 @@ void step(const DeltaArgs& a, hipStream_t stream) {
 
 template <int DK>
 void commit(const DeltaCommitArgs& a, hipStream_t stream) {
-  delta_commit_kernel<DK, 1><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+  // two columns a lane halve the LDS reads of a key; they need 128 columns
+  if (a.dv >= 128 && DK <= 128)
+    delta_commit_kernel<DK, 2><<<dim3(a.layers * (a.dv / 128), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+  else delta_commit_kernel<DK, 1><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
 }
 
 }  // namespace

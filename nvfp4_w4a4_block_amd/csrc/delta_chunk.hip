@@ -14,12 +14,12 @@ namespace {
 
 constexpr int kTiles = kChunk / 16;
 
-// Blocks c0 .. c1 - 1 of every sequence; what is prepared of them, and the states
-// between two such rounds.
+// Blocks c0 .. c1 - 1 of the sequences from b0 on; what is prepared of them, and the
+// states between two such rounds.
 struct Round {
-  int c0, c1, last;
-  h8_t *keys, *heads;  // [seqs][c1 - c0][key_heads or heads][units]
-  float* carry;        // [seqs][heads][dv][dk]
+  int b0, c0, c1, last;
+  h8_t *keys, *heads;  // [sequence - b0][c1 - c0][key_heads or heads][units]
+  float* carry;        // [sequence - b0][heads][dv][dk]
 };
 
 // grid (heads, c1 - c0, seqs).
@@ -27,14 +27,14 @@ template <int DK, bool BF16>
 __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
   __shared__ BlockShared<DK, BF16, kTiles, false> sh;
-  const int h = blockIdx.x, b = blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
+  const int h = blockIdx.x, b = r.b0 + blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
   const int kh = h / group;
   BlockRows<DK, BF16> rows;
   load_block_rows<DK, BF16, kTiles, false>(a, (int64_t)b * a.nodes + t0, a.nodes - t0, h, kh, rows);
   const int count = delta_used(a.src[b], a.slots) ? delta_count(a.counts, a.nodes, b) : 0;
   if (t0 >= count) return;
   const int n = count - t0 < kChunk ? count - t0 : kChunk;
-  const int64_t block = (int64_t)b * (r.c1 - r.c0) + blockIdx.y;
+  const int64_t block = (int64_t)blockIdx.z * (r.c1 - r.c0) + blockIdx.y;
   h8_t* key_to = h % group == 0 ? r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits : nullptr;
   prepare_block<DK, BF16, kTiles, false, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
   __shared__ Handed<DK, BF16> handed[SLABS];
-  const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int h = blockIdx.x, b = r.b0 + blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slab = wave % SLABS;
   const int col0 = (blockIdx.y * SLABS + slab) * 16, kh = h / (a.heads / a.key_heads);
   const bool states = wave < SLABS;
@@ -111,10 +111,10 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   const int count = delta_count(a.counts, a.nodes, b);
   const int end_block = (count + kChunk - 1) / kChunk < r.c1 ? (count + kChunk - 1) / kChunk : r.c1;
   const auto keys_of = [&](int c) {
-    return r.keys + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.key_heads + kh) * Ops::kKeyUnits;
+    return r.keys + (((int64_t)blockIdx.z * (r.c1 - r.c0) + c - r.c0) * a.key_heads + kh) * Ops::kKeyUnits;
   };
   const auto heads_of = [&](int c) {
-    return r.heads + (((int64_t)b * (r.c1 - r.c0) + c - r.c0) * a.heads + h) * Ops::kHeadUnits;
+    return r.heads + (((int64_t)blockIdx.z * (r.c1 - r.c0) + c - r.c0) * a.heads + h) * Ops::kHeadUnits;
   };
   const auto buffer_of = [&](int c) { return ops[BUFFERS == 2 ? (c - r.c0) & 1 : 0]; };
   const auto key_ops = [&](int c) { return (BUFFERS ? buffer_of(c) : keys_of(c)) + lane; };
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   Handed<DK, BF16>& hand = handed[slab];
   if (states) {
-    float* carry = r.carry + ((int64_t)b * a.heads + h) * state_size + (int64_t)col0 * DK;
+    float* carry = r.carry + ((int64_t)blockIdx.z * a.heads + h) * state_size + (int64_t)col0 * DK;
     StateTile<DK, 1> st;
     if (r.c0 > 0) load_state<DK, 1>(carry, st);
     else if (src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + (int64_t)col0 * DK, st);
@@ -407,12 +407,11 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
 }
 
-// Bytes of a block of every sequence, and blocks of a round: what is prepared of them
-// stays within 128 MB, half the Infinity Cache.
+// Bytes of a block of one sequence.
 template <int DK, bool BF16>
 int64_t block_bytes(const DeltaArgs& a) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  return (int64_t)a.seqs * 16 * ((int64_t)a.key_heads * Ops::kKeyUnits + (int64_t)a.heads * Ops::kHeadUnits);
+  return 16 * ((int64_t)a.key_heads * Ops::kKeyUnits + (int64_t)a.heads * Ops::kHeadUnits);
 }
 
 int64_t block_bytes(const DeltaArgs& a) {
@@ -421,50 +420,80 @@ int64_t block_bytes(const DeltaArgs& a) {
   return a.bf16 ? block_bytes<256, true>(a) : block_bytes<256, false>(a);
 }
 
+// What a round takes on: so many sequences, so many of their blocks, that what is
+// prepared stays within 128 MB, half the Infinity Cache.
 constexpr int64_t kRoundBytes = (int64_t)128 << 20;
 
-int round_blocks(const DeltaArgs& a) {
-  const int all = (a.nodes + kChunk - 1) / kChunk;
-  const int64_t fit = kRoundBytes / block_bytes(a);
-  return fit < 1 ? 1 : fit < all ? (int)fit : all;
+struct Rounds {
+  int seqs, blocks, all;
+};
+
+Rounds rounds_of(const DeltaArgs& a) {
+  const auto within = [](int64_t n, int64_t most) { return (int)(n < 1 ? 1 : n < most ? n : most); };
+  Rounds r;
+  r.all = (a.nodes + kChunk - 1) / kChunk;
+  const int64_t bytes = block_bytes(a);
+  r.seqs = within(kRoundBytes / bytes, a.seqs);
+  r.blocks = within(kRoundBytes / (bytes * r.seqs), r.all);
+  return r;
 }
 
-int64_t carry_bytes(const DeltaArgs& a) {
-  const int all = (a.nodes + kChunk - 1) / kChunk;
-  return round_blocks(a) < all ? (int64_t)a.seqs * a.heads * a.dv * a.dk * 4 : 0;
+int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) {
+  return r.blocks < r.all ? (int64_t)r.seqs * a.heads * a.dv * a.dk * 4 : 0;
 }
 
 constexpr int kLds = 160 * 1024;
 
-template <int DK, bool BF16>
-void scan(const DeltaArgs& a, const Round& r, hipStream_t stream) {
+template <int DK, bool BF16, int SLABS>
+constexpr int scan_lds(int buffers) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  constexpr int slabs = 2, bytes = 16 * (Ops::kQuery + Ops::kP), hand = slabs * (int)sizeof(Handed<DK, BF16>);
-  constexpr int buffers = 2 * bytes + hand <= kLds ? 2 : bytes + hand <= kLds ? 1 : 0;
-  delta_scan_kernel<DK, BF16, slabs, buffers><<<dim3(a.heads, a.dv / (16 * slabs), a.seqs), 64 * (2 * slabs + 1), 0,
-                                                    stream>>>(a, r);
+  return buffers * 16 * (Ops::kQuery + Ops::kP) + SLABS * (int)sizeof(Handed<DK, BF16>);
+}
+
+template <int DK, bool BF16, int SLABS, int BUFFERS>
+void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
+  const dim3 grid(a.heads, a.dv / (16 * SLABS), seqs);
+  delta_scan_kernel<DK, BF16, SLABS, BUFFERS><<<grid, 64 * (2 * SLABS + 1), 0, stream>>>(a, r);
+}
+
+// A CU holds one workgroup.  32 columns a workgroup spread a few heads over the most
+// CUs; where that gives more workgroups than there are CUs, 64 columns share a block's
+// operands (both measured: in DESIGN's words, see the times at the kernel).
+template <int DK, bool BF16>
+void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
+  if constexpr (scan_lds<DK, BF16, 4>(2) <= kLds)
+    if ((int64_t)seqs * a.heads * (a.dv / 32) > 256) {
+      scan<DK, BF16, 4, 2>(a, r, seqs, stream);
+      return;
+    }
+  scan<DK, BF16, 2, scan_lds<DK, BF16, 2>(2) <= kLds ? 2 : scan_lds<DK, BF16, 2>(1) <= kLds ? 1 : 0>(a, r, seqs, stream);
 }
 
 template <int DK, bool BF16>
 void run(const DeltaArgs& a, hipStream_t stream) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  const int all = (a.nodes + kChunk - 1) / kChunk, step = round_blocks(a);
+  const Rounds n = rounds_of(a);
   Round r = {};
   r.carry = static_cast<float*>(a.workspace);
-  r.keys = reinterpret_cast<h8_t*>(static_cast<char*>(a.workspace) + carry_bytes(a));
-  r.heads = r.keys + (int64_t)a.seqs * step * a.key_heads * Ops::kKeyUnits;
-  for (int c = 0; c < all; c += step) {
-    r.c0 = c;
-    r.c1 = c + step < all ? c + step : all;
-    r.last = r.c1 == all;
-    delta_prepare_kernel<DK, BF16><<<dim3(a.heads, r.c1 - r.c0, a.seqs), 64 * kTiles, 0, stream>>>(a, r);
-    scan<DK, BF16>(a, r, stream);
+  r.keys = reinterpret_cast<h8_t*>(static_cast<char*>(a.workspace) + carry_bytes(a, n));
+  r.heads = r.keys + (int64_t)n.seqs * n.blocks * a.key_heads * Ops::kKeyUnits;
+  for (r.b0 = 0; r.b0 < a.seqs; r.b0 += n.seqs) {
+    const int seqs = a.seqs - r.b0 < n.seqs ? a.seqs - r.b0 : n.seqs;
+    for (r.c0 = 0; r.c0 < n.all; r.c0 = r.c1) {
+      r.c1 = r.c0 + n.blocks < n.all ? r.c0 + n.blocks : n.all;
+      r.last = r.c1 == n.all;
+      delta_prepare_kernel<DK, BF16><<<dim3(a.heads, r.c1 - r.c0, seqs), 64 * kTiles, 0, stream>>>(a, r);
+      scan<DK, BF16>(a, r, seqs, stream);
+    }
   }
 }
 
 }  // namespace
 
-int64_t delta_chunk_workspace_bytes(const DeltaArgs& a) { return carry_bytes(a) + round_blocks(a) * block_bytes(a); }
+int64_t delta_chunk_workspace_bytes(const DeltaArgs& a) {
+  const Rounds r = rounds_of(a);
+  return carry_bytes(a, r) + r.seqs * r.blocks * block_bytes(a);
+}
 
 void launch_delta_chunks(const DeltaArgs& a, hipStream_t stream) {
   if (a.dk == 64) a.bf16 ? run<64, true>(a, stream) : run<64, false>(a, stream);

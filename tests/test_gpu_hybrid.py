@@ -164,6 +164,26 @@ def test_ragged_chains_new_and_unused(dtype, M):
         assert np.array_equal(after[s], c.states[s]), s
 
 
+@pytest.mark.parametrize("nb,M,dtype", [(900, 130, FP), (1900, 70, FP), (1200, 200, BF)])
+def test_calls_that_take_several_rounds(nb, M, dtype):
+    """What is prepared of a block of so many sequences is past a round's workspace: states are carried from one
+    round to the next, and the sequences themselves taken in turns."""
+    counts = np.full(nb, M)
+    counts[::7] = 65
+    c = Delta(dtype, nb, M, 1, 1, 64, 64, slots=nb, src=np.arange(nb), dst=np.arange(nb), seed=21)
+    c.counts = counts
+    need = B.load().nvfp4_delta_rule_workspace_bytes(nb, M, 1, 1, 64, 64, B.NVFP4_F32 if dtype == FP else B.NVFP4_BF16)
+    assert 64 << 20 < need < 256 << 20
+    out, states = c.chain()
+    some = np.random.default_rng(0).permutation(nb)[:24]
+    some = np.concatenate([some, [0, 7, nb - 1]])
+    for name in ("qf", "kf", "vf", "g", "beta", "states"):
+        setattr(c, name, getattr(c, name)[some])
+    c.counts, c.src, c.dst, n = counts[some], np.arange(len(some)), np.arange(len(some)), len(some)
+    c.dims = (n,) + c.dims[1:]
+    c.check_chain(out[torch.from_numpy(some).to(DEV)], states[torch.from_numpy(some).to(DEV)])
+
+
 @pytest.mark.parametrize("M", [1, 20, 100])
 def test_slots_that_two_sequences_name(M):
     # 0 and 1: the first goes into 5, the second nowhere; 2's dst is 3's src; 4 and 5 share a src, 4 stays in place
