@@ -79,22 +79,26 @@ template <int DK, bool BF16>
 struct Handed {
   h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
   h8_t w[BF16 ? 1 : 2][2][64];        // u
-  Rows16<BF16> v, o;                  // the other way: the block's values; and outputs on their way to memory
   int es[64], er[64];                 // their exponents
+  Rows16<BF16> v;                     // the other way: the block's values
 };
 
 // grid (heads, dv / (16 SLABS), seqs).  SLABS waves have 16 columns of the state each:
 // r, u and the new state, one block after the other.  SLABS more make the outputs of
 // the same columns, of which no state waits, and one fetches the next block's operands
-// and values, so that none of the others stands in the queue to memory.  BUFFERS: blocks whose K, K^T, T and factors are in LDS; 2:
-// those of the next block come while one is worked on; 0: they are read where they
-// are.
-template <int DK, bool BF16, int SLABS, int BUFFERS>
+// and values, so that none of the others stands in the queue to memory.  BUFFERS:
+// blocks whose K, K^T, T and factors are in LDS; 2: those of the next block come while
+// one is worked on; 0: they are read where they are.  HANDS: blocks that are handed
+// over at a time; 2: outputs are a block behind the states, and all waves meet once a
+// block; 1: they meet when S is ready, and when u is.
+template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
 __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
   constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
-  __shared__ Handed<DK, BF16> handed[SLABS];
+  static_assert(HANDS == 1 || BUFFERS == 2, "outputs a block behind leave no barrier between blocks");
+  __shared__ Handed<DK, BF16> handed[HANDS][SLABS];
+  __shared__ Rows16<BF16> outs[SLABS];  // on their way to memory
   const int h = blockIdx.x, b = r.b0 + blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slab = wave % SLABS;
   const int col0 = (blockIdx.y * SLABS + slab) * 16, kh = h / (a.heads / a.key_heads);
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   const auto key_ops = [&](int c) { return (BUFFERS ? buffer_of(c) : keys_of(c)) + lane; };
   const auto head_ops = [&](int c) { return BUFFERS ? buffer_of(c) + Ops::kQuery : heads_of(c); };
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  Handed<DK, BF16>& hand = handed[slab];
+  const auto hand_of = [&](int c) { return handed[HANDS == 2 ? (c - r.c0) & 1 : 0]; };
   if (states) {
     float* carry = r.carry + ((int64_t)blockIdx.z * a.heads + h) * state_size + (int64_t)col0 * DK;
     StateTile<DK, 1> st;
@@ -139,7 +143,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
     }
     for (int c = r.c0; c < end_block; ++c) {
-      lds_barrier();  // the block's operands are here
+      lds_barrier();  // the block's operands and values are here
+      Handed<DK, BF16>& hand = hand_of(c)[slab];
       const h8_t* key = key_ops(c);
       const h8_t* head = head_ops(c) + lane;
       const float* factors = reinterpret_cast<const float*>(head - lane + Ops::kFactors);
@@ -165,7 +170,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
           }
       }
       hand.es[lane] = es;
-      lds_barrier();  // S is handed over
+      if constexpr (HANDS == 1) lds_barrier();  // S is handed over
       // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
       f4_t v[kTiles];
       float m = 0.0f;
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         }
       }
       hand.er[lane] = er;
-      lds_barrier();  // u is handed over
+      if constexpr (HANDS == 1) lds_barrier();  // u is handed over
       // X = diag(e^(G_end - G)) u, and S <- e^G_end S + K^T X
       const float end = factors[4 * kChunk];
       float mx = 0.0f, ms = 0.0f;
@@ -246,6 +251,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
       if constexpr (BUFFERS == 1) lds_barrier();  // the operands have been read
     }
+    if (HANDS == 2 && r.c0 < end_block) lds_barrier();  // for the last outputs
 #pragma unroll
     for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
     if (!r.last) {
@@ -258,12 +264,11 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   }
   constexpr int size = BF16 ? 2 : 4;
   if (wave == 2 * SLABS) {
-    const h8_t* heads = nullptr;
     const auto fetch_part = [&](int c, int part) {
       if constexpr (BUFFERS > 0) {
         constexpr int loads = (Ops::kQuery + Ops::kP) / 64, third = (loads + 2) / 3;
         const h8_t* keys = keys_of(c) + lane;
-        heads = heads_of(c) + lane - Ops::kQuery;
+        const h8_t* heads = heads_of(c) + lane - Ops::kQuery;
         h8_t* to = buffer_of(c);
 #pragma unroll 4
         for (int i = part * third; i < (part + 1) * third; ++i)
@@ -280,16 +285,16 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
                                                            (blockIdx.y * SLABS + u) * 16) * size,
                           a.v_stride * size, count - c * kChunk, v[u]);
     };
-    const auto hand_next = [&]() {
+    const auto hand_next = [&](int c) {
 #pragma unroll
       for (int u = 0; u < SLABS; ++u)
 #pragma unroll
-        for (int i = 0; i < Rows16<BF16>::kLoads; ++i) *reinterpret_cast<u4_t*>(handed[u].v.piece(i)) = v[u][i];
+        for (int i = 0; i < Rows16<BF16>::kLoads; ++i) *reinterpret_cast<u4_t*>(hand_of(c)[u].v.piece(i)) = v[u][i];
     };
     if (r.c0 < end_block) {
       load_next(r.c0);
       for (int part = 0; part < 3; ++part) fetch_part(r.c0, part);
-      hand_next();
+      hand_next(r.c0);
     }
     for (int c = r.c0; c < end_block; ++c) {
       const bool more = c + 1 < end_block, ahead = BUFFERS == 2 && more;
@@ -297,10 +302,10 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       lds_barrier();
       if (more) load_next(c + 1);
       if (ahead) fetch_part(c + 1, 0);
-      lds_barrier();  // S is handed over
+      if constexpr (HANDS == 1) lds_barrier();  // S is handed over
       if (ahead) fetch_part(c + 1, 1);
-      lds_barrier();  // u is handed over, the values have been read
-      if (more) hand_next();
+      if constexpr (HANDS == 1) lds_barrier();  // u is handed over, the values have been read
+      if (more) hand_next(c + 1);
       if (ahead) fetch_part(c + 1, 2);
       if constexpr (BUFFERS == 1) {
         lds_barrier();
@@ -308,6 +313,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
           for (int part = 0; part < 3; ++part) fetch_part(c + 1, part);
       }
     }
+    if (HANDS == 2 && r.c0 < end_block) lds_barrier();
     return;
   }
   // Q and P are this wave's alone: straight to registers, Q where it fits
@@ -337,7 +343,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
 #pragma unroll
     for (int u = 0; u < Rows16<BF16>::kLoads; ++u) {
       const int i = 64 * u + lane, row = i / Rows16<BF16>::kPieces;
-      const u4_t x = *reinterpret_cast<const u4_t*>(hand.o.piece(u));
+      const u4_t x = *reinterpret_cast<const u4_t*>(outs[slab].piece(u));
       if (row < n) *reinterpret_cast<u4_t*>(rows + row * out_row + i % Rows16<BF16>::kPieces * 16) = x;
     }
   };
@@ -345,11 +351,26 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     load_q(r.c0);
     load_p(r.c0);
   }
+  constexpr int lag = HANDS - 1;
+  const auto factor = [&](int c, int which, int t) {
+    const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
+    return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
+  };
+  f4_t fq[kTiles], fp[kTiles];  // a block that is behind takes them before the next one's come
+  const auto load_factors = [&](int c) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) fq[t] = factor(c, kFactorQ, t), fp[t] = factor(c, kFactorP, t);
+  };
+  if (r.c0 < end_block && lag) {
+    lds_barrier();
+    load_factors(r.c0);
+  }
   for (int c = r.c0; c < end_block; ++c) {
+    const bool more = c + 1 < end_block;
     lds_barrier();
     if (c > r.c0) store_out(c - 1);
-    const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
-    lds_barrier();  // S is handed over
+    const Handed<DK, BF16>& hand = hand_of(c)[slab];
+    if constexpr (!lag) lds_barrier();  // S is handed over
     f4_t y[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) y[t] = zero;
@@ -369,8 +390,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
     }
     const int es = hand.es[lane];
-    if (c + 1 < end_block) load_q(c + 1);
-    lds_barrier();  // u is handed over
+    if (more) load_q(c + 1);
+    if constexpr (!lag) lds_barrier();  // u is handed over
     const int er = hand.er[lane];
     f4_t z[kTiles];
 #pragma unroll
@@ -388,17 +409,17 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         }
       }
     }
-    if (c + 1 < end_block) load_p(c + 1);
+    if (more) load_p(c + 1);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const f4_t fq = *reinterpret_cast<const f4_t*>(factors + kFactorQ * kChunk + 16 * t + 4 * g);
-      const f4_t fp = *reinterpret_cast<const f4_t*>(factors + kFactorP * kChunk + 16 * t + 4 * g);
+      if constexpr (!lag) fq[t] = factor(c, kFactorQ, t), fp[t] = factor(c, kFactorP, t);
       const f4_t qs = scale4(y[t], -es), pu = scale4(z[t], -er);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        store1<BF16>(hand.o.value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[e], qs[e], fp[e] * pu[e]));
+        store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[t][e], qs[e], fp[t][e] * pu[e]));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (lag && more) load_factors(c + 1);
     if constexpr (BUFFERS == 1) lds_barrier();
   }
   if (r.c0 < end_block) store_out(end_block - 1);
@@ -444,29 +465,40 @@ int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) {
 
 constexpr int kLds = 160 * 1024;
 
-template <int DK, bool BF16, int SLABS>
+template <int DK, bool BF16, int SLABS, int HANDS>
 constexpr int scan_lds(int buffers) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  return buffers * 16 * (Ops::kQuery + Ops::kP) + SLABS * (int)sizeof(Handed<DK, BF16>);
+  return buffers * 16 * (Ops::kQuery + Ops::kP) +
+         SLABS * (HANDS * (int)sizeof(Handed<DK, BF16>) + (int)sizeof(Rows16<BF16>));
 }
 
-template <int DK, bool BF16, int SLABS, int BUFFERS>
+template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
   const dim3 grid(a.heads, a.dv / (16 * SLABS), seqs);
-  delta_scan_kernel<DK, BF16, SLABS, BUFFERS><<<grid, 64 * (2 * SLABS + 1), 0, stream>>>(a, r);
+  delta_scan_kernel<DK, BF16, SLABS, BUFFERS, HANDS><<<grid, 64 * (2 * SLABS + 1), 0, stream>>>(a, r);
 }
 
 // A CU holds one workgroup.  32 columns a workgroup spread a few heads over the most
 // CUs; where that gives more workgroups than there are CUs, 64 columns share a block's
-// operands (both measured: in DESIGN's words, see the times at the kernel).
+// operands, if LDS has room (4 sequences of 2,047 tokens, 48 heads of 128, bf16: 375 us
+// by 32 columns, 335 by 64).  Outputs are a block behind in long rounds, if LDS has room
+// (8,192 tokens of 48 heads, bf16: 435 -> 400 us; 3 of 4,099 of 8 heads of 64, fp32: 187
+// -> 157): they cost a block's outputs more at the end (2,048 tokens 104 -> 105 us, 512
+// tokens 37.7 -> 39.3).
 template <int DK, bool BF16>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
-  if constexpr (scan_lds<DK, BF16, 4>(2) <= kLds)
+  if constexpr (scan_lds<DK, BF16, 4, 1>(2) <= kLds)
     if ((int64_t)seqs * a.heads * (a.dv / 32) > 256) {
-      scan<DK, BF16, 4, 2>(a, r, seqs, stream);
+      scan<DK, BF16, 4, 2, 1>(a, r, seqs, stream);
       return;
     }
-  scan<DK, BF16, 2, scan_lds<DK, BF16, 2>(2) <= kLds ? 2 : scan_lds<DK, BF16, 2>(1) <= kLds ? 1 : 0>(a, r, seqs, stream);
+  if constexpr (scan_lds<DK, BF16, 2, 2>(2) <= kLds)
+    if (r.c1 - r.c0 > 32) {
+      scan<DK, BF16, 2, 2, 2>(a, r, seqs, stream);
+      return;
+    }
+  constexpr int buffers = scan_lds<DK, BF16, 2, 1>(2) <= kLds ? 2 : scan_lds<DK, BF16, 2, 1>(1) <= kLds ? 1 : 0;
+  scan<DK, BF16, 2, buffers, 1>(a, r, seqs, stream);
 }
 
 template <int DK, bool BF16>

@@ -148,6 +148,18 @@ def test_long_chains(dtype, M, shape):
     c.check_chain(*c.chain())
 
 
+@pytest.mark.parametrize("M,shape,dtype", [(2300, (1, 1, 128, 64), BF), (2200, (1, 2, 64, 64), BF),
+                                           (2113, (1, 1, 64, 128), FP), (2500, (1, 1, 128, 64), FP)])
+def test_chains_of_more_than_32_blocks(M, shape, dtype):
+    """Sequences that end in the first block, between and at the end, new ones and ones without tokens."""
+    counts = [M, 2112, 63, 0, 2049, 1]
+    c = Delta(dtype, 6, M, *shape, counts=counts, slots=13, src=[0, -1, 2, 3, 4, 5], dst=[6, 7, 8, 9, 4, 11], seed=M,
+              decay=5.0)
+    out, states = c.chain()
+    c.check_chain(out, states)
+    assert not out[2, 63:].any() and not out[3].any() and not out[5, 1:].any()
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("M", [3, 12, 70, 200])
 def test_ragged_chains_new_and_unused(dtype, M):
