@@ -29,35 +29,31 @@ __device__ __forceinline__ void stage_row(const void* rows, int64_t at, float ep
   if (lane < DK / 4) *reinterpret_cast<f4_t*>(to + 4 * lane) = x * scale;
 }
 
-template <int DK, int COLS>
-__device__ __forceinline__ void dots(const StateTile<DK, COLS>& x, const float* row, float (&sum)[COLS]) {
+// Each of a wave's 16 rows of the state with one row of q or k.
+template <int DK>
+__device__ __forceinline__ float dot(const StateTile<DK, 1>& x, const float* row) {
   const int g = (threadIdx.x & 63) >> 4;
-  f4_t acc[COLS];
+  f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int c = 0; c < COLS; ++c) acc[c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int t = 0; t < DK / 16; ++t) {
-    const f4_t r = *reinterpret_cast<const f4_t*>(row + 16 * t + 4 * g);
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) acc[c] += x.s[c][t] * r;
-  }
-#pragma unroll
-  for (int c = 0; c < COLS; ++c) sum[c] = sum_of_groups((acc[c][0] + acc[c][1]) + (acc[c][2] + acc[c][3]));
+  for (int t = 0; t < DK / 16; ++t) acc += x.s[0][t] * *reinterpret_cast<const f4_t*>(row + 16 * t + 4 * g);
+  return sum_of_groups((acc[0] + acc[1]) + (acc[2] + acc[3]));
 }
 
-// A chain, one token after the other.  grid (dv / (64 COLS), heads, seqs).
-template <int DK, int COLS, bool BF16>
+// A chain, one token after the other.  Bound by reading and writing the states once:
+// one token of 64 sequences, 48 heads of 128 x 128, 82 us, 4.9 TB/s of the 403 MB; of
+// one sequence 5.9 us, of which its 6.3 MB are 1.3.  grid (dv / 64, heads, seqs).
+template <int DK, bool BF16>
 __global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
   __shared__ float rows[2][kTile][DK];  // k, q
   const int b = blockIdx.z, h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15;
-  const int kh = h / (a.heads / a.key_heads), row0 = (blockIdx.x * kWaves + wave) * 16 * COLS;
+  const int kh = h / (a.heads / a.key_heads), row0 = (blockIdx.x * kWaves + wave) * 16;
   const int src = a.src[b];
   const bool used = delta_used(src, a.slots);
   const int count = used ? delta_count(a.counts, a.nodes, b) : 0;
   const int64_t state_size = (int64_t)a.dv * DK;
-  StateTile<DK, COLS> x;
-  if (used && src >= 0) load_state<DK, COLS>(a.states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
-  else zero_state<DK, COLS>(x);
+  StateTile<DK, 1> x;
+  if (used && src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
+  else zero_state<DK, 1>(x);
   const int64_t first = (int64_t)b * a.nodes;
   for (int t0 = 0; t0 < count; t0 += kTile) {
     const int n = count - t0 < kTile ? count - t0 : kTile;
@@ -71,45 +67,29 @@ __global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
     for (int t = 0; t < n; ++t) {
       const int64_t r = first + t0 + t;
       const float decay = expf(a.g[r * a.heads + h]), beta = a.beta[r * a.heads + h];
-      float v[COLS], sk[COLS], o[COLS];
+      float v;
+      const int64_t at = r * a.v_stride + h * a.dv + row0 + j;
+      if constexpr (BF16) v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
+      else v = static_cast<const float*>(a.v)[at];
 #pragma unroll
-      for (int c = 0; c < COLS; ++c) {
-        const int64_t at = r * a.v_stride + h * a.dv + row0 + 16 * c + j;
-        if constexpr (BF16) v[c] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
-        else v[c] = static_cast<const float*>(a.v)[at];
-      }
+      for (int e = 0; e < DK / 16; ++e) x.s[0][e] *= decay;
+      const float u = beta * (v - dot<DK>(x, rows[0][t]));
 #pragma unroll
-      for (int c = 0; c < COLS; ++c)
-#pragma unroll
-        for (int e = 0; e < DK / 16; ++e) x.s[c][e] *= decay;
-      dots<DK, COLS>(x, rows[0][t], sk);
-#pragma unroll
-      for (int c = 0; c < COLS; ++c) sk[c] = beta * (v[c] - sk[c]);
-#pragma unroll
-      for (int e = 0; e < DK / 16; ++e) {
-        const f4_t k = *reinterpret_cast<const f4_t*>(&rows[0][t][16 * e + 4 * (lane >> 4)]);
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) x.s[c][e] += sk[c] * k;
-      }
-      dots<DK, COLS>(x, rows[1][t], o);
-      if (lane < 16)
-#pragma unroll
-        for (int c = 0; c < COLS; ++c)
-          store1<BF16>(a.out, (r * a.heads + h) * a.dv + row0 + 16 * c + j, o[c]);
+      for (int e = 0; e < DK / 16; ++e)
+        x.s[0][e] += u * *reinterpret_cast<const f4_t*>(&rows[0][t][16 * e + 4 * (lane >> 4)]);
+      const float o = dot<DK>(x, rows[1][t]);
+      if (lane < 16) store1<BF16>(a.out, (r * a.heads + h) * a.dv + row0 + j, o);
     }
   }
   for (int t = count; t < a.nodes; ++t)
-    if (lane < 16)
-#pragma unroll
-      for (int c = 0; c < COLS; ++c)
-        store1<BF16>(a.out, ((first + t) * a.heads + h) * a.dv + row0 + 16 * c + j, 0.0f);
+    if (lane < 16) store1<BF16>(a.out, ((first + t) * a.heads + h) * a.dv + row0 + j, 0.0f);
   if (!used) return;
   const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
-  if (to >= 0) store_state<DK, COLS>(a.states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
+  if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
 }
 
-// Drafted trees of more than 48 fp32 nodes with keys of 256, node after node (the others are
-// delta_single.hip's).  With the sums G of the decays along each node's line,
+// Drafted trees of more than 48 fp32 nodes with keys of 256, whose block does not fit
+// LDS, node after node (the others are delta_single.hip's).  With the sums G of the decays along each node's line,
 //   u_v = beta_v (v_v - e^G_v S k_v - sum_a e^(G_v - G_a) (k_a . k_v) u_a),
 //   o_v = scale (e^G_v S q_v + sum_a e^(G_v - G_a) (k_a . q_v) u_a),
 // a the ancestors of v (and v itself in o).  grid (dv / 64, heads, seqs).
@@ -170,9 +150,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
       }
     }
     __syncthreads();
-    float sk[1], sq[1];
-    dots<DK, 1>(x, rows[0], sk);
-    dots<DK, 1>(x, rows[1], sq);
+    const float sk = dot<DK>(x, rows[0]), sq = dot<DK>(x, rows[1]);
     double all = 0.0;
     for (int i = 0; i <= v; ++i)
       if ((line >> i) & 1) all += (double)a.g[(first + i) * a.heads + h];
@@ -181,7 +159,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
     float value;
     if constexpr (BF16) value = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
     else value = static_cast<const float*>(a.v)[at];
-    float w = value - into * sk[0], o = into * sq[0];
+    float w = value - into * sk, o = into * sq;
     for (int n = 0; n < v; ++n)
       if ((line >> n) & 1) {
         w -= near[0][n] * u[n][col];
@@ -210,24 +188,28 @@ __global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
 
 // The accepted path of a tree into one state: e^G_end S + sum_i e^(G_end - G_i)
 // u_i k_i^T over the root and the path, the sums of the decays behind each node in
-// 64 bits.  A wave holds COLS * 16 rows of the state and takes the keys from LDS.
-// grid (layers * dv / (64 COLS), heads, seqs).
-template <int DK, int COLS>
+// 64 bits.  A wave holds 16 rows of the state and takes the keys from LDS.  Bound by
+// reading and writing the states once: 48 layers of one sequence, 48 heads of 128 x
+// 128, a path of four: 62 us, 4.9 TB/s of the 302 MB; 5 layers of 24 sequences, 8 heads
+// of 64 x 128, where a tile's latencies count as much: 18.8.  32 rows a wave halve the
+// LDS reads of a key, but also the waves: 64.9 and 18.0.
+// grid (layers * dv / 64, heads, seqs).
+template <int DK>
 __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitArgs a) {
   __shared__ float keys[kTile][DK];
-  const int b = blockIdx.z, h = blockIdx.y, parts = a.dv / (64 * COLS), layer = blockIdx.x / parts;
+  const int b = blockIdx.z, h = blockIdx.y, parts = a.dv / 64, layer = blockIdx.x / parts;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int src = a.src[b];
   if (!delta_used(src, a.slots)) return;
   const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
   if (to < 0) return;
   const int kh = h / (a.heads / a.key_heads);
-  const int row0 = ((blockIdx.x - layer * parts) * kWaves + wave) * 16 * COLS;
+  const int row0 = ((blockIdx.x - layer * parts) * kWaves + wave) * 16;
   const int64_t state_size = (int64_t)a.dv * DK;
   float* states = a.states + (int64_t)layer * a.slots * a.heads * state_size;
-  StateTile<DK, COLS> x;
-  if (src >= 0) load_state<DK, COLS>(states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
-  else zero_state<DK, COLS>(x);
+  StateTile<DK, 1> x;
+  if (src >= 0) load_state<DK, 1>(states + ((int64_t)src * a.heads + h) * state_size + row0 * DK, x);
+  else zero_state<DK, 1>(x);
   // lane i: node i of the path (the root first), its decay and what follows it
   const int32_t* res = a.result + (int64_t)b * (3 + a.nodes);
   int n = res[1] + 1;
@@ -248,23 +230,18 @@ __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitAr
     after = lane < 63 ? o : 0.0;
     const float f = expf((float)all);
 #pragma unroll
-    for (int c = 0; c < COLS; ++c)
-#pragma unroll
-      for (int t = 0; t < DK / 16; ++t) x.s[c][t] *= f;
+    for (int t = 0; t < DK / 16; ++t) x.s[0][t] *= f;
   }
   const float weight = node >= 0 ? expf((float)after) : 0.0f;
   for (int t0 = 0; t0 < n; t0 += kTile) {
     // a tile's u at once, one latency for all; a place without a node adds 0 times 0
-    float u[kTile][COLS];
+    float u[kTile];
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       const int v = __builtin_amdgcn_readlane(node, t0 + i);
       const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), t0 + i));
-#pragma unroll
-      for (int c = 0; c < COLS; ++c) {
-        const float y = a.updates[((first + (v < 0 ? 0 : v)) * a.heads + h) * a.dv + row0 + 16 * c + j];
-        u[i][c] = v < 0 ? 0.0f : w * y;
-      }
+      const float y = a.updates[((first + (v < 0 ? 0 : v)) * a.heads + h) * a.dv + row0 + j];
+      u[i] = v < 0 ? 0.0f : w * y;
     }
     __syncthreads();
     for (int i = wave; i < kTile; i += kWaves) {
@@ -278,32 +255,28 @@ __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitAr
     for (int i = 0; i < kTile; ++i) {
       if (t0 + i >= n) break;
 #pragma unroll
-      for (int t = 0; t < DK / 16; ++t) {
-        const f4_t k = *reinterpret_cast<const f4_t*>(&keys[i][16 * t + 4 * g]);
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) x.s[c][t] += u[i][c] * k;
-      }
+      for (int t = 0; t < DK / 16; ++t) x.s[0][t] += u[i] * *reinterpret_cast<const f4_t*>(&keys[i][16 * t + 4 * g]);
     }
   }
-  store_state<DK, COLS>(states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
+  store_state<DK, 1>(states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
 }
 
 template <int DK, bool BF16>
 void step(const DeltaArgs& a, hipStream_t stream) {
-  delta_step_kernel<DK, 1, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+  delta_step_kernel<DK, BF16><<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
 }
 
 template <int DK>
 void commit(const DeltaCommitArgs& a, hipStream_t stream) {
-  // two columns a lane halve the LDS reads of a key; they need 128 columns
-  if (a.dv >= 128 && DK <= 128)
-    delta_commit_kernel<DK, 2><<<dim3(a.layers * (a.dv / 128), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
-  else delta_commit_kernel<DK, 1><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+  delta_commit_kernel<DK><<<dim3(a.layers * (a.dv / 64), a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
 }
 
 }  // namespace
 
-// Up to four tokens go one after the other, up to 64 as one block, more block by block.
+// Up to four tokens go one after the other, up to 64 as one block, more block by
+// block.  Steps and one block, us, 16 key and 48 value heads of 128, bf16: 4 tokens of
+// one sequence 8.5 and 9.0, of 8 sequences 16.9 and 16.5, of 64 99.5 and 97; 16 tokens
+// of one sequence 19.9 and 9.1, of 64 208 and 103.
 constexpr int kFewTokens = 4;
 
 int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {

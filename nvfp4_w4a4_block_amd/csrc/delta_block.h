@@ -319,8 +319,9 @@ __device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t firs
 // Prepares the n tokens of a block of value head h, n <= 16 NT, from its rows,
 // by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
 // head's part (NULL: not wanted), head_to: the value head's.  LOCAL: the workgroup
-// goes on with the block itself, K and Q stay in sh.  Trees: factor X is u's power of two alone, and `keys` (or NULL) the keys'
-// rows as used, `key_row` values apart, for all `nodes` of them.
+// goes on with the block itself, K and Q stay in sh.  Trees: factor X is u's power of
+// two alone, and `keys` (or NULL) the keys' rows as used, `key_row` values apart, for
+// all `nodes` of them.
 template <int DK, bool BF16, int NT, bool TREE, bool LOCAL>
 __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
                                               BlockShared<DK, BF16, NT, LOCAL>& sh, h8_t* key_to, h8_t* head_to,

@@ -6,7 +6,16 @@
 //
 // delta_block.h has the mathematics.  delta_prepare_kernel makes the blocks' T, P and
 // operands, all blocks at once; delta_scan_kernel walks each sequence, a wave with
-// its 16 columns of the state in registers, without any exchange between waves.
+// its 16 columns of the state in registers, which nothing else waits for.
+//
+// Bounds.  The walk is a chain of dependent products: a block's K S, T r and K^T X
+// take a wave about 1,100, 1,450 and 1,650 cycles, of which its matrix instructions
+// are half and the rest is LDS and the rounding of results into operands.  512 tokens
+// of one sequence, 16 key and 48 value heads of 128, bf16: 14.4 us of preparation and
+// 22.6 of walking (memory's share is 5, the products' 1); 3 sequences of up to 4,099
+// tokens, 4 and 8 heads of 64, fp32: 19 and 129.  A second walk over pieces of a
+// sequence at once, joined after, needs a piece's effect on a state, dk x dk: as many
+// products again as there are columns.
 #include "delta_block.h"
 
 namespace nvfp4 {

@@ -10,6 +10,10 @@
 // A workgroup has 64 columns of one head's state, a wave 16 of them; its first waves
 // prepare the block (the other workgroups of the head do the same), while all of them
 // wait for their columns.
+//
+// Bounds.  Latency: one load, the block's inverse and the products behind it.  A tree
+// of 16 nodes, 16 key and 48 value heads of 128, bf16: 7.4 us on the device, of which
+// its 4.5 MB are 0.9; 16 trees of up to 33 fp32 nodes, 4 and 8 heads of 64: 10.5.
 #include "delta_block.h"
 
 namespace nvfp4 {

@@ -26,6 +26,11 @@
 // sorted.  So the loop over the logits does nothing for `top` but the maxima, where
 // lists of first keys that are kept up batch by batch cost 26 us of 58 (512 rows of
 // 151,936, five alternatives) and 9 of 21 (16 rows, twenty).
+//
+// Bounds.  512 bf16 rows of 151,936: 40.4 us, 3.9 TB/s of 156 MB (32.5 us, 4.8 TB/s,
+// without alternatives, whose blocks are found and sorted behind the last logit).  16
+// fp32 rows, twenty alternatives: 7 us for the parts and 9 for the rows, of which the
+// 9.7 MB are 2: what is left is latency, of the launches, loads and sorts.
 #include <type_traits>
 
 #include "device_common.h"
