@@ -536,9 +536,9 @@ nvfp4_status nvfp4_kv_fork(int64_t n, int64_t S, int64_t W, int64_t P, int64_t p
  *            takes it.  Node v stands at position lens[b] plus the number of its
  *            ancestors (NULL: lens[b] + v), and is written at token lens[b] + v.
  * Pair (x, y) at position p becomes rope_scale * (x cos w - y sin w, y cos w +
- * x sin w), w = p * inv_freq[j]; the angle is reduced in 64 bits, sine and
- * cosine are fp32.  A query is rounded to dt; a key goes from fp32 to the
- * cache's bytes (nvfp4_kv_fp8_encode of the rotated fp32 values).  Query rows
+ * x sin w), w = p * inv_freq[j], all in 64 bits.  A query is rounded to fp32 and
+ * from that to dt; a rotated key times 1 / k_scale (fp32) is rounded once, to the
+ * cache's bytes, and other values go there as nvfp4_kv_append's do.  Query rows
  * of an unused sequence and behind counts[b] are zero.  The other arguments,
  * limits and the rule of shared pages are nvfp4_kv_append's.
  * Cites: the pages "Using tree-based multi-token prediction to accelerate LLM
@@ -579,14 +579,14 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
  *            turn's snapshot, to begin others from.
  *   counts   int32 [B], device, or NULL: only a sequence's first counts[b] rows
  *            are tokens (more than M counts as M; none: the state is copied).
- *   out      [B][M][H][Dv] in dt, not overlapping q, k or v.  Rows that are no
+ *   out      [B][M][H][Dv] in dt, no part of q, k, v or states.  Rows that are no
  *            tokens are zero, and what they hold in q, k, v, g and beta is not
  *            read.
  *   Shapes: Dk and Dv 64, 128 or 256; 1 <= H <= 1024, H a multiple of Hk; B and M
  *   at most 65535, B * M <= 2^24; 1 <= S < 2^31.
  * States, sums, decays and norms are fp32 (the decays' sums within a block of
- * tokens 64 bits).  Chains of some length go through the matrix cores block by
- * block; there every factor of a state is split into f16 parts that keep 22 bits
+ * tokens 64 bits).  Trees, and chains of more than four tokens, go through the
+ * matrix cores, 64 tokens at a time; there every factor of a state is split into f16 parts that keep 22 bits
  * of it relative to its row's or column's largest value, and in bf16 calls the
  * factors that reach nothing but out are rounded to f16 (11 bits).  A NaN or an
  * infinity in a sequence's rows or state may reach all of that sequence's rows
@@ -618,7 +618,7 @@ nvfp4_status nvfp4_delta_rule(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
  *   keys     out fp32 [B][M][Hk][Dk]: the nodes' keys as used (normalised).
  *   updates  out fp32 [B][M][H][Dv]: their u.
  * Both are what nvfp4_delta_commit needs of the step, zero in rows that are no
- * tokens. */
+ * tokens, and no part of the other arrays or of each other. */
 nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, int64_t S,
                               const void* q, const void* k, const void* v, nvfp4_dtype dt, int64_t q_stride,
                               int64_t k_stride, int64_t v_stride, const float* g, const float* beta, float scale,

@@ -59,6 +59,15 @@ nvfp4::DeltaArgs delta_of(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t D
   return a;
 }
 
+// Whether an output's bytes are some of q's, k's, v's or the states': several
+// workgroups read a row or state that one of them would write.
+bool shared(const nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* out, int64_t bytes) {
+  const int64_t n = (int64_t)a.seqs * a.nodes, key_row = (int64_t)a.key_heads * a.dk, row = (int64_t)a.heads * a.dv;
+  return overlap(a.q, n, key_row, a.q_stride, dt, out, bytes) || overlap(a.k, n, key_row, a.k_stride, dt, out, bytes) ||
+         overlap(a.v, n, row, a.v_stride, dt, out, bytes) ||
+         overlap(a.states, a.slots, row * a.dk, row * a.dk, NVFP4_F32, out, bytes);
+}
+
 // The rows that a chain and a tree have in common; M == 0 needs none of them.
 nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, const void* k, const void* v,
                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* g, const float* beta,
@@ -69,13 +78,6 @@ nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, cons
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(states, 16) ||
       !aligned(g, 4) || !aligned(beta, 4) || !aligned(src, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;
-  if (rows) {  // several workgroups read a row that one of them writes
-    const int64_t n = (int64_t)a.seqs * a.nodes, bytes = n * a.heads * a.dv * size_of(dt);
-    const int64_t key_row = (int64_t)a.key_heads * a.dk;
-    if (overlap(q, n, key_row, q_stride, dt, out, bytes) || overlap(k, n, key_row, k_stride, dt, out, bytes) ||
-        overlap(v, n, (int64_t)a.heads * a.dv, v_stride, dt, out, bytes))
-      return NVFP4_ERR_SHAPE;
-  }
   a.q = q;
   a.k = k;
   a.v = v;
@@ -90,6 +92,7 @@ nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, cons
   a.src = src;
   a.counts = counts;
   a.out = out;
+  if (rows && shared(a, dt, out, (int64_t)a.seqs * a.nodes * a.heads * a.dv * size_of(dt))) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
@@ -210,6 +213,11 @@ nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
                                      src, counts, out);
   if (st != NVFP4_OK) return st;
   if (!aligned(parent, 4) || !aligned(keys, 16) || !aligned(updates, 16)) return NVFP4_ERR_ALIGN;
+  const int64_t n = B * M, key_bytes = n * Hk * Dk * 4, update_bytes = n * H * Dv * 4;
+  if (shared(a, dt, keys, key_bytes) || shared(a, dt, updates, update_bytes) ||
+      overlap(out, n, H * Dv, H * Dv, dt, keys, key_bytes) || overlap(out, n, H * Dv, H * Dv, dt, updates, update_bytes) ||
+      overlap(keys, n, Hk * Dk, Hk * Dk, NVFP4_F32, updates, update_bytes))
+    return NVFP4_ERR_SHAPE;
   a.parent = parent;
   a.keys = keys;
   a.updates = updates;

@@ -51,6 +51,21 @@ def test_tree_refuses_shapes(lib, bad):
     assert lib.nvfp4_delta_tree(*changed(TREE, **bad)) == B.NVFP4_ERR_SHAPE
 
 
+@pytest.mark.parametrize("bad", [dict(states=16 * A + 4000), dict(states=16 * A - 4 * 5 * 4 * 64 * 128 + 16)])
+def test_rule_refuses_outputs_in_the_states(lib, bad):
+    assert lib.nvfp4_delta_rule(*changed(RULE, **bad)) == B.NVFP4_ERR_SHAPE
+    assert lib.nvfp4_delta_tree(*changed(TREE, **bad)) == B.NVFP4_ERR_SHAPE
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "states", "out", "updates"])
+def test_tree_refuses_outputs_that_share_bytes(lib, name):
+    apart = changed(TREE, q=A, k=2 * A, v=3 * A, states=8 * A, out=4 * A, keys=5 * A, updates=6 * A)
+    apart = dict(zip(TREE, apart))
+    assert lib.nvfp4_delta_tree(*changed(apart, keys=apart[name] + 16)) == B.NVFP4_ERR_SHAPE
+    other = "keys" if name == "updates" else name
+    assert lib.nvfp4_delta_tree(*changed(apart, updates=apart[other] + 16)) == B.NVFP4_ERR_SHAPE
+
+
 @pytest.mark.parametrize("bad", SHAPES + [dict(M=0), dict(M=65), dict(L=-1), dict(L=4097)])
 def test_commit_refuses_shapes(lib, bad):
     assert lib.nvfp4_delta_commit(*changed(COMMIT, **bad)) == B.NVFP4_ERR_SHAPE
