@@ -553,6 +553,51 @@ def test_rope_without_turning_is_append():
     assert np.array_equal(pages[0].cpu().numpy(), KC.append(c.kf, KS, c.start[0], c.table, c.lens))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_turned_codes_are_the_nearest(dtype, interleaved):
+    """A turned key times fl32(1 / scale) is rounded once.  Up to position 60,500 the angle is off by no more than
+    2^-52 * 60,500 + 2e-11, so a value within 4e-11 of its pair's size from the middle of two codes may go to either."""
+    c = Rope(dtype, [60000], 500, 1, 4, 128, 128, 64, interleaved=interleaved, scale=1.25, seed=9)
+    q, pages = c.gpu()
+    ref, size = RP.rotate(c.kf[0].astype(np.float64), 60000 + np.arange(500), c.inv, c.scale, interleaved)
+    y, near = ref * float(np.float32(1) / KS), 4e-11 * size * float(np.float32(1) / KS)
+    grid = KV.decode_f32(np.arange(127, dtype=np.uint8), np.float32(1.0)).astype(np.float64)
+    grid = np.concatenate([-grid[:0:-1], grid])
+    mid = (grid[1:] + grid[:-1]) / 2
+    low, high = (grid[np.searchsorted(mid, y + s * near)] for s in (-1, 1))
+    k = pages[0].cpu().numpy()
+    for t in range(500):
+        page, at = KC._slot(k, c.table, 0, 60000 + t)
+        got = KV.decode_f32(k[page, :, at], np.float32(1.0)).astype(np.float64)
+        assert ((got == low[t]) | (got == high[t])).all(), t
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_keeps_nan_and_saturates_infinities(dtype, interleaved):
+    c = Rope(dtype, [5, 20], 4, 2, 2, 64, 32, 16, interleaved=interleaved, seed=10)
+    for x in (c.q, c.k):
+        x[0, 1, 0, 3], x[0, 2, 1, 40], x[1, 0, 1, 2], x[1, 3, 0, 50] = (float("nan"), float("nan"), float("inf"),
+                                                                       -float("inf"))
+    q, pages = c.gpu()
+    other = (lambda d: d ^ 1) if interleaved else (lambda d: d ^ 16)
+    bad = np.zeros((2, 4, 2, 64), dtype=bool)
+    bad[0, 1, 0, [3, other(3)]] = bad[0, 2, 1, 40] = True
+    got = q.float().cpu().numpy()
+    assert np.array_equal(np.isnan(got), bad)
+    big = np.zeros_like(bad)
+    big[1, 0, 1, [2, other(2)]] = big[1, 3, 0, 50] = True
+    assert np.array_equal(np.isinf(got), big)
+    k = pages[0].cpu().numpy()
+    for b in range(2):
+        for t in range(4):
+            page, at = KC._slot(k, c.table, b, int(c.lens[b]) + t)
+            code = k[page, :, at] & 127
+            assert np.array_equal(code == 127, bad[b, t])
+            assert (code[big[b, t]] == 126).all()
+
+
 # ----------------------------------------------------------------------------------------------- log probabilities
 
 
