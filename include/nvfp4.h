@@ -586,11 +586,13 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
  *   at most 65535, B * M <= 2^24; 1 <= S < 2^31.
  * States, sums, decays and norms are fp32 (the decays' sums within a block of
  * tokens 64 bits).  Trees, and chains of more than four tokens, go through the
- * matrix cores, 64 tokens at a time; there every factor of a state is split into f16 parts that keep 22 bits
- * of it relative to its row's or column's largest value, and in bf16 calls the
- * factors that reach nothing but out are rounded to f16 (11 bits).  A NaN or an
- * infinity in a sequence's rows or state may reach all of that sequence's rows
- * and its new state, and nothing of another sequence.
+ * matrix cores, 64 tokens at a time.  What a token adds keeps its own size beside other
+ * tokens' (16 bits of it in what reaches out alone, in bf16 calls of more than 64
+ * tokens).  In products over a row's Dk values, and where a token's change is added to a
+ * state, factors are split into f16 parts that keep 22 bits relative to their row's or
+ * column's largest value; in bf16 calls those that reach nothing but out are rounded to
+ * f16 (11 bits).  A NaN or an infinity in a sequence's rows or state may reach all of
+ * that sequence's rows and its new state, and nothing of another sequence.
  * Cites: the page section "Reusing KV cache across agent turns" (the model is a
  * hybrid; its recurrent states are kept and restored with the cached pages). */
 

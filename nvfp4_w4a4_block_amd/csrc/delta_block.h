@@ -13,17 +13,25 @@
 // Operands.  A 16x16x32 f16 product wants 8 values of its inner dimension a lane.
 // With the inner order 32 s + 4 g .. + 3, 32 s + 16 + 4 g .. + 3 for lane group g, a
 // result (rows 4 g .. 4 g + 3 of a tile, one column a lane) is an operand as it
-// stands.  So S, r and u stay in the registers of the wave whose columns they are,
-// and everything prepared is stored in operand order: one 16-byte load a lane.
+// stands; so it is of four 16x16x4 fp32 products, one for each of its values.  So S, r
+// and u stay in the registers of the wave whose columns they are, and everything
+// prepared is stored in operand order: one 16-byte load a lane.
 //
-// Accuracy.  Every factor on the way to a state keeps 22 bits: two f16 parts (rounded
-// to nearest, the second the rest of the first), of which the product of the two
-// second ones is left out, 2^-22.  A bf16 row of k is exact in one part.  f16's range
-// is 2^40: rows of k, q, T and P are scaled by a power of two to a largest value of 1
-// to 2, columns of r by one to 8 to 16, and a column of S, with what is added to it, by
-// one to 32 to 64, so that 64 products fit (values 2^-30 below a row's or column's
-// largest lose bits: as fp32 sums would). In bf16 calls what reaches out alone (S
-// and Q in Q S, P and u in P u) is rounded to f16, an eighth of out's own step.
+// Accuracy.  T r and P u add up tokens, between which a decay may stand: a value of
+// any size counts as e^(G_i - G_j) leaves it, or not at all beside another branch of a
+// tree.  Their factors keep fp32's range: fp32 products in the one-block kernel, bf16
+// parts in a scan, three each (24 bits, six products; P and u of bf16 calls two, 16
+// bits, three).  A scan waits for T r: 40 fp32 products of 32 cycles there take 27.4 us
+// for 512 tokens, 36 bf16 ones of 16 cycles 24.5.
+// K S and Q S add up a row's values, K^T X what is in a state at one time: there every
+// factor on the way to a state keeps 22 bits of its row's or column's largest value, in
+// two f16 parts (rounded to nearest, the second the rest of the first), of which the
+// product of the two second ones is left out, 2^-22.  A bf16 row of k is exact in one
+// part.  f16's least step is 2^-24: rows of k and q are scaled by a power of two to a
+// largest value of 1 to 2, and a column of S, with what is added to it, by one to 32
+// to 64, so that 64 products fit; values are off by 2^-25 of the one, by 2^-30 of the
+// other, at least.  In bf16 calls S and Q in Q S, which reaches out alone, are rounded to
+// f16, an eighth of out's own step.
 #pragma once
 
 #include "delta_common.h"
@@ -67,6 +75,26 @@ __device__ __forceinline__ f4_t rest_of(f4_t x, h4_t hi) {
 }
 __device__ __forceinline__ h8_t join8(h4_t a, h4_t b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
+// Two result tiles as the operand of a product over their rows, in N bf16 parts: each
+// the nearest to what the ones before it leave.
+typedef __bf16 b4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
+
+template <int N>
+__device__ __forceinline__ void wide_parts(f4_t a, f4_t b, b8_t (&part)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const b4_t p = __builtin_convertvector(a, b4_t), q = __builtin_convertvector(b, b4_t);
+    part[i] = __builtin_shufflevector(p, q, 0, 1, 2, 3, 4, 5, 6, 7);
+    a -= __builtin_convertvector(p, f4_t);
+    b -= __builtin_convertvector(q, f4_t);
+  }
+}
+
+__device__ __forceinline__ f4_t mfma16x16x32(b8_t a, b8_t b, f4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 // Two result tiles as the operand of a product over their rows.
 __device__ __forceinline__ h8_t operand_hi(f4_t a, f4_t b) { return join8(to_half(a), to_half(b)); }
 
@@ -77,40 +105,46 @@ __device__ __forceinline__ void operand_parts(f4_t a, f4_t b, h8_t& hi, h8_t& lo
 }
 
 // What is prepared of a block, in units of an operand of one lane (16 bytes).  PARTS:
-// f16 parts of rows of k and q, and of P.
+// f16 parts of rows of k and q.
 template <int DK, bool BF16, int NT>
 struct BlockOps {
   static constexpr int kParts = BF16 ? 1 : 2;
-  static constexpr int kSteps = DK / 32;                 // inner steps over dk
-  static constexpr int kTokenSteps = (NT + 1) / 2;       // over tokens
-  static constexpr int kLower = NT == 1 ? 1 : NT == 2 ? 2 : NT == 3 ? 4 : 6;  // of lower triangular rows
-  static constexpr int kRows = NT * kSteps * 64;         // K or Q, one part
+  static constexpr int kSteps = DK / 32;            // inner steps over dk
+  static constexpr int kTokenSteps = (NT + 1) / 2;  // over tokens
+  static constexpr int kTiles = NT * (NT + 1) / 2;  // of a lower triangle
+  static constexpr int kLower = kTokenSteps * (kTokenSteps + 1) - (NT & 1 ? kTokenSteps : 0);  // steps of its rows
+  static constexpr int kRows = NT * kSteps * 64;            // K or Q, one part
   static constexpr int kCols = DK / 16 * kTokenSteps * 64;  // K transposed, one part
   // of a key head: K and its transpose, what a scan's states need, before Q
   static constexpr int kKey = 0, kKeyT = kParts * kRows, kQuery = kKeyT + kParts * kCols;
   static constexpr int kKeyUnits = kQuery + kParts * kRows;
-  // of a value head: T, the factors [4][16 NT] with e^G_end behind them, before P
-  static constexpr int kT = 0, kFactors = 2 * kLower * 64;
-  static constexpr int kP = (kFactors + 4 * 4 * NT + 1 + 63) / 64 * 64;
-  static constexpr int kHeadUnits = kP + kParts * kLower * 64;
+  // of a value head: the factors [3][16 NT] with e^G_end behind them, T in three bf16
+  // parts and P in two (bf16 calls) or three
+  static constexpr int kPartsOfP = BF16 ? 2 : 3;
+  static constexpr int kFactors = 0, kT = (3 * 4 * NT + 1 + 63) / 64 * 64;
+  static constexpr int kP = kT + 3 * kLower * 64;
+  static constexpr int kHeadUnits = kP + kPartsOfP * kLower * 64;
   // steps of the rows of tile rt begin at this one
   static __device__ constexpr int lower(int rt) { return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? 2 : 4; }
 };
 
+__device__ constexpr int tile_at(int row, int column) { return row * (row + 1) / 2 + column; }
+
 // Factors of a block's rows.
-enum { kFactorR, kFactorX, kFactorQ, kFactorP };
+enum { kFactorR, kFactorX, kFactorQ };
+
+constexpr int kPitch = 20;  // of a tile's rows in LDS: rows 0 .. 7 begin in banks of their own
 
 template <int DK, bool BF16, int NT, bool LOCAL>
 struct BlockShared {
-  static constexpr int kPitch = 16 * NT + 4;
   h8_t key[BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows];
-  float a[16 * NT][kPitch];  // A, then T
-  float p[16 * NT][kPitch];  // P
-  double decay[64];          // G in exponents of 2
-  uint64_t line[64];         // trees: ancestors and self
+  float a[BlockOps<DK, BF16, NT>::kTiles][16 * kPitch];  // A, then (I + A)^-1
+  float p[BlockOps<DK, BF16, NT>::kTiles][16 * kPitch];  // P
+  double decay[64];                                      // G in exponents of 2
+  uint64_t line[64];                                     // trees: ancestors and self
   h8_t query[LOCAL ? BlockOps<DK, BF16, NT>::kParts * BlockOps<DK, BF16, NT>::kRows : 1];
   float beta[64], key_factor[64], query_factor[64];
-  int t_exponent[64];
+  float factor[3][16 * NT], end;  // e^G_end
 };
 
 // A row of k or q as it comes: lane j + 16 g has its share of row j of a tile.
@@ -208,35 +242,94 @@ __device__ __forceinline__ f4_t rows_product(const h8_t (&a)[PARTS][STEPS], cons
   return acc;
 }
 
-// c + a b of 16x16 blocks in fp32, a in LDS with `pitch`, b as a result stands.
-__device__ __forceinline__ f4_t block_product(const float* a, int pitch, f4_t b, f4_t c) {
-  const int lane = threadIdx.x & 63;
-  const f4_t x = *reinterpret_cast<const f4_t*>(a + (lane & 15) * pitch + 4 * (lane >> 4));
+// c + a b of 16x16 tiles in fp32, b as a result stands; a: row j's values 4 g .. + 3.
+__device__ __forceinline__ f4_t tile_product(f4_t a, f4_t b, f4_t c) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], b[i], c, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
   return c;
 }
 
-__device__ __forceinline__ f4_t load_block(const float* a, int pitch) {
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  return f4_t{a[(4 * g) * pitch + j], a[(4 * g + 1) * pitch + j], a[(4 * g + 2) * pitch + j], a[(4 * g + 3) * pitch + j]};
+__device__ __forceinline__ f4_t tile_rows(const float* a) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const f4_t*>(a + (lane & 15) * kPitch + 4 * (lane >> 4));
 }
 
-__device__ __forceinline__ void store_block(float* a, int pitch, f4_t x) {
+__device__ __forceinline__ f4_t load_tile(const float* a) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  return f4_t{a[(4 * g) * kPitch + j], a[(4 * g + 1) * kPitch + j], a[(4 * g + 2) * kPitch + j],
+              a[(4 * g + 3) * kPitch + j]};
+}
+
+__device__ __forceinline__ void store_tile(float* a, f4_t x) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[(4 * g + i) * pitch + j] = x[i];
+  for (int i = 0; i < 4; ++i) a[(4 * g + i) * kPitch + j] = x[i];
 }
 
-// (I + A)^-1 of a 16x16 block in place, by substitution, a column a lane: each value
+// The lower triangle `rows` of tiles, each as tile_rows has it, times x.  Products of
+// different rows of tiles stand side by side: one waits for none of its own.
+template <int NT, typename F>
+__device__ __forceinline__ void lower_product(F rows, const f4_t (&x)[NT], f4_t (&y)[NT]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) y[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    f4_t a[NT];
+#pragma unroll
+    for (int t = c; t < NT; ++t) a[t] = rows(tile_at(t, c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = c; t < NT; ++t) y[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[t][i], x[c][i], y[t], 0, 0, 0);
+  }
+}
+
+// The same of rows in N bf16 parts, part p of step l at rows(p, l): the products of
+// parts that reach N bits by eight.
+template <int NT, int N, typename F>
+__device__ __forceinline__ void wide_product(F rows, const f4_t (&x)[NT], f4_t (&y)[NT]) {
+  static_assert(NT % 2 == 0, "whole steps");
+  typedef BlockOps<64, true, NT> Ops;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) y[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < NT / 2; ++s) {
+    b8_t part[N];
+    wide_parts<N>(x[2 * s], x[2 * s + 1], part);
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        if (p + q >= N && !(N == 3 && p == 1 && q == 1)) continue;
+#pragma unroll
+        for (int t = 2 * s; t < NT; ++t) y[t] = mfma16x16x32(rows(p, Ops::lower(t) + s), part[q], y[t]);
+      }
+  }
+}
+
+// N bf16 parts of row j of a row of tiles, its own one the `last`: steps from 0 on.
+template <int N, typename F>
+__device__ __forceinline__ void store_wide(F values, int last, h8_t* to, int pitch) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (2 * s > last) continue;
+    b8_t part[N];
+    wide_parts<N>(values(2 * s), 2 * s < last ? values(2 * s + 1) : f4_t{0.0f, 0.0f, 0.0f, 0.0f}, part);
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i * pitch + s * 64 + lane] = __builtin_bit_cast(h8_t, part[i]);
+  }
+}
+
+// (I + A)^-1 of a 16x16 tile in place, by substitution, a column a lane: each value
 // found is taken off all rows below it, which do not wait for each other.
-__device__ __forceinline__ void invert_block(float* a, int pitch) {
+__device__ __forceinline__ void invert_tile(float* a) {
   const int j = threadIdx.x & 15;
   f4_t r[16][4];
 #pragma unroll
   for (int i = 1; i < 16; ++i)
 #pragma unroll
-    for (int m = 0; m < (i + 3) / 4; ++m) r[i][m] = *reinterpret_cast<const f4_t*>(a + i * pitch + 4 * m);
+    for (int m = 0; m < (i + 3) / 4; ++m) r[i][m] = *reinterpret_cast<const f4_t*>(a + i * kPitch + 4 * m);
   float x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.0f : 0.0f;
@@ -246,32 +339,7 @@ __device__ __forceinline__ void invert_block(float* a, int pitch) {
     for (int i = m + 1; i < 16; ++i) x[i] = __builtin_fmaf(-r[i][m >> 2][m & 3], x[m], x[i]);
   if ((threadIdx.x & 63) < 16)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a[i * pitch + j] = x[i];
-}
-
-// The largest magnitude of a row of operands to 1 .. 2; returns its exponent.
-template <int PARTS>
-__device__ __forceinline__ int store_rows(const f4_t (&x)[2][2], int steps, h8_t* to, int pitch) {
-  const int lane = threadIdx.x & 63;
-  float m = 0.0f;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (s < steps) m = max4(max4(m, x[s][0]), x[s][1]);
-  const int e = exponent_of(max_of_groups(m));
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s >= steps) continue;
-    const f4_t p = scale4(x[s][0], -e), q = scale4(x[s][1], -e);
-    if constexpr (PARTS == 1) {
-      to[s * 64 + lane] = operand_hi(p, q);
-    } else {
-      h8_t hi, lo;
-      operand_parts(p, q, hi, lo);
-      to[s * 64 + lane] = hi;
-      to[pitch + s * 64 + lane] = lo;
-    }
-  }
-  return e;
+    for (int i = 0; i < 16; ++i) a[i * kPitch + j] = x[i];
 }
 
 // An operand of K transposed from K's: lane j + 16 g has tokens 32 s + 4 g .., 32 s +
@@ -319,26 +387,27 @@ __device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t firs
 // Prepares the n tokens of a block of value head h, n <= 16 NT, from its rows,
 // by a workgroup of at least NT waves, the first NT of which work.  key_to: the key
 // head's part (NULL: not wanted), head_to: the value head's.  LOCAL: the workgroup
-// goes on with the block itself, K and Q stay in sh.  Trees: factor X is u's power of
-// two alone, and `keys` (or NULL) the keys' rows as used, `key_row` values apart, for
-// all `nodes` of them.
+// goes on with the block itself, after a barrier: K, Q, (I + A)^-1, P and the factors
+// stay in sh.  Trees: `keys` (or NULL) takes the keys' rows as used, `key_row` values
+// apart, for all `nodes` of them.
 template <int DK, bool BF16, int NT, bool TREE, bool LOCAL>
 __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
                                               BlockShared<DK, BF16, NT, LOCAL>& sh, h8_t* key_to, h8_t* head_to,
                                               float* keys = nullptr, int64_t key_row = 0, int nodes = 0) {
   typedef BlockOps<DK, BF16, NT> Ops;
-  constexpr int P = Ops::kParts, pitch = BlockShared<DK, BF16, NT, LOCAL>::kPitch;
+  constexpr int P = Ops::kParts;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const bool works = w < NT;
   const bool there = works && 16 * w + j < n;
   h8_t key[P][Ops::kSteps], query[P][Ops::kSteps];
+  float kf = 0.0f, qf = 0.0f;
   if (works) {
     float* as_used = TREE && keys && 16 * w + j < nodes ? keys + (16 * w + j) * key_row : nullptr;
-    const float kf = row_operand<DK, BF16>(rows.k, there, a.norm_eps, key, as_used);
-    const float qf = row_operand<DK, BF16>(rows.q, there, a.norm_eps, query);
+    kf = row_operand<DK, BF16>(rows.k, there, a.norm_eps, key, as_used);
+    qf = row_operand<DK, BF16>(rows.q, there, a.norm_eps, query) * a.scale;
     if (g == 0) {
       sh.key_factor[16 * w + j] = kf;
-      sh.query_factor[16 * w + j] = qf * a.scale;
+      sh.query_factor[16 * w + j] = qf;
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -399,13 +468,7 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-      if (c > w) {
-        if (c == w + 1 && (w & 1) == 0) {  // the other half of a step over tokens
-          store_block(&sh.a[16 * w][16 * c], pitch, f4_t{0.0f, 0.0f, 0.0f, 0.0f});
-          store_block(&sh.p[16 * w][16 * c], pitch, f4_t{0.0f, 0.0f, 0.0f, 0.0f});
-        }
-        continue;
-      }
+      if (c > w) continue;
       const h8_t* kc = sh.key + c * Ops::kSteps * 64;
       f4_t kk = rows_product<Ops::kSteps, P>(key, kc, Ops::kRows);
       f4_t qk = rows_product<Ops::kSteps, P>(query, kc, Ops::kRows);
@@ -420,20 +483,29 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
         kk[e] = seen && col < i ? bi[e] * ki[e] * d * kk[e] : 0.0f;
         qk[e] = seen ? qi[e] * d * qk[e] : 0.0f;
       }
-      store_block(&sh.a[16 * w][16 * c], pitch, kk);
-      store_block(&sh.p[16 * w][16 * c], pitch, qk);
+      store_tile(sh.a[tile_at(w, c)], kk);
+      store_tile(sh.p[tile_at(w, c)], qk);
+    }
+    if (g == 0) {
+      const int i = 16 * w + j;
+      const double at = sh.decay[i], end = sh.decay[16 * NT - 1];
+      const float into = __builtin_amdgcn_exp2f((float)at);
+      sh.factor[kFactorR][i] = -into * kf;
+      sh.factor[kFactorX][i] = kf * __builtin_amdgcn_exp2f((float)(end - at));
+      sh.factor[kFactorQ][i] = into * qf;
+      if (i == 0) sh.end = __builtin_amdgcn_exp2f((float)end);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    invert_block(&sh.a[16 * w][16 * w], pitch);
+    invert_tile(sh.a[tile_at(w, w)]);
   }
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (NT >= 2) {
     __syncthreads();
     if (w < NT / 2) {  // -T_11 A_10 T_00 of each pair of tiles
-      float* at = &sh.a[32 * w + 16][32 * w];
-      const f4_t y = block_product(at, pitch, load_block(&sh.a[32 * w][32 * w], pitch), zero);
-      store_block(at, pitch, -block_product(at + 16, pitch, y, zero));
+      float* at = sh.a[tile_at(2 * w + 1, 2 * w)];
+      const f4_t y = tile_product(tile_rows(at), load_tile(sh.a[tile_at(2 * w, 2 * w)]), zero);
+      store_tile(at, -tile_product(tile_rows(sh.a[tile_at(2 * w + 1, 2 * w + 1)]), y, zero));
     }
   }
   if constexpr (NT >= 3) {
@@ -442,66 +514,31 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
     const int c = w & 1, r = 2 + (w >> 1);
     f4_t z = zero;
     if (works && r < NT) {
-      const f4_t t0 = load_block(&sh.a[0][16 * c], pitch), t1 = load_block(&sh.a[16][16 * c], pitch);
+      const f4_t t1 = load_tile(sh.a[tile_at(1, c)]);
 #pragma unroll
       for (int m = 2; m < NT; ++m) {
         if (m > r) continue;
-        f4_t y = block_product(&sh.a[16 * m][16], pitch, t1, zero);
-        if (c == 0) y = block_product(&sh.a[16 * m][0], pitch, t0, y);
-        z = block_product(&sh.a[16 * r][16 * m], pitch, y, z);
+        f4_t y = tile_product(tile_rows(sh.a[tile_at(m, 1)]), t1, zero);
+        if (c == 0) y = tile_product(tile_rows(sh.a[tile_at(m, 0)]), load_tile(sh.a[tile_at(0, 0)]), y);
+        z = tile_product(tile_rows(sh.a[tile_at(r, m)]), y, z);
       }
     }
     __syncthreads();
-    if (works && r < NT) store_block(&sh.a[16 * r][16 * c], pitch, -z);
+    if (works && r < NT) store_tile(sh.a[tile_at(r, c)], -z);
   }
-  __syncthreads();
-  float* factors = reinterpret_cast<float*>(head_to + Ops::kFactors);
-  const int steps = w / 2 + 1;
-  if (works) {
-    f4_t x[2][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int col = 32 * s + 16 * half + 4 * g;
-        if (s >= steps || col >= 16 * NT) {
-          x[s][half] = zero;
-          continue;
-        }
-        x[s][half] = *reinterpret_cast<const f4_t*>(&sh.a[16 * w + j][col]) * *reinterpret_cast<const f4_t*>(&sh.beta[col]);
-      }
-    const int e = store_rows<2>(x, steps, head_to + Ops::kT + Ops::lower(w) * 64, Ops::kLower * 64);
-    if (g == 0) sh.t_exponent[16 * w + j] = e;
-  }
-  __syncthreads();
-  if (works) {
-    f4_t x[2][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int col = 32 * s + 16 * half + 4 * g;
-        if (s >= steps || col >= 16 * NT) {
-          x[s][half] = zero;
-          continue;
-        }
-        const f4_t y = *reinterpret_cast<const f4_t*>(&sh.p[16 * w + j][col]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[s][half][i] = __builtin_amdgcn_ldexpf(y[i], sh.t_exponent[col + i]);
-      }
-    const int e = store_rows<P>(x, steps, head_to + Ops::kP + Ops::lower(w) * 64, Ops::kLower * 64);
-    if (g == 0) {
-      const int i = 16 * w + j;
-      const double at = sh.decay[i], end = sh.decay[16 * NT - 1];
-      const float into = __builtin_amdgcn_exp2f((float)at), kf = sh.key_factor[i];
-      factors[kFactorR * 16 * NT + i] = -into * kf;
-      factors[kFactorX * 16 * NT + i] =
-          __builtin_amdgcn_ldexpf(TREE ? 1.0f : kf * __builtin_amdgcn_exp2f((float)(end - at)), sh.t_exponent[i]);
-      factors[kFactorQ * 16 * NT + i] = into * sh.query_factor[i];
-      factors[kFactorP * 16 * NT + i] = __builtin_amdgcn_ldexpf(1.0f, e);
-      if (i == 0) factors[4 * 16 * NT] = __builtin_amdgcn_exp2f((float)end);
-    }
-    if constexpr (!LOCAL)
+  if constexpr (!LOCAL) {
+    __syncthreads();
+    if (works) {
+      // T's columns have their rates
+      const auto t_rows = [&](int c) {
+        return tile_rows(sh.a[tile_at(w, c)]) * *reinterpret_cast<const f4_t*>(&sh.beta[16 * c + 4 * g]);
+      };
+      store_wide<3>(t_rows, w, head_to + Ops::kT + Ops::lower(w) * 64, Ops::kLower * 64);
+      store_wide<Ops::kPartsOfP>([&](int c) { return tile_rows(sh.p[tile_at(w, c)]); }, w,
+                                 head_to + Ops::kP + Ops::lower(w) * 64, Ops::kLower * 64);
+      float* factors = reinterpret_cast<float*>(head_to + Ops::kFactors);
+      if (g < 3) factors[g * 16 * NT + 16 * w + j] = sh.factor[g][16 * w + j];
+      if (w == 0 && lane == 0) factors[3 * 16 * NT] = sh.end;
       if (key_to)
 #pragma unroll 1
         for (int u = w; u < P * (DK / 16) * Ops::kTokenSteps; u += NT) {
@@ -509,6 +546,7 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
           key_to[Ops::kKeyT + part * Ops::kCols + v * 64 + lane] =
               transposed_operand<DK, BF16, NT>(sh.key, part, v / Ops::kTokenSteps, v % Ops::kTokenSteps);
         }
+    }
   }
 }
 

@@ -8,14 +8,11 @@
 // operands, all blocks at once; delta_scan_kernel walks each sequence, a wave with
 // its 16 columns of the state in registers, which nothing else waits for.
 //
-// Bounds.  The walk is a chain of dependent products: a block's K S, T r and K^T X
-// take a wave about 1,100, 1,450 and 1,650 cycles, of which its matrix instructions
-// are half and the rest is LDS and the rounding of results into operands.  512 tokens
-// of one sequence, 16 key and 48 value heads of 128, bf16: 14.4 us of preparation and
-// 22.6 of walking (memory's share is 5, the products' 1); 3 sequences of up to 4,099
-// tokens, 4 and 8 heads of 64, fp32: 19 and 129.  A second walk over pieces of a
-// sequence at once, joined after, needs a piece's effect on a state, dk x dk: as many
-// products again as there are columns.
+// Bounds.  The walk is a chain of dependent products: a block's K S, T r and K^T X,
+// half of whose time is the matrix instructions' and the rest LDS and the rounding of
+// results into operands.  512 tokens of one sequence, 16 key and 48 value heads of 128,
+// bf16: 14.5 us of preparation and 24.5 of walking (memory's share is 5, the products' 1);
+// 3 sequences of up to 4,099 tokens, 4 and 8 heads of 64, fp32: 20 and 118.
 #include "delta_block.h"
 
 namespace nvfp4 {
@@ -83,12 +80,22 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// T is in a state wave's registers where they have room: with 32 columns a workgroup, and
+// rows of k that take one part or are short; else it comes to LDS with the others.
+template <int DK, bool BF16, int SLABS, int BUFFERS>
+constexpr bool kHoldT = SLABS == 2 && (BF16 || DK == 64 || BUFFERS == 0);
+
+// Units of a block that come to LDS.
+template <int DK, bool BF16, bool HOLD>
+constexpr int kUnitsHere = BlockOps<DK, BF16, kTiles>::kQuery +
+                           (HOLD ? BlockOps<DK, BF16, kTiles>::kT : BlockOps<DK, BF16, kTiles>::kP);
+
 // What a state's wave leaves for the wave of its outputs.
 template <int DK, bool BF16>
 struct Handed {
   h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
-  h8_t w[BF16 ? 1 : 2][2][64];        // u
-  int es[64], er[64];                 // their exponents
+  f4_t w[kTiles][64];                 // u
+  int es[64];                         // S's exponent
   Rows16<BF16> v;                     // the other way: the block's values
 };
 
@@ -103,7 +110,8 @@ struct Handed {
 template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
 __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(DeltaArgs a, Round r) {
   typedef BlockOps<DK, BF16, kTiles> Ops;
-  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = Ops::kQuery + Ops::kP;
+  constexpr bool kHold = kHoldT<DK, BF16, SLABS, BUFFERS>;
+  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = kUnitsHere<DK, BF16, kHold>;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
   static_assert(HANDS == 1 || BUFFERS == 2, "outputs a block behind leave no barrier between blocks");
   __shared__ Handed<DK, BF16> handed[HANDS][SLABS];
@@ -151,6 +159,17 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
 #pragma unroll
       for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], es);
     }
+    h8_t own[kHold ? 3 : 1][kHold ? Ops::kLower : 1];
+    const auto load_own = [&](int c) {
+      if constexpr (kHold) {
+        const h8_t* from = heads_of(c) + Ops::kT + lane;
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int l = 0; l < Ops::kLower; ++l) own[p][l] = from[(p * Ops::kLower + l) * 64];
+      }
+    };
+    if (r.c0 < end_block) load_own(r.c0);
     for (int c = r.c0; c < end_block; ++c) {
       lds_barrier();  // the block's operands and values are here
       Handed<DK, BF16>& hand = hand_of(c)[slab];
@@ -180,9 +199,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
       hand.es[lane] = es;
       if constexpr (HANDS == 1) lds_barrier();  // S is handed over
-      // r, and u = T r: w is u times 2^er, but for the rows' powers that P and X have
-      f4_t v[kTiles];
-      float m = 0.0f;
+      // r, and u = T r
+      f4_t v[kTiles], w[kTiles];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
@@ -194,39 +212,19 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
-        m = max4(m, v[t]);
       }
-      const int er = 3 - exponent_of(max_of_groups(m));
-      f4_t w[kTiles];
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) w[t] = zero;
-#pragma unroll
-      for (int x = 0; x < Ops::kTokenSteps; ++x) {
-        h8_t hi, lo;
-        operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int t = 2 * x; t < kTiles; ++t) {
-            const int at = Ops::kT + (Ops::lower(t) + x) * 64;
-            w[t] = mfma16x16x32(head[part == 2 ? at + Ops::kLower * 64 : at], part == 1 ? lo : hi, w[t]);
-          }
+      if constexpr (kHold) {
+        wide_product<kTiles, 3>([&](int p, int l) { return __builtin_bit_cast(b8_t, own[p][l]); }, v, w);
+        if (c + 1 < end_block) load_own(c + 1);
+      } else {
+        wide_product<kTiles, 3>(
+            [&](int p, int l) { return __builtin_bit_cast(b8_t, head[Ops::kT + (p * Ops::kLower + l) * 64]); }, v, w);
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if constexpr (P == 1) {
-          hand.w[0][x][lane] = operand_hi(w[2 * x], w[2 * x + 1]);
-        } else {
-          h8_t hi, lo;
-          operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
-          hand.w[0][x][lane] = hi;
-          hand.w[1][x][lane] = lo;
-        }
-      }
-      hand.er[lane] = er;
+      for (int t = 0; t < kTiles; ++t) hand.w[t][lane] = w[t];
       if constexpr (HANDS == 1) lds_barrier();  // u is handed over
       // X = diag(e^(G_end - G)) u, and S <- e^G_end S + K^T X
-      const float end = factors[4 * kChunk];
+      const float end = factors[3 * kChunk];
       float mx = 0.0f, ms = 0.0f;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       for (int t = 0; t < KT; ++t) ms = max4(ms, s[t]);
       const int before = es;
       {
-        const float most = fmaxf(__builtin_amdgcn_ldexpf(mx, -er), __builtin_amdgcn_ldexpf(ms, -es) * end);
+        const float most = fmaxf(mx, __builtin_amdgcn_ldexpf(ms, -es) * end);
         es = 5 - exponent_of(max_of_groups(most));
       }
       // e^G_end times a power of two, one factor: it takes the largest of s, 2^-30 at least
@@ -249,7 +247,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
 #pragma unroll
       for (int x = 0; x < Ops::kTokenSteps; ++x) {
         h8_t hi, lo;
-        operand_parts(scale4(w[2 * x], es - er), scale4(w[2 * x + 1], es - er), hi, lo);
+        operand_parts(scale4(w[2 * x], es), scale4(w[2 * x + 1], es), hi, lo);
 #pragma unroll
         for (int part = 0; part < P + 1; ++part)
 #pragma unroll
@@ -275,7 +273,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   if (wave == 2 * SLABS) {
     const auto fetch_part = [&](int c, int part) {
       if constexpr (BUFFERS > 0) {
-        constexpr int loads = (Ops::kQuery + Ops::kP) / 64, third = (loads + 2) / 3;
+        constexpr int loads = kUnits / 64, third = (loads + 2) / 3;
         const h8_t* keys = keys_of(c) + lane;
         const h8_t* heads = heads_of(c) + lane - Ops::kQuery;
         h8_t* to = buffer_of(c);
@@ -325,9 +323,13 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     if (HANDS == 2 && r.c0 < end_block) lds_barrier();
     return;
   }
-  // Q and P are this wave's alone: straight to registers, Q where it fits
+  // Q and P are this wave's alone: straight to registers, Q where it fits.  Outputs that
+  // are not behind fetch one while they work on the other.
+  constexpr int lag = HANDS - 1;
   constexpr bool hold = P * Ops::kSteps <= 8;
-  h8_t q[P][kTiles][hold ? Ops::kSteps : 1], p[P][Ops::kLower];
+  h8_t q[P][kTiles][hold ? Ops::kSteps : 1];
+  constexpr int kOfP = (Ops::kHeadUnits - Ops::kP) / 64;
+  h8_t p[kOfP];
   const auto load_q = [&](int c) {
     if constexpr (!hold) return;
     const h8_t* from = keys_of(c) + Ops::kQuery + lane;
@@ -341,9 +343,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   const auto load_p = [&](int c) {
     const h8_t* from = heads_of(c) + Ops::kP + lane;
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int x = 0; x < Ops::kLower; ++x) p[i][x] = from[(i * Ops::kLower + x) * 64];
+    for (int i = 0; i < kOfP; ++i) p[i] = from[i * 64];
   };
   const auto store_out = [&](int c) {
     const int64_t out_row = (int64_t)a.heads * a.dv * size;
@@ -358,17 +358,16 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   };
   if (r.c0 < end_block) {
     load_q(r.c0);
-    load_p(r.c0);
+    if (lag) load_p(r.c0);
   }
-  constexpr int lag = HANDS - 1;
   const auto factor = [&](int c, int which, int t) {
     const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
     return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
   };
-  f4_t fq[kTiles], fp[kTiles];  // a block that is behind takes them before the next one's come
+  f4_t fq[kTiles];  // a block that is behind takes them before the next one's come
   const auto load_factors = [&](int c) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) fq[t] = factor(c, kFactorQ, t), fp[t] = factor(c, kFactorP, t);
+    for (int t = 0; t < kTiles; ++t) fq[t] = factor(c, kFactorQ, t);
   };
   if (r.c0 < end_block && lag) {
     lds_barrier();
@@ -399,33 +398,28 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
     }
     const int es = hand.es[lane];
-    if (more) load_q(c + 1);
-    if constexpr (!lag) lds_barrier();  // u is handed over
-    const int er = hand.er[lane];
-    f4_t z[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) z[t] = zero;
-#pragma unroll
-    for (int x = 0; x < Ops::kTokenSteps; ++x) {
-      const h8_t hi = hand.w[0][x][lane];
-#pragma unroll
-      for (int t = 2 * x; t < kTiles; ++t) {
-        const int at = Ops::lower(t) + x;
-        z[t] = mfma16x16x32(p[0][at], hi, z[t]);
-        if constexpr (P == 2) {
-          z[t] = mfma16x16x32(p[0][at], hand.w[1][x][lane], z[t]);
-          z[t] = mfma16x16x32(p[1][at], hi, z[t]);
-        }
-      }
+    if constexpr (lag) {
+      if (more) load_q(c + 1);
+    } else {
+      load_p(c);
+      lds_barrier();  // u is handed over
     }
-    if (more) load_p(c + 1);
+    f4_t u[kTiles], z[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) u[t] = hand.w[t][lane];
+    wide_product<kTiles, Ops::kPartsOfP>(
+        [&](int part, int l) { return __builtin_bit_cast(b8_t, p[part * Ops::kLower + l]); }, u, z);
+    if (more) {
+      if constexpr (lag) load_p(c + 1);
+      else load_q(c + 1);
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      if constexpr (!lag) fq[t] = factor(c, kFactorQ, t), fp[t] = factor(c, kFactorP, t);
-      const f4_t qs = scale4(y[t], -es), pu = scale4(z[t], -er);
+      if constexpr (!lag) fq[t] = factor(c, kFactorQ, t);
+      const f4_t qs = scale4(y[t], -es);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[t][e], qs[e], fp[t][e] * pu[e]));
+        store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[t][e], qs[e], z[t][e]));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (lag && more) load_factors(c + 1);
@@ -474,10 +468,9 @@ int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) {
 
 constexpr int kLds = 160 * 1024;
 
-template <int DK, bool BF16, int SLABS, int HANDS>
-constexpr int scan_lds(int buffers) {
-  typedef BlockOps<DK, BF16, kTiles> Ops;
-  return buffers * 16 * (Ops::kQuery + Ops::kP) +
+template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
+constexpr int scan_lds() {
+  return BUFFERS * 16 * kUnitsHere<DK, BF16, kHoldT<DK, BF16, SLABS, BUFFERS>> +
          SLABS * (HANDS * (int)sizeof(Handed<DK, BF16>) + (int)sizeof(Rows16<BF16>));
 }
 
@@ -496,17 +489,17 @@ void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
 // tokens 37.7 -> 39.3).
 template <int DK, bool BF16>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
-  if constexpr (scan_lds<DK, BF16, 4, 1>(2) <= kLds)
+  if constexpr (scan_lds<DK, BF16, 4, 2, 1>() <= kLds)
     if ((int64_t)seqs * a.heads * (a.dv / 32) > 256) {
       scan<DK, BF16, 4, 2, 1>(a, r, seqs, stream);
       return;
     }
-  if constexpr (scan_lds<DK, BF16, 2, 2>(2) <= kLds)
+  if constexpr (scan_lds<DK, BF16, 2, 2, 2>() <= kLds)
     if (r.c1 - r.c0 > 32) {
       scan<DK, BF16, 2, 2, 2>(a, r, seqs, stream);
       return;
     }
-  constexpr int buffers = scan_lds<DK, BF16, 2, 1>(2) <= kLds ? 2 : scan_lds<DK, BF16, 2, 1>(1) <= kLds ? 1 : 0;
+  constexpr int buffers = scan_lds<DK, BF16, 2, 2, 1>() <= kLds ? 2 : scan_lds<DK, BF16, 2, 1, 1>() <= kLds ? 1 : 0;
   scan<DK, BF16, 2, buffers, 1>(a, r, seqs, stream);
 }
 

@@ -25,7 +25,6 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
   typedef BlockOps<DK, BF16, NT> Ops;
   constexpr int P = Ops::kParts, KT = DK / 16;
   __shared__ BlockShared<DK, BF16, NT, true> sh;
-  __shared__ h8_t head[Ops::kHeadUnits];
   const int h = blockIdx.x, b = blockIdx.z, lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int group = a.heads / a.key_heads, kh = h / group, col0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 16;
   const int64_t first = (int64_t)b * a.nodes, value_at = (int64_t)h * a.dv + col0 + j, row = (int64_t)a.heads * a.dv;
@@ -49,7 +48,7 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
       else raw[t][e] = static_cast<const uint32_t*>(a.v)[at];
     }
   float* keys = TREE && h % group == 0 && blockIdx.y == 0 ? a.keys + (first * a.key_heads + kh) * DK : nullptr;
-  prepare_block<DK, BF16, NT, TREE, true>(a, rows, n, sh, nullptr, head, keys, (int64_t)a.key_heads * DK, a.nodes);
+  prepare_block<DK, BF16, NT, TREE, true>(a, rows, n, sh, nullptr, nullptr, keys, (int64_t)a.key_heads * DK, a.nodes);
   __syncthreads();
   float m = 0.0f;
 #pragma unroll
@@ -73,63 +72,29 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
         if (P == 2 || part == 0) qs[t] = mfma16x16x32(sh.query[at], part == 1 ? lo : hi, qs[t]);
       }
   }
-  const float* factors = reinterpret_cast<const float*>(head + Ops::kFactors);
-  const auto factor = [&](int which, int t) {
-    return *reinterpret_cast<const f4_t*>(factors + which * 16 * NT + 16 * t + 4 * g);
-  };
-  f4_t v[NT + (NT & 1)], w[NT + (NT & 1)], pu[NT];
-  m = 0.0f;
+  const auto factor = [&](const float* of, int t) { return *reinterpret_cast<const f4_t*>(of + 16 * t + 4 * g); };
+  f4_t v[NT], w[NT], pu[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const f4_t f = factor(kFactorR, t), y = scale4(ks[t], -es);
+    const f4_t f = factor(sh.factor[kFactorR], t), beta = factor(sh.beta, t), y = scale4(ks[t], -es);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float x = __uint_as_float(BF16 ? raw[t][e] << 16 : raw[t][e]);
-      v[t][e] = 16 * t + 4 * g + e < n ? __builtin_fmaf(f[e], y[e], x) : 0.0f;
+      v[t][e] = 16 * t + 4 * g + e < n ? beta[e] * __builtin_fmaf(f[e], y[e], x) : 0.0f;
     }
-    m = max4(m, v[t]);
-    w[t] = pu[t] = zero;
   }
-  if constexpr (NT & 1) v[NT] = w[NT] = zero;
-  const int er = 3 - exponent_of(max_of_groups(m));
-#pragma unroll
-  for (int x = 0; x < Ops::kTokenSteps; ++x) {
-    h8_t hi, lo;
-    operand_parts(scale4(v[2 * x], er), scale4(v[2 * x + 1], er), hi, lo);
-#pragma unroll
-    for (int part = 0; part < 3; ++part)
-#pragma unroll
-      for (int t = 2 * x; t < NT; ++t) {
-        const int at = Ops::kT + (Ops::lower(t) + x) * 64 + (part == 2 ? Ops::kLower * 64 : 0) + lane;
-        w[t] = mfma16x16x32(head[at], part == 1 ? lo : hi, w[t]);
-      }
-  }
-#pragma unroll
-  for (int x = 0; x < Ops::kTokenSteps; ++x) {
-    h8_t hi, lo;
-    if constexpr (P == 1) lo = hi = operand_hi(w[2 * x], w[2 * x + 1]);
-    else operand_parts(w[2 * x], w[2 * x + 1], hi, lo);
-#pragma unroll
-    for (int part = 0; part < (P == 1 ? 1 : 3); ++part)
-#pragma unroll
-      for (int t = 2 * x; t < NT; ++t) {
-        const int at = Ops::kP + (Ops::lower(t) + x) * 64 + (part == 2 ? Ops::kLower * 64 : 0) + lane;
-        pu[t] = mfma16x16x32(head[at], part == 1 ? lo : hi, pu[t]);
-      }
-  }
+  lower_product<NT>([&](int t) { return tile_rows(sh.a[t]); }, v, w);
+  lower_product<NT>([&](int t) { return tile_rows(sh.p[t]); }, w, pu);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const f4_t fq = factor(kFactorQ, t), fp = factor(kFactorP, t);
-    const f4_t y = scale4(qs[t], -es), z = scale4(pu[t], -er);
-    w[t] *= factor(kFactorX, t);
-    const f4_t u = scale4(w[t], -er);
+    const f4_t fq = factor(sh.factor[kFactorQ], t), y = scale4(qs[t], -es);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * t + 4 * g + e;
       if (i >= a.nodes) continue;
       const bool in = i < n;
-      if constexpr (TREE) a.updates[(first + i) * row + value_at] = in ? u[e] : 0.0f;
-      store1<BF16>(a.out, (first + i) * row + value_at, in ? __builtin_fmaf(fq[e], y[e], fp[e] * z[e]) : 0.0f);
+      if constexpr (TREE) a.updates[(first + i) * row + value_at] = in ? w[t][e] : 0.0f;
+      store1<BF16>(a.out, (first + i) * row + value_at, in ? __builtin_fmaf(fq[e], y[e], pu[t][e]) : 0.0f);
     }
   }
   if constexpr (!TREE) {
@@ -138,23 +103,27 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
     if (to < 0) return;
     if (n > 0) {
       // S <- e^G_end S + K^T X, X = diag(e^(G_end - G)) u
-      const float end = factors[4 * 16 * NT];
+      f4_t x[NT + (NT & 1)];
       float mx = 0.0f;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mx = max4(mx, w[t]);
-      const int en = 5 - exponent_of(max_of_groups(fmaxf(__builtin_amdgcn_ldexpf(mx, -er), m_state * end)));
+      for (int t = 0; t < NT; ++t) {
+        x[t] = w[t] * factor(sh.factor[kFactorX], t);
+        mx = max4(mx, x[t]);
+      }
+      if constexpr (NT & 1) x[NT] = zero;
+      const int en = 5 - exponent_of(max_of_groups(fmaxf(mx, m_state * sh.end)));
 #pragma unroll
-      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * end, en);
+      for (int t = 0; t < KT; ++t) s[t] = scale4(s[t] * sh.end, en);
 #pragma unroll
-      for (int x = 0; x < Ops::kTokenSteps; ++x) {
+      for (int y = 0; y < Ops::kTokenSteps; ++y) {
         h8_t hi, lo;
-        operand_parts(scale4(w[2 * x], en - er), scale4(w[2 * x + 1], en - er), hi, lo);
+        operand_parts(scale4(x[2 * y], en), scale4(x[2 * y + 1], en), hi, lo);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-          const h8_t k = transposed_operand<DK, BF16, NT>(sh.key, 0, t, x);
+          const h8_t k = transposed_operand<DK, BF16, NT>(sh.key, 0, t, y);
           s[t] = mfma16x16x32(k, hi, s[t]);
           s[t] = mfma16x16x32(k, lo, s[t]);
-          if constexpr (P == 2) s[t] = mfma16x16x32(transposed_operand<DK, BF16, NT>(sh.key, 1, t, x), hi, s[t]);
+          if constexpr (P == 2) s[t] = mfma16x16x32(transposed_operand<DK, BF16, NT>(sh.key, 1, t, y), hi, s[t]);
         }
       }
 #pragma unroll

@@ -1,0 +1,61 @@
+"""GPU parity of the gated delta rule, the rotary append and the token log probabilities against oracle/ where sizes,
+lengths and values go to their ends.  Pages "TensorRT Edge-LLM Completes the MLPerf Edge Agentic Benchmark 6.4x Faster on
+Jetson AGX Thor", sections on KV-cache reuse (a hybrid's recurrent states are kept with its pages) and tree-based
+multi-token prediction.
+
+The bounds of the delta rule are oracle/delta.py's, taken as tests/test_gpu_hybrid.py takes them."""
+import numpy as np
+import pytest
+import torch
+
+import gpu_util as U
+import test_gpu_hybrid as T
+
+pytestmark = pytest.mark.gpu
+BF, FP = T.BF, T.FP
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    U.require_gpu_lib()
+
+
+def scaled_values(c, at, ratio):
+    c.v[:, at] *= ratio
+    c.vf = c.v.float().cpu().numpy()
+
+
+# ----------------------------------------------------------------------------------------------- forgotten values
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,shape", [(4, (1, 2, 128, 64)), (8, (1, 2, 64, 64)), (33, (1, 2, 128, 64)),
+                                     (64, (1, 1, 256, 64)), (130, (1, 2, 128, 64)), (200, (1, 1, 64, 64))])
+@pytest.mark.parametrize("decay", [-12.0, -30.0, -np.inf])
+@pytest.mark.parametrize("ratio", [1e4, 1e7, 1e10])
+def test_tokens_behind_a_large_forgotten_one(dtype, M, shape, decay, ratio):
+    """A token's value `ratio` times the others', and the next token's decay takes it away: what follows keeps the
+    bits that its own sizes ask for."""
+    c = T.Delta(dtype, 2, M, *shape, seed=M)
+    for at in (0, M // 2):
+        scaled_values(c, at, ratio)
+        if at + 1 < M:
+            c.g[:, at + 1] = decay
+    c.check_chain(*c.chain())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,shape", [(3, (1, 2, 128, 64)), (12, (1, 2, 64, 64)), (30, (1, 1, 256, 64)),
+                                     (48, (1, 2, 128, 64)), (60, (1, 1, 256, 64)), (64, (1, 2, 64, 64))])
+@pytest.mark.parametrize("ratio", [1e4, 1e10, 1e25])
+def test_nodes_beside_a_large_sibling(dtype, M, shape, ratio):
+    """Node 1 and every fifth one have a large value; the others hang on the root and on each other and see none."""
+    rng = np.random.default_rng(M)
+    c = T.Delta(dtype, 2, M, *shape, seed=M)
+    large = [v for v in range(1, M) if v % 5 == 1]
+    scaled_values(c, large, ratio)
+    parent = np.full((2, M), -1, dtype=np.int32)
+    for b in range(2):
+        for v in range(1, M):
+            parent[b, v] = rng.choice([u for u in range(max(0, v - 6), v) if u not in large])
+    T.check_tree(c, parent, T.run_tree(c, parent))
