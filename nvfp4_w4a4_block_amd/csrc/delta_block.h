@@ -19,10 +19,12 @@
 //
 // Accuracy.  T r and P u add up tokens, between which a decay may stand: a value of
 // any size counts as e^(G_i - G_j) leaves it, or not at all beside another branch of a
-// tree.  Their factors keep fp32's range: fp32 products in the one-block kernel, bf16
-// parts in a scan, three each (24 bits, six products; P and u of bf16 calls two, 16
-// bits, three).  A scan waits for T r: 40 fp32 products of 32 cycles there take 27.4 us
-// for 512 tokens, 36 bf16 ones of 16 cycles 24.5.
+// tree.  Their factors keep fp32's range: fp32 products in the one-block kernel and in
+// T r of a scan by 64 columns, where T's 10 KB count more than the products; else bf16
+// parts, three each (24 bits, six products; P and u of bf16 calls two, 16 bits, three).
+// A scan waits for T r: 40 fp32 products of 32 cycles there take 27.4 us for 512 tokens,
+// 36 bf16 ones of 16 cycles 24.5.  4 sequences of 2,047 tokens, by 64 columns: 428 us in
+// parts, 392 in tiles.
 // K S and Q S add up a row's values, K^T X what is in a state at one time: there every
 // factor on the way to a state keeps 22 bits of its row's or column's largest value, in
 // two f16 parts (rounded to nearest, the second the rest of the first), of which the
@@ -105,8 +107,9 @@ __device__ __forceinline__ void operand_parts(f4_t a, f4_t b, h8_t& hi, h8_t& lo
 }
 
 // What is prepared of a block, in units of an operand of one lane (16 bytes).  PARTS:
-// f16 parts of rows of k and q.
-template <int DK, bool BF16, int NT>
+// f16 parts of rows of k and q.  TILES: T as the fp32 tiles of a lower triangle, row
+// after row, instead of three bf16 parts.
+template <int DK, bool BF16, int NT, bool TILES = false>
 struct BlockOps {
   static constexpr int kParts = BF16 ? 1 : 2;
   static constexpr int kSteps = DK / 32;            // inner steps over dk
@@ -118,11 +121,11 @@ struct BlockOps {
   // of a key head: K and its transpose, what a scan's states need, before Q
   static constexpr int kKey = 0, kKeyT = kParts * kRows, kQuery = kKeyT + kParts * kCols;
   static constexpr int kKeyUnits = kQuery + kParts * kRows;
-  // of a value head: the factors [3][16 NT] with e^G_end behind them, T in three bf16
-  // parts and P in two (bf16 calls) or three
+  // of a value head: the factors [3][16 NT] with e^G_end behind them, T, and P in two
+  // bf16 parts (bf16 calls) or three
   static constexpr int kPartsOfP = BF16 ? 2 : 3;
   static constexpr int kFactors = 0, kT = (3 * 4 * NT + 1 + 63) / 64 * 64;
-  static constexpr int kP = kT + 3 * kLower * 64;
+  static constexpr int kP = kT + (TILES ? kTiles : 3 * kLower) * 64;
   static constexpr int kHeadUnits = kP + kPartsOfP * kLower * 64;
   // steps of the rows of tile rt begin at this one
   static __device__ constexpr int lower(int rt) { return rt == 0 ? 0 : rt == 1 ? 1 : rt == 2 ? 2 : 4; }
@@ -284,14 +287,12 @@ __device__ __forceinline__ void lower_product(F rows, const f4_t (&x)[NT], f4_t 
   }
 }
 
-// The same of rows in N bf16 parts, part p of step l at rows(p, l): the products of
-// parts that reach N bits by eight.
+// y plus the same of rows in N bf16 parts, part p of step l at rows(p, l): the products
+// of parts that reach N bits by eight.
 template <int NT, int N, typename F>
-__device__ __forceinline__ void wide_product(F rows, const f4_t (&x)[NT], f4_t (&y)[NT]) {
+__device__ __forceinline__ void add_wide_product(F rows, const f4_t (&x)[NT], f4_t (&y)[NT]) {
   static_assert(NT % 2 == 0, "whole steps");
   typedef BlockOps<64, true, NT> Ops;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) y[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int s = 0; s < NT / 2; ++s) {
     b8_t part[N];
@@ -390,11 +391,11 @@ __device__ __forceinline__ void load_block_rows(const DeltaArgs& a, int64_t firs
 // goes on with the block itself, after a barrier: K, Q, (I + A)^-1, P and the factors
 // stay in sh.  Trees: `keys` (or NULL) takes the keys' rows as used, `key_row` values
 // apart, for all `nodes` of them.
-template <int DK, bool BF16, int NT, bool TREE, bool LOCAL>
+template <int DK, bool BF16, int NT, bool TREE, bool LOCAL, bool TILES = false>
 __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRows<DK, BF16>& rows, int n,
                                               BlockShared<DK, BF16, NT, LOCAL>& sh, h8_t* key_to, h8_t* head_to,
                                               float* keys = nullptr, int64_t key_row = 0, int nodes = 0) {
-  typedef BlockOps<DK, BF16, NT> Ops;
+  typedef BlockOps<DK, BF16, NT, TILES> Ops;
   constexpr int P = Ops::kParts;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const bool works = w < NT;
@@ -533,7 +534,13 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
       const auto t_rows = [&](int c) {
         return tile_rows(sh.a[tile_at(w, c)]) * *reinterpret_cast<const f4_t*>(&sh.beta[16 * c + 4 * g]);
       };
-      store_wide<3>(t_rows, w, head_to + Ops::kT + Ops::lower(w) * 64, Ops::kLower * 64);
+      if constexpr (TILES) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (c <= w) reinterpret_cast<f4_t*>(head_to + Ops::kT)[tile_at(w, c) * 64 + lane] = t_rows(c);
+      } else {
+        store_wide<3>(t_rows, w, head_to + Ops::kT + Ops::lower(w) * 64, Ops::kLower * 64);
+      }
       store_wide<Ops::kPartsOfP>([&](int c) { return tile_rows(sh.p[tile_at(w, c)]); }, w,
                                  head_to + Ops::kP + Ops::lower(w) * 64, Ops::kLower * 64);
       float* factors = reinterpret_cast<float*>(head_to + Ops::kFactors);

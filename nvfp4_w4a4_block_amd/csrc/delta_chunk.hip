@@ -29,9 +29,9 @@ struct Round {
 };
 
 // grid (heads, c1 - c0, seqs).
-template <int DK, bool BF16>
+template <int DK, bool BF16, bool TILES>
 __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a, Round r) {
-  typedef BlockOps<DK, BF16, kTiles> Ops;
+  typedef BlockOps<DK, BF16, kTiles, TILES> Ops;
   __shared__ BlockShared<DK, BF16, kTiles, false> sh;
   const int h = blockIdx.x, b = r.b0 + blockIdx.z, t0 = (r.c0 + blockIdx.y) * kChunk, group = a.heads / a.key_heads;
   const int kh = h / group;
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * kTiles) void delta_prepare_kernel(DeltaArgs a,
   const int n = count - t0 < kChunk ? count - t0 : kChunk;
   const int64_t block = (int64_t)blockIdx.z * (r.c1 - r.c0) + blockIdx.y;
   h8_t* key_to = h % group == 0 ? r.keys + (block * a.key_heads + kh) * Ops::kKeyUnits : nullptr;
-  prepare_block<DK, BF16, kTiles, false, false>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
+  prepare_block<DK, BF16, kTiles, false, false, TILES>(a, rows, n, sh, key_to, r.heads + (block * a.heads + h) * Ops::kHeadUnits);
 }
 
 // 64 rows of 16 values, one after the other in LDS; the pitch keeps the four rows that
@@ -86,9 +86,10 @@ template <int DK, bool BF16, int SLABS, int BUFFERS>
 constexpr bool kHoldT = SLABS == 2 && (BF16 || DK == 64 || BUFFERS == 0);
 
 // Units of a block that come to LDS.
-template <int DK, bool BF16, bool HOLD>
-constexpr int kUnitsHere = BlockOps<DK, BF16, kTiles>::kQuery +
-                           (HOLD ? BlockOps<DK, BF16, kTiles>::kT : BlockOps<DK, BF16, kTiles>::kP);
+template <int DK, bool BF16, int SLABS, int BUFFERS>
+constexpr int kUnitsHere = BlockOps<DK, BF16, kTiles, SLABS == 4>::kQuery +
+                           (kHoldT<DK, BF16, SLABS, BUFFERS> ? BlockOps<DK, BF16, kTiles, SLABS == 4>::kT
+                                                             : BlockOps<DK, BF16, kTiles, SLABS == 4>::kP);
 
 // What a state's wave leaves for the wave of its outputs.
 template <int DK, bool BF16>
@@ -109,9 +110,10 @@ struct Handed {
 // block; 1: they meet when S is ready, and when u is.
 template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
 __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(DeltaArgs a, Round r) {
-  typedef BlockOps<DK, BF16, kTiles> Ops;
+  constexpr bool kInTiles = SLABS == 4;
+  typedef BlockOps<DK, BF16, kTiles, kInTiles> Ops;
   constexpr bool kHold = kHoldT<DK, BF16, SLABS, BUFFERS>;
-  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = kUnitsHere<DK, BF16, kHold>;
+  constexpr int P = Ops::kParts, KT = DK / 16, kUnits = kUnitsHere<DK, BF16, SLABS, BUFFERS>;
   __shared__ h8_t ops[BUFFERS ? BUFFERS : 1][BUFFERS ? kUnits : 1];
   static_assert(HANDS == 1 || BUFFERS == 2, "outputs a block behind leave no barrier between blocks");
   __shared__ Handed<DK, BF16> handed[HANDS][SLABS];
@@ -213,12 +215,18 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[t][e] = __builtin_fmaf(f[e], y[e], v[t][e]);
       }
-      if constexpr (kHold) {
-        wide_product<kTiles, 3>([&](int p, int l) { return __builtin_bit_cast(b8_t, own[p][l]); }, v, w);
-        if (c + 1 < end_block) load_own(c + 1);
+      if constexpr (kInTiles) {
+        lower_product<kTiles>([&](int t) { return __builtin_bit_cast(f4_t, head[Ops::kT + t * 64]); }, v, w);
       } else {
-        wide_product<kTiles, 3>(
-            [&](int p, int l) { return __builtin_bit_cast(b8_t, head[Ops::kT + (p * Ops::kLower + l) * 64]); }, v, w);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) w[t] = zero;
+        add_wide_product<kTiles, 3>(
+            [&](int p, int l) {
+              if constexpr (kHold) return __builtin_bit_cast(b8_t, own[p][l]);
+              else return __builtin_bit_cast(b8_t, head[Ops::kT + (p * Ops::kLower + l) * 64]);
+            },
+            v, w);
+        if (kHold && c + 1 < end_block) load_own(c + 1);
       }
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) hand.w[t][lane] = w[t];
@@ -323,9 +331,11 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     if (HANDS == 2 && r.c0 < end_block) lds_barrier();
     return;
   }
-  // Q and P are this wave's alone: straight to registers, Q where it fits.  Outputs that
-  // are not behind fetch one while they work on the other.
+  // Q and P are this wave's alone: straight to registers, Q where it fits.  They come a
+  // block ahead; in fp32 calls, where they are twice as large, outputs that are not
+  // behind fetch one while they work on the other.
   constexpr int lag = HANDS - 1;
+  constexpr bool ahead = BF16 || lag;
   constexpr bool hold = P * Ops::kSteps <= 8;
   h8_t q[P][kTiles][hold ? Ops::kSteps : 1];
   constexpr int kOfP = (Ops::kHeadUnits - Ops::kP) / 64;
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   };
   if (r.c0 < end_block) {
     load_q(r.c0);
-    if (lag) load_p(r.c0);
+    if (ahead) load_p(r.c0);
   }
   const auto factor = [&](int c, int which, int t) {
     const float* factors = reinterpret_cast<const float*>(head_ops(c) + Ops::kFactors);
@@ -398,29 +408,38 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
     }
     const int es = hand.es[lane];
-    if constexpr (lag) {
+    if constexpr (ahead) {
       if (more) load_q(c + 1);
     } else {
       load_p(c);
-      lds_barrier();  // u is handed over
     }
-    f4_t u[kTiles], z[kTiles];
+    const auto add_read = [&](f4_t(&z)[kTiles]) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        if constexpr (!lag) fq[t] = factor(c, kFactorQ, t);
+        z[t] += fq[t] * scale4(y[t], -es);
+      }
+    };
+    // bf16 calls add P u to Q S, which saves registers; in fp32 calls, whose outputs have
+    // more products than their states, two sums do not wait for each other (3 prompts of
+    // up to 4,099 tokens: 138 us, 166 with one)
+    f4_t z[kTiles] = {zero, zero, zero, zero};
+    if constexpr (BF16) add_read(z);
+    if constexpr (!lag) lds_barrier();  // u is handed over
+    f4_t u[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) u[t] = hand.w[t][lane];
-    wide_product<kTiles, Ops::kPartsOfP>(
+    add_wide_product<kTiles, Ops::kPartsOfP>(
         [&](int part, int l) { return __builtin_bit_cast(b8_t, p[part * Ops::kLower + l]); }, u, z);
     if (more) {
-      if constexpr (lag) load_p(c + 1);
+      if constexpr (ahead) load_p(c + 1);
       else load_q(c + 1);
     }
+    if constexpr (!BF16) add_read(z);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      if constexpr (!lag) fq[t] = factor(c, kFactorQ, t);
-      const f4_t qs = scale4(y[t], -es);
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, __builtin_fmaf(fq[t][e], qs[e], z[t][e]));
-    }
+      for (int e = 0; e < 4; ++e) store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, z[t][e]);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (lag && more) load_factors(c + 1);
     if constexpr (BUFFERS == 1) lds_barrier();
@@ -431,11 +450,27 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     if (lane < 16) store1<BF16>(a.out, (first + t) * a.heads * a.dv + value_at, 0.0f);
 }
 
+constexpr int kLds = 160 * 1024;
+
+template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
+constexpr int scan_lds() {
+  return BUFFERS * 16 * kUnitsHere<DK, BF16, SLABS, BUFFERS> +
+         SLABS * (HANDS * (int)sizeof(Handed<DK, BF16>) + (int)sizeof(Rows16<BF16>));
+}
+
+// Whether a workgroup has 64 columns: where 32 give more workgroups than there are CUs,
+// of which each holds one, and LDS has room.
+template <int DK, bool BF16>
+bool four_slabs(const DeltaArgs& a) {
+  return BF16 && a.bf16 && scan_lds<DK, BF16, 4, 2, 1>() <= kLds && (int64_t)a.seqs * a.heads * (a.dv / 32) > 256;
+}
+
 // Bytes of a block of one sequence.
 template <int DK, bool BF16>
 int64_t block_bytes(const DeltaArgs& a) {
-  typedef BlockOps<DK, BF16, kTiles> Ops;
-  return 16 * ((int64_t)a.key_heads * Ops::kKeyUnits + (int64_t)a.heads * Ops::kHeadUnits);
+  const int head = four_slabs<DK, BF16>(a) ? BlockOps<DK, BF16, kTiles, true>::kHeadUnits
+                                           : BlockOps<DK, BF16, kTiles, false>::kHeadUnits;
+  return 16 * ((int64_t)a.key_heads * BlockOps<DK, BF16, kTiles>::kKeyUnits + (int64_t)a.heads * head);
 }
 
 int64_t block_bytes(const DeltaArgs& a) {
@@ -466,14 +501,6 @@ int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) {
   return r.blocks < r.all ? (int64_t)r.seqs * a.heads * a.dv * a.dk * 4 : 0;
 }
 
-constexpr int kLds = 160 * 1024;
-
-template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
-constexpr int scan_lds() {
-  return BUFFERS * 16 * kUnitsHere<DK, BF16, kHoldT<DK, BF16, SLABS, BUFFERS>> +
-         SLABS * (HANDS * (int)sizeof(Handed<DK, BF16>) + (int)sizeof(Rows16<BF16>));
-}
-
 template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
   const dim3 grid(a.heads, a.dv / (16 * SLABS), seqs);
@@ -489,8 +516,8 @@ void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
 // tokens 37.7 -> 39.3).
 template <int DK, bool BF16>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
-  if constexpr (scan_lds<DK, BF16, 4, 2, 1>() <= kLds)
-    if ((int64_t)seqs * a.heads * (a.dv / 32) > 256) {
+  if constexpr (BF16 && scan_lds<DK, BF16, 4, 2, 1>() <= kLds)
+    if (four_slabs<DK, BF16>(a)) {
       scan<DK, BF16, 4, 2, 1>(a, r, seqs, stream);
       return;
     }
@@ -505,18 +532,20 @@ void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
 
 template <int DK, bool BF16>
 void run(const DeltaArgs& a, hipStream_t stream) {
-  typedef BlockOps<DK, BF16, kTiles> Ops;
   const Rounds n = rounds_of(a);
+  const bool tiles = four_slabs<DK, BF16>(a);
   Round r = {};
   r.carry = static_cast<float*>(a.workspace);
   r.keys = reinterpret_cast<h8_t*>(static_cast<char*>(a.workspace) + carry_bytes(a, n));
-  r.heads = r.keys + (int64_t)n.seqs * n.blocks * a.key_heads * Ops::kKeyUnits;
+  r.heads = r.keys + (int64_t)n.seqs * n.blocks * a.key_heads * BlockOps<DK, BF16, kTiles>::kKeyUnits;
   for (r.b0 = 0; r.b0 < a.seqs; r.b0 += n.seqs) {
     const int seqs = a.seqs - r.b0 < n.seqs ? a.seqs - r.b0 : n.seqs;
     for (r.c0 = 0; r.c0 < n.all; r.c0 = r.c1) {
       r.c1 = r.c0 + n.blocks < n.all ? r.c0 + n.blocks : n.all;
       r.last = r.c1 == n.all;
-      delta_prepare_kernel<DK, BF16><<<dim3(a.heads, r.c1 - r.c0, seqs), 64 * kTiles, 0, stream>>>(a, r);
+      const dim3 grid(a.heads, r.c1 - r.c0, seqs);
+      if (tiles) delta_prepare_kernel<DK, BF16, true><<<grid, 64 * kTiles, 0, stream>>>(a, r);
+      else delta_prepare_kernel<DK, BF16, false><<<grid, 64 * kTiles, 0, stream>>>(a, r);
       scan<DK, BF16>(a, r, seqs, stream);
     }
   }
