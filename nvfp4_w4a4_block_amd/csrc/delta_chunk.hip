@@ -465,6 +465,10 @@ bool four_slabs(const DeltaArgs& a) {
   return BF16 && a.bf16 && scan_lds<DK, BF16, 4, 2, 1>() <= kLds && (int64_t)a.seqs * a.heads * (a.dv / 32) > 256;
 }
 
+bool four_slabs(const DeltaArgs& a) {
+  return a.dk == 64 ? four_slabs<64, true>(a) : a.dk == 128 ? four_slabs<128, true>(a) : four_slabs<256, true>(a);
+}
+
 // Bytes of a block of one sequence.
 template <int DK, bool BF16>
 int64_t block_bytes(const DeltaArgs& a) {
@@ -479,26 +483,50 @@ int64_t block_bytes(const DeltaArgs& a) {
   return a.bf16 ? block_bytes<256, true>(a) : block_bytes<256, false>(a);
 }
 
-// What a round takes on: so many sequences, so many of their blocks, that what is
-// prepared stays within 128 MB, half the Infinity Cache.
+// What a round takes on: what is prepared of it, and the states that it leaves to the next
+// one, stay within 128 MB, half the Infinity Cache (one block of one sequence is the
+// least, whatever its size).
 constexpr int64_t kRoundBytes = (int64_t)128 << 20;
 
 struct Rounds {
   int seqs, blocks, all;
 };
 
-Rounds rounds_of(const DeltaArgs& a) {
-  const auto within = [](int64_t n, int64_t most) { return (int)(n < 1 ? 1 : n < most ? n : most); };
-  Rounds r;
-  r.all = (a.nodes + kChunk - 1) / kChunk;
-  const int64_t bytes = block_bytes(a);
-  r.seqs = within(kRoundBytes / bytes, a.seqs);
-  r.blocks = within(kRoundBytes / (bytes * r.seqs), r.all);
-  return r;
-}
+int64_t state_bytes(const DeltaArgs& a) { return (int64_t)a.heads * a.dv * a.dk * 4; }
+int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) { return r.blocks < r.all ? r.seqs * state_bytes(a) : 0; }
 
-int64_t carry_bytes(const DeltaArgs& a, const Rounds& r) {
-  return r.blocks < r.all ? (int64_t)r.seqs * a.heads * a.dv * a.dk * 4 : 0;
+// The sequences of a round that cost least, by its number of rounds, each as many blocks
+// as the workgroups, one a CU, go over the chip, and four for its launches.  A round that
+// does not reach the sequences' ends moves their states as well.  us, 48 heads of 128,
+// bf16, by as many sequences as fit with one block each, and so: 64 sequences of 200
+// tokens 1,033 (their states go out and in at every block), 713; 4 of 2,047 368, 356.
+Rounds rounds_of(const DeltaArgs& a) {
+  const auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+  const int64_t bytes = block_bytes(a), groups = over((int64_t)a.heads * a.dv, four_slabs(a) ? 64 : 32);
+  const int64_t all = over(a.nodes, kChunk), fit = kRoundBytes / bytes < 1 ? 1 : kRoundBytes / bytes;
+  const int64_t most = fit < a.seqs ? fit : a.seqs, filled = over(8 * 256, groups);
+  Rounds best = {1, 1, (int)all};
+  double least = 0.0;
+  // eight times over the chip and more, the sequences that fit are as good as any
+  for (int64_t n = 1, next; n <= most; n = next) {
+    next = n + n / 16 + 1;
+    next = n == most || (next < filled && next < most) ? next : most;
+    const int64_t seqs = over(a.seqs, over(a.seqs, n));
+    int64_t blocks = all;
+    if (seqs * all * bytes > kRoundBytes) {
+      blocks = (kRoundBytes - seqs * state_bytes(a)) / (seqs * bytes);
+      blocks = over(all, over(all, blocks < 1 ? 1 : blocks));
+    }
+    const double moved = blocks < all ? (double)state_bytes(a) / bytes : 0.0;
+    const double cost =
+        over(a.seqs, seqs) * over(all, blocks) * (over(seqs * groups, 256) * (blocks + moved) + 4.0);
+    if (n == 1 || cost < least) {
+      least = cost;
+      best.seqs = (int)seqs;
+      best.blocks = (int)blocks;
+    }
+  }
+  return best;
 }
 
 template <int DK, bool BF16, int SLABS, int BUFFERS, int HANDS>

@@ -59,3 +59,32 @@ def test_nodes_beside_a_large_sibling(dtype, M, shape, ratio):
         for v in range(1, M):
             parent[b, v] = rng.choice([u for u in range(max(0, v - 6), v) if u not in large])
     T.check_tree(c, parent, T.run_tree(c, parent))
+
+
+# ----------------------------------------------------------------------------------------------- rounds
+
+
+def some_heads(c, out, states, heads):
+    """The step c, its outputs and its states, of some value heads alone (heads are independent of each other)."""
+    nb, M, Hk, H, Dk, Dv = c.dims
+    kh = np.asarray(heads) // (H // Hk)
+    for name in ("q", "k", "qf", "kf"):
+        setattr(c, name, getattr(c, name)[:, :, kh])
+    for name in ("v", "vf", "g", "beta"):
+        setattr(c, name, getattr(c, name)[:, :, heads])
+    c.states = np.ascontiguousarray(c.states[:, heads])
+    c.dims = (nb, M, len(heads), len(heads), Dk, Dv)
+    return out[:, :, heads], states[:, heads].contiguous()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_states_carried_from_round_to_round(dtype):
+    """1,024 heads: a round has room for a few blocks.  A sequence that reaches the last round, one that ends in the
+    first, and one that begins from zeros."""
+    M, heads = 430, [0, 255, 256, 700, 1023]
+    c = T.Delta(dtype, 3, M, 4, 1024, 64, 64, counts=[M, 130, 300], slots=5, src=[0, 1, -1], dst=[3, 1, 4], seed=5,
+                decay=5.0)
+    need = T.B.load().nvfp4_delta_rule_workspace_bytes(3, M, 4, 1024, 64, 64, T.B.NVFP4_BF16 if dtype == BF else T.B.NVFP4_F32)
+    assert need <= 128 << 20
+    out, states = c.chain()
+    c.check_chain(*some_heads(c, out, states, heads))
