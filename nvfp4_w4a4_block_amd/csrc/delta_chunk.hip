@@ -515,6 +515,7 @@ Rounds rounds_of(const DeltaArgs& a) {
     int64_t blocks = all;
     if (seqs * all * bytes > kRoundBytes) {
       blocks = (kRoundBytes - seqs * state_bytes(a)) / (seqs * bytes);
+      if (blocks < 1 && n > 1) break;
       blocks = over(all, over(all, blocks < 1 ? 1 : blocks));
     }
     const double moved = blocks < all ? (double)state_bytes(a) / bytes : 0.0;

@@ -36,3 +36,8 @@ def test_a_block_of_the_largest_shape_is_the_least(lib):
     """1,024 key and value heads of 256 in fp32: one block is past a round, and is taken nevertheless."""
     one = lib.nvfp4_delta_rule_workspace_bytes(1, 64 + 1, 1024, 1024, 256, 256, B.NVFP4_F32)
     assert 128 * MB < one < 512 * MB and one == lib.nvfp4_delta_rule_workspace_bytes(1, 65535, 1024, 1024, 256, 256, B.NVFP4_F32)
+
+
+@pytest.mark.parametrize("seqs", [2, 3, 7, 100])
+def test_sequences_whose_blocks_and_states_do_not_fit_come_in_turns(lib, seqs):
+    assert 0 < lib.nvfp4_delta_rule_workspace_bytes(seqs, 430, 4, 1024, 64, 64, B.NVFP4_F32) <= 128 * MB
