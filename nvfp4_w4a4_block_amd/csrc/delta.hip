@@ -1,5 +1,5 @@
-// Gated delta rule, token by token: decoding steps, drafted trees, and the
-// accepted path of a tree put into the states.
+// Gated delta rule, token by token: decoding steps, and the accepted path of a tree put
+// into the states.
 //
 // The model of the page "TensorRT Edge-LLM Completes the MLPerf Edge Agentic
 // Benchmark 6.4x Faster on Jetson AGX Thor" is a hybrid whose recurrent states are
@@ -10,7 +10,6 @@
 // S <- S + u k^T, o = scale S q.  Rows of S are independent of each other, so a
 // wave that holds some of them whole needs nothing from any other.
 #include "delta_common.h"
-#include "kv_tree.h"
 
 namespace nvfp4 {
 namespace {
@@ -86,104 +85,6 @@ __global__ __launch_bounds__(64 * kWaves) void delta_step_kernel(DeltaArgs a) {
   if (!used) return;
   const int to = delta_dst(a.src, a.dst, a.seqs, a.slots, b);
   if (to >= 0) store_state<DK, 1>(a.states + ((int64_t)to * a.heads + h) * state_size + row0 * DK, x);
-}
-
-// Drafted trees of more than 48 fp32 nodes with keys of 256, whose block does not fit
-// LDS, node after node (the others are delta_single.hip's).  With the sums G of the decays along each node's line,
-//   u_v = beta_v (v_v - e^G_v S k_v - sum_a e^(G_v - G_a) (k_a . k_v) u_a),
-//   o_v = scale (e^G_v S q_v + sum_a e^(G_v - G_a) (k_a . q_v) u_a),
-// a the ancestors of v (and v itself in o).  grid (dv / 64, heads, seqs).
-__global__ __launch_bounds__(64 * kWaves) void delta_tree_kernel(DeltaArgs a) {
-  constexpr int DK = 256;
-  constexpr bool BF16 = false;
-  __shared__ float rows[2][DK];      // k_v, q_v
-  __shared__ float near[2][64];      // e^(G_v - G_a) k_a . (k_v, q_v)
-  __shared__ float u[64][64];        // nodes x rows of S
-  __shared__ uint64_t lines[64];
-  __shared__ float length[64];       // the factor that normalises k_a
-  const int b = blockIdx.z, h = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 15;
-  const int kh = h / (a.heads / a.key_heads), col = 16 * wave + j, row = blockIdx.x * 64 + col;
-  const int src = a.src[b];
-  const bool used = delta_used(src, a.slots);
-  const int count = used ? delta_count(a.counts, a.nodes, b) : 0;
-  const int64_t first = (int64_t)b * a.nodes;
-  StateTile<DK, 1> x;
-  if (used && src >= 0)
-    load_state<DK, 1>(a.states + (((int64_t)src * a.heads + h) * a.dv + blockIdx.x * 64 + 16 * wave) * DK, x);
-  else zero_state<DK, 1>(x);
-  if (wave == 0) lines[lane] = ancestors_of_wave(lane < count ? a.parent[first + lane] : -1);
-  for (int v = 0; v < count; ++v) {
-    const int64_t r = first + v;
-    __syncthreads();
-    if (wave == 0) stage_row<DK, BF16>(a.k, r * a.k_stride + kh * DK, a.norm_eps, 1.0f, rows[0]);
-    if (wave == 1) stage_row<DK, BF16>(a.q, r * a.q_stride + kh * DK, a.norm_eps, a.scale, rows[1]);
-    if (wave == 2) {
-      float s = 1.0f;
-      if (a.norm_eps >= 0.0f) {
-        f4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (lane < DK / 4) y = load4<BF16>(a.k, r * a.k_stride + kh * DK + 4 * lane);
-        s = 1.0f / __builtin_sqrtf(sum_of_wave(y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3]) + a.norm_eps);
-      }
-      if (lane == 0) length[v] = s;
-    }
-    __syncthreads();
-    const uint64_t line = lines[v];
-    for (int n = wave; n <= v; n += kWaves) {
-      if (!((line >> n) & 1)) continue;
-      double far = 0.0;  // the decays between n and v
-      for (int i = n + 1; i <= v; ++i)
-        if (((line >> i) & 1)) far += (double)a.g[(first + i) * a.heads + h];
-      float kk = 0.0f, qk = 0.0f;
-      if (lane < DK / 4) {
-        const f4_t y = load4<BF16>(a.k, (first + n) * a.k_stride + kh * DK + 4 * lane) * length[n];
-        const f4_t k = *reinterpret_cast<const f4_t*>(&rows[0][4 * lane]);
-        const f4_t q = *reinterpret_cast<const f4_t*>(&rows[1][4 * lane]);
-        kk = y[0] * k[0] + y[1] * k[1] + y[2] * k[2] + y[3] * k[3];
-        qk = y[0] * q[0] + y[1] * q[1] + y[2] * q[2] + y[3] * q[3];
-      }
-      kk = sum_of_wave(kk);
-      qk = sum_of_wave(qk);
-      const float decay = expf((float)far);
-      if (lane == 0) {
-        near[0][n] = decay * kk;
-        near[1][n] = decay * qk;
-      }
-    }
-    __syncthreads();
-    const float sk = dot<DK>(x, rows[0]), sq = dot<DK>(x, rows[1]);
-    double all = 0.0;
-    for (int i = 0; i <= v; ++i)
-      if ((line >> i) & 1) all += (double)a.g[(first + i) * a.heads + h];
-    const float into = expf((float)all), beta = a.beta[r * a.heads + h];
-    const int64_t at = r * a.v_stride + h * a.dv + row;
-    float value;
-    if constexpr (BF16) value = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.v)[at] << 16);
-    else value = static_cast<const float*>(a.v)[at];
-    float w = value - into * sk, o = into * sq;
-    for (int n = 0; n < v; ++n)
-      if ((line >> n) & 1) {
-        w -= near[0][n] * u[n][col];
-        o += near[1][n] * u[n][col];
-      }
-    w *= beta;
-    o += near[1][v] * w;
-    if (lane < 16) {
-      u[v][col] = w;
-      a.updates[(r * a.heads + h) * a.dv + row] = w;
-      store1<BF16>(a.out, (r * a.heads + h) * a.dv + row, o);
-    }
-    if (blockIdx.x == 0 && h % (a.heads / a.key_heads) == 0)
-      for (int i = threadIdx.x; i < DK; i += 64 * kWaves) a.keys[(r * a.key_heads + kh) * DK + i] = rows[0][i];
-  }
-  for (int v = count; v < a.nodes; ++v) {
-    const int64_t r = first + v;
-    if (lane < 16) {
-      a.updates[(r * a.heads + h) * a.dv + row] = 0.0f;
-      store1<BF16>(a.out, (r * a.heads + h) * a.dv + row, 0.0f);
-    }
-    if (blockIdx.x == 0 && h % (a.heads / a.key_heads) == 0)
-      for (int i = threadIdx.x; i < DK; i += 64 * kWaves) a.keys[(r * a.key_heads + kh) * DK + i] = 0.0f;
-  }
 }
 
 // The accepted path of a tree into one state: e^G_end S + sum_i e^(G_end - G_i)
@@ -280,19 +181,17 @@ void commit(const DeltaCommitArgs& a, hipStream_t stream) {
 constexpr int kFewTokens = 4;
 
 int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {
-  return a.nodes <= kFewTokens || delta_single_block(a) ? 0 : delta_chunk_workspace_bytes(a);
+  return a.nodes <= kChunk ? 0 : delta_chunk_workspace_bytes(a);
 }
 
 hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
-  if (a.nodes > kFewTokens) {
-    if (delta_single_block(a)) {
-      launch_delta_block(a, stream);
-      return hipGetLastError();
-    }
-    if (a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
-      launch_delta_chunks(a, stream);
-      return hipGetLastError();
-    }
+  if (a.nodes > kFewTokens && a.nodes <= kChunk) {
+    launch_delta_block(a, stream);
+    return hipGetLastError();
+  }
+  if (a.nodes > kChunk && a.workspace_bytes >= delta_chunk_workspace_bytes(a)) {
+    launch_delta_chunks(a, stream);
+    return hipGetLastError();
   }
   if (a.dk == 64) a.bf16 ? step<64, true>(a, stream) : step<64, false>(a, stream);
   else if (a.dk == 128) a.bf16 ? step<128, true>(a, stream) : step<128, false>(a, stream);
@@ -301,8 +200,7 @@ hipError_t launch_delta_rule(const DeltaArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_delta_tree(const DeltaArgs& a, hipStream_t stream) {
-  if (delta_single_block(a)) launch_delta_block(a, stream);
-  else delta_tree_kernel<<<dim3(a.dv / 64, a.heads, a.seqs), 64 * kWaves, 0, stream>>>(a);
+  launch_delta_block(a, stream);
   return hipGetLastError();
 }
 

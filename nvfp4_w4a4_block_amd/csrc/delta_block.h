@@ -42,8 +42,6 @@ namespace nvfp4 {
 
 typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kChunk = 64;  // tokens of a block
-
 __device__ __forceinline__ f4_t scale4(f4_t x, int e) {
   return f4_t{__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e), __builtin_amdgcn_ldexpf(x[2], e),
               __builtin_amdgcn_ldexpf(x[3], e)};

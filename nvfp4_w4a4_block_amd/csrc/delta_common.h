@@ -11,7 +11,7 @@ int64_t delta_chunk_workspace_bytes(const DeltaArgs& a);
 void launch_delta_chunks(const DeltaArgs& a, hipStream_t stream);
 
 // Trees (with parents) and chains of one block (delta_single.hip).
-bool delta_single_block(const DeltaArgs& a);
+constexpr int kChunk = 64;  // tokens of a block
 void launch_delta_block(const DeltaArgs& a, hipStream_t stream);
 
 // Four values of a row of q, k or v from value `at` on, at a multiple of four.
@@ -45,9 +45,9 @@ __device__ __forceinline__ float sum_of_groups(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// Tokens of a sequence; 0 where it is not in use.
 __device__ __forceinline__ bool delta_used(int src, int slots) { return src >= -1 && src < slots; }
 
+// Tokens of a sequence in use.
 __device__ __forceinline__ int delta_count(const int32_t* counts, int nodes, int b) {
   const int n = counts ? counts[b] : nodes;
   return n < 0 ? 0 : n < nodes ? n : nodes;

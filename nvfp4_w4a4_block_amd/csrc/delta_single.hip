@@ -145,13 +145,10 @@ void run(const DeltaArgs& a, hipStream_t stream) {
   if (a.nodes <= 16) run<DK, BF16, 1>(a, stream);
   else if (a.nodes <= 32) run<DK, BF16, 2>(a, stream);
   else if (a.nodes <= 48) run<DK, BF16, 3>(a, stream);
-  else if constexpr (DK < 256 || BF16) run<DK, BF16, 4>(a, stream);
+  else run<DK, BF16, 4>(a, stream);
 }
 
 }  // namespace
-
-// What the block of 64 fp32 rows of 256 needs is past a CU's LDS.
-bool delta_single_block(const DeltaArgs& a) { return a.nodes <= (a.dk < 256 || a.bf16 ? 64 : 48); }
 
 void launch_delta_block(const DeltaArgs& a, hipStream_t stream) {
   if (a.dk == 64) a.bf16 ? run<64, true>(a, stream) : run<64, false>(a, stream);

@@ -88,3 +88,46 @@ def test_states_carried_from_round_to_round(dtype):
     assert need <= 128 << 20
     out, states = c.chain()
     c.check_chain(*some_heads(c, out, states, heads))
+
+
+# ----------------------------------------------------------------------------------------------- every form
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("Dk", [64, 128, 256])
+@pytest.mark.parametrize("M", [5, 16, 17, 32, 33, 48, 49, 64, 65])
+def test_blocks_of_every_width(dtype, Dk, M):
+    """Chains and trees at the ends of each number of row tiles, ragged, with roots and decays at their ends."""
+    rng = np.random.default_rng(M)
+    c = T.Delta(dtype, 4, M, 1, 3, Dk, 64, counts=[M, M - 1, (M + 1) // 2, 0], slots=9, src=[0, -1, 2, 3],
+                dst=[4, 5, 6, 7], seed=M + Dk)
+    c.g[:, ::5, 0] = -np.inf
+    c.g[:, :, 1], c.beta[:, :, 1] = 0.0, 1.0
+    c.g[:, :, 2] *= 300
+    c.check_chain(*c.chain())
+    if M > 64:
+        return
+    c.counts, c.src = [M, M - 1, M, 0], np.array([0, -1, 99, 3], dtype=np.int32)
+    parent = T.random_trees(rng, 4, M)
+    parent[:, 3], parent[0, M // 2], parent[1, 4] = -1, M, 4
+    got = T.run_tree(c, parent)
+    T.check_tree(c, parent, got)
+    for x in got:
+        assert not x[1, M - 1:].any() and not x[2:].any()
+
+
+@pytest.mark.parametrize("nb,M", [(2, 65), (2, 200), (3, 130), (6, 100)])
+def test_several_sequences_of_the_models_shape(nb, M):
+    """16 key and 48 value heads of 128: from two sequences on a workgroup has 64 columns of a state."""
+    heads = [0, 1, 20, 47]
+    c = T.Delta(BF, nb, M, 16, 48, 128, 128, counts=[M, 70, M - 1, 64, 1, 0][:nb], seed=M, decay=4.0)
+    out, states = c.chain()
+    c.check_chain(*some_heads(c, out, states, heads))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (256, 128)])
+def test_several_sequences_of_many_heads(dtype, Dk, Dv):
+    c = T.Delta(dtype, 3, 135, 8, 64, Dk, Dv, counts=[135, 64, 100], seed=Dk, decay=4.0)
+    out, states = c.chain()
+    c.check_chain(*some_heads(c, out, states, [0, 7, 33, 63]))
