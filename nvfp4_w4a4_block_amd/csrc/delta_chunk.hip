@@ -70,6 +70,46 @@ __device__ __forceinline__ void load_values(const char* rows, int64_t stride, in
   }
 }
 
+// The largest bits of magnitudes, two of them in bf16; whether they are not finite.
+typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t most_of(uint32_t most, u4_t x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16)
+      most = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, most),
+                                                                    __builtin_bit_cast(us2_t, x[i] & 0x7FFF7FFFu)));
+    else
+      most = max(most, x[i] & 0x7FFFFFFFu);
+  }
+  return most;
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(uint32_t most) {
+  return BF16 ? (most & 0xFFFF) >= 0x7F80 || most >> 16 >= 0x7F80 : most >= 0x7F800000u;
+}
+
+// Zeros in place of values that are not finite; a column's first one to `lost`.
+template <bool BF16>
+__device__ __forceinline__ void take_out(Rows16<BF16>& v, int* lost) {
+  wave_sync();
+  const int j = threadIdx.x & 15;
+#pragma unroll 1
+  for (int i = (threadIdx.x & 63) >> 4; i < kChunk; i += 4) {
+    char* at = v.value(i);
+    if constexpr (BF16) {
+      if ((*reinterpret_cast<uint16_t*>(at) & 0x7F80) != 0x7F80) continue;
+      *reinterpret_cast<uint16_t*>(at) = 0;
+    } else {
+      if (finite(*reinterpret_cast<float*>(at))) continue;
+      *reinterpret_cast<float*>(at) = 0.0f;
+    }
+    atomicMin(&lost[j], i);
+  }
+}
+
 #define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(uintptr_t)(p))
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(uintptr_t)(p))
 
@@ -91,13 +131,17 @@ constexpr int kUnitsHere = BlockOps<DK, BF16, kTiles, SLABS == 4>::kQuery +
                            (kHoldT<DK, BF16, SLABS, BUFFERS> ? BlockOps<DK, BF16, kTiles, SLABS == 4>::kT
                                                              : BlockOps<DK, BF16, kTiles, SLABS == 4>::kP);
 
-// What a state's wave leaves for the wave of its outputs.
+// What a state's wave leaves for the wave of its outputs, and the fetching one for it.  A
+// token of which a column keeps nothing (k, g, beta or its value are not finite, or the
+// state is not) and what follows it are NaN there; the products go on without it.
 template <int DK, bool BF16>
 struct Handed {
   h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
   f4_t w[kTiles][64];                 // u
   int es[64];                         // S's exponent
-  Rows16<BF16> v;                     // the other way: the block's values
+  int first[64];                      // first token of which nothing is left, 64: none
+  Rows16<BF16> v;                     // the other way: the block's values,
+  int lost[16];                       // and a column's first token that is not finite
 };
 
 // grid (heads, dv / (16 SLABS), seqs).  SLABS waves have 16 columns of the state each:
@@ -143,6 +187,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
   const auto key_ops = [&](int c) { return (BUFFERS ? buffer_of(c) : keys_of(c)) + lane; };
   const auto head_ops = [&](int c) { return BUFFERS ? buffer_of(c) + Ops::kQuery : heads_of(c); };
   const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float nan = __builtin_nanf("");
   const auto hand_of = [&](int c) { return handed[HANDS == 2 ? (c - r.c0) & 1 : 0]; };
   if (states) {
     float* carry = r.carry + ((int64_t)blockIdx.z * a.heads + h) * state_size + (int64_t)col0 * DK;
@@ -151,6 +196,18 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     else if (src >= 0) load_state<DK, 1>(a.states + ((int64_t)src * a.heads + h) * state_size + (int64_t)col0 * DK, st);
     else zero_state<DK, 1>(st);
     f4_t(&s)[KT] = st.s[0];
+    bool gone = false;  // nothing is left of the column
+    if (r.c0 < end_block) {
+      float m = 0.0f;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) m = max4_nan(m, s[t]);
+      const uint64_t odd = __ballot(!finite(m));
+      if (odd) {
+        gone = ((odd | odd >> 16 | odd >> 32 | odd >> 48) >> j) & 1;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) s[t] = gone ? zero : s[t];
+      }
+    }
     // s holds S times 2^es
     int es = 0;
     if (r.c0 < end_block) {
@@ -181,6 +238,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       const auto factor = [&](int which, int t) {
         return *reinterpret_cast<const f4_t*>(factors + which * kChunk + 16 * t + 4 * g);
       };
+      const int lost = hand.lost[j];
       // K S
       f4_t ks[kTiles];
 #pragma unroll
@@ -200,6 +258,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
           }
       }
       hand.es[lane] = es;
+      hand.first[lane] = gone ? 0 : lost;
+      gone |= lost < kChunk;
       if constexpr (HANDS == 1) lds_barrier();  // S is handed over
       // r, and u = T r
       f4_t v[kTiles], w[kTiles];
@@ -268,7 +328,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     }
     if (HANDS == 2 && r.c0 < end_block) lds_barrier();  // for the last outputs
 #pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -es);
+    for (int t = 0; t < KT; ++t) s[t] = gone ? f4_t{nan, nan, nan, nan} : scale4(s[t], -es);
     if (!r.last) {
       store_state<DK, 1>(carry, st);
       return;
@@ -293,7 +353,9 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       }
     };
     u4_t v[SLABS][Rows16<BF16>::kLoads];
+    u2_t of_block;  // tokens whose k, g or beta is not finite
     const auto load_next = [&](int c) {
+      of_block = *reinterpret_cast<const u2_t*>(reinterpret_cast<const float*>(heads_of(c) + Ops::kFactors) + 3 * kChunk + 2);
 #pragma unroll
       for (int u = 0; u < SLABS; ++u)
         load_values<BF16>(static_cast<const char*>(a.v) + ((first + c * kChunk) * a.v_stride + (int64_t)h * a.dv +
@@ -301,10 +363,20 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
                           a.v_stride * size, count - c * kChunk, v[u]);
     };
     const auto hand_next = [&](int c) {
+      const uint64_t lost = of_block.x | (uint64_t)of_block.y << 32;
+      uint32_t most = 0;
 #pragma unroll
-      for (int u = 0; u < SLABS; ++u)
+      for (int u = 0; u < SLABS; ++u) {
+        if (lane < 16) hand_of(c)[u].lost[lane] = lost ? __builtin_ctzll(lost) : kChunk;
 #pragma unroll
-        for (int i = 0; i < Rows16<BF16>::kLoads; ++i) *reinterpret_cast<u4_t*>(hand_of(c)[u].v.piece(i)) = v[u][i];
+        for (int i = 0; i < Rows16<BF16>::kLoads; ++i) {
+          *reinterpret_cast<u4_t*>(hand_of(c)[u].v.piece(i)) = v[u][i];
+          most = most_of<BF16>(most, v[u][i]);
+        }
+      }
+      if (__any(not_finite<BF16>(most)))
+#pragma unroll
+        for (int u = 0; u < SLABS; ++u) take_out<BF16>(hand_of(c)[u].v, hand_of(c)[u].lost);
     };
     if (r.c0 < end_block) {
       load_next(r.c0);
@@ -320,8 +392,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
       if constexpr (HANDS == 1) lds_barrier();  // S is handed over
       if (ahead) fetch_part(c + 1, 1);
       if constexpr (HANDS == 1) lds_barrier();  // u is handed over, the values have been read
-      if (more) hand_next(c + 1);
       if (ahead) fetch_part(c + 1, 2);
+      if (more) hand_next(c + 1);
       if constexpr (BUFFERS == 1) {
         lds_barrier();
         if (more)
@@ -407,7 +479,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         }
       }
     }
-    const int es = hand.es[lane];
+    const int es = hand.es[lane], none_from = hand.first[lane];
     if constexpr (ahead) {
       if (more) load_q(c + 1);
     } else {
@@ -440,6 +512,10 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) store1<BF16>(outs[slab].value(16 * t + 4 * g + e), 0, z[t][e]);
+    if (__any(none_from < kChunk))
+#pragma unroll 1
+      for (int i = g; i < kChunk; i += 4)
+        if (i >= none_from) store1<BF16>(outs[slab].value(i), 0, nan);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (lag && more) load_factors(c + 1);
     if constexpr (BUFFERS == 1) lds_barrier();

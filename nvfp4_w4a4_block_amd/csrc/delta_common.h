@@ -33,6 +33,12 @@ __device__ __forceinline__ void store1(void* out, int64_t at, float x) {
   else static_cast<float*>(out)[at] = x;
 }
 
+// The wave's own LDS stores before its loads: no other wave has part in them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ float sum_of_wave(float x) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);

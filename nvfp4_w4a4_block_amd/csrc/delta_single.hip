@@ -83,6 +83,9 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
       v[t][e] = 16 * t + 4 * g + e < n ? beta[e] * __builtin_fmaf(f[e], y[e], x) : 0.0f;
     }
   }
+  const uint64_t lost = lost_values<NT>(lost_tokens(sh), v);
+  const bool any_lost = __any(lost != 0);
+  const float nan = __builtin_nanf("");
   lower_product<NT>([&](int t) { return tile_rows(sh.a[t]); }, v, w);
   lower_product<NT>([&](int t) { return tile_rows(sh.p[t]); }, w, pu);
 #pragma unroll
@@ -93,8 +96,10 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
       const int i = 16 * t + 4 * g + e;
       if (i >= a.nodes) continue;
       const bool in = i < n;
-      if constexpr (TREE) a.updates[(first + i) * row + value_at] = in ? w[t][e] : 0.0f;
-      store1<BF16>(a.out, (first + i) * row + value_at, in ? __builtin_fmaf(fq[e], y[e], pu[t][e]) : 0.0f);
+      float u = w[t][e], o = __builtin_fmaf(fq[e], y[e], pu[t][e]);
+      if (any_lost && ((TREE ? sh.line[i] : up_to(i)) & lost)) u = o = nan;
+      if constexpr (TREE) a.updates[(first + i) * row + value_at] = in ? u : 0.0f;
+      store1<BF16>(a.out, (first + i) * row + value_at, in ? o : 0.0f);
     }
   }
   if constexpr (!TREE) {
@@ -128,6 +133,9 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
       }
 #pragma unroll
       for (int t = 0; t < KT; ++t) s[t] = scale4(s[t], -en);
+      if (any_lost && lost)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) s[t] = f4_t{nan, nan, nan, nan};
     }
     store_state<DK, 1>(a.states + (((int64_t)to * a.heads + h) * a.dv + col0) * DK, st);
   }

@@ -131,3 +131,120 @@ def test_several_sequences_of_many_heads(dtype, Dk, Dv):
     c = T.Delta(dtype, 3, 135, 8, 64, Dk, Dv, counts=[135, 64, 100], seed=Dk, decay=4.0)
     out, states = c.chain()
     c.check_chain(*some_heads(c, out, states, [0, 7, 33, 63]))
+
+
+# ----------------------------------------------------------------------------------------------- NaN and infinity
+
+
+def lines_of(parent):
+    seen = np.eye(len(parent), dtype=bool)
+    for v, p in enumerate(parent):
+        if 0 <= p < v:
+            seen[v] |= seen[p]
+    return seen
+
+
+def spoil(c, b, t, what, value):
+    """Puts value into one place of token t of sequence b: of head 1's (and key head 0's) of four heads."""
+    if what in ("k", "q", "v"):
+        getattr(c, what)[b, t, 0 if what != "v" else 1, 3] = value
+    else:
+        getattr(c, what)[b, t, 1] = value
+
+
+SPOILT = [("k", np.nan), ("k", np.inf), ("q", np.nan), ("v", np.nan), ("v", -np.inf), ("g", np.nan), ("g", np.inf),
+          ("beta", np.nan), ("beta", -np.inf)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("what,value", SPOILT)
+@pytest.mark.parametrize("M,Dk", [(7, 128), (16, 64), (33, 128), (64, 64), (50, 256)])
+def test_a_spoilt_node_reaches_what_sees_it(dtype, what, value, M, Dk):
+    """Other branches, and where a value is spoilt other columns, keep every bit; a path without the node commits."""
+    c = T.Delta(dtype, 2, M, 2, 4, Dk, 64, src=[0, 1], slots=2, seed=M)
+    parent = T.random_trees(np.random.default_rng(M), 2, M)
+    parent[:, 2] = 0
+    ref = [x.clone() for x in T.run_tree(c, parent)]
+    spoil(c, 0, 2, what, value)
+    out, keys, updates = T.run_tree(c, parent)
+    seen = lines_of(parent[0])[:, 2]
+    assert seen.any() and not seen.all()
+    heads = [0, 1] if what in ("k", "q") else [1]
+    hit = torch.zeros((2, M, 4, 64), dtype=torch.bool, device=T.DEV)
+    for h in heads:
+        rows = torch.from_numpy(np.flatnonzero(seen)).to(T.DEV)
+        if what == "q":
+            hit[0, 2, h] = True
+        elif what == "v":
+            hit[0, rows, h, 3] = True
+        else:
+            hit[0, rows, h] = True
+    bad = lambda x: ~x.float().isfinite()  # noqa: E731
+    assert torch.equal(bad(out), hit)
+    assert torch.equal(out[~hit], ref[0][~hit])
+    if what == "q":
+        hit = torch.zeros_like(hit)
+    assert torch.equal(bad(updates), hit) and torch.equal(updates[~hit], ref[2][~hit])
+    spoilt_keys = torch.zeros((2, M, 2), dtype=torch.bool, device=T.DEV)
+    spoilt_keys[0, 2, 0] = what == "k"
+    assert torch.equal(bad(keys).any(-1), spoilt_keys) and torch.equal(keys[~spoilt_keys], ref[1][~spoilt_keys])
+    # the longest path without the node, and one through it
+    g = torch.nan_to_num(T.floats(c.g), 0.0, 0.0) if what == "g" else T.floats(c.g)
+    for through in (False, True):
+        v = max(i for i in range(M) if seen[i] == through)
+        path = [i for i in range(1, M) if lines_of(parent[0])[v, i]]
+        result = T.ints([[v, len(path), 0] + path + [-1] * (M - len(path)), [0, 0, 0] + [-1] * M])
+        states = [T.floats(c.states)[None] for _ in range(2)]
+        for st, k, u in zip(states, (keys, ref[1]), (updates, ref[2])):
+            T.B.nvfp4_delta_commit(st, k[None], u[None], g[None], result, T.ints([0, 1]), T.ints([0, 1]))
+        gone = bad(states[0])
+        if through and what != "q":
+            assert gone[0, 0, heads].any(-1).any(-1).all() and not gone[0, 0, 2:].any() and not gone[0, 1].any()
+            assert what != "v" or torch.equal(gone[0, 0, 1].any(-1).nonzero()[:, 0].cpu(), torch.tensor([3]))
+        else:
+            assert torch.equal(states[0], states[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("what,value", SPOILT)
+@pytest.mark.parametrize("M,at", [(3, 1), (9, 4), (40, 17), (64, 63), (150, 20), (150, 64), (200, 149), (2200, 700)])
+def test_a_spoilt_token_reaches_what_follows(dtype, what, value, M, at):
+    c = T.Delta(dtype, 2, M, 2, 4, 64, 64, src=[0, 1], dst=[2, 3], slots=4, seed=M, decay=4.0)
+    ref, ref_states = (x.clone() for x in c.chain())
+    spoil(c, 0, at, what, value)
+    out, states = c.chain()
+    heads, columns = [0, 1] if what in ("k", "q") else [1], 3 if what == "v" else slice(None)
+    hit = torch.zeros((2, M, 4, 64), dtype=torch.bool, device=T.DEV)
+    for h in heads:
+        hit[0, at if what == "q" else slice(at, None), h, columns] = True
+    assert torch.equal(out[~hit], ref[~hit])
+    assert not out[hit].float().isfinite().any()
+    lost = torch.zeros((4, 4, 64), dtype=torch.bool, device=T.DEV)
+    for h in heads:
+        lost[2, h, columns] = what != "q"
+    assert torch.equal(states[~lost], ref_states[~lost])
+    assert not states[lost].isfinite().all(-1).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M", [2, 30, 64, 130])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_a_spoilt_row_of_a_state_stays_in_its_column(dtype, M, value):
+    c = T.Delta(dtype, 2, M, 1, 2, 128, 64, src=[0, 1], dst=[0, 1], slots=2, seed=M)
+    ref, ref_states = (x.clone() for x in c.chain())
+    c.states[0, 1, 7, 5] = value
+    out, states = c.chain()
+    hit = torch.zeros((2, M, 2, 64), dtype=torch.bool, device=T.DEV)
+    hit[0, :, 1, 7] = True
+    assert torch.equal(out[~hit], ref[~hit]) and not out[hit].float().isfinite().any()
+    assert not states[0, 1, 7].isfinite().all()
+    states[0, 1, 7] = ref_states[0, 1, 7]
+    assert torch.equal(states, ref_states)
+
+
+@pytest.mark.parametrize("M", [3, 20, 100])
+def test_a_spoilt_state_without_tokens_is_copied_as_it_is(M):
+    c = T.Delta(FP, 2, M, 1, 2, 64, 64, counts=[0, M], src=[0, 1], dst=[2, 3], slots=4, seed=M)
+    c.states[0, 1, 7, 5], c.states[0, 0, 3, 2] = np.nan, np.inf
+    _, states = c.chain()
+    assert np.array_equal(states[2].cpu().numpy(), c.states[0], equal_nan=True) and states[3].isfinite().all()
