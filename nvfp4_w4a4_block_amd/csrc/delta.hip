@@ -17,14 +17,29 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 8;  // tokens whose q and k stand in LDS
 
+__device__ __forceinline__ float sum_of_squares(f4_t x) {
+  return sum_of_wave(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]);
+}
+
 // One row of q or k (DK values) as used, by a whole wave: normalised, times scale.
 template <int DK, bool BF16>
 __device__ __forceinline__ void stage_row(const void* rows, int64_t at, float eps, float scale, float* to) {
   const int lane = threadIdx.x & 63;
   f4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
   if (lane < DK / 4) x = load4<BF16>(rows, at + 4 * lane);
-  if (eps >= 0.0f)
-    scale *= 1.0f / __builtin_sqrtf(sum_of_wave(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]) + eps);
+  if (eps >= 0.0f) {
+    float square = sum_of_squares(x) + eps;
+    if (!(square > 0x1p-100f && square < 0x1p126f)) {
+      // past what fp32's squares hold: of the row over a power of two.  Where eps, scaled
+      // alike, is past fp32 it is all
+      const int e = exponent_of(max_of_wave(max4(0.0f, x)));
+      const float small = __builtin_amdgcn_ldexpf(eps, -2 * e);
+      const bool all = small > 1e38f;
+      if (!all) x = scale4(x, -e);
+      square = all ? eps : sum_of_squares(x) + small;
+    }
+    scale *= 1.0f / __builtin_sqrtf(square);
+  }
   if (lane < DK / 4) *reinterpret_cast<f4_t*>(to + 4 * lane) = x * scale;
 }
 

@@ -49,16 +49,6 @@ namespace nvfp4 {
 
 typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ f4_t scale4(f4_t x, int e) {
-  return f4_t{__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e), __builtin_amdgcn_ldexpf(x[2], e),
-              __builtin_amdgcn_ldexpf(x[3], e)};
-}
-
-__device__ __forceinline__ float max4(float m, f4_t x) {
-  m = fmaxf(fmaxf(m, fabsf(x[0])), fabsf(x[1]));
-  return fmaxf(fmaxf(m, fabsf(x[2])), fabsf(x[3]));
-}
-
 // NaN stays.
 __device__ __forceinline__ float max4_nan(float m, f4_t x) {
   m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(x[0])), fabsf(x[1]));
@@ -73,11 +63,6 @@ __device__ __forceinline__ float max_of_groups(float x) {
   const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(p.x), __uint_as_float(p.y)));
   const pair_t q = __builtin_bit_cast(pair_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
   return fmaxf(__uint_as_float(q.x), __uint_as_float(q.y));
-}
-
-// floor(log2 x) of x > 0; 0 of 0.
-__device__ __forceinline__ int exponent_of(float x) {
-  return x > 0.0f ? (int)((__float_as_uint(x) >> 23) & 255) - 127 : 0;
 }
 
 __device__ __forceinline__ h4_t to_half(f4_t x) { return __builtin_convertvector(x, h4_t); }

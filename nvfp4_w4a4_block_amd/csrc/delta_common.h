@@ -39,6 +39,27 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+__device__ __forceinline__ f4_t scale4(f4_t x, int e) {
+  return f4_t{__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e), __builtin_amdgcn_ldexpf(x[2], e),
+              __builtin_amdgcn_ldexpf(x[3], e)};
+}
+
+__device__ __forceinline__ float max4(float m, f4_t x) {
+  m = fmaxf(fmaxf(m, fabsf(x[0])), fabsf(x[1]));
+  return fmaxf(fmaxf(m, fabsf(x[2])), fabsf(x[3]));
+}
+
+// floor(log2 x) of x > 0; 0 of 0.
+__device__ __forceinline__ int exponent_of(float x) {
+  return x > 0.0f ? (int)((__float_as_uint(x) >> 23) & 255) - 127 : 0;
+}
+
+__device__ __forceinline__ float max_of_wave(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+  return x;
+}
+
 __device__ __forceinline__ float sum_of_wave(float x) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);

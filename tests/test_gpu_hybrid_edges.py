@@ -248,3 +248,25 @@ def test_a_spoilt_state_without_tokens_is_copied_as_it_is(M):
     c.states[0, 1, 7, 5], c.states[0, 0, 3, 2] = np.nan, np.inf
     _, states = c.chain()
     assert np.array_equal(states[2].cpu().numpy(), c.states[0], equal_nan=True) and states[3].isfinite().all()
+
+
+# ----------------------------------------------------------------------------------------------- lengths of rows
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M", [1, 4, 5, 65])
+@pytest.mark.parametrize("power,eps", [(70, 1e-6), (110, 1e-6), (-70, 0.0), (-110, 0.0), (-70, 1e-30), (62, 0.0)])
+def test_rows_of_any_length_are_normalised(dtype, M, power, eps):
+    """Rows whose squares are past fp32's range, or below it, at every form's number of tokens."""
+    c = T.Delta(dtype, 1, M, 2, 4, 128, 64, seed=M)
+    for name in ("q", "k"):
+        x = getattr(c, name)
+        x.copy_((x.double() * 2.0 ** power).to(dtype))
+        if M > 2:  # rows of either size beside them
+            x[:, 1] = x[:, 1].double().mul(2.0 ** -power).to(dtype)
+        setattr(c, name + "f", x.float().cpu().numpy())
+    c.eps = eps
+    c.check_chain(*c.chain())
+    parent = np.arange(M, dtype=np.int32)[None] - 1
+    if M <= 64:
+        T.check_tree(c, parent, T.run_tree(c, parent))
