@@ -128,8 +128,8 @@ __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitAr
   else zero_state<DK, 1>(x);
   // lane i: node i of the path (the root first), its decay and what follows it
   const int32_t* res = a.result + (int64_t)b * (3 + a.nodes);
-  int n = res[1] + 1;
-  n = n < 1 ? 1 : n < a.nodes ? n : a.nodes;
+  int n = res[1];
+  n = 1 + (n < 0 ? 0 : n < a.nodes ? n : a.nodes - 1);
   int node = lane == 0 ? 0 : lane < n ? res[2 + lane] : -1;
   if (node >= a.nodes) node = -1;
   const int64_t first = ((int64_t)layer * a.seqs + b) * a.nodes;

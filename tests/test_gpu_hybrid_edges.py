@@ -270,3 +270,21 @@ def test_rows_of_any_length_are_normalised(dtype, M, power, eps):
     parent = np.arange(M, dtype=np.int32)[None] - 1
     if M <= 64:
         T.check_tree(c, parent, T.run_tree(c, parent))
+
+
+# ----------------------------------------------------------------------------------------------- commit
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 2, 7, 5, 0, -1, -2 ** 31])
+def test_a_commit_of_any_written_length(length):
+    """A length past the nodes counts as all of them, one below none as none, to the ends of its type."""
+    rng = np.random.default_rng(0)
+    f32 = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    states, keys, updates, g = f32(1, 2, 1, 64, 64), f32(1, 1, 6, 1, 64), f32(1, 1, 6, 1, 64), -np.abs(f32(1, 1, 6, 1))
+    got = []
+    for n in (length, max(0, min(5, length))):
+        st = T.floats(states)
+        T.B.nvfp4_delta_commit(st, T.floats(keys), T.floats(updates), T.floats(g), T.ints([[0, n, 0, 1, 2, 3, 4, 5, -1]]),
+                               T.ints([0]), T.ints([1]))
+        got.append(st)
+    assert torch.equal(*got)
