@@ -642,10 +642,21 @@ nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
  *            and nvfp4_tree_verify write them, as nvfp4_kv_compact takes them.  A
  *            path entry outside [0, M) is passed over.
  *   src, dst as above, the same slots in every layer.  The decays' sums are 64
- *            bits, the others fp32. */
+ *            bits, the others fp32.
+ * The g of node 0 and of the path's nodes is read.  Where some are no tokens (a
+ * tree with counts), nvfp4_delta_commit_counts is the call. */
 nvfp4_status nvfp4_delta_commit(int64_t L, int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv,
                                 int64_t S, float* states, const float* keys, const float* updates, const float* g,
                                 const int32_t* result, const int32_t* src, const int32_t* dst, void* stream);
+
+/* The same of trees with counts (int32 [B], device, or NULL), as given to
+ * nvfp4_delta_tree: nodes that are no tokens are passed over, node 0 too, and
+ * what g holds for them is not read.  A sequence with none copies its state. */
+nvfp4_status nvfp4_delta_commit_counts(int64_t L, int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk,
+                                       int64_t Dv, int64_t S, float* states, const float* keys,
+                                       const float* updates, const float* g, const int32_t* result,
+                                       const int32_t* src, const int32_t* dst, const int32_t* counts,
+                                       void* stream);
 
 /* Size in bytes of nvfp4_token_logprobs's workspace (0 for an invalid or empty
  * call). */

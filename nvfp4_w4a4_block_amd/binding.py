@@ -31,8 +31,9 @@ KERNEL_NAMES = {KERNEL_GEMV_FP4: "gemv_fp4_kernel", KERNEL_GEMV_FLAT: "gemv_flat
                 KERNEL_TILED_PERSISTENT: "gemm_wg_tiled_kernel", KERNEL_TILED: "gemm_tiled_kernel",
                 KERNEL_M16_STREAM: "gemm_m16_stream_kernel"}
 
-EXPORTS = ("nvfp4_abi_version", "nvfp4_act_global_scale", "nvfp4_delta_commit", "nvfp4_delta_rule",
-           "nvfp4_delta_rule_workspace_bytes", "nvfp4_delta_tree", "nvfp4_gemm", "nvfp4_gemm_dispatch", "nvfp4_gemm_ex",
+EXPORTS = ("nvfp4_abi_version", "nvfp4_act_global_scale", "nvfp4_delta_commit", "nvfp4_delta_commit_counts",
+           "nvfp4_delta_rule", "nvfp4_delta_rule_workspace_bytes", "nvfp4_delta_tree", "nvfp4_gemm",
+           "nvfp4_gemm_dispatch", "nvfp4_gemm_ex",
            "nvfp4_gemm_quantize_output", "nvfp4_gemm_scratch", "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_ws",
            "nvfp4_kv_append", "nvfp4_kv_append_rope", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_kv_compact",
            "nvfp4_kv_fork", "nvfp4_kv_fp8_decode", "nvfp4_kv_fp8_encode", "nvfp4_kv_resize",
@@ -94,11 +95,12 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_delta_rule.argtypes = [i64] * 7 + [p, p, p, i32, i64, i64, i64, p, p, f32, f32, p, p, p, p, p, p, i64, p]
     lib.nvfp4_delta_tree.argtypes = [i64] * 7 + [p, p, p, i32, i64, i64, i64, p, p, f32, f32, p, p, p, p, p, p, p, p]
     lib.nvfp4_delta_commit.argtypes = [i64] * 8 + [p] * 8
+    lib.nvfp4_delta_commit_counts.argtypes = [i64] * 8 + [p] * 9
     lib.nvfp4_token_logprobs_workspace_bytes.argtypes = [i64] * 3 + [i32]
     lib.nvfp4_token_logprobs_workspace_bytes.restype = i64
     lib.nvfp4_token_logprobs.argtypes = [i64] * 3 + [p, i32, i64, p, p, p, p, p, p, i64, p]
     for f in ("nvfp4_kv_append_rope", "nvfp4_delta_rule", "nvfp4_delta_tree", "nvfp4_delta_commit",
-              "nvfp4_token_logprobs", "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_compact", "nvfp4_kv_resize", "nvfp4_kv_fork",
+              "nvfp4_delta_commit_counts", "nvfp4_token_logprobs", "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_compact", "nvfp4_kv_resize", "nvfp4_kv_fork",
               "nvfp4_quantize_weights", "nvfp4_quantize_act", "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_gemm_ws",
               "nvfp4_gemm_scratch",
               "nvfp4_gemm_quantize_output",
@@ -913,11 +915,12 @@ def nvfp4_delta_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
 
 def nvfp4_delta_commit(states: torch.Tensor, keys: torch.Tensor, updates: torch.Tensor, g: torch.Tensor,
-                       result: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> None:
+                       result: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                       counts: Optional[torch.Tensor] = None) -> None:
     """Takes each sequence's state through the root and the accepted path of its tree, in all layers: states [L, S,
     H, Dv, Dk], slot src[b] to slot dst[b]; keys [L, B, M, Hk, Dk] and updates [L, B, M, H, Dv] as nvfp4_delta_tree
     gives them, g float32 [L, B, M, H] the layers' log decays, result int32 [B, 3 + M]: rows of nvfp4_tree_accept /
-    nvfp4_tree_verify."""
+    nvfp4_tree_verify.  counts int32 [B]: those of the tree; nodes that are no tokens change nothing."""
     on, slots, rows, paths = states.get_device(), states.shape, keys.shape, result.shape
     if on < 0 or states.dtype is not _F32 or len(slots) != 5 or not states.is_contiguous():
         raise ValueError("states must be a contiguous float32 [L, S, H, Dv, Dk] on a GPU")
@@ -931,8 +934,13 @@ def nvfp4_delta_commit(states: torch.Tensor, keys: torch.Tensor, updates: torch.
     _floats(on, (L, B, M, H, Dv), "updates", updates)
     _floats(on, (L, B, M, H), "g", g)
     _ints(on, "result, src and dst", result, src, dst)
-    _call(on, "nvfp4_delta_commit", load().nvfp4_delta_commit, L, B, M, Hk, H, Dk, Dv, S, states.data_ptr(),
-          keys.data_ptr(), updates.data_ptr(), g.data_ptr(), result.data_ptr(), src.data_ptr(), dst.data_ptr())
+    if counts is not None:
+        _ints(on, "counts", counts)
+        if counts.shape != (B,):
+            raise ValueError("counts must be [B]")
+    _call(on, "nvfp4_delta_commit", load().nvfp4_delta_commit_counts, L, B, M, Hk, H, Dk, Dv, S,
+          states.data_ptr(), keys.data_ptr(), updates.data_ptr(), g.data_ptr(), result.data_ptr(), src.data_ptr(),
+          dst.data_ptr(), counts.data_ptr() if counts is not None else None)
 
 
 def nvfp4_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,

@@ -227,12 +227,21 @@ nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
 nvfp4_status nvfp4_delta_commit(int64_t L, int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv,
                                 int64_t S, float* states, const float* keys, const float* updates, const float* g,
                                 const int32_t* result, const int32_t* src, const int32_t* dst, void* stream) {
+  return nvfp4_delta_commit_counts(L, B, M, Hk, H, Dk, Dv, S, states, keys, updates, g, result, src, dst, nullptr,
+                                   stream);
+}
+
+nvfp4_status nvfp4_delta_commit_counts(int64_t L, int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk,
+                                       int64_t Dv, int64_t S, float* states, const float* keys,
+                                       const float* updates, const float* g, const int32_t* result,
+                                       const int32_t* src, const int32_t* dst, const int32_t* counts,
+                                       void* stream) {
   if (!delta_shape_ok(B, M, Hk, H, Dk, Dv, S) || M < 1 || M > 64 || L < 0 || L > 4096)
     return NVFP4_ERR_SHAPE;
   if (L == 0 || B == 0) return NVFP4_OK;
   if (!states || !keys || !updates || !g || !result || !src || !dst) return NVFP4_ERR_NULL;
   if (!aligned(states, 16) || !aligned(keys, 16) || !aligned(updates, 16) || !aligned(g, 4) || !aligned(result, 4) ||
-      !aligned(src, 4) || !aligned(dst, 4))
+      !aligned(src, 4) || !aligned(dst, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;
   nvfp4::DeltaCommitArgs a;
   a.layers = (int)L;
@@ -250,6 +259,7 @@ nvfp4_status nvfp4_delta_commit(int64_t L, int64_t B, int64_t M, int64_t Hk, int
   a.result = result;
   a.src = src;
   a.dst = dst;
+  a.counts = counts;
   return from_hip(nvfp4::launch_delta_commit(a, static_cast<hipStream_t>(stream)));
 }
 

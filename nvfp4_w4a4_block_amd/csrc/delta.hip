@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * kWaves) void delta_commit_kernel(DeltaCommitAr
   int n = res[1];
   n = 1 + (n < 0 ? 0 : n < a.nodes ? n : a.nodes - 1);
   int node = lane == 0 ? 0 : lane < n ? res[2 + lane] : -1;
-  if (node >= a.nodes) node = -1;
+  if (node >= delta_count(a.counts, a.nodes, b)) node = -1;
   const int64_t first = ((int64_t)layer * a.seqs + b) * a.nodes;
   const double decay = node >= 0 ? (double)a.g[(first + node) * a.heads + h] : 0.0;
   double after = 0.0;  // sum of the decays behind this node

@@ -46,6 +46,7 @@ struct DeltaCommitArgs {
   float* states;                      // [layers][slots][heads][dv][dk]
   const float *keys, *updates, *g;    // [layers][seqs][nodes] rows
   const int32_t *result, *src, *dst;  // [seqs][3 + nodes], [seqs], [seqs]
+  const int32_t* counts;              // optional [seqs]
 };
 
 struct LogprobArgs {

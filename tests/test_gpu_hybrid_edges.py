@@ -288,3 +288,25 @@ def test_a_commit_of_any_written_length(length):
                                T.ints([0]), T.ints([1]))
         got.append(st)
     assert torch.equal(*got)
+def test_a_commit_of_padded_trees():
+    """Sequences without tokens, with some and with all; what stands in g behind them is not read."""
+    M = 12
+    c = T.Delta(FP, 4, M, 1, 2, 64, 64, counts=[0, 5, M, -3], src=[0, 1, 2, -1], dst=[4, 5, 6, 7], slots=9, seed=3)
+    parent = np.tile(np.arange(M, dtype=np.int32)[None] - 1, (4, 1))
+    for b, n in enumerate(c.counts):
+        c.g[b, max(0, n):] = np.nan
+    out, keys, updates = T.run_tree(c, parent)
+    path = list(range(1, M))
+    result = T.ints([[M - 1, M - 1, 0] + path + [-1]] * 4)
+    st = T.floats(c.states)
+    T.B.nvfp4_delta_commit(st[None], keys[None], updates[None], T.floats(c.g)[None], result, T.ints(c.src), T.ints(c.dst),
+                           counts=T.ints(c.counts))
+    assert torch.equal(st[4], T.floats(c.states)[0]) and not st[7].any()  # no tokens: the state is copied
+    after, off = c.chain_ref()[2:4]
+    err = np.sqrt(((st.double().cpu().numpy() - after) ** 2).sum(-1))
+    assert (err <= 8 * off + 100 * 2.0 ** -23 * np.sqrt((after ** 2).sum(-1))).all()
+    with pytest.raises(ValueError, match="counts"):
+        T.B.nvfp4_delta_commit(st[None], keys[None], updates[None], T.floats(c.g)[None], result, T.ints(c.src),
+                               T.ints(c.dst), counts=T.ints([1]))
+
+

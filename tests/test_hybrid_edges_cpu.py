@@ -41,3 +41,21 @@ def test_a_block_of_the_largest_shape_is_the_least(lib):
 @pytest.mark.parametrize("seqs", [2, 3, 7, 100])
 def test_sequences_whose_blocks_and_states_do_not_fit_come_in_turns(lib, seqs):
     assert 0 < lib.nvfp4_delta_rule_workspace_bytes(seqs, 430, 4, 1024, 64, 64, B.NVFP4_F32) <= 128 * MB
+
+
+# ----------------------------------------------------------------------------------------------- refusals
+
+A = 0x100000  # a fake, aligned address: never dereferenced by a rejected call
+
+
+def test_commit_with_counts_refuses_as_without(lib):
+    ok = dict(L=2, B=2, M=3, Hk=2, H=4, Dk=64, Dv=128, S=5, states=16 * A, keys=A, updates=2 * A, g=3 * A, result=4 * A,
+              src=4 * A, dst=4 * A, counts=4 * A, stream=None)
+    call = lambda **new: lib.nvfp4_delta_commit_counts(*{**ok, **new}.values())  # noqa: E731
+    for bad in (dict(M=0), dict(M=65), dict(L=-1), dict(Hk=3), dict(Dk=96), dict(S=0)):
+        assert call(**bad) == B.NVFP4_ERR_SHAPE
+    for name in ("states", "keys", "updates", "g", "result", "src", "dst"):
+        assert call(**{name: None}) == B.NVFP4_ERR_NULL
+        assert call(**{name: ok[name] + 1}) == B.NVFP4_ERR_ALIGN
+    assert call(counts=A + 1) == B.NVFP4_ERR_ALIGN
+    assert call(B=0) == call(L=0, counts=None) == B.NVFP4_OK
