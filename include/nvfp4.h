@@ -524,7 +524,7 @@ nvfp4_status nvfp4_kv_fork(int64_t n, int64_t S, int64_t W, int64_t P, int64_t p
  * keys with rotary positions, and gives the step's queries theirs.
  *   q        [B * M] rows of Hq * D values in dt, device (Hq >= 1); q_out out
  *            [B][M][Hq][D] in dt: q itself (contiguous rows: q_stride Hq * D)
- *            or no part of q, k or v.
+ *            or no part of q, and no part of the other arrays.
  *   R        the first R of a head's D values are rotated (a multiple of 16, 16
  *            .. D), the others pass.  Pair j < R / 2 is (x[j], x[j + R / 2]), or
  *            (x[2 j], x[2 j + 1]) with interleaved != 0.
@@ -579,7 +579,7 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
  *            turn's snapshot, to begin others from.
  *   counts   int32 [B], device, or NULL: only a sequence's first counts[b] rows
  *            are tokens (more than M counts as M; none: the state is copied).
- *   out      [B][M][H][Dv] in dt, no part of q, k, v or states.  Rows that are no
+ *   out      [B][M][H][Dv] in dt, no part of the other arrays.  Rows that are no
  *            tokens are zero, and what they hold in q, k, v, g and beta is not
  *            read.
  *   Shapes: Dk and Dv 64, 128 or 256; 1 <= H <= 1024, H a multiple of Hk; B and M
@@ -609,8 +609,9 @@ int64_t nvfp4_delta_rule_workspace_bytes(int64_t B, int64_t M, int64_t Hk, int64
 /* A chain of tokens: one (decoding), a suffix or a prompt.
  *   workspace  device memory, 16-byte aligned, of workspace_bytes bytes, or
  *            NULL; with less than nvfp4_delta_rule_workspace_bytes the tokens go
- *            one after the other (slower, same contract).  It needs no clearing.
- *            Calls that may overlap need one each. */
+ *            one after the other (slower, same contract).  It needs no clearing,
+ *            and is no part of the other arrays.  Calls that may overlap need one
+ *            each. */
 nvfp4_status nvfp4_delta_rule(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, int64_t S,
                               const void* q, const void* k, const void* v, nvfp4_dtype dt, int64_t q_stride,
                               int64_t k_stride, int64_t v_stride, const float* g, const float* beta, float scale,
@@ -635,8 +636,8 @@ nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
 /* Puts the accepted path of each sequence's tree into its states, in all L
  * layers: S = the state of src[b] taken through node 0 and the path's nodes, S <-
  * exp(g_p) S + u_p k_p^T, written to dst[b].
- *   states   fp32 [L][S][H][Dv][Dk]; keys, updates: [L][B][M] rows as
- *            nvfp4_delta_tree writes them; g fp32 [L][B][M][H], the layers' log
+ *   states   fp32 [L][S][H][Dv][Dk], no part of the other arrays; keys, updates:
+ *            [L][B][M] rows as nvfp4_delta_tree writes them; g fp32 [L][B][M][H], the layers' log
  *            decays.
  *   result   int32 [B][3 + M], device, 1 <= M <= 64: rows as nvfp4_tree_accept
  *            and nvfp4_tree_verify write them, as nvfp4_kv_compact takes them.  A
@@ -678,6 +679,7 @@ int64_t nvfp4_token_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t top, 
  *   workspace  device memory, 16-byte aligned, at least
  *            nvfp4_token_logprobs_workspace_bytes; it needs no clearing.  Calls
  *            that may overlap need one each.
+ * The outputs and the workspace share no bytes with the other arrays or each other.
  * A row that holds a NaN or +infinity, or nothing above -infinity, is no
  * distribution: its numbers are NaN and its top tokens -1.  Sums are fp32.
  *   Shapes: M at most 65535, 1 <= N < 2^24.

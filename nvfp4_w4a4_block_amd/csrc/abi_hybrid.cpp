@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "hybrid_launch.h"
 
 namespace {
@@ -33,11 +35,36 @@ bool stride_ok(int64_t stride, int64_t row, nvfp4_dtype dt) {
   return stride >= row && stride < kMaxInt && stride * size_of(dt) % 16 == 0;
 }
 
-// Whether rows (n of them, `row` values, `stride` apart) and out's bytes share any.
-bool overlap(const void* rows, int64_t n, int64_t row, int64_t stride, nvfp4_dtype dt, const void* out,
-             int64_t out_bytes) {
-  const uintptr_t r0 = (uintptr_t)rows, o0 = (uintptr_t)out;
-  return r0 < o0 + out_bytes && o0 < r0 + ((n - 1) * stride + row) * size_of(dt);
+// Bytes of an array; none of a NULL one.
+struct Span {
+  uintptr_t begin;
+  int64_t bytes;
+};
+
+Span span(const void* p, __int128 bytes) {
+  const __int128 most = (int64_t)1 << 62;  // past any address
+  return {(uintptr_t)p, p == nullptr || bytes <= 0 ? 0 : (int64_t)(bytes < most ? bytes : most)};
+}
+
+// n rows of `row` values, `stride` apart.
+Span rows_span(const void* p, int64_t n, int64_t row, int64_t stride, int64_t size) {
+  return span(p, n > 0 ? ((__int128)(n - 1) * stride + row) * size : 0);
+}
+
+bool apart(const Span& x, const Span& y) {
+  return x.bytes == 0 || y.bytes == 0 || x.begin + x.bytes <= y.begin || y.begin + y.bytes <= x.begin;
+}
+
+// Whether outputs share no bytes with each other or with what is read: several
+// workgroups read what one of them would write.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> read) {
+  for (const Span* x = outs.begin(); x != outs.end(); ++x) {
+    for (const Span* y = outs.begin(); y != x; ++y)
+      if (!apart(*x, *y)) return false;
+    for (const Span& y : read)
+      if (!apart(*x, y)) return false;
+  }
+  return true;
 }
 
 bool delta_shape_ok(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t Dk, int64_t Dv, int64_t S) {
@@ -59,17 +86,23 @@ nvfp4::DeltaArgs delta_of(int64_t B, int64_t M, int64_t Hk, int64_t H, int64_t D
   return a;
 }
 
-// Whether an output's bytes are some of q's, k's, v's or the states': several
-// workgroups read a row or state that one of them would write.
-bool shared(const nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* out, int64_t bytes) {
+// Whether the outputs of a chain or tree share no bytes with each other or with its rows,
+// states and numbers.
+bool delta_apart(const nvfp4::DeltaArgs& a, std::initializer_list<Span> outs) {
   const int64_t n = (int64_t)a.seqs * a.nodes, key_row = (int64_t)a.key_heads * a.dk, row = (int64_t)a.heads * a.dv;
-  return overlap(a.q, n, key_row, a.q_stride, dt, out, bytes) || overlap(a.k, n, key_row, a.k_stride, dt, out, bytes) ||
-         overlap(a.v, n, row, a.v_stride, dt, out, bytes) ||
-         overlap(a.states, a.slots, row * a.dk, row * a.dk, NVFP4_F32, out, bytes);
+  const int64_t size = a.bf16 ? 2 : 4;
+  return apart(outs, {rows_span(a.q, n, key_row, a.q_stride, size), rows_span(a.k, n, key_row, a.k_stride, size),
+                      rows_span(a.v, n, row, a.v_stride, size), span(a.g, 4 * n * a.heads), span(a.beta, 4 * n * a.heads),
+                      span(a.states, (__int128)4 * a.slots * row * a.dk), span(a.src, 4 * a.seqs),
+                      span(a.dst, 4 * a.seqs), span(a.parent, 4 * n), span(a.counts, 4 * a.seqs)});
+}
+
+Span delta_out(const nvfp4::DeltaArgs& a) {
+  return span(a.out, (__int128)a.seqs * a.nodes * a.heads * a.dv * (a.bf16 ? 2 : 4));
 }
 
 // The rows that a chain and a tree have in common; M == 0 needs none of them.
-nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, const void* k, const void* v,
+nvfp4_status delta_rows(nvfp4::DeltaArgs& a, const void* q, const void* k, const void* v,
                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* g, const float* beta,
                         float scale, float norm_eps, const float* states, const int32_t* src, const int32_t* counts,
                         void* out) {
@@ -92,7 +125,6 @@ nvfp4_status delta_rows(nvfp4::DeltaArgs& a, nvfp4_dtype dt, const void* q, cons
   a.src = src;
   a.counts = counts;
   a.out = out;
-  if (rows && shared(a, dt, out, (int64_t)a.seqs * a.nodes * a.heads * a.dv * size_of(dt))) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
@@ -129,10 +161,15 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
       !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;
   if (k_pages == v_pages) return NVFP4_ERR_SHAPE;  // two writers of a row
-  const int64_t n = B * M, bytes = n * Hq * D * size_of(dt);
+  const int64_t n = B * M, size = size_of(dt);
+  const Span out = span(q_out, n * Hq * D * size);
+  const int64_t page_bytes = (P - 1) * page_stride + H * page_size * D;
   const bool in_place = q_out == q && q_stride == Hq * D;  // each value is read and written by one thread
-  if ((!in_place && overlap(q, n, Hq * D, q_stride, dt, q_out, bytes)) ||
-      overlap(k, n, H * D, k_stride, dt, q_out, bytes) || overlap(v, n, H * D, v_stride, dt, q_out, bytes))
+  if (!apart({out}, {rows_span(in_place ? nullptr : q, n, Hq * D, q_stride, size),
+                     rows_span(k, n, H * D, k_stride, size), rows_span(v, n, H * D, v_stride, size),
+                     span(inv_freq, 4 * R), span(k_scale, 4), span(v_scale, 4), span(k_pages, page_bytes),
+                     span(v_pages, page_bytes), span(table, 4 * B * W), span(lens, 4 * B), span(parent, 4 * n),
+                     span(counts, 4 * B)}))
     return NVFP4_ERR_SHAPE;
   nvfp4::KvRopeArgs a = {};
   nvfp4::KvCache& c = a.append.c;
@@ -187,13 +224,15 @@ nvfp4_status nvfp4_delta_rule(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
   if (B == 0) return NVFP4_OK;
   if (!dst || (workspace_bytes > 0 && !workspace)) return NVFP4_ERR_NULL;
   nvfp4::DeltaArgs a = delta_of(B, M, Hk, H, Dk, Dv, S, dt);
-  const nvfp4_status st = delta_rows(a, dt, q, k, v, q_stride, k_stride, v_stride, g, beta, scale, norm_eps, states,
+  const nvfp4_status st = delta_rows(a, q, k, v, q_stride, k_stride, v_stride, g, beta, scale, norm_eps, states,
                                      src, counts, out);
   if (st != NVFP4_OK) return st;
   if (!aligned(dst, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
   a.dst = dst;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
+  if (!delta_apart(a, {delta_out(a), span(workspace, workspace_bytes)}))
+    return NVFP4_ERR_SHAPE;
   return from_hip(nvfp4::launch_delta_rule(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -209,18 +248,16 @@ nvfp4_status nvfp4_delta_tree(int64_t B, int64_t M, int64_t Hk, int64_t H, int64
   if (B == 0 || M == 0) return NVFP4_OK;
   if (!parent || !keys || !updates) return NVFP4_ERR_NULL;
   nvfp4::DeltaArgs a = delta_of(B, M, Hk, H, Dk, Dv, S, dt);
-  const nvfp4_status st = delta_rows(a, dt, q, k, v, q_stride, k_stride, v_stride, g, beta, scale, norm_eps, states,
+  const nvfp4_status st = delta_rows(a, q, k, v, q_stride, k_stride, v_stride, g, beta, scale, norm_eps, states,
                                      src, counts, out);
   if (st != NVFP4_OK) return st;
   if (!aligned(parent, 4) || !aligned(keys, 16) || !aligned(updates, 16)) return NVFP4_ERR_ALIGN;
-  const int64_t n = B * M, key_bytes = n * Hk * Dk * 4, update_bytes = n * H * Dv * 4;
-  if (shared(a, dt, keys, key_bytes) || shared(a, dt, updates, update_bytes) ||
-      overlap(out, n, H * Dv, H * Dv, dt, keys, key_bytes) || overlap(out, n, H * Dv, H * Dv, dt, updates, update_bytes) ||
-      overlap(keys, n, Hk * Dk, Hk * Dk, NVFP4_F32, updates, update_bytes))
-    return NVFP4_ERR_SHAPE;
   a.parent = parent;
   a.keys = keys;
   a.updates = updates;
+  const int64_t n = B * M;
+  if (!delta_apart(a, {delta_out(a), span(keys, 4 * n * Hk * Dk), span(updates, 4 * n * H * Dv)}))
+    return NVFP4_ERR_SHAPE;
   return from_hip(nvfp4::launch_delta_tree(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -243,6 +280,11 @@ nvfp4_status nvfp4_delta_commit_counts(int64_t L, int64_t B, int64_t M, int64_t 
   if (!aligned(states, 16) || !aligned(keys, 16) || !aligned(updates, 16) || !aligned(g, 4) || !aligned(result, 4) ||
       !aligned(src, 4) || !aligned(dst, 4) || !aligned(counts, 4))
     return NVFP4_ERR_ALIGN;
+  const __int128 n = (__int128)L * B * M;
+  if (!apart({span(states, (__int128)4 * L * S * H * Dv * Dk)},
+             {span(keys, 4 * n * Hk * Dk), span(updates, 4 * n * H * Dv), span(g, 4 * n * H),
+              span(result, 4 * B * (3 + M)), span(src, 4 * B), span(dst, 4 * B), span(counts, 4 * B)}))
+    return NVFP4_ERR_SHAPE;
   nvfp4::DeltaCommitArgs a;
   a.layers = (int)L;
   a.seqs = (int)B;
@@ -287,6 +329,10 @@ nvfp4_status nvfp4_token_logprobs(int64_t M, int64_t N, int64_t top, const void*
   if (!aligned(logits, size_of(dt)) || !aligned(workspace, 16) || !aligned(tokens, 4) || !aligned(logprobs, 4) ||
       !aligned(entropy, 4) || !aligned(top_logprobs, 4) || !aligned(top_tokens, 4))
     return NVFP4_ERR_ALIGN;
+  if (!apart({span(logprobs, 4 * M), span(entropy, 4 * M), span(top > 0 ? top_logprobs : nullptr, 4 * M * top),
+              span(top > 0 ? top_tokens : nullptr, 4 * M * top), span(workspace, workspace_bytes)},
+             {rows_span(logits, M, N, stride, size_of(dt)), span(tokens, 4 * M)}))
+    return NVFP4_ERR_SHAPE;
   nvfp4::LogprobArgs a = {};
   a.rows = (int)M;
   a.vocab = (int)N;
