@@ -310,3 +310,96 @@ def test_a_commit_of_padded_trees():
                                T.ints(c.dst), counts=T.ints([1]))
 
 
+
+
+# ----------------------------------------------------------------------------------------------- log probabilities
+
+
+def exact_row(z, token, top):
+    """As oracle/logprobs.py, with the bounds of an fp32 implementation: every e^(z - m) is off by 2^-22 and by 2^-23
+    |z - m| (the difference and its product with log2 e are rounded), and passes through at most 64 + N / 8192 roundings
+    of sums (16 of a lane's batch, its batches, 9 of lanes and waves, the parts)."""
+    lp, ent, best, ids = T.LP.row(z, token, top)
+    m = z.max()
+    d = z - m
+    p = np.exp(d)
+    w = p.sum()
+    sums = (64 + len(z) / 8192) * 2.0 ** -24
+    off = np.abs(np.where(p > 0, d, 0))
+    rel = 2.0 ** -22 + 2.0 ** -23 * (p * off).sum() / w + sums
+    # the largest's own 1 is exact
+    small, l = 1 - 1 / w, np.log(w)
+    t = (p * off).sum() / w
+    t_off = (p * off * (2.0 ** -22 + 2.0 ** -23 * off + 2.0 ** -23)).sum() / w + t * (sums + rel)
+    last = lambda y: 2.0 ** -23 * (abs(y + l) + 2 * l + abs(y))  # noqa: E731
+    tol = lambda y: rel * small + last(y) + 1e-37 if np.isfinite(y) else 0.0  # noqa: E731
+    return (lp, tol(lp)), (ent, rel * small + t_off + 2.0 ** -22 * (l + t) + 1e-37), (best, [tol(y) for y in best]), ids
+
+
+def check_rows(t, tokens, top, got, rows):
+    lp, ent, best, ids = got
+    for i in rows:
+        a, e, b, o = exact_row(t[i].double().cpu().numpy(), int(tokens[i]), top)
+        assert np.array_equal(ids[i].cpu().numpy(), o), (i, ids[i].tolist(), o)
+        assert abs(lp[i].item() - a[0]) <= a[1], (i, "logprob", lp[i].item(), a)
+        assert abs(ent[i].item() - e[0]) <= e[1], (i, "entropy", ent[i].item(), e)
+        assert (np.abs(best[i].double().cpu().numpy() - b[0]) <= b[1]).all(), (i, "top")
+
+
+def some_logits(dtype, M, N, seed):
+    """Rows as a model gives them, and in every eighth one maxima that rise or fall with every batch, come first or
+    last, or stand in the middle."""
+    g = torch.Generator(device=T.DEV).manual_seed(seed)
+    t = torch.empty((M, N), dtype=dtype, device=T.DEV)
+    for part in t.split(32):
+        part.copy_(torch.randn(part.shape, generator=g, device=T.DEV) * 2)
+    line = torch.linspace(-9, 9, N, device=T.DEV)
+    for i, row in enumerate(t):
+        if i % 8 == 1:
+            row.copy_(line)
+        elif i % 8 == 2:
+            row.copy_(-line)
+        elif i % 8 in (3, 4, 5):
+            row[{3: 0, 4: N - 1, 5: N // 2}[i % 8]] = 15.0
+    return t
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,N,top", [(600, 20000, 7), (512, 151936, 5), (512, 151936, 0), (520, 151935, 64),
+                                     (64, 151936, 20), (16, 151936, 64), (2, 300000, 33), (600, 300000, 5),
+                                     (1, 600000, 64), (3, 1000003, 10), (300, 50257, 1)])
+def test_logprobs_of_rows_of_many_batches(dtype, M, N, top):
+    """One part a row, several, more than 64, and more blocks than LDS has room for."""
+    t = some_logits(dtype, M, N, N)
+    tokens = torch.randint(0, N, (M,), device=T.DEV, dtype=torch.int32)
+    got = T.B.nvfp4_token_logprobs(t, tokens, top)
+    rows = sorted({i for i in list(range(8)) + [M // 2, M - 1] if i < M})
+    check_rows(t, tokens, top, got, rows)
+    if top:  # the others: their first one, and a sum of p that is 1
+        z = t.float()
+        assert torch.equal(z.gather(1, got[3][:, :1].long())[:, 0], z.max(1).values)
+        assert (got[0] <= got[2][:, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,N", [(1, 50257), (600, 50257), (1, 151935), (3, 151936), (520, 151937), (2, 600001)])
+def test_logprobs_count_every_column_once(dtype, M, N):
+    """Equal logits: whole numbers are summed, exactly, and a column more or less is 1 / N of the sum."""
+    t = torch.full((M, N), -3.25, dtype=dtype, device=T.DEV)
+    lp, ent, best, ids = T.B.nvfp4_token_logprobs(t, torch.full((M,), N - 1, device=T.DEV, dtype=torch.int32), 3)
+    want = -np.log(N)  # of log1p: 2^-23 of it, and rounded once more (up to 160,000 columns that tells half of one)
+    assert np.abs(lp.double().cpu().numpy() - want).max() <= 2.0 ** -22 * -want
+    assert np.abs(ent.double().cpu().numpy() + want).max() <= 2.0 ** -22 * -want
+    assert (ids == torch.arange(3, device=T.DEV)).all() and torch.equal(best, lp[:, None].expand(-1, 3))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,N", [(4, 700), (4, 20000), (600, 20000), (2, 300000)])
+def test_logprobs_order_zeros_across_blocks(dtype, M, N):
+    """+0.0 in some blocks of a row of -0.0, first, last and in the middle of a block."""
+    t = torch.full((M, N), -0.0, dtype=dtype, device=T.DEV)
+    at = [N - 1, N // 2, 64 * 5, 64 * 5 + 31, 64 * 7 - 1, 1]
+    t[:, at] = 0.0
+    _, _, _, ids = T.B.nvfp4_token_logprobs(t, torch.zeros((M,), device=T.DEV, dtype=torch.int32), 8)
+    want = sorted(set(at)) + [c for c in range(N) if c not in at][: 8 - len(set(at))]
+    assert ids.tolist() == [want] * M
