@@ -277,7 +277,10 @@ __device__ __forceinline__ void add_batch(const float (&z)[kBatch], float top, S
 constexpr int kBlock = 64;         // columns that share a maximum
 constexpr int kLocalBlocks = 4096;  // blocks of a row whose maxima stay in LDS
 
-// Largest numbers of the blocks of a wave's batch, from `blocks` on.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
+// Largest numbers of the blocks of a wave's batch, from `blocks` on.  +0.0 is above -0.0,
+// as it is in the keys (fmaxf leaves that open); a NaN stays, and its row has no results.
 template <bool BF16>
 __device__ __forceinline__ void store_maxima(const float (&z)[kBatch], uint32_t* blocks) {
   constexpr int per = BF16 ? 8 : 4, lanes = kBlock / per;
@@ -286,11 +289,11 @@ __device__ __forceinline__ void store_maxima(const float (&z)[kBatch], uint32_t*
   for (int i = 0; i < kBatch / per; ++i) {
     float m = z[i * per];
 #pragma unroll
-    for (int e = 1; e < per; ++e) m = fmaxf(m, z[i * per + e]);
-    m = fmaxf(m, dpp_float<kXor1>(m));
-    m = fmaxf(m, dpp_float<kXor2>(m));
-    m = fmaxf(m, dpp_float<kXor7>(m));
-    if constexpr (!BF16) m = fmaxf(m, dpp_float<kXor8>(m));  // of either half's eight alike
+    for (int e = 1; e < per; ++e) m = larger(m, z[i * per + e]);
+    m = larger(m, dpp_float<kXor1>(m));
+    m = larger(m, dpp_float<kXor2>(m));
+    m = larger(m, dpp_float<kXor7>(m));
+    if constexpr (!BF16) m = larger(m, dpp_float<kXor8>(m));  // of either half's eight alike
     if ((lane & (lanes - 1)) == 0) blocks[i * (64 / lanes) + lane / lanes] = ordered(m);
   }
 }
