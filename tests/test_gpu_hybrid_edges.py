@@ -403,3 +403,115 @@ def test_logprobs_order_zeros_across_blocks(dtype, M, N):
     _, _, _, ids = T.B.nvfp4_token_logprobs(t, torch.zeros((M,), device=T.DEV, dtype=torch.int32), 8)
     want = sorted(set(at)) + [c for c in range(N) if c not in at][: 8 - len(set(at))]
     assert ids.tolist() == [want] * M
+
+
+# ----------------------------------------------------------------------------------------------- rotary append
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("start", [0, 60000, 1 << 20, (1 << 24) + 1, (1 << 27) - 40, (1 << 29) + 3])
+def test_turns_are_those_of_64_bits(dtype, interleaved, start):
+    """The angle is off by 2^-51 of the position (three roundings here and one in the oracle, each 2^-53 of it), sine
+    and cosine by 2e-11 together with that of the oracle: a query is off by its roundings to fp32 and to its type and
+    that much of its pair's size, and a key's code is the nearest but within that of the middle of two."""
+    n = 120
+    c = T.Rope(dtype, [start], n, 2, 3, 128, 128, 1024, interleaved=interleaved, scale=1.25, seed=9)
+    q, pages = c.gpu()
+    positions = start + np.arange(n)
+    angle = 4e-11 + positions[:, None, None] * 2.0 ** -51
+    ref, size = T.RP.rotate(c.qf[0].astype(np.float64), positions, c.inv, c.scale, interleaved)
+    half = 2.0 ** -24 + (2.0 ** -8 if dtype == BF else 0.0)
+    err = np.abs(q[0].double().cpu().numpy() - ref)
+    assert (err <= half * np.abs(ref) + 1.01 * angle * size + 1e-44).all(), (err / (half * np.abs(ref) + angle * size)).max()
+    inv = float(np.float32(1) / T.KS)
+    ref, size = T.RP.rotate(c.kf[0].astype(np.float64), positions, c.inv, c.scale, interleaved)
+    grid = T.KV.decode_f32(np.arange(127, dtype=np.uint8), np.float32(1.0)).astype(np.float64)
+    grid = np.concatenate([-grid[:0:-1], grid])
+    mid = (grid[1:] + grid[:-1]) / 2
+    near = angle * size * inv + 2.0 ** -52 * np.abs(ref) * inv
+    low, high = (grid[np.searchsorted(mid, ref * inv + s * near)] for s in (-1, 1))
+    k = pages[0].cpu().numpy()
+    for t in range(n):
+        page, at = T.KC._slot(k, c.table, 0, start + t)
+        got = T.KV.decode_f32(k[page, :, at], np.float32(1.0)).astype(np.float64)
+        assert ((got == low[t]) | (got == high[t])).all(), t
+
+
+# ----------------------------------------------------------------------------------------------- graphs
+
+
+def every_call():
+    """One call of each operator and form: (run, what it writes or NULL where it allocates that, how many of these count:
+    a workspace behind them does not)."""
+    made = []
+    for dtype, nb, M, shape in ((BF, 2, 1, (2, 4, 128, 128)), (FP, 1, 9, (1, 2, 64, 64)), (BF, 1, 150, (1, 2, 128, 128)),
+                                (FP, 2, 70, (1, 2, 64, 64)), (BF, 3, 70, (8, 48, 128, 128))):
+        c = T.Delta(dtype, nb, M, *shape, seed=M)
+        rows, kw = c.common()
+        st, s, d = T.floats(c.states), T.ints(c.src), T.ints(c.dst)
+        out = torch.empty_like(rows[2])
+        need = T.B.load().nvfp4_delta_rule_workspace_bytes(nb, M, *shape, T.B.NVFP4_BF16 if dtype == BF else T.B.NVFP4_F32)
+        ws = torch.empty((need,), dtype=torch.uint8, device=T.DEV) if need else None
+        made.append((lambda rows=rows, st=st, s=s, d=d, out=out, ws=ws, kw=kw: T.B.nvfp4_delta_rule(
+            *rows, st, s, d, out=out, workspace=ws, **kw), [out, st] + ([ws] if need else []), 2))
+    c = T.Delta(FP, 2, 23, 1, 2, 64, 64, counts=[23, 0], seed=2)
+    rows, kw = c.common()
+    parent = T.ints(T.random_trees(np.random.default_rng(0), 2, 23))
+    st, s, d = T.floats(c.states), T.ints(c.src), T.ints(c.dst)
+    out, keys, updates = torch.empty_like(rows[2]), torch.empty((2, 23, 1, 64), device=T.DEV), torch.empty((2, 23, 2, 64), device=T.DEV)
+    made.append((lambda: T.B.nvfp4_delta_tree(*rows, st, s, parent, out=out, keys=keys, updates=updates, **kw),
+                 [out, keys, updates], 3))
+    k2, u2 = torch.randn((1, 2, 23, 1, 64), device=T.DEV), torch.randn((1, 2, 23, 2, 64), device=T.DEV)
+    cst, g, counts = T.floats(c.states)[None], T.floats(c.g)[None], T.ints([23, 0])
+    result = T.ints([[0, 2, 0, 1, 4] + [-1] * 21, [0, 0, 0] + [-1] * 23])
+    made.append((lambda: T.B.nvfp4_delta_commit(cst, k2, u2, g, result, s, d, counts=counts), [cst], 1))
+    r = T.Rope(BF, [40, 7], 16, 4, 2, 128, 64, 16, tree=True)
+    pages = [torch.from_numpy(x.copy()).to(T.DEV) for x in r.start]
+    inv, ks, vs, tab, lens, par = (torch.from_numpy(r.inv).to(T.DEV), U.scalar(T.KS), U.scalar(T.VS), T.ints(r.table),
+                                   T.ints(r.lens), T.ints(r.parent))
+    q_out = torch.empty_like(r.q)
+    made.append((lambda: T.B.nvfp4_kv_append_rope(r.q, r.k, r.v, inv, ks, vs, *pages, tab, lens, parent=par, q_out=q_out),
+                 [q_out] + pages, 3))
+    for M, N in ((16, 9001), (600, 3000)):
+        z, tokens = T.typed(np.random.default_rng(3).standard_normal((M, N)) * 3, FP)[0], T.ints(np.arange(M))
+        made.append((lambda z=z, tokens=tokens: T.B.nvfp4_token_logprobs(z, tokens, 20), None, 4))
+    return made
+
+
+def test_replays_write_every_output_anew():
+    """Before each replay everything that a call writes holds what it starts from, or nothing of use."""
+    runs = every_call()
+    def begin(seed):
+        g = torch.Generator(device=T.DEV).manual_seed(seed)
+        for _, bufs, _ in runs:
+            for x in bufs or []:
+                if x.dtype is torch.uint8:
+                    x.copy_(torch.randint(0, 256, x.shape, generator=g, device=T.DEV, dtype=torch.uint8))
+                else:
+                    x.copy_(torch.randn(x.shape, generator=g, device=T.DEV))
+
+    def results(outs):
+        return [[x.clone() for x in (bufs or out)[:n]] for (_, bufs, n), out in zip(runs, outs)]
+
+    begin(0)
+    for run, _, _ in runs:
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [run() for run, _, _ in runs]
+    for seed in (1, 2, 1):
+        begin(seed)
+        want = results([run() for run, _, _ in runs])
+        begin(seed)
+        for (_, bufs, _), out in zip(runs, held):
+            if bufs is None:
+                for x in out:
+                    x.fill_(-7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (got, ref) in enumerate(zip(results(held), want)):
+            for x, y in zip(got, ref):
+                assert torch.equal(x, y), (seed, i)
