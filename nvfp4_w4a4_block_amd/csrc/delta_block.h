@@ -44,6 +44,7 @@
 #pragma once
 
 #include "delta_common.h"
+#include "kv_tree.h"
 
 namespace nvfp4 {
 
@@ -484,22 +485,10 @@ __device__ __forceinline__ void prepare_block(const DeltaArgs& a, const BlockRow
     const float gl = lane >= n || lost ? 0.0f : rows.g < -1e4f ? -1e4f : rows.g;
     double sum = (double)gl * 1.4426950408889634074;  // exponents of 2
     if constexpr (TREE) {
-      const int par = lane < n ? rows.parent : -1;
-      uint64_t mask = 1ull << lane;
-      int up = par >= 0 && par < lane ? par : -1;
-#pragma unroll
-      for (int s = 0; s < 6; ++s) {  // pointers doubled
-        const int at = up < 0 ? lane : up;
-        const uint64_t m = __shfl(mask, at);
+      sh.line[lane] = ancestors_of_wave(lane < n ? rows.parent : -1, [&](int at, bool on) {
         const double d = __shfl(sum, at);
-        const int u = __shfl(up, at);
-        if (up >= 0) {
-          mask |= m;
-          sum += d;
-          up = u;
-        }
-      }
-      sh.line[lane] = mask;
+        sum += on ? d : 0.0;
+      });
     } else {
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
