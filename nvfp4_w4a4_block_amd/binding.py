@@ -759,8 +759,10 @@ def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none", 
     that the slowest pair alone is stretched in full); "yarn" (pairs that turn more than `fast` times within the
     trained length stay, those that turn less than `slow` times are stretched in full, the others by a part
     between; rotated values times 0.1 ln factor + 1)."""
-    if rotary < 16 or rotary % 16 or base <= 1.0 or factor < 1.0 or trained < 1 or not fast > slow > 0.0:
-        raise ValueError("rotary must be a multiple of 16, base above 1, factor at least 1, fast above slow above 0")
+    if rotary < 16 or rotary % 16 or not 1.0 < base < math.inf or not 1.0 <= factor < math.inf or \
+            not 1 <= trained < math.inf or not math.inf > fast > slow > 0.0:
+        raise ValueError("rotary must be a multiple of 16, base above 1, factor at least 1, fast above slow above 0, "
+                         "all finite")
     if scaling == "ntk":
         base *= factor ** (rotary / (rotary - 2))
     elif scaling not in ("none", "linear", "yarn"):

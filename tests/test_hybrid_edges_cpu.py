@@ -117,3 +117,12 @@ def test_states_of_the_largest_counts_are_compared_as_they_are(lib):
     """Their bytes do not fit 64 bits: an array behind them shares theirs."""
     many = dict(L=4096, H=1024, Hk=1, Dk=256, Dv=256, S=(1 << 31) - 1, B=1, M=1)
     assert lib.nvfp4_delta_commit_counts(*{**COMMIT, **many}.values()) == B.NVFP4_ERR_SHAPE
+
+
+@pytest.mark.parametrize("bad", [dict(base=x) for x in (float("nan"), float("inf"))] +
+                         [dict(factor=x, scaling=s) for x in (float("nan"), float("inf")) for s in ("linear", "ntk", "yarn")] +
+                         [dict(trained=float("nan"), scaling="yarn"), dict(trained=float("inf"), scaling="yarn"),
+                          dict(fast=float("inf"), scaling="yarn"), dict(slow=float("nan"), scaling="yarn")])
+def test_frequencies_of_numbers_that_are_not_finite(bad):
+    with pytest.raises(ValueError):
+        B.rope_frequencies(32, **bad)
