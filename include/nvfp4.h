@@ -590,8 +590,7 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
  * tokens' (16 bits of it in what reaches out alone, in bf16 calls of more than 64
  * tokens).  In products over a row's Dk values, and where a token's change is added to a
  * state, factors are split into f16 parts that keep 22 bits relative to their row's or
- * column's largest value; in bf16 calls those that reach nothing but out are rounded to
- * f16 (11 bits).
+ * column's largest value.
  * What is not finite reaches what sees it and nothing else: a token's k, g (-infinity is
  * a decay like others) or beta its own outputs and updates, those of the tokens behind
  * it or its descendants, and the new state; its v the one of Dv columns of all these; its

@@ -32,8 +32,7 @@
 // part.  f16's least step is 2^-24: rows of k and q are scaled by a power of two to a
 // largest value of 1 to 2, and a column of S, with what is added to it, by one to 32
 // to 64, so that 64 products fit; values are off by 2^-25 of the one, by 2^-30 of the
-// other, at least.  In bf16 calls S and Q in Q S, which reaches out alone, are rounded to
-// f16, an eighth of out's own step.
+// other, at least.
 //
 // NaN and infinities.  A product of a whole tile adds 0 times what a row does not see.  So
 // a token whose k, g or beta is not finite takes part with zeros, a column's values that

@@ -136,10 +136,10 @@ constexpr int kUnitsHere = BlockOps<DK, BF16, kTiles, SLABS == 4>::kQuery +
 // state is not) and what follows it are NaN there; the products go on without it.
 template <int DK, bool BF16>
 struct Handed {
-  h8_t s[BF16 ? 1 : 2][DK / 32][64];  // S as an operand
+  h8_t s[2][DK / 32][64];             // S as an operand
   f4_t w[kTiles][64];                 // u
-  int es[64];                         // S's exponent
-  int first[64];                      // first token of which nothing is left, 64: none
+  int es[16];                         // S's exponent, by column
+  int first[16];                      // first token of which nothing is left, 64: none
   Rows16<BF16> v;                     // the other way: the block's values,
   int lost[16];                       // and a column's first token that is not finite
 };
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         h8_t hi, lo;
         operand_parts(s[2 * x], s[2 * x + 1], hi, lo);
         hand.s[0][x][lane] = hi;
-        if constexpr (P == 2) hand.s[1][x][lane] = lo;
+        hand.s[1][x][lane] = lo;
 #pragma unroll
         for (int part = 0; part < P + 1; ++part)
 #pragma unroll
@@ -257,8 +257,8 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
             ks[t] = mfma16x16x32(key[part == 2 ? at + Ops::kRows : at], part == 1 ? lo : hi, ks[t]);
           }
       }
-      hand.es[lane] = es;
-      hand.first[lane] = gone ? 0 : lost;
+      hand.es[j] = es;
+      hand.first[j] = gone ? 0 : lost;
       gone |= lost < kChunk;
       if constexpr (HANDS == 1) lds_barrier();  // S is handed over
       // r, and u = T r
@@ -472,14 +472,14 @@ __global__ __launch_bounds__(64 * (2 * SLABS + 1), 1) void delta_scan_kernel(Del
         const h8_t* in_place = keys_of(c) + Ops::kQuery + (t * Ops::kSteps + x) * 64 + lane;
         const h8_t q0 = hold ? q[0][t][hold ? x : 0] : in_place[0];
         y[t] = mfma16x16x32(q0, hi, y[t]);
+        y[t] = mfma16x16x32(q0, hand.s[1][x][lane], y[t]);
         if constexpr (P == 2) {
           const h8_t q1 = hold ? q[1][t][hold ? x : 0] : in_place[Ops::kRows];
-          y[t] = mfma16x16x32(q0, hand.s[1][x][lane], y[t]);
           y[t] = mfma16x16x32(q1, hi, y[t]);
         }
       }
     }
-    const int es = hand.es[lane], none_from = hand.first[lane];
+    const int es = hand.es[j], none_from = hand.first[j];
     if constexpr (ahead) {
       if (more) load_q(c + 1);
     } else {

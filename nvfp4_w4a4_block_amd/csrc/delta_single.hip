@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void delta_block_kernel(DeltaArgs a) {
       for (int t = 0; t < NT; ++t) {
         const int at = (part == 2 ? Ops::kRows : 0) + (t * Ops::kSteps + x) * 64 + lane;
         ks[t] = mfma16x16x32(sh.key[at], part == 1 ? lo : hi, ks[t]);
-        if (P == 2 || part == 0) qs[t] = mfma16x16x32(sh.query[at], part == 1 ? lo : hi, qs[t]);
+        qs[t] = mfma16x16x32(sh.query[at], part == 1 ? lo : hi, qs[t]);
       }
   }
   const auto factor = [&](const float* of, int t) { return *reinterpret_cast<const f4_t*>(of + 16 * t + 4 * g); };
