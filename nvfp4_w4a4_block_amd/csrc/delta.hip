@@ -190,9 +190,10 @@ void commit(const DeltaCommitArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Up to four tokens go one after the other, up to 64 as one block, more block by
-// block.  Steps and one block, us, 16 key and 48 value heads of 128, bf16: 4 tokens of
-// one sequence 8.5 and 9.0, of 8 sequences 16.9 and 16.5, of 64 99.5 and 97; 16 tokens
-// of one sequence 19.9 and 9.1, of 64 208 and 103.
+// block.  us a call in steps and as one block, 16 key and 48 value heads of 128, of 1, 8
+// and 64 sequences: 4 bf16 tokens 10.3, 16.1, 101 and 10.3, 15.4, 93, 4 fp32 ones 10.4,
+// 16.2, 107 and 10.4, 20.8, 122; 2 bf16 ones 10.6, 13.5, 86 and 10.5, 15.0, 91; 16 bf16
+// ones 19.8, 31.6, 214 and 10.6, 15.7, 101.
 constexpr int kFewTokens = 4;
 
 int64_t delta_rule_workspace_bytes(const DeltaArgs& a) {

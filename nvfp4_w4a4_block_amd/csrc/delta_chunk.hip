@@ -614,11 +614,12 @@ void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
 
 // A CU holds one workgroup.  32 columns a workgroup spread a few heads over the most
 // CUs; where that gives more workgroups than there are CUs, 64 columns share a block's
-// operands, if LDS has room (4 sequences of 2,047 tokens, 48 heads of 128, bf16: 375 us
-// by 32 columns, 335 by 64).  Outputs are a block behind in long rounds, if LDS has room
-// (8,192 tokens of 48 heads, bf16: 435 -> 400 us; 3 of 4,099 of 8 heads of 64, fp32: 187
-// -> 157): they cost a block's outputs more at the end (2,048 tokens 104 -> 105 us, 512
-// tokens 37.7 -> 39.3).
+// operands, if LDS has room (48 heads of 128, bf16, us by 32 and by 64 columns: 4
+// sequences of 2,047 tokens 403, 365; 64 of 200 930, 733).  By 32 columns outputs are a
+// block behind, if LDS has room: all waves meet once a block, where those that are not
+// behind meet three times (8,192 tokens of 48 heads, bf16, 409 us and 450; 2,048 tokens
+// 101 and 105; 512 tokens 36.5 and 37.2; 3 of up to 4,099 of 8 heads of 64, fp32, 143 and
+// 167).
 template <int DK, bool BF16>
 void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
   if constexpr (BF16 && scan_lds<DK, BF16, 4, 2, 1>() <= kLds)
@@ -626,13 +627,12 @@ void scan(const DeltaArgs& a, const Round& r, int seqs, hipStream_t stream) {
       scan<DK, BF16, 4, 2, 1>(a, r, seqs, stream);
       return;
     }
-  if constexpr (scan_lds<DK, BF16, 2, 2, 2>() <= kLds)
-    if (r.c1 - r.c0 > 32) {
-      scan<DK, BF16, 2, 2, 2>(a, r, seqs, stream);
-      return;
-    }
-  constexpr int buffers = scan_lds<DK, BF16, 2, 2, 1>() <= kLds ? 2 : scan_lds<DK, BF16, 2, 1, 1>() <= kLds ? 1 : 0;
-  scan<DK, BF16, 2, buffers, 1>(a, r, seqs, stream);
+  if constexpr (scan_lds<DK, BF16, 2, 2, 2>() <= kLds) {
+    scan<DK, BF16, 2, 2, 2>(a, r, seqs, stream);
+  } else {
+    constexpr int buffers = scan_lds<DK, BF16, 2, 1, 1>() <= kLds ? 1 : 0;
+    scan<DK, BF16, 2, buffers, 1>(a, r, seqs, stream);
+  }
 }
 
 template <int DK, bool BF16>
