@@ -11,8 +11,8 @@
 // Bounds.  The walk is a chain of dependent products: a block's K S, T r and K^T X,
 // half of whose time is the matrix instructions' and the rest LDS and the rounding of
 // results into operands.  512 tokens of one sequence, 16 key and 48 value heads of 128,
-// bf16: 14.5 us of preparation and 24.5 of walking (memory's share is 5, the products' 1);
-// 3 sequences of up to 4,099 tokens, 4 and 8 heads of 64, fp32: 20 and 118.
+// bf16: 14.8 us of preparation and 23.8 of walking (memory's share is 5, the products' 1);
+// 3 sequences of up to 4,099 tokens, 4 and 8 heads of 64, fp32: 20 and 125.
 #include "delta_block.h"
 
 namespace nvfp4 {

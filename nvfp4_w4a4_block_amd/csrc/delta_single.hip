@@ -12,8 +12,9 @@
 // wait for their columns.
 //
 // Bounds.  Latency: one load, the block's inverse and the products behind it.  A tree
-// of 16 nodes, 16 key and 48 value heads of 128, bf16: 7.4 us on the device, of which
-// its 4.5 MB are 0.9; 16 trees of up to 33 fp32 nodes, 4 and 8 heads of 64: 10.5.
+// of 16 nodes, 16 key and 48 value heads of 128, bf16: 7.2 us on the device, of which
+// its 4.5 MB are 0.9; 16 trees of up to 33 fp32 nodes, 4 and 8 heads of 64: 10.1; one of
+// 64 fp32 nodes, 4 and 8 heads of 256, whose block takes a CU's whole LDS: 20.8.
 #include "delta_block.h"
 
 namespace nvfp4 {

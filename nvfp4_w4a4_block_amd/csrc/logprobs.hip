@@ -27,10 +27,11 @@
 // lists of first keys that are kept up batch by batch cost 26 us of 58 (512 rows of
 // 151,936, five alternatives) and 9 of 21 (16 rows, twenty).
 //
-// Bounds.  512 bf16 rows of 151,936: 40.4 us, 3.9 TB/s of 156 MB (32.5 us, 4.8 TB/s,
-// without alternatives, whose blocks are found and sorted behind the last logit).  16
-// fp32 rows, twenty alternatives: 7 us for the parts and 9 for the rows, of which the
-// 9.7 MB are 2: what is left is latency, of the launches, loads and sorts.
+// Bounds (us of calls one after the other).  512 bf16 rows of 151,936, five
+// alternatives: 39.7, 3.9 TB/s of 156 MB (32.5, 4.8 TB/s, without alternatives, whose
+// blocks are found and sorted behind the last logit).  16 fp32 rows, twenty alternatives:
+// 18.9, by trace 6.3 for the parts and 10.2 for the rows, of which the 9.7 MB are 2: what
+// is left is latency, of the launches, loads and sorts.
 #include <type_traits>
 
 #include "device_common.h"
@@ -48,6 +49,9 @@ struct Stat {
   float m, a, t;
 };
 
+// e^d of d <= 0: off by 2^-24 |d| of itself, from the product's rounding, and 2^-23.  A
+// term so far down weighs e^d; a second multiply-add for it would be one of nine
+// instructions a logit.
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2E); }
 
 __device__ __forceinline__ Stat join(const Stat& x, const Stat& y) {
@@ -555,10 +559,9 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_row_kernel(LogprobArgs a,
 
 // Parts of a row: one where there are rows enough for the chip (two workgroups a
 // CU), else as many as give it that, a batch for every wave at least.  With one, two
-// and four workgroups a CU, us, rows of 151,936: 16 fp32 with twenty alternatives 17.4,
-// 17.0, 16.7; 64 bf16 with five 19.5, 18.0, 18.7; 300 bf16 41.3, 37.5, 35.7; 512 bf16
-// 43.0, 42.6, 46.5 (two parts a row).  Columns are counted from the 16-byte border
-// before the row.
+// and four workgroups a CU, us a call, rows of 151,936: 16 fp32 with twenty alternatives
+// and 64 bf16 with five 18.9 to 19.0 each; 300 bf16 38.8, 36.0, 33.8; 512 bf16 39.6, 39.7,
+// 43.6 (two parts a row).  Columns are counted from the 16-byte border before the row.
 Plan plan_of(const LogprobArgs& a) {
   constexpr int batch = kWaves * kCols;
   const int columns = a.vocab + (a.bf16 ? 7 : 3);
