@@ -591,12 +591,12 @@ nvfp4_status nvfp4_kv_append_rope(int64_t B, int64_t M, int64_t Hq, int64_t H, i
  * tokens).  In products over a row's Dk values, and where a token's change is added to a
  * state, factors are split into f16 parts that keep 22 bits relative to their row's or
  * column's largest value.
- * What is not finite reaches what sees it and nothing else: a token's k, g (-infinity is
- * a decay like others) or beta its own outputs and updates, those of the tokens behind
- * it or its descendants, and the new state; its v the one of Dv columns of all these; its
- * q its own outputs; a row of a state that row and its column of the outputs.  There it
- * is NaN or infinite.  (Finite values whose sums overflow may reach their head's rows of
- * the same 64 tokens in their column.)
+ * What is not finite reaches what sees it and nothing else: a token's k as it is used
+ * (zeros with norm_eps 0 are not), g (-infinity is a decay like others) or beta its own
+ * outputs and updates, those of the tokens behind it or its descendants, and the new
+ * state; its v the one of Dv columns of all these; its q its own outputs; a row of a
+ * state that row and its column of the outputs.  There it is NaN or infinite.  (Finite values that overflow on the way may reach their head's
+ * rows of the same 64 tokens.)
  * Cites: the page section "Reusing KV cache across agent turns" (the model is a
  * hybrid; its recurrent states are kept and restored with the cached pages). */
 

@@ -210,7 +210,7 @@ __device__ __forceinline__ void load_row(const void* rows, int64_t at, RawRow<DK
 
 // The row as an operand, zeros where it is not there.  Returns the factor that makes
 // the stored row the row as used; `as_used` (or NULL) is where that goes.  `lost` (or
-// NULL): whether the row is not finite, in which case it is as if it were not there.
+// NULL): whether the row as used is not finite; then it is as if it were not there.
 template <int DK, bool BF16>
 __device__ __forceinline__ float row_operand(const RawRow<DK, BF16>& raw, bool there, float eps,
                                              h8_t (&op)[BF16 ? 1 : 2][DK / 32], float* as_used = nullptr,
@@ -264,7 +264,8 @@ __device__ __forceinline__ float row_operand(const RawRow<DK, BF16>& raw, bool t
             there ? x[s][h] * factor : f4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
   if (lost) {
-    *lost = !finite(ss);  // of a finite row it is 4 DK at most
+    // of a finite row ss is 4 DK at most; a row of zeros without eps has no factor
+    *lost = there && !(finite(ss) && finite(factor));
     if (__any(*lost)) {
 #pragma unroll
       for (int part = 0; part < (BF16 ? 1 : 2); ++part)

@@ -242,6 +242,31 @@ def test_a_spoilt_row_of_a_state_stays_in_its_column(dtype, M, value):
     assert torch.equal(states, ref_states)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M", [4, 9, 40, 64, 100])
+def test_a_key_that_has_no_direction_reaches_what_sees_it(dtype, M):
+    """Zeros divided by their length with norm_eps 0 are NaN: of that token's key head, from that token on."""
+    c = T.Delta(dtype, 2, M, 2, 4, 64, 64, src=[0, 1], dst=[2, 3], slots=4, seed=M)
+    c.eps = 0.0
+    parent = T.random_trees(np.random.default_rng(M), 2, M)
+    parent[:, 2] = 0
+    ref, ref_states = (x.clone() for x in c.chain())
+    tree_ref = [x.clone() for x in T.run_tree(c, parent)] if M <= 64 else None
+    c.k[0, 2, 0] = 0
+    out, states = c.chain()
+    hit = torch.zeros((2, M, 4, 64), dtype=torch.bool, device=T.DEV)
+    hit[0, 2:, :2] = True
+    assert torch.equal(out[~hit], ref[~hit]) and not out[hit].float().isfinite().any()
+    assert torch.equal(states[3], ref_states[3]) and torch.equal(states[2, 2:], ref_states[2, 2:])
+    assert not states[2, :2].isfinite().all(-1).any()
+    if tree_ref:
+        out, keys, updates = T.run_tree(c, parent)
+        hit[0] = False
+        hit[0, torch.from_numpy(np.flatnonzero(lines_of(parent[0])[:, 2])).to(T.DEV), :2] = True
+        for got, want in ((out, tree_ref[0]), (updates, tree_ref[2])):
+            assert torch.equal(got[~hit], want[~hit]) and not got[hit].float().isfinite().any()
+
+
 @pytest.mark.parametrize("M", [3, 20, 100])
 def test_a_spoilt_state_without_tokens_is_copied_as_it_is(M):
     c = T.Delta(FP, 2, M, 1, 2, 64, 64, counts=[0, M], src=[0, 1], dst=[2, 3], slots=4, seed=M)
